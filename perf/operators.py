@@ -329,9 +329,10 @@ def _pack(x):
     v = torch.nn.functional.pad(x.float(), (0, pad)).unflatten(-1, (-1, GROUP))
     amax = v.abs().amax(-1)
     keep = ~(amax < 1e-30)
-    inv = torch.where(keep, 127.0 / amax, torch.zeros_like(amax))
+    top = torch.full_like(amax, 127.0)     # divided as tensors: not by way of a reciprocal
+    inv = torch.where(keep, top / amax, torch.zeros_like(amax))
     q = torch.round(v * inv[..., None]).to(torch.int8).flatten(-2)[..., :n].contiguous()
-    return q, torch.where(keep, amax / 127.0, torch.zeros_like(amax))
+    return q, torch.where(keep, amax / top, torch.zeros_like(amax))
 
 
 def _unpack(q, sc):
