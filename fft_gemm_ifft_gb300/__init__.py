@@ -1,10 +1,11 @@
 """GB300 (sm_103a) Fourier Neural Operator spectral-convolution library.
 
 The compute lives in ``libfno.so`` (hand-written CUDA, C ABI in
-``include/fno.h``).  This package only marshals arguments: ``capi`` mirrors
-the C entry points one to one, and the two small classes below hold a plan
-plus a torch-allocated workspace and pass tensor pointers and the current
-stream to the library.  PyTorch is used for device memory and streams only.
+``include/fno.h`` and ``include/fno_ops.h``).  This package only marshals
+arguments: ``capi`` mirrors the C entry points one to one, and the two small
+classes below (and those of ``sequence``) hold a plan plus a torch-allocated
+workspace and pass tensor pointers and the current stream to the library.
+PyTorch is used for device memory and streams only.
 """
 from __future__ import annotations
 
@@ -12,7 +13,17 @@ from . import capi
 from .capi import (FNO_BF16, FNO_F16, FNO_F32, FNO_PLAN_DEFAULT,  # noqa: F401
                    FNO_PLAN_UNFUSED, fno_status_string)
 
-__all__ = ["capi", "FnoError", "SpectralConv", "FnoModel", "check"]
+_SEQUENCE = ("SandwichNorm", "PackedActivation", "pack_activation", "LinearGrad",
+             "LinearAttention")
+__all__ = ["capi", "FnoError", "SpectralConv", "FnoModel", "check", *_SEQUENCE]
+
+
+def __getattr__(name):
+    # the sequence operators, loaded at first use (their module imports torch)
+    if name in _SEQUENCE:
+        from . import sequence
+        return getattr(sequence, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class FnoError(RuntimeError):

@@ -39,7 +39,14 @@ FNO_PLAN_PACKED_WEIGHTS = 128
 FNO_PLAN_TENSOR_EXTRA = 256
 FNO_PLAN_SPLIT_LAYER = 512
 
-# Every symbol include/fno.h declares.
+# include/fno_ops.h
+FNO_ACT8_GROUP = 128
+FNO_LINATTN_BACKWARD = 1
+LAYOUT_CODES = {"grid": 0, "tokens": 1}
+NORM_CODES = {"rms": 0, "layer": 1}
+GATE_CODES = {"none": 0, "channel": 1, "full": 2}
+
+# Every symbol include/fno.h and include/fno_ops.h declare.
 EXPORTS = (
     "fno_status_string", "fno_version",
     "fno_spectral_conv_query", "fno_spectral_conv_plan",
@@ -50,6 +57,14 @@ EXPORTS = (
     "fno_spectral_conv_pack_weights", "fno_plan_check_bounded_wait",
     "fno_model_plan", "fno_model_workspace_size", "fno_model_kernel_count",
     "fno_forward", "fno_model_get_device_error", "fno_model_destroy",
+    "fno_sandwich_plan", "fno_sandwich_workspace_size", "fno_sandwich_forward",
+    "fno_sandwich_backward", "fno_sandwich_destroy",
+    "fno_act8_pack", "fno_act8_unpack", "fno_act8_gelu_backward",
+    "fno_linear_grad_plan", "fno_linear_grad_workspace_size", "fno_linear_grad",
+    "fno_linear_grad_get_device_error", "fno_linear_grad_destroy",
+    "fno_linattn_plan", "fno_linattn_workspace_size", "fno_linattn_forward",
+    "fno_linattn_backward", "fno_linattn_step", "fno_linattn_get_device_error",
+    "fno_linattn_destroy",
 )
 
 _vp = ctypes.c_void_p
@@ -63,6 +78,14 @@ class fno_model_desc_t(ctypes.Structure):
                 ("h", ctypes.c_int64), ("w", ctypes.c_int64),
                 ("modes", ctypes.c_int32 * 2), ("dtype", ctypes.c_int),
                 ("flags", ctypes.c_uint32)]
+
+
+class fno_sandwich_desc_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("points", ctypes.c_int64),
+                ("channels", ctypes.c_int32), ("layout", ctypes.c_int),
+                ("norm", ctypes.c_int), ("gate", ctypes.c_int),
+                ("gate_sigmoid", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int)]
 
 
 class fno_trace_record_t(ctypes.Structure):
@@ -134,6 +157,26 @@ def lib() -> ctypes.CDLL:
             L.fno_forward.argtypes = [_vp, _vp, ctypes.POINTER(fno_model_params_t), _vp, _vp, _vp]
             L.fno_model_get_device_error.argtypes = [_vp, _vp]
             L.fno_model_destroy.argtypes = [_vp]
+            pvp, i64, i32, f32 = (ctypes.POINTER(_vp), ctypes.c_int64, ctypes.c_int32,
+                                  ctypes.c_float)
+            L.fno_sandwich_plan.argtypes = [pvp, ctypes.POINTER(fno_sandwich_desc_t)]
+            L.fno_sandwich_forward.argtypes = [_vp] * 14
+            L.fno_sandwich_backward.argtypes = [_vp] * 22
+            L.fno_act8_pack.argtypes = [i64, i64, _st] + [_vp] * 4
+            L.fno_act8_unpack.argtypes = [i64, i64, _st] + [_vp] * 4
+            L.fno_act8_gelu_backward.argtypes = [i64, i64, _st] + [_vp] * 5
+            L.fno_linear_grad_plan.argtypes = [pvp, i64, i32, i32, i64, _st]
+            L.fno_linear_grad.argtypes = [_vp] * 8
+            L.fno_linattn_plan.argtypes = [pvp, i64, i64, i32, i32, i32, i32, _st,
+                                           ctypes.c_uint32]
+            L.fno_linattn_forward.argtypes = [_vp] * 5 + [f32] + [_vp] * 6
+            L.fno_linattn_backward.argtypes = [_vp] * 5 + [f32] + [_vp] * 10
+            L.fno_linattn_step.argtypes = [_vp] * 5 + [f32, _vp, i64] + [_vp] * 4
+            for name in ("sandwich", "linear_grad", "linattn"):
+                getattr(L, f"fno_{name}_workspace_size").argtypes = [_vp, psz]
+                getattr(L, f"fno_{name}_destroy").argtypes = [_vp]
+            for name in ("linear_grad", "linattn"):
+                getattr(L, f"fno_{name}_get_device_error").argtypes = [_vp, _vp]
             for name in EXPORTS[2:]:
                 getattr(L, name).restype = _st
             _lib = L
@@ -270,3 +313,104 @@ def fno_model_get_device_error(model, stream):
 
 def fno_model_destroy(model):
     return lib().fno_model_destroy(model)
+
+
+def fno_sandwich_plan(desc: fno_sandwich_desc_t):
+    h = _vp(0)
+    st = lib().fno_sandwich_plan(ctypes.byref(h), ctypes.byref(desc))
+    return st, h.value
+
+
+def fno_sandwich_workspace_size(plan):
+    v = ctypes.c_size_t(0)
+    return lib().fno_sandwich_workspace_size(plan, ctypes.byref(v)), v.value
+
+
+def fno_sandwich_forward(plan, x_ptr, f_ptr, gate_ptr, s_ptr, w2_ptr, b2_ptr, w1_ptr, b1_ptr,
+                         y_ptr, u_ptr, f8_ptr, f8_scale_ptr, stream):
+    return lib().fno_sandwich_forward(plan, x_ptr, f_ptr, gate_ptr, s_ptr, w2_ptr, b2_ptr, w1_ptr,
+                                      b1_ptr, y_ptr, u_ptr, f8_ptr, f8_scale_ptr, stream)
+
+
+def fno_sandwich_backward(plan, *ptrs_and_stream):
+    return lib().fno_sandwich_backward(plan, *ptrs_and_stream)
+
+
+def fno_sandwich_destroy(plan):
+    return lib().fno_sandwich_destroy(plan)
+
+
+def fno_act8_pack(rows, cols, dtype, x_ptr, codes_ptr, scales_ptr, stream):
+    return lib().fno_act8_pack(rows, cols, dtype, x_ptr, codes_ptr, scales_ptr, stream)
+
+
+def fno_act8_unpack(rows, cols, dtype, codes_ptr, scales_ptr, x_ptr, stream):
+    return lib().fno_act8_unpack(rows, cols, dtype, codes_ptr, scales_ptr, x_ptr, stream)
+
+
+def fno_act8_gelu_backward(rows, cols, dtype, codes_ptr, scales_ptr, dy_ptr, dx_ptr, stream):
+    return lib().fno_act8_gelu_backward(rows, cols, dtype, codes_ptr, scales_ptr, dy_ptr, dx_ptr,
+                                        stream)
+
+
+def fno_linear_grad_plan(batch, cin, cout, points, dtype):
+    h = _vp(0)
+    st = lib().fno_linear_grad_plan(ctypes.byref(h), batch, cin, cout, points, dtype)
+    return st, h.value
+
+
+def fno_linear_grad_workspace_size(plan):
+    v = ctypes.c_size_t(0)
+    return lib().fno_linear_grad_workspace_size(plan, ctypes.byref(v)), v.value
+
+
+def fno_linear_grad(plan, dy_ptr, codes_ptr, scales_ptr, dw_ptr, db_ptr, ws_ptr, stream):
+    return lib().fno_linear_grad(plan, dy_ptr, codes_ptr, scales_ptr, dw_ptr, db_ptr, ws_ptr,
+                                 stream)
+
+
+def fno_linear_grad_get_device_error(plan, stream):
+    return lib().fno_linear_grad_get_device_error(plan, stream)
+
+
+def fno_linear_grad_destroy(plan):
+    return lib().fno_linear_grad_destroy(plan)
+
+
+def fno_linattn_plan(batch, length, heads, kv_heads, dk, dv, dtype, flags=0):
+    h = _vp(0)
+    st = lib().fno_linattn_plan(ctypes.byref(h), batch, length, heads, kv_heads, dk, dv, dtype,
+                                flags)
+    return st, h.value
+
+
+def fno_linattn_workspace_size(plan):
+    v = ctypes.c_size_t(0)
+    return lib().fno_linattn_workspace_size(plan, ctypes.byref(v)), v.value
+
+
+def fno_linattn_forward(plan, q_ptr, k_ptr, v_ptr, decay_ptr, scale, lengths_ptr, s0_ptr, o_ptr,
+                        sT_ptr, ws_ptr, stream):
+    return lib().fno_linattn_forward(plan, q_ptr, k_ptr, v_ptr, decay_ptr, scale, lengths_ptr,
+                                     s0_ptr, o_ptr, sT_ptr, ws_ptr, stream)
+
+
+def fno_linattn_backward(plan, q_ptr, k_ptr, v_ptr, decay_ptr, scale, lengths_ptr, s0_ptr, go_ptr,
+                         gsT_ptr, dq_ptr, dk_ptr, dv_ptr, ds0_ptr, ws_ptr, stream):
+    return lib().fno_linattn_backward(plan, q_ptr, k_ptr, v_ptr, decay_ptr, scale, lengths_ptr,
+                                      s0_ptr, go_ptr, gsT_ptr, dq_ptr, dk_ptr, dv_ptr, ds0_ptr,
+                                      ws_ptr, stream)
+
+
+def fno_linattn_step(plan, q_ptr, k_ptr, v_ptr, decay_ptr, scale, slots_ptr, num_slots, state_ptr,
+                     new_state_ptr, o_ptr, stream):
+    return lib().fno_linattn_step(plan, q_ptr, k_ptr, v_ptr, decay_ptr, scale, slots_ptr,
+                                  num_slots, state_ptr, new_state_ptr, o_ptr, stream)
+
+
+def fno_linattn_get_device_error(plan, stream):
+    return lib().fno_linattn_get_device_error(plan, stream)
+
+
+def fno_linattn_destroy(plan):
+    return lib().fno_linattn_destroy(plan)

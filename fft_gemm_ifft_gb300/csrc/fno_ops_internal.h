@@ -1,0 +1,119 @@
+// fno_ops_internal.h -- shared host and device helpers of the operators
+// declared in fno_ops.h (not installed).
+#pragma once
+
+#include <cstdlib>
+#include <cstring>
+#include <initializer_list>
+#include <new>
+#include <type_traits>
+
+#include "fno_internal.cuh"
+#include "fno_ops.h"
+
+namespace fno {
+namespace ops {
+
+constexpr double kMaxElems = 4398046511104.0;   // 2^42: int64 offsets stay far from overflow
+constexpr int kGroup = FNO_ACT8_GROUP;
+
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool valid_dtype(fno_dtype_t t) { return t == FNO_F32 || t == FNO_F16 || t == FNO_BF16; }
+inline size_t elem_bytes(fno_dtype_t t) { return t == FNO_F32 ? 4 : 2; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Host-side fault injection of the failure-path tests (as in the spectral
+// calls): FNO_FAULT_INJECT names the site at which the library behaves as if
+// the CUDA call there had failed.
+inline bool inject(const char *site) {
+    const char *v = std::getenv("FNO_FAULT_INJECT");
+    return v && std::strcmp(v, site) == 0;
+}
+
+// An operand of a call: its bytes, whether the call writes it, and an input
+// that it may coincide with exactly (an in-place update).
+struct Operand {
+    const void *p;
+    size_t bytes;
+    bool out;
+    const void *same = nullptr;
+};
+
+// MISALIGNED / ALIASING checks over a call's operands (NULL ones are absent).
+inline fno_status_t check_operands(std::initializer_list<Operand> all) {
+    for (const Operand &a : all)
+        if (!aligned16(a.p)) return FNO_ERR_MISALIGNED;
+    for (const Operand &a : all) {
+        if (!a.out || !a.p) continue;
+        for (const Operand &b : all) {
+            if (&a == &b || !b.p || (b.p == a.p && a.same == b.p && !b.out)) continue;
+            const char *pa = static_cast<const char *>(a.p), *pb = static_cast<const char *>(b.p);
+            if (pa < pb + b.bytes && pb < pa + a.bytes) return FNO_ERR_ALIASING;
+        }
+    }
+    return FNO_OK;
+}
+
+// The status of the launches since the last check; clears the CUDA error.
+inline fno_status_t launched() {
+    return cudaGetLastError() == cudaSuccess ? FNO_OK : FNO_ERR_CUDA;
+}
+
+// The number of SMs of the current device.
+inline fno_status_t device_sms(int *sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return FNO_ERR_CUDA;
+    }
+    return FNO_OK;
+}
+
+// Plan-owned device error word (as the spectral plans': first error wins).
+inline fno_status_t make_error_word(int **word) {
+    if (inject("plan_alloc")) return FNO_ERR_OUT_OF_MEMORY;
+    if (cudaMalloc(word, 256) != cudaSuccess) {
+        cudaGetLastError();
+        *word = nullptr;
+        return FNO_ERR_OUT_OF_MEMORY;
+    }
+    if (cudaMemset(*word, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(*word);
+        *word = nullptr;
+        return FNO_ERR_CUDA;
+    }
+    return FNO_OK;
+}
+inline fno_status_t read_error_word(int *word, fno_stream_t stream) {
+    int v = 0;
+    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        cudaMemcpy(&v, word, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
+        cudaMemset(word, 0, sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        return FNO_ERR_CUDA;
+    }
+    return v == kDevTimeout ? FNO_ERR_DEVICE_TIMEOUT : v == kDevBounds ? FNO_ERR_DEVICE_BOUNDS
+                                                                       : FNO_OK;
+}
+
+// The 8-bit code of a group's elements: scale = m / 127, code = rint(x (127 / m)),
+// with IEEE division and multiplication so that the codes are those of the
+// written formula.  `mbits` = the largest |x| of the group as its bit pattern
+// (unsigned order: NaN above infinity above every finite value).
+struct Group8 {
+    float scale, inv;
+};
+__device__ __forceinline__ Group8 group8(uint32_t mbits) {
+    const float m = __uint_as_float(mbits);
+    const bool keep = !(m < 1e-30f);
+    return {keep ? __fdiv_rn(m, 127.0f) : 0.0f, keep ? __fdiv_rn(127.0f, m) : 0.0f};
+}
+__device__ __forceinline__ int code8(float x, float inv) {
+    return __float2int_rn(__fmul_rn(x, inv));
+}
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+}  // namespace ops
+}  // namespace fno
