@@ -13,66 +13,197 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One warp per group of 128 elements, lane l on elements l, l + 32, ...
+// Rows whose length is a multiple of a 16-byte load: 128 / kVec lanes hold a
+// group, each one load of it, so a warp packs 1 (float32) or 2 groups a step,
+// and takes four steps' loads before the first is used.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 k_act8_pack(const T *__restrict__ x, int8_t *__restrict__ codes, float *__restrict__ scales,
             int64_t cols, int64_t groups_per_row, int64_t groups) {
-    const int lane = threadIdx.x & 31;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t g = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); g < groups;
-         g += step) {
-        const int64_t row = g / groups_per_row, c0 = (g - row * groups_per_row) * kGroup;
-        const int64_t base = row * cols + c0;
-        const int n = (int)min((int64_t)kGroup, cols - c0);
+    constexpr int V = kVec<T>, L = kGroup / V, N = 32 / L, U = 4;
+    const int lane = threadIdx.x & 31, sub = lane / L, off = (lane % L) * V;
+    const uint32_t mask = L == 32 ? 0xffffffffu : 0xffffu << (16 * sub);
+    const int64_t first = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * (N * U);
+    Pack<T, V> d[U];
+    int64_t at[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int64_t g = first + k * N + sub, row = g / groups_per_row;
+        const int64_t c = (g - row * groups_per_row) * kGroup + off;
+        at[k] = g < groups && c < cols ? row * cols + c : -1;
+        if (at[k] >= 0) d[k] = *reinterpret_cast<const Pack<T, V> *>(x + at[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        float v[V];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] = at[k] >= 0 ? Storage<T>::load(&d[k].v[i]) : 0.0f;
+            m = max(m, abs_bits(v[i]));
+        }
+        m = __reduce_max_sync(mask, m);
+        const Group8 s = group8(m);
+        Pack<int8_t, V> q;
+#pragma unroll
+        for (int i = 0; i < V; ++i) q.v[i] = (int8_t)code8(v[i], s.inv);
+        if (at[k] >= 0) {
+            *reinterpret_cast<Pack<int8_t, V> *>(codes + at[k]) = q;
+            if (off == 0) scales[first + k * N + sub] = s.scale;
+        }
+    }
+}
+
+// Rows of any length: consecutive groups are consecutive in memory, so a CTA
+// brings 32 groups in by aligned 16-byte loads of the range that they cover,
+// packs them from shared memory, and writes the codes back by aligned 16-byte
+// stores (single bytes at the two ends).
+constexpr int kStage = 32;    // groups
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+k_act8_pack_any(const T *__restrict__ x, int8_t *__restrict__ codes, float *__restrict__ scales,
+                int64_t cols, int64_t groups_per_row, int64_t groups, int64_t n) {
+    constexpr int V = kVec<T>;
+    __shared__ alignas(16) T sx[kStage * kGroup + V];
+    __shared__ alignas(16) int8_t sq[kStage * kGroup + 16];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t g0 = (int64_t)blockIdx.x * kStage, g1 = min(groups, g0 + kStage);
+    const auto start = [&](int64_t g) {
+        const int64_t row = g / groups_per_row;
+        return row * cols + (g - row * groups_per_row) * kGroup;
+    };
+    const int64_t e0 = start(g0), e1 = start(g1);      // elements (start(groups) = n)
+    const int64_t a0 = e0 / V * V;
+    for (int64_t e = a0 + (int64_t)threadIdx.x * V; e < e1; e += (int64_t)kThreads * V) {
+        if (e + V <= n) {
+            *reinterpret_cast<Pack<T, V> *>(sx + (e - a0)) =
+                *reinterpret_cast<const Pack<T, V> *>(x + e);
+        } else {
+            for (int i = 0; i < V && e + i < n; ++i) sx[e - a0 + i] = x[e + i];
+        }
+    }
+    __syncthreads();
+    const int64_t c0 = e0 / 16 * 16;                   // the codes' 16-byte window
+#pragma unroll
+    for (int k = 0; k < kStage / 8; ++k) {
+        const int64_t g = g0 + w + 8 * k;
+        if (g >= g1) break;
+        const int64_t b = start(g);
+        const int len = (int)(start(g + 1) - b);
+        const T *src = sx + (b - a0);
         float v[4];
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = lane + 32 * j;
-            v[j] = e < n ? Storage<T>::load(x + base + e) : 0.0f;
+            v[j] = lane + 32 * j < len ? Storage<T>::load(src + lane + 32 * j) : 0.0f;
             m = max(m, abs_bits(v[j]));
         }
         m = __reduce_max_sync(0xffffffffu, m);
         const Group8 s = group8(m);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = lane + 32 * j;
-            if (e < n) codes[base + e] = (int8_t)code8(v[j], s.inv);
-        }
+        for (int j = 0; j < 4; ++j)
+            if (lane + 32 * j < len) sq[b - c0 + lane + 32 * j] = (int8_t)code8(v[j], s.inv);
         if (lane == 0) scales[g] = s.scale;
+    }
+    __syncthreads();
+    for (int64_t e = c0 + (int64_t)threadIdx.x * 16; e < e1; e += (int64_t)kThreads * 16) {
+        if (e >= e0 && e + 16 <= e1) {
+            *reinterpret_cast<uint4 *>(codes + e) = *reinterpret_cast<uint4 *>(sq + (e - c0));
+        } else {
+            for (int i = 0; i < 16; ++i)
+                if (e + i >= e0 && e + i < e1) codes[e + i] = sq[e - c0 + i];
+        }
     }
 }
 
 // Derivative of GELU: Phi(v) + v phi(v), the normal distribution and density.
+// 1 - erf is Abramowitz & Stegun 7.1.26, poly(t) e^{-x^2} with x = |v| / sqrt 2
+// (absolute error 1.5e-7, as in fno_gelu.cuh), whose exponential is also the
+// density's: one exponential and one reciprocal an element, where erfcf and
+// expf would make the arithmetic cost more than the bytes.
 __device__ __forceinline__ float gelu_slope(float v) {
-    const float phi = 0.3989422804014327f * expf(-0.5f * v * v);
-    return fmaf(v, phi, 0.5f * erfcf(-0.70710678118654752f * v));
+    constexpr float p = 0.3275911f * 0.70710678118654752f;
+    constexpr float a1 = 0.254829592f, a2 = -0.284496736f, a3 = 1.421413741f,
+                    a4 = -1.453152027f, a5 = 1.061405429f;
+    const float m = fabsf(v);
+    const float t = __fdividef(1.0f, fmaf(p, m, 1.0f));
+    const float e = __expf(-0.5f * m * m);
+    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, a5, a4), a3), a2), a1);
+    const float half = 0.5f * q * e;                   // Phi(-|v|)
+    return fmaf(v * 0.3989422804014327f, e, v < 0.0f ? half : 1.0f - half);
 }
 
-
-// out = value, or dy * GELU'(value), element by element
-template <typename T, bool GELU>
+// out = value, or dy * GELU'(value).  The tensors are walked as flat arrays by
+// 16-byte vectors of the storage type whatever the row length; a vector that
+// crosses a group's or a row's end looks its scales up one by one.  I: 32 bits
+// where the element count allows (the division by the row length is the
+// largest part of the index arithmetic).
+template <typename T, bool GELU, typename I>
 __global__ void __launch_bounds__(kThreads)
 k_act8_read(const int8_t *__restrict__ codes, const float *__restrict__ scales, const T *dy,
-            T *out, int64_t cols, int64_t groups_per_row, int64_t n) {
-    const int64_t step = (int64_t)gridDim.x * kThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-        const int64_t row = i / cols, c = i - row * cols;
-        const float v = (float)codes[i] * scales[row * groups_per_row + c / kGroup];
-        Storage<T>::store(out + i, GELU ? Storage<T>::load(dy + i) * gelu_slope(v) : v);
+            T *out, I cols, I groups_per_row, I n) {
+    constexpr int V = kVec<T>, U = 2;
+    const I block = (I)blockIdx.x * (kThreads * V * U);
+    Pack<int8_t, V> q[U];
+    Pack<T, V> d[U];
+    I first[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        first[k] = block + (I)(k * kThreads + threadIdx.x) * V;
+        if (first[k] < n && n - first[k] >= V) {
+            q[k] = *reinterpret_cast<const Pack<int8_t, V> *>(codes + first[k]);
+            if (GELU) d[k] = *reinterpret_cast<const Pack<T, V> *>(dy + first[k]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (first[k] < n && (I)i < n - first[k]) {
+                    q[k].v[i] = codes[first[k] + i];
+                    if (GELU) d[k].v[i] = dy[first[k] + i];
+                }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (first[k] >= n) continue;
+        const I row = first[k] / cols, col = first[k] - row * cols;
+        const bool one = cols - col >= V && col % kGroup <= kGroup - V;
+        const bool whole = n - first[k] >= V;
+        I at = row * groups_per_row + col / kGroup;
+        float s = scales[at];
+        I c = col;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!one && i > 0 && (whole || (I)i < n - first[k])) {
+                ++c;
+                if (c == cols) {
+                    c = 0;
+                    s = scales[++at];          // a row's first group follows the last row's last
+                } else if (c % kGroup == 0) {
+                    s = scales[++at];
+                }
+            }
+            const float v = (float)q[k].v[i] * s;
+            const float r = GELU ? Storage<T>::load(&d[k].v[i]) * gelu_slope(v) : v;
+            Storage<T>::store(&d[k].v[i], r);
+        }
+        if (whole) {
+            *reinterpret_cast<Pack<T, V> *>(out + first[k]) = d[k];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if ((I)i < n - first[k]) out[first[k] + i] = d[k].v[i];
+        }
     }
 }
 
 fno_status_t check_shape(int64_t rows, int64_t cols, fno_dtype_t dtype) {
     if (rows < 1 || cols < 1 || !valid_dtype(dtype)) return FNO_ERR_INVALID_ARG;
-    if ((double)rows * (double)cols > kMaxElems) return FNO_ERR_UNSUPPORTED;
+    // (the second: a grid of 32 groups a block)
+    if ((double)rows * (double)cols > kMaxElems ||
+        (double)rows * (double)ceil_div(cols, kGroup) > 32.0 * 2147483647.0)
+        return FNO_ERR_UNSUPPORTED;
     return FNO_OK;
-}
-
-int blocks_for(int64_t items, int64_t per_block) {
-    const int64_t b = ceil_div(items, per_block);
-    return (int)(b < 152 * 8 ? b : 152 * 8);
 }
 
 template <bool GELU>
@@ -89,9 +220,17 @@ fno_status_t read_call(int64_t rows, int64_t cols, fno_dtype_t dtype, const int8
     if (inject("launch")) return FNO_ERR_CUDA;
     with_storage(dtype, [&](auto t) {
         using T = decltype(t);
-        k_act8_read<T, GELU><<<blocks_for(n, kThreads), kThreads, 0,
-                               reinterpret_cast<cudaStream_t>(stream)>>>(
-            codes, scales, static_cast<const T *>(dy), static_cast<T *>(out), cols, gpr, n);
+        const unsigned blocks = (unsigned)ceil_div(n, (int64_t)kThreads * kVec<T> * 2);
+        const auto launch = [&](auto i) {
+            using I = decltype(i);
+            k_act8_read<T, GELU, I><<<blocks, kThreads, 0,
+                                      reinterpret_cast<cudaStream_t>(stream)>>>(
+                codes, scales, static_cast<const T *>(dy), static_cast<T *>(out), (I)cols, (I)gpr,
+                (I)n);
+        };
+        // a block's first element may lie a block beyond n
+        if (n < (int64_t)1 << 31) launch(uint32_t());
+        else launch(uint64_t());
     });
     return launched();
 }
@@ -112,9 +251,16 @@ fno_status_t fno_act8_pack(int64_t rows, int64_t cols, fno_dtype_t dtype, const 
     if (inject("launch")) return FNO_ERR_CUDA;
     with_storage(dtype, [&](auto t) {
         using T = decltype(t);
-        k_act8_pack<T><<<blocks_for(rows * gpr, kThreads / 32), kThreads, 0,
-                         reinterpret_cast<cudaStream_t>(stream)>>>(
-            static_cast<const T *>(x), codes, scales, cols, gpr, rows * gpr);
+        cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+        const int64_t groups = rows * gpr;
+        if (cols % kVec<T> == 0) {
+            const int64_t per = (kThreads / 32) * 4 * (kVec<T> * 32 / kGroup);
+            k_act8_pack<T><<<(unsigned)ceil_div(groups, per), kThreads, 0, cs>>>(
+                static_cast<const T *>(x), codes, scales, cols, gpr, groups);
+        } else {
+            k_act8_pack_any<T><<<(unsigned)ceil_div(groups, kStage), kThreads, 0, cs>>>(
+                static_cast<const T *>(x), codes, scales, cols, gpr, groups, n);
+        }
     });
     return launched();
 }

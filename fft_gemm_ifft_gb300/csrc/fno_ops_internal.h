@@ -14,7 +14,7 @@
 namespace fno {
 namespace ops {
 
-constexpr double kMaxElems = 4398046511104.0;   // 2^42: int64 offsets stay far from overflow
+constexpr double kMaxElems = 274877906944.0;    // 2^38: a byte each would fill the GPU
 constexpr int kGroup = FNO_ACT8_GROUP;
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -97,6 +97,12 @@ inline fno_status_t read_error_word(int *word, fno_stream_t stream) {
     return v == kDevTimeout ? FNO_ERR_DEVICE_TIMEOUT : v == kDevBounds ? FNO_ERR_DEVICE_BOUNDS
                                                                        : FNO_OK;
 }
+
+// Elements of one 16-byte load, and a run of N elements moved as one (in
+// 16-byte pieces at most: operands are no better aligned).
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+template <typename T, int N>
+struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Pack { T v[N]; };
 
 // The 8-bit code of a group's elements: scale = m / 127, code = rint(x (127 / m)),
 // with IEEE division and multiplication so that the codes are those of the

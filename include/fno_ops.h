@@ -74,7 +74,7 @@ typedef struct fno_sandwich_desc_s {
 } fno_sandwich_desc_t;
 
 /* Validate the description and make a plan (host memory only).  *plan is NULL
- * on failure.  Errors: INVALID_ARG, UNSUPPORTED (more than 2^42 elements),
+ * on failure.  Errors: INVALID_ARG, UNSUPPORTED (more than 2^38 elements),
  * OUT_OF_MEMORY, CUDA.                                                        */
 fno_status_t fno_sandwich_plan(fno_sandwich_t *plan, const fno_sandwich_desc_t *desc);
 
@@ -132,7 +132,7 @@ fno_status_t fno_sandwich_destroy(fno_sandwich_t plan);
  * a code is code * scale, at most m / 254 (and rounding) from x.  A group that
  * holds a NaN or an infinity has that scale, and reads back as NaN.
  * codes: int8, rows x cols.  scales: float32, rows x ceil(cols / GROUP).
- * rows, cols >= 1, at most 2^42 elements (FNO_ERR_UNSUPPORTED).
+ * rows, cols >= 1, at most 2^38 elements (else FNO_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 #define FNO_ACT8_GROUP 128
 
