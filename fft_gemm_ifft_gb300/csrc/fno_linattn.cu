@@ -21,11 +21,14 @@ struct fno_linattn_s {
     int *dev_err;
     size_t workspace;
     size_t group_off[2];     // backward with shared heads: dk, dv of every query head
+    int segments;            // parts of the time axis that run side by side
+    int64_t seg_len;
 };
 
 namespace {
 
 constexpr int kMaxWidth = 256;
+constexpr int kChunkWidth = 128;     // widest key of the chunked kernel
 
 // One scan of the recurrence  Z = gamma Z + kw k_t v_t^T,  o_t = qw q_t Z + ...
 // over one (sequence, query head, slice of 8 value columns): a warp per value
@@ -101,11 +104,446 @@ __global__ void __launch_bounds__(256) k_linattn_scan(ScanArgs a) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// The scan in chunks of 64 tokens, on the tensor cores.  Within a chunk, with
+// Z the state in front of it and g_i = gamma^i,
+//   O = diag(g_{i+1}) Q Z + (Q K^T * [i >= j] g_{i-j}) V
+//   Z <- gamma^64 Z + sum_j g_{63-j} k_j v_j^T
+// (a reversed scan: g_i in the first, g_{64-j} in the last).  Every exponent is
+// >= 0, so nothing overflows.
+//
+// Numbers.  Operands are sums of bfloat16 terms: 1 for bfloat16 inputs, 2 for
+// fp16 (exact: 11 bits in 16), 3 for float32 (24 bits), and products of terms
+// below the result's own rounding are left out (i + j > L).  All sums are
+// float32.  For bfloat16 the chunk's weights and the state in front of it are
+// rounded to one term (the size of the output's own rounding); the state itself
+// is carried in float32 and its update takes the decayed values in three terms,
+// so that a final state has float32's digits.
+//
+// A warp owns 16 rows of the transposed state Z^T (value columns x key rows) in
+// registers, in the accumulator layout, which is also the layout of the left
+// operand of O^T = Z^T Q^T: the state never leaves the registers.  V^T is the
+// other left operand, of O^T += V^T P^T and of the update, read with a
+// transposing ldmatrix; the chunk's weights P go through shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kC = 64;
+
+struct ChunkArgs {
+    ScanArgs s;
+    float *states;             // [b, h, segment][e][a]: local, then initial states
+    int segments;
+    int64_t seg_len;
+    float scale_p;             // of a chunk's weights
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two floats as the next bfloat16 term; they keep what it leaves
+__device__ __forceinline__ uint32_t take_term(float &x, float &y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const float2 f = __bfloat1622float2(h);
+    x -= f.x;
+    y -= f.y;
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+}
+__device__ __forceinline__ float2 term_value(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+template <typename T> constexpr int kTerms = std::is_same<T, float>::value ? 3
+                                             : std::is_same<T, __half>::value ? 2 : 1;
+
+// Rows t0 .. t0 + m - 1 (in scan order), w columns, of a (length, heads, full)
+// tensor into `terms` planes of 64 x W (+ 8) bfloat16; the rest zeros.  Every
+// head's rows start on 16 bytes when `full` is a multiple of 8.
+template <typename T, bool REV>
+__device__ __forceinline__ void load_rows(__nv_bfloat16 *dst, const T *src, int64_t stride,
+                                          int64_t n, int64_t t0, int m, int w, int full,
+                                          int W) {
+    constexpr int NT = kTerms<T>;
+    const int plane = kC * (W + 8), vecs = W / 8;
+    const bool fast = full % 8 == 0;
+    for (int i = threadIdx.x; i < kC * vecs; i += blockDim.x) {
+        const int r = i / vecs, c = (i - r * vecs) * 8;
+        Pack<T, 8> x = {};
+        if (r < m && c < w) {
+            const T *at = src + (REV ? n - 1 - (t0 + r) : t0 + r) * stride + c;
+            if (fast) {
+                x = *reinterpret_cast<const Pack<T, 8> *>(at);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + k < w) x.v[k] = at[k];
+            }
+        }
+        if constexpr (NT == 1) {
+            *reinterpret_cast<Pack<T, 8> *>(dst + r * (W + 8) + c) = x;
+        } else {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = Storage<T>::load(&x.v[k]);
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                uint4 u;
+                u.x = take_term(f[0], f[1]);
+                u.y = take_term(f[2], f[3]);
+                u.z = take_term(f[4], f[5]);
+                u.w = take_term(f[6], f[7]);
+                *reinterpret_cast<uint4 *>(dst + q * plane + r * (W + 8) + c) = u;
+            }
+        }
+    }
+}
+
+// O: outputs (false: only the segment's local state).  KT: terms of the decayed
+// values in the state's update.
+template <typename T, typename TO, int AP, bool REV, bool O, int KT>
+__global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
+    constexpr int NT = kTerms<T>, LA = AP + 8, PL = kC * LA, LP = kC + 8, PP = kC * LP;
+    constexpr int L = NT - 1;
+    extern __shared__ __align__(16) char smem_chunk[];
+    const ScanArgs &p = ca.s;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int ET = warps * 16, LE = ET + 8, PE = kC * LE;
+    __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(smem_chunk);
+    __nv_bfloat16 *sv = sk + NT * PL;
+    __nv_bfloat16 *sq = sv + NT * PE;
+    __nv_bfloat16 *sp = sq + NT * PL;
+    __shared__ float pw[kC + 2];
+    const int seg = blockIdx.x % ca.segments;
+    if (!O && seg == ca.segments - 1) return;      // no segment starts from its state
+    const int64_t bh = blockIdx.x / ca.segments;
+    const int h = (int)(bh % p.heads);
+    const int64_t b = bh / p.heads;
+    const int e0 = blockIdx.y * ET;
+    int64_t n = p.length;
+    if (p.lengths) n = max((int64_t)0, min((int64_t)p.lengths[b], n));
+    const int64_t first = seg * ca.seg_len, last = min(n, first + ca.seg_len);
+    const int nq = p.heads / p.gq, nk = p.heads / p.gk, nv = p.heads / p.gv;
+    const T *q = static_cast<const T *>(p.q) + (b * p.length * nq + h / p.gq) * p.dk;
+    const T *k = static_cast<const T *>(p.k) + (b * p.length * nk + h / p.gk) * p.dk;
+    const T *v = static_cast<const T *>(p.v) + (b * p.length * nv + h / p.gv) * p.dv + e0;
+    const int ew = min(ET, p.dv - e0);
+    const float ld = p.log_decay[h];
+    for (int i = threadIdx.x; i < kC + 2; i += blockDim.x) pw[i] = i ? expf(ld * (float)i) : 1.0f;
+    const int g = lane >> 2, c2 = (lane & 3) * 2;
+    const int er = w * 16 + g;                     // the lane's rows er, er + 8 of the tile
+    const int64_t sbase = bh * (int64_t)p.dk * p.dv;
+    float *seg_state = ca.states + (bh * ca.segments + seg) * (int64_t)p.dk * p.dv;
+    // element (e, a) of a state: the segment's own layout, or the caller's
+    const auto own = [&](int e, int a) { return (int64_t)(e0 + e) * p.dk + a; };
+    const auto caller = [&](int e, int a) {
+        return p.s_transposed ? (int64_t)(e0 + e) * p.dk + a : (int64_t)a * p.dv + e0 + e;
+    };
+    float Z[AP / 8][4];
+    bool zero = true;                              // Z is known to be 0
+    {
+        const float *src = nullptr;
+        bool mine = false;
+        if (O && ca.segments > 1) {
+            src = seg_state;
+            mine = true;
+        } else if (O && p.s0) {
+            src = p.s0 + sbase;
+        }
+        zero = !src;
+#pragma unroll
+        for (int j = 0; j < AP / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = er + (i >> 1) * 8, a = j * 8 + c2 + (i & 1);
+                Z[j][i] = src && e < ew && a < p.dk ? src[mine ? own(e, a) : caller(e, a)] : 0.0f;
+            }
+    }
+    // ldmatrix rows of a 16 x 16 block: left operand / transposed right operand
+    // (rows 0-7, 8-15 of column 0, then of column 8), and right operand
+    const int ra = lane & 15, ka = (lane >> 4) * 8;
+    const int rb = (lane & 7) + (lane >> 4) * 8, kb = ((lane >> 3) & 1) * 8;
+    const uint32_t uk = smem_u32(sk), uv = smem_u32(sv), uq = smem_u32(sq), up = smem_u32(sp);
+    for (int64_t t0 = first; t0 < last; t0 += kC) {
+        const int m = (int)min((int64_t)kC, last - t0), blocks = (m + 15) / 16;
+        __syncthreads();
+        load_rows<T, REV>(sk, k, (int64_t)nk * p.dk, n, t0, m, p.dk, p.dk, AP);
+        load_rows<T, REV>(sv, v, (int64_t)nv * p.dv, n, t0, m, ew, p.dv, ET);
+        if (O) load_rows<T, REV>(sq, q, (int64_t)nq * p.dk, n, t0, m, p.dk, p.dk, AP);
+        __syncthreads();
+        if (O) {
+            // the chunk's weights, in 16 x 16 blocks on and below the diagonal
+            for (int u = w; u < blocks * (blocks + 1) / 2; u += warps) {
+                int i = 0;
+                while ((i + 1) * (i + 2) / 2 <= u) ++i;
+                const int j = u - i * (i + 1) / 2;
+                float s[2][4] = {};
+#pragma unroll
+                for (int kk = 0; kk < AP; kk += 16) {
+                    uint32_t A[NT][4], B[NT][4];
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        ldsm4(A[x], uq + 2 * (x * PL + (i * 16 + ra) * LA + kk + ka));
+                        ldsm4(B[x], uk + 2 * (x * PL + (j * 16 + rb) * LA + kk + kb));
+                    }
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int y = 0; y < NT; ++y)
+                            if (x + y <= L) {
+                                mma16816(s[0], A[x], B[y][0], B[y][1]);
+                                mma16816(s[1], A[x], B[y][2], B[y][3]);
+                            }
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int t = i * 16 + g + 8 * x, sc = j * 16 + y * 8 + c2;
+                        float f0 = t >= sc ? s[y][2 * x] * (pw[max(0, t - sc)] * ca.scale_p) : 0.0f;
+                        float f1 = t > sc
+                                       ? s[y][2 * x + 1] * (pw[max(0, t - sc - 1)] * ca.scale_p)
+                                       : 0.0f;
+#pragma unroll
+                        for (int z = 0; z < NT; ++z)
+                            *reinterpret_cast<uint32_t *>(sp + z * PP + t * LP + sc) =
+                                take_term(f0, f1);
+                    }
+            }
+            __syncthreads();
+            float acc[kC / 8][4] = {};
+            if (!zero) {
+#pragma unroll
+                for (int kk = 0; kk < AP / 16; ++kk) {
+                    uint32_t A[NT][4];
+                    float z[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        z[i] = Z[2 * kk][i];
+                        z[4 + i] = Z[2 * kk + 1][i];
+                    }
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) A[x][i] = take_term(z[2 * i], z[2 * i + 1]);
+#pragma unroll
+                    for (int tb = 0; tb < kC / 16; ++tb) {
+                        if (tb >= blocks) break;
+                        uint32_t B[NT][4];
+#pragma unroll
+                        for (int x = 0; x < NT; ++x)
+                            ldsm4(B[x], uq + 2 * (x * PL + (tb * 16 + rb) * LA + kk * 16 + kb));
+#pragma unroll
+                        for (int x = 0; x < NT; ++x)
+#pragma unroll
+                            for (int y = 0; y < NT; ++y)
+                                if (x + y <= L) {
+                                    mma16816(acc[2 * tb], A[x], B[y][0], B[y][1]);
+                                    mma16816(acc[2 * tb + 1], A[x], B[y][2], B[y][3]);
+                                }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kC / 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] *= pw[j * 8 + c2 + (i & 1) + !REV];
+            }
+#pragma unroll
+            for (int sb = 0; sb < kC / 16; ++sb) {
+                if (sb >= blocks) break;
+                uint32_t A[NT][4];
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    uint32_t r[4];
+                    ldsm4t(r, uv + 2 * (x * PE + (sb * 16 + ra) * LE + w * 16 + ka));
+                    A[x][0] = r[0];
+                    A[x][1] = r[2];
+                    A[x][2] = r[1];
+                    A[x][3] = r[3];
+                }
+#pragma unroll
+                for (int tb = 0; tb < kC / 16; ++tb) {
+                    if (tb < sb || tb >= blocks) continue;
+                    uint32_t B[NT][4];
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+                        ldsm4(B[x], up + 2 * (x * PP + (tb * 16 + rb) * LP + sb * 16 + kb));
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int y = 0; y < NT; ++y)
+                            if (x + y <= L) {
+                                mma16816(acc[2 * tb], A[x], B[y][0], B[y][1]);
+                                mma16816(acc[2 * tb + 1], A[x], B[y][2], B[y][3]);
+                            }
+                }
+            }
+            TO *o = static_cast<TO *>(p.o) + (b * p.length * p.heads + h) * p.dv + e0;
+#pragma unroll
+            for (int j = 0; j < kC / 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = j * 8 + c2 + (i & 1), e = er + (i >> 1) * 8;
+                    if (r < m && e < ew)
+                        Storage<TO>::store(
+                            o + (REV ? n - 1 - (t0 + r) : t0 + r) * p.heads * p.dv + e,
+                            p.scale_o * acc[j][i]);
+                }
+        }
+        // the state after the chunk
+        const float carry = pw[m];
+#pragma unroll
+        for (int j = 0; j < AP / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Z[j][i] *= carry;
+        zero = false;
+#pragma unroll
+        for (int sb = 0; sb < kC / 16; ++sb) {
+            if (sb >= blocks) break;
+            float f[8] = {};
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                uint32_t r[4];
+                ldsm4t(r, uv + 2 * (x * PE + (sb * 16 + ra) * LE + w * 16 + ka));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 t = term_value(r[i == 1 ? 2 : i == 2 ? 1 : i]);
+                    f[2 * i] += t.x;
+                    f[2 * i + 1] += t.y;
+                }
+            }
+            uint32_t A[KT][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int s = sb * 16 + (i >> 1) * 8 + c2;
+                f[2 * i] *= pw[max(0, m - 1 - s + REV)] * p.scale_k;
+                f[2 * i + 1] *= pw[max(0, m - 2 - s + REV)] * p.scale_k;
+            }
+#pragma unroll
+            for (int x = 0; x < KT; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) A[x][i] = take_term(f[2 * i], f[2 * i + 1]);
+#pragma unroll
+            for (int ab = 0; ab < AP / 16; ++ab) {
+                uint32_t B[NT][4];
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+                    ldsm4t(B[x], uk + 2 * (x * PL + (sb * 16 + ra) * LA + ab * 16 + ka));
+#pragma unroll
+                for (int x = 0; x < KT; ++x)
+#pragma unroll
+                    for (int y = 0; y < NT; ++y)
+                        if (x + y < KT) {
+                            mma16816(Z[2 * ab], A[x], B[y][0], B[y][1]);
+                            mma16816(Z[2 * ab + 1], A[x], B[y][2], B[y][3]);
+                        }
+            }
+        }
+    }
+    if (O) {
+        // tokens beyond the sequence, in the tile's segment
+        TO *o = static_cast<TO *>(p.o) + (b * p.length * p.heads + h) * p.dv + e0;
+        const int64_t from = max(n, first), to = min(p.length, first + ca.seg_len);
+        for (int64_t t = from + w; t < to; t += warps)
+            for (int e = lane; e < ew; e += 32)
+                Storage<TO>::store(o + t * p.heads * p.dv + e, 0.0f);
+        // the segment with the last token (the first one, of an empty sequence)
+        if (!p.sT || !(n > first ? n <= first + ca.seg_len : n == 0 && seg == 0)) return;
+    }
+    float *dst = O ? p.sT + sbase : seg_state;
+#pragma unroll
+    for (int j = 0; j < AP / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = er + (i >> 1) * 8, a = j * 8 + c2 + (i & 1);
+            if (e < ew && a < p.dk) dst[O ? caller(e, a) : own(e, a)] = Z[j][i];
+        }
+}
+
+// local states -> the states in front of the segments, in place
+__global__ void k_linattn_prefix(ChunkArgs ca, int64_t n_states) {
+    const ScanArgs &p = ca.s;
+    const int64_t size = (int64_t)p.dk * p.dv;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n_states * size) return;
+    const int64_t bh = i / size, at = i - bh * size;
+    const int e = (int)(at / p.dk), a = (int)(at - (int64_t)e * p.dk);
+    int64_t n = p.length;
+    if (p.lengths) n = max((int64_t)0, min((int64_t)p.lengths[bh / p.heads], n));
+    const float ld = p.log_decay[bh % p.heads];
+    float z = p.s0 ? p.s0[bh * size + (p.s_transposed ? at : (int64_t)a * p.dv + e)] : 0.0f;
+    float *s = ca.states + bh * ca.segments * size + at;
+    for (int k = 0; k < ca.segments; ++k) {
+        const int64_t len = max((int64_t)0, min(ca.seg_len, n - k * ca.seg_len));
+        const float local = k + 1 < ca.segments && len > 0 ? s[k * size] : 0.0f;
+        s[k * size] = z;
+        if (len > 0) z = fmaf(z, expf(ld * (float)len), local);
+    }
+}
+
+template <typename T>
+size_t chunk_smem(int AP, int warps) {
+    const int NT = kTerms<T>;
+    return (size_t)NT * kC * (2 * (AP + 8) + warps * 16 + 8 + kC + 8) * 2;
+}
+int chunk_warps(int dv) {
+    const int w = (dv + 15) / 16;
+    return w < 8 ? w : 8;
+}
+
+// Calls f with the padded key width.
+template <class F>
+fno_status_t with_width(int dk, F &&f) {
+    if (dk <= 32) return f(std::integral_constant<int, 32>());
+    if (dk <= 64) return f(std::integral_constant<int, 64>());
+    return f(std::integral_constant<int, 128>());
+}
+
+// One scan: in chunks up to 128 key columns, token by token beyond (the state
+// of a wider key does not fit the registers).  p.segments > 1: the segments'
+// local states, their prefix, then all segments side by side.
 template <typename T, typename TO, bool REV>
-fno_status_t scan(const ScanArgs &a, int64_t batch, cudaStream_t s) {
-    const dim3 grid((unsigned)(batch * a.heads), (unsigned)ceil_div(a.dv, 8));
-    k_linattn_scan<T, TO, REV><<<grid, 256, 0, s>>>(a);
-    return launched();
+fno_status_t scan(const fno_linattn_s &p, const ScanArgs &a, float *states, float scale_p,
+                  cudaStream_t s) {
+    if (a.dk > kChunkWidth) {
+        const dim3 grid((unsigned)(p.batch * a.heads), (unsigned)ceil_div(a.dv, 8));
+        k_linattn_scan<T, TO, REV><<<grid, 256, 0, s>>>(a);
+        return launched();
+    }
+    const ChunkArgs ca{a, states, p.segments, p.seg_len, scale_p};
+    const int warps = chunk_warps(a.dv);
+    const int64_t bh = p.batch * a.heads;
+    const dim3 grid((unsigned)(bh * p.segments), (unsigned)ceil_div(a.dv, warps * 16));
+    return with_width(a.dk, [&](auto ap) {
+        constexpr int AP = decltype(ap)::value;
+        const size_t smem = chunk_smem<T>(AP, warps);
+        const auto run = [&](auto kernel) {
+            if (raise_smem_limit(kernel, smem) != cudaSuccess) return FNO_ERR_CUDA;
+            kernel<<<grid, warps * 32, smem, s>>>(ca);
+            return launched();
+        };
+        if (p.segments > 1) {
+            fno_status_t st = run(k_linattn_chunk<T, TO, AP, REV, false, 3>);
+            if (st != FNO_OK) return st;
+            const int64_t n = bh * a.dk * a.dv;
+            k_linattn_prefix<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(ca, bh);
+        }
+        return run(k_linattn_chunk<T, TO, AP, REV, true, 3>);
+    });
 }
 
 // sum of the `g` query heads' float32 gradients of each shared head
@@ -198,11 +636,23 @@ fno_status_t fno_linattn_plan(fno_linattn_t *out, int64_t batch, int64_t length,
         fno_linattn_destroy(p);
         return st;
     }
+    // time is split when the heads alone leave SMs idle: two CTAs an SM, and
+    // segments of 4 chunks at least (a segment costs a second pass over k and v)
+    const int64_t ctas = batch * heads * ceil_div(dv, 128);
+    int64_t segs = 2 * p->sms / ctas;
+    const int64_t most = ceil_div(length, 4 * kC);
+    segs = segs < 1 ? 1 : segs < most ? segs : most;
+    p->seg_len = ceil_div(ceil_div(length, segs), kC) * kC;
+    p->segments = (int)ceil_div(length, p->seg_len);
+    size_t at = 0;
+    if (p->segments > 1) at = (size_t)batch * heads * p->segments * dk * dv * 4;
     if ((flags & FNO_LINATTN_BACKWARD) && heads != kv_heads) {
         const size_t n = (size_t)batch * length * heads;
-        p->group_off[1] = (n * dk * 4 + 255) & ~size_t(255);
-        p->workspace = p->group_off[1] + n * dv * 4;
+        p->group_off[0] = (at + 255) & ~size_t(255);
+        p->group_off[1] = (p->group_off[0] + n * dk * 4 + 255) & ~size_t(255);
+        at = p->group_off[1] + n * dv * 4;
     }
+    p->workspace = at;
     *out = p;
     return FNO_OK;
 }
@@ -232,7 +682,8 @@ fno_status_t fno_linattn_forward(fno_linattn_t p, const void *q, const void *k, 
                p->dk, p->dv, scale, 1.0f, false};
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
-        return scan<T, T, false>(a, p->batch, reinterpret_cast<cudaStream_t>(stream));
+        return scan<T, T, false>(*p, a, static_cast<float *>(workspace), 1.0f,
+                                 reinterpret_cast<cudaStream_t>(stream));
     });
 }
 
@@ -254,7 +705,8 @@ fno_status_t fno_linattn_backward(fno_linattn_t p, const void *q, const void *k,
     if (inject("launch")) return FNO_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int g = p->heads / p->kv_heads;
-    float *gk = static_cast<float *>(workspace);
+    float *states = static_cast<float *>(workspace);
+    float *gk = reinterpret_cast<float *>(static_cast<char *>(workspace) + p->group_off[0]);
     float *gv = reinterpret_cast<float *>(static_cast<char *>(workspace) + p->group_off[1]);
     // dq: queries go, keys v, values k, the state transposed
     const ScanArgs aq{go, v, k, log_decay, lengths, s0, dq, nullptr, p->length, p->heads, 1, g, g,
@@ -266,14 +718,14 @@ fno_status_t fno_linattn_backward(fno_linattn_t p, const void *q, const void *k,
                       p->length, p->heads, g, 1, 1, p->dk, p->dv, 1.0f, scale, false};
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
-        fno_status_t r = scan<T, T, false>(aq, p->batch, s);
+        fno_status_t r = scan<T, T, false>(*p, aq, states, 1.0f, s);
         if (r != FNO_OK) return r;
         if (g == 1) {
-            r = scan<T, T, true>(ak, p->batch, s);
-            return r == FNO_OK ? scan<T, T, true>(av, p->batch, s) : r;
+            r = scan<T, T, true>(*p, ak, states, scale, s);
+            return r == FNO_OK ? scan<T, T, true>(*p, av, states, scale, s) : r;
         }
-        r = scan<T, float, true>(ak, p->batch, s);
-        if (r == FNO_OK) r = scan<T, float, true>(av, p->batch, s);
+        r = scan<T, float, true>(*p, ak, states, scale, s);
+        if (r == FNO_OK) r = scan<T, float, true>(*p, av, states, scale, s);
         if (r != FNO_OK) return r;
         const int64_t rows = p->batch * p->length * p->kv_heads;
         k_linattn_group_sum<T><<<p->sms * 4, 256, 0, s>>>(gk, static_cast<T *>(dk), rows * p->dk,
