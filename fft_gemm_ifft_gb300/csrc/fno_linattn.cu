@@ -171,46 +171,92 @@ __device__ __forceinline__ float2 term_value(uint32_t u) {
 template <typename T> constexpr int kTerms = std::is_same<T, float>::value ? 3
                                              : std::is_same<T, __half>::value ? 2 : 1;
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Rows t0 .. t0 + m - 1 (in scan order), w columns, of a (length, heads, full)
-// tensor into `terms` planes of 64 x W (+ 8) bfloat16; the rest zeros.  Every
-// head's rows start on 16 bytes when `full` is a multiple of 8.
+// tensor into kTerms planes of 64 x W (+ 8) bfloat16; the rest zeros.  Every
+// head's rows start on 16 bytes when `full` is a multiple of 8.  bfloat16 rows
+// that do are copied asynchronously (the caller waits); others go through
+// registers, four vectors' loads in flight.
 template <typename T, bool REV>
 __device__ __forceinline__ void load_rows(__nv_bfloat16 *dst, const T *src, int64_t stride,
-                                          int64_t n, int64_t t0, int m, int w, int full,
-                                          int W) {
-    constexpr int NT = kTerms<T>;
+                                          int64_t n, int64_t t0, int m, int w, int full, int W,
+                                          bool async) {
+    constexpr int NT = kTerms<T>, U = 4;
     const int plane = kC * (W + 8), vecs = W / 8;
     const bool fast = full % 8 == 0;
-    for (int i = threadIdx.x; i < kC * vecs; i += blockDim.x) {
-        const int r = i / vecs, c = (i - r * vecs) * 8;
-        Pack<T, 8> x = {};
-        if (r < m && c < w) {
-            const T *at = src + (REV ? n - 1 - (t0 + r) : t0 + r) * stride + c;
-            if (fast) {
-                x = *reinterpret_cast<const Pack<T, 8> *>(at);
-            } else {
+    if (NT == 1 && async) {
+        for (int i = threadIdx.x; i < kC * vecs; i += blockDim.x) {
+            const int r = i / vecs, c = (i - r * vecs) * 8;
+            const bool have = r < m && c < w;
+            const T *at = have ? src + (REV ? n - 1 - (t0 + r) : t0 + r) * stride + c : src;
+            cp_async16(smem_u32(dst + r * (W + 8) + c), at, have);
+        }
+        return;
+    }
+    for (int i0 = threadIdx.x; i0 < kC * vecs; i0 += U * blockDim.x) {
+        Pack<T, 8> x[U] = {};
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (c + k < w) x.v[k] = at[k];
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * blockDim.x, r = i / vecs, c = (i - r * vecs) * 8;
+            if (r < m && c < w) {
+                const T *at = src + (REV ? n - 1 - (t0 + r) : t0 + r) * stride + c;
+                if (fast) {
+                    x[u] = *reinterpret_cast<const Pack<T, 8> *>(at);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (c + k < w) x[u].v[k] = at[k];
+                }
             }
         }
-        if constexpr (NT == 1) {
-            *reinterpret_cast<Pack<T, 8> *>(dst + r * (W + 8) + c) = x;
-        } else {
-            float f[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = Storage<T>::load(&x.v[k]);
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * blockDim.x, r = i / vecs, c = (i - r * vecs) * 8;
+            if (i >= kC * vecs) break;
+            if constexpr (NT == 1) {
+                *reinterpret_cast<Pack<T, 8> *>(dst + r * (W + 8) + c) = x[u];
+            } else {
+                float f[8];
 #pragma unroll
-            for (int q = 0; q < NT; ++q) {
-                uint4 u;
-                u.x = take_term(f[0], f[1]);
-                u.y = take_term(f[2], f[3]);
-                u.z = take_term(f[4], f[5]);
-                u.w = take_term(f[6], f[7]);
-                *reinterpret_cast<uint4 *>(dst + q * plane + r * (W + 8) + c) = u;
+                for (int k = 0; k < 8; ++k) f[k] = Storage<T>::load(&x[u].v[k]);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                    uint4 t;
+                    t.x = take_term(f[0], f[1]);
+                    t.y = take_term(f[2], f[3]);
+                    t.z = take_term(f[4], f[5]);
+                    t.w = take_term(f[6], f[7]);
+                    *reinterpret_cast<uint4 *>(dst + q * plane + r * (W + 8) + c) = t;
+                }
             }
         }
     }
+}
+
+// D += sum over the terms' products i + j <= L.  The leading product's sum and
+// the others' are kept apart: the tensor cores truncate what they add to a sum,
+// which costs the leading sum a digit for every small product added to it.
+template <int NA, int NB, int L>
+__device__ __forceinline__ void mma_terms(float (&hi)[2][4], float (&lo)[2][4],
+                                          const uint32_t (&A)[NA][4], const uint32_t (&B)[NB][4]) {
+#pragma unroll
+    for (int x = 0; x < NA; ++x)
+#pragma unroll
+        for (int y = 0; y < NB; ++y) {
+            if (x + y > L) continue;
+            mma16816(x + y ? lo[0] : hi[0], A[x], B[y][0], B[y][1]);
+            mma16816(x + y ? lo[1] : hi[1], A[x], B[y][2], B[y][3]);
+        }
 }
 
 // O: outputs (false: only the segment's local state).  KT: terms of the decayed
@@ -223,10 +269,10 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
     const ScanArgs &p = ca.s;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int ET = warps * 16, LE = ET + 8, PE = kC * LE;
-    __nv_bfloat16 *sk = reinterpret_cast<__nv_bfloat16 *>(smem_chunk);
-    __nv_bfloat16 *sv = sk + NT * PL;
-    __nv_bfloat16 *sq = sv + NT * PE;
-    __nv_bfloat16 *sp = sq + NT * PL;
+    // weights, then one (two with asynchronous copies) of k, v, q
+    __nv_bfloat16 *sp = reinterpret_cast<__nv_bfloat16 *>(smem_chunk);
+    __nv_bfloat16 *sbuf = sp + (O ? NT * PP : 0);
+    const int buf = NT * (PL + PE + (O ? PL : 0));
     __shared__ float pw[kC + 2];
     const int seg = blockIdx.x % ca.segments;
     if (!O && seg == ca.segments - 1) return;      // no segment starts from its state
@@ -277,21 +323,43 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
     // (rows 0-7, 8-15 of column 0, then of column 8), and right operand
     const int ra = lane & 15, ka = (lane >> 4) * 8;
     const int rb = (lane & 7) + (lane >> 4) * 8, kb = ((lane >> 3) & 1) * 8;
-    const uint32_t uk = smem_u32(sk), uv = smem_u32(sv), uq = smem_u32(sq), up = smem_u32(sp);
+    const uint32_t up = smem_u32(sp);
+    const bool async = NT == 1 && p.dk % 8 == 0 && p.dv % 8 == 0;
+    const auto load = [&](int64_t t0, int which) {
+        const int m = (int)min((int64_t)kC, last - t0);
+        __nv_bfloat16 *d = sbuf + which * buf;
+        load_rows<T, REV>(d, k, (int64_t)nk * p.dk, n, t0, m, p.dk, p.dk, AP, async);
+        load_rows<T, REV>(d + NT * PL, v, (int64_t)nv * p.dv, n, t0, m, ew, p.dv, ET, async);
+        if (O)
+            load_rows<T, REV>(d + NT * (PL + PE), q, (int64_t)nq * p.dk, n, t0, m, p.dk, p.dk, AP,
+                              async);
+    };
+    if (async && first < last) {
+        load(first, 0);
+        cp_async_commit();
+    }
+    int which = 0;
     for (int64_t t0 = first; t0 < last; t0 += kC) {
         const int m = (int)min((int64_t)kC, last - t0), blocks = (m + 15) / 16;
+        __syncthreads();                           // the last chunk's readers are done
+        if (async) {
+            if (t0 + kC < last) load(t0 + kC, which ^ 1);
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            load(t0, 0);
+        }
         __syncthreads();
-        load_rows<T, REV>(sk, k, (int64_t)nk * p.dk, n, t0, m, p.dk, p.dk, AP);
-        load_rows<T, REV>(sv, v, (int64_t)nv * p.dv, n, t0, m, ew, p.dv, ET);
-        if (O) load_rows<T, REV>(sq, q, (int64_t)nq * p.dk, n, t0, m, p.dk, p.dk, AP);
-        __syncthreads();
+        const uint32_t uk = smem_u32(sbuf + which * buf), uv = uk + 2 * NT * PL,
+                       uq = uv + 2 * NT * PE;
+        which ^= async;
         if (O) {
             // the chunk's weights, in 16 x 16 blocks on and below the diagonal
             for (int u = w; u < blocks * (blocks + 1) / 2; u += warps) {
                 int i = 0;
                 while ((i + 1) * (i + 2) / 2 <= u) ++i;
                 const int j = u - i * (i + 1) / 2;
-                float s[2][4] = {};
+                float s[2][4] = {}, sl[2][4] = {};
 #pragma unroll
                 for (int kk = 0; kk < AP; kk += 16) {
                     uint32_t A[NT][4], B[NT][4];
@@ -300,15 +368,13 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                         ldsm4(A[x], uq + 2 * (x * PL + (i * 16 + ra) * LA + kk + ka));
                         ldsm4(B[x], uk + 2 * (x * PL + (j * 16 + rb) * LA + kk + kb));
                     }
-#pragma unroll
-                    for (int x = 0; x < NT; ++x)
-#pragma unroll
-                        for (int y = 0; y < NT; ++y)
-                            if (x + y <= L) {
-                                mma16816(s[0], A[x], B[y][0], B[y][1]);
-                                mma16816(s[1], A[x], B[y][2], B[y][3]);
-                            }
+                    mma_terms<NT, NT, L>(s, sl, A, B);
                 }
+                if (NT > 1)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[y][x] += sl[y][x];
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -325,7 +391,7 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                     }
             }
             __syncthreads();
-            float acc[kC / 8][4] = {};
+            float acc[kC / 16][2][4] = {}, acl[NT > 1 ? kC / 16 : 1][2][4] = {};
             if (!zero) {
 #pragma unroll
                 for (int kk = 0; kk < AP / 16; ++kk) {
@@ -347,20 +413,17 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
 #pragma unroll
                         for (int x = 0; x < NT; ++x)
                             ldsm4(B[x], uq + 2 * (x * PL + (tb * 16 + rb) * LA + kk * 16 + kb));
-#pragma unroll
-                        for (int x = 0; x < NT; ++x)
-#pragma unroll
-                            for (int y = 0; y < NT; ++y)
-                                if (x + y <= L) {
-                                    mma16816(acc[2 * tb], A[x], B[y][0], B[y][1]);
-                                    mma16816(acc[2 * tb + 1], A[x], B[y][2], B[y][3]);
-                                }
+                        mma_terms<NT, NT, L>(acc[tb], acl[NT > 1 ? tb : 0], A, B);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < kC / 8; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][i] *= pw[j * 8 + c2 + (i & 1) + !REV];
+                    for (int i = 0; i < 4; ++i) {
+                        const float f = pw[j * 8 + c2 + (i & 1) + !REV];
+                        acc[j / 2][j % 2][i] *= f;
+                        if (NT > 1) acl[NT > 1 ? j / 2 : 0][j % 2][i] *= f;
+                    }
             }
 #pragma unroll
             for (int sb = 0; sb < kC / 16; ++sb) {
@@ -382,14 +445,7 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x)
                         ldsm4(B[x], up + 2 * (x * PP + (tb * 16 + rb) * LP + sb * 16 + kb));
-#pragma unroll
-                    for (int x = 0; x < NT; ++x)
-#pragma unroll
-                        for (int y = 0; y < NT; ++y)
-                            if (x + y <= L) {
-                                mma16816(acc[2 * tb], A[x], B[y][0], B[y][1]);
-                                mma16816(acc[2 * tb + 1], A[x], B[y][2], B[y][3]);
-                            }
+                    mma_terms<NT, NT, L>(acc[tb], acl[NT > 1 ? tb : 0], A, B);
                 }
             }
             TO *o = static_cast<TO *>(p.o) + (b * p.length * p.heads + h) * p.dv + e0;
@@ -401,19 +457,16 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                     if (r < m && e < ew)
                         Storage<TO>::store(
                             o + (REV ? n - 1 - (t0 + r) : t0 + r) * p.heads * p.dv + e,
-                            p.scale_o * acc[j][i]);
+                            p.scale_o * (NT > 1 ? acc[j / 2][j % 2][i] +
+                                                      acl[NT > 1 ? j / 2 : 0][j % 2][i]
+                                                : acc[j / 2][j % 2][i]));
                 }
         }
-        // the state after the chunk
-        const float carry = pw[m];
-#pragma unroll
-        for (int j = 0; j < AP / 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) Z[j][i] *= carry;
-        zero = false;
+        // the state after the chunk: the chunk's own sum is made apart and added
+        // rounded, so that the tensor cores' truncation does not pile up in Z
+        uint32_t A[kC / 16][KT][4];
 #pragma unroll
         for (int sb = 0; sb < kC / 16; ++sb) {
-            if (sb >= blocks) break;
             float f[8] = {};
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
@@ -426,7 +479,6 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                     f[2 * i + 1] += t.y;
                 }
             }
-            uint32_t A[KT][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int s = sb * 16 + (i >> 1) * 8 + c2;
@@ -436,22 +488,27 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
 #pragma unroll
             for (int x = 0; x < KT; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) A[x][i] = take_term(f[2 * i], f[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) A[sb][x][i] = take_term(f[2 * i], f[2 * i + 1]);
+        }
+        const float carry = pw[m];
+        zero = false;
 #pragma unroll
-            for (int ab = 0; ab < AP / 16; ++ab) {
+        for (int ab = 0; ab < AP / 16; ++ab) {
+            float hi[2][4] = {}, lo[2][4] = {};
+#pragma unroll
+            for (int sb = 0; sb < kC / 16; ++sb) {
+                if (sb >= blocks) break;
                 uint32_t B[NT][4];
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
                     ldsm4t(B[x], uk + 2 * (x * PL + (sb * 16 + ra) * LA + ab * 16 + ka));
-#pragma unroll
-                for (int x = 0; x < KT; ++x)
-#pragma unroll
-                    for (int y = 0; y < NT; ++y)
-                        if (x + y < KT) {
-                            mma16816(Z[2 * ab], A[x], B[y][0], B[y][1]);
-                            mma16816(Z[2 * ab + 1], A[x], B[y][2], B[y][3]);
-                        }
+                mma_terms<KT, NT, KT - 1>(hi, lo, A[sb], B);
             }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    Z[2 * ab + y][i] = fmaf(Z[2 * ab + y][i], carry, hi[y][i] + lo[y][i]);
         }
     }
     if (O) {
@@ -496,9 +553,10 @@ __global__ void k_linattn_prefix(ChunkArgs ca, int64_t n_states) {
 }
 
 template <typename T>
-size_t chunk_smem(int AP, int warps) {
-    const int NT = kTerms<T>;
-    return (size_t)NT * kC * (2 * (AP + 8) + warps * 16 + 8 + kC + 8) * 2;
+size_t chunk_smem(int AP, int warps, bool outputs) {
+    const int NT = kTerms<T>, bufs = NT == 1 ? 2 : 1;
+    return (size_t)NT * kC * 2 * (bufs * ((outputs ? 2 : 1) * (AP + 8) + warps * 16 + 8) +
+                                  (outputs ? kC + 8 : 0));
 }
 int chunk_warps(int dv) {
     const int w = (dv + 15) / 16;
@@ -508,7 +566,6 @@ int chunk_warps(int dv) {
 // Calls f with the padded key width.
 template <class F>
 fno_status_t with_width(int dk, F &&f) {
-    if (dk <= 32) return f(std::integral_constant<int, 32>());
     if (dk <= 64) return f(std::integral_constant<int, 64>());
     return f(std::integral_constant<int, 128>());
 }
@@ -530,19 +587,19 @@ fno_status_t scan(const fno_linattn_s &p, const ScanArgs &a, float *states, floa
     const dim3 grid((unsigned)(bh * p.segments), (unsigned)ceil_div(a.dv, warps * 16));
     return with_width(a.dk, [&](auto ap) {
         constexpr int AP = decltype(ap)::value;
-        const size_t smem = chunk_smem<T>(AP, warps);
-        const auto run = [&](auto kernel) {
+        const auto run = [&](auto kernel, bool outputs) {
+            const size_t smem = chunk_smem<T>(AP, warps, outputs);
             if (raise_smem_limit(kernel, smem) != cudaSuccess) return FNO_ERR_CUDA;
             kernel<<<grid, warps * 32, smem, s>>>(ca);
             return launched();
         };
         if (p.segments > 1) {
-            fno_status_t st = run(k_linattn_chunk<T, TO, AP, REV, false, 3>);
+            fno_status_t st = run(k_linattn_chunk<T, T, AP, REV, false, 3>, false);
             if (st != FNO_OK) return st;
             const int64_t n = bh * a.dk * a.dv;
             k_linattn_prefix<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(ca, bh);
         }
-        return run(k_linattn_chunk<T, TO, AP, REV, true, 3>);
+        return run(k_linattn_chunk<T, TO, AP, REV, true, 3>, true);
     });
 }
 
@@ -596,6 +653,25 @@ k_linattn_step(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
     }
 }
 
+// CTAs of the chunked kernel that an SM holds
+fno_status_t chunk_occupancy(const fno_linattn_s &p, int *ctas) {
+    return with_storage(p.dtype, [&](auto t) {
+        using T = decltype(t);
+        return with_width(p.dk, [&](auto ap) {
+            constexpr int AP = decltype(ap)::value;
+            const int warps = chunk_warps(p.dv);
+            const size_t smem = chunk_smem<T>(AP, warps, true);
+            const auto kernel = k_linattn_chunk<T, T, AP, false, true, 3>;
+            if (raise_smem_limit(kernel, smem) == cudaSuccess &&
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, warps * 32, smem) ==
+                    cudaSuccess && *ctas > 0)
+                return FNO_OK;
+            cudaGetLastError();
+            return FNO_ERR_CUDA;
+        });
+    });
+}
+
 struct Sizes {
     size_t q, k, v, o, s;    // bytes
 };
@@ -636,10 +712,17 @@ fno_status_t fno_linattn_plan(fno_linattn_t *out, int64_t batch, int64_t length,
         fno_linattn_destroy(p);
         return st;
     }
-    // time is split when the heads alone leave SMs idle: two CTAs an SM, and
-    // segments of 4 chunks at least (a segment costs a second pass over k and v)
+    // time is split when the heads alone leave SMs idle, into one wave of CTAs
+    // and segments of 4 chunks at least (a segment costs a second pass over k
+    // and v)
+    int per_sm = 1;
+    if (dk <= kChunkWidth) st = chunk_occupancy(*p, &per_sm);
+    if (st != FNO_OK) {
+        fno_linattn_destroy(p);
+        return st;
+    }
     const int64_t ctas = batch * heads * ceil_div(dv, 128);
-    int64_t segs = 2 * p->sms / ctas;
+    int64_t segs = (int64_t)per_sm * p->sms / ctas;
     const int64_t most = ceil_div(length, 4 * kC);
     segs = segs < 1 ? 1 : segs < most ? segs : most;
     p->seg_len = ceil_div(ceil_div(length, segs), kC) * kC;
