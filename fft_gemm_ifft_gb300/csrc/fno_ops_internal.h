@@ -121,5 +121,16 @@ __device__ __forceinline__ int code8(float x, float inv) {
 }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// The values of four codes: the biased byte under the exponent of 2^23, less
+// 2^23 + 128 (two instructions a code at full rate; a conversion runs at a
+// quarter of it or less).
+__device__ __forceinline__ void code_values4(uint32_t w, float *f) {
+    w ^= 0x80808080u;
+    f[0] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)) - 8388736.0f;
+    f[1] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)) - 8388736.0f;
+    f[2] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)) - 8388736.0f;
+    f[3] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)) - 8388736.0f;
+}
+
 }  // namespace ops
 }  // namespace fno
