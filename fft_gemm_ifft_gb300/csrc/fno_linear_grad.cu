@@ -23,7 +23,8 @@ struct fno_linear_grad_s {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kRows = kThreads / 16;              // rows that the threads load at a time
 constexpr int kM = 128;                          // inputs of a tile: the tensor cores' rows
 constexpr uint32_t kChunkA = kM * 128;           // 64 points of the codes: 128 rows x 128 bytes
 // float32 dy as a sum of three bfloat16 terms (24 bits); 16-bit dy as it is
@@ -33,40 +34,86 @@ template <typename T> constexpr int kMaxN = std::is_same<T, float>::value ? 64 :
 template <typename T> using Operand =
     typename std::conditional<std::is_same<T, __half>::value, __half, __nv_bfloat16>::type;
 
-// Eight elements from `at` on, of which `n` are wanted (the others read as 0),
-// by 16-byte loads where the address allows; elsewhere by the 4-byte words that
-// hold them, shifted into place.  `end`: the tensor's end, past which nothing is
-// read.
-template <typename T>
-__device__ __forceinline__ Pack<T, 8> load8(const T *at, int n, const T *end) {
-    Pack<T, 8> r = {};
-    constexpr int B = 8 * (int)sizeof(T), A = B < 16 ? B : 16;
-    const uintptr_t u = reinterpret_cast<uintptr_t>(at);
-    if (n <= 0) return r;
-    if (u % A == 0 && n >= 8) return *reinterpret_cast<const Pack<T, 8> *>(at);
-    if (sizeof(T) == 4) {
+// Eight consecutive elements as they come from memory.  Where every row starts
+// on 16 bytes (VEC: a point count that is a multiple of 8) they are one or two
+// vector loads.  Elsewhere 8- and 16-bit elements come as the 4-byte words that
+// hold them and are shifted into place when they are used, float32 one by one.
+// Every load is a predicated instruction without a branch, so that a thread's
+// loads are all in flight together (with the choice made at each load, the
+// branches kept them apart: 611 us in place of 110 for 8 x 40 -> 60 x 64^3).
+template <typename T, bool VEC>
+struct Raw8 {
+    static constexpr int kWords = 8 * (int)sizeof(T) / 4 + (VEC || sizeof(T) == 4 ? 0 : 1);
+    uint32_t w[kWords];
+    // `n` elements from `at` on are wanted.  Words may reach 4 bytes past them.
+    __device__ __forceinline__ void load(const T *at, int n) {
+        if constexpr (VEC) {
+            constexpr int B = 8 * (int)sizeof(T);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) r.v[i] = at[i];
+            for (int i = 0; i < kWords; ++i) w[i] = 0;
+            if (n > 0) {
+                if constexpr (B == 8) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(at);
+                    w[0] = u.x;
+                    w[1] = u.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < B / 16; ++i) {
+                        const uint4 u = reinterpret_cast<const uint4 *>(at)[i];
+                        w[4 * i] = u.x;
+                        w[4 * i + 1] = u.y;
+                        w[4 * i + 2] = u.z;
+                        w[4 * i + 3] = u.w;
+                    }
+                }
+            }
+        } else {
+            const uint32_t *p =
+                reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(3));
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                w[i] = 0;
+                if (n > 0 && i * 4 < n * (int)sizeof(T) + (sizeof(T) == 4 ? 0 : 4)) w[i] = p[i];
+            }
+        }
+    }
+    // the same without a byte past the n elements (at the tensor's end)
+    __device__ __forceinline__ void load_exact(const T *at, int n) {
+        const unsigned char *from = reinterpret_cast<const unsigned char *>(at),
+                            *to = from + n * sizeof(T),
+                            *p = reinterpret_cast<const unsigned char *>(
+                                reinterpret_cast<uintptr_t>(at) & ~uintptr_t(3));
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            w[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (p + 4 * i + j >= from && p + 4 * i + j < to)
+                    w[i] |= (uint32_t)p[4 * i + j] << (8 * j);
+        }
+    }
+    // the elements, those from n on 0; `shift`: 8 (address mod 4)
+    __device__ __forceinline__ Pack<T, 8> get(int n, int shift) const {
+        Pack<T, 8> r;
+        if constexpr (VEC || sizeof(T) == 4) {
+            memcpy(&r, w, sizeof(r));
+        } else {
+            uint32_t y[kWords - 1];
+#pragma unroll
+            for (int i = 0; i < kWords - 1; ++i) y[i] = __funnelshift_r(w[i], w[i + 1], shift);
+            if (n < 8) {
+                constexpr int E = 4 / (int)sizeof(T), B = 8 * (int)sizeof(T);
+#pragma unroll
+                for (int i = 0; i < kWords - 1; ++i) {
+                    const int keep = n - i * E;            // elements of this word
+                    y[i] = keep <= 0 ? 0u : keep >= E ? y[i] : y[i] & ((1u << (keep * B)) - 1u);
+                }
+            }
+            memcpy(&r, y, sizeof(r));
+        }
         return r;
     }
-    constexpr int W = B / 4;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(u & ~uintptr_t(3));
-    const int sh = (int)(u & 3) * 8;
-    if (n >= 8 && reinterpret_cast<const char *>(w + W + 1) <= reinterpret_cast<const char *>(end)) {
-        uint32_t x[W + 1], y[W];
-#pragma unroll
-        for (int i = 0; i <= W; ++i) x[i] = w[i];
-#pragma unroll
-        for (int i = 0; i < W; ++i) y[i] = __funnelshift_r(x[i], x[i + 1], sh);
-        memcpy(&r, y, sizeof(y));
-        return r;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) r.v[i] = at[i];
-    return r;
-}
+};
 
 // two floats as the next bfloat16 term; they keep what it leaves
 __device__ __forceinline__ uint32_t take_term(float &x, float &y) {
@@ -103,14 +150,15 @@ template <typename T> __device__ __forceinline__ uint32_t pack2(float x, float y
 // tiles (the codes become 16-bit numbers, float32 dy three terms; rows of any
 // length and alignment need it too), the next block's loads in flight over the
 // conversion, the MMAs and the drain of this one.
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
 k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
                    const float *__restrict__ scales, float *__restrict__ part, int64_t batch,
                    int64_t points, int cin, int cout, int64_t groups, int *err) {
     using TO = Operand<T>;
     constexpr int NT = kTerms<T>;
-    constexpr int RA = kM / 16, RB = kMaxN<T> / 16;         // rows of a thread: codes, dy
+    constexpr int RA = kM / kRows, RB = kMaxN<T> / kRows;   // rows of a thread: codes, dy
+    constexpr int NC = kMaxN<T> / 4;                     // accumulators of a thread
     extern __shared__ char smem_raw[];
     char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                           ~static_cast<uintptr_t>(1023));
@@ -133,40 +181,76 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
     // rows past the channels are never written: zero, once
     for (uint32_t e = tid; e < 2 * stage / 16; e += kThreads)
         reinterpret_cast<uint4 *>(base)[e] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    // a row of ones below the codes gives the sum of dy; a full tile of inputs
+    // has no row for it, and the threads add up what they load
+    const bool ones = mi < kM;
+    if (ones && tid < kGroup)
+        for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<TO *>(base + k * stage + (tid >> 6) * kChunkA +
+                                    sw_off16(mi, tid & 63)) = TO(1.0f);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = s_tmem, sb = tc_smem_addr(base);
     const int64_t items = batch * groups;
-    const int r0 = tid >> 4, c8 = (tid & 15) * 8;        // rows r0 + 16 k, points c8 .. c8 + 7
+    const int r0 = tid >> 4, c8 = (tid & 15) * 8;        // rows r0 + 32 k, points c8 .. c8 + 7
     const int row_i = i0 + (w & 3) * 32 + lane;          // this thread's accumulator row
-    const int hn = (N / 2 + 15) / 16 * 16;               // and columns half .. half + hn - 1
-    const int half = (w >> 2) * hn;
-    Pack<int8_t, 8> qa[RA];
-    Pack<T, 8> yb[RB];
-    float sc_next = 0.0f, sc = 0.0f, acc[kMaxN<T> / 2] = {}, bias[RB] = {};
-    const auto load = [&](int64_t it) {
-        const int64_t b = it / groups, g = it - b * groups, p = g * kGroup + c8;
-        const int n = (int)min((int64_t)8, points - p);
+    const int hn = (N / 4 + 15) / 16 * 16;               // and columns c0 .. c0 + hn - 1
+    const int c0 = (w >> 2) * hn;
+    // two blocks' loads are in flight while a third is worked on
+    struct Next {
+        Raw8<int8_t, VEC> q[RA];
+        Raw8<T, VEC> y[RB];
+        int n, sh_q, sh_y;                               // (32 rows apart: the same shift)
+        float scale;
+    } next[2] = {};
+    float sc = 0.0f, acc[NC] = {}, bias[RB] = {};
+    // the loads run over this CTA's blocks in order: (b, g) is the next one
+    int64_t it = blockIdx.z, b = it / groups, g = it - b * groups;
+    const int64_t row_step = (int64_t)kRows * points;
+    const auto load = [&](Next &x) {
+        if (it >= items) return;
+        const int64_t p = g * kGroup + c8;
+        x.n = (int)max((int64_t)0, min((int64_t)8, points - p));
+        const int8_t *q = codes + (b * cin + i0 + r0) * points + p;
+        const T *y = dy + (b * cout + o0 + r0) * points + p;
+        if (!VEC) {
+            x.sh_q = (int)(reinterpret_cast<uintptr_t>(q) & 3) * 8;
+            x.sh_y = (int)(reinterpret_cast<uintptr_t>(y) & 3) * 8;
+        }
+        // words reach up to 4 bytes past the wanted elements: there are as many in
+        // the tensor when 4 blocks follow, each of an element a row at least
+        if (VEC || it + 4 < items) {
 #pragma unroll
-        for (int k = 0; k < RA; ++k)
-            if (r0 + 16 * k < mi)
-                qa[k] = load8(codes + (b * cin + i0 + r0 + 16 * k) * points + p, n,
-                              codes + batch * cin * points);
+            for (int k = 0; k < RA; ++k)
+                x.q[k].load(q + k * row_step, r0 + kRows * k < mi ? x.n : 0);
 #pragma unroll
-        for (int k = 0; k < RB; ++k)
-            if (r0 + 16 * k < no)
-                yb[k] = load8(dy + (b * cout + o0 + r0 + 16 * k) * points + p, n,
-                              dy + batch * cout * points);
-        sc_next = row_i < cin ? scales[(b * cin + row_i) * groups + g] : 0.0f;
+            for (int k = 0; k < RB; ++k)
+                x.y[k].load(y + k * row_step, r0 + kRows * k < no ? x.n : 0);
+        } else {                                         // near the tensors' ends
+#pragma unroll
+            for (int k = 0; k < RA; ++k)
+                x.q[k].load_exact(q + k * row_step, r0 + kRows * k < mi ? x.n : 0);
+#pragma unroll
+            for (int k = 0; k < RB; ++k)
+                x.y[k].load_exact(y + k * row_step, r0 + kRows * k < no ? x.n : 0);
+        }
+        x.scale = row_i < i0 + mi ? scales[(b * cin + row_i) * groups + g] : 1.0f;
+        it += gridDim.z;
+        g += gridDim.z;
+        while (g >= groups) {
+            g -= groups;
+            ++b;
+        }
     };
     const auto drain = [&](int n, float s) {             // D of block n, times the scales
         mbar_wait(&bar[n & 1], (uint32_t)(n >> 1), err);
         tc_after_sync();
-        const uint32_t at = tmem + (n & 1) * kMaxN<T> + half + ((uint32_t)(w & 3) << 21);
+        const uint32_t at = tmem + (n & 1) * kMaxN<T> + c0 + ((uint32_t)(w & 3) << 21);
 #pragma unroll
-        for (int k = 0; k < kMaxN<T> / 2; k += 16) {
-            if (k >= hn || half + k >= N) break;
+        for (int k = 0; k < NC; k += 16) {
+            if (k >= hn || c0 + k >= N) break;
             float d[16];
             tmem_ld16(at + k, d);
 #pragma unroll
@@ -175,18 +259,18 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
         tc_before_sync();
     };
     int n = 0;
-    if (blockIdx.z < items) load(blockIdx.z);
-    for (int64_t it = blockIdx.z; it < items; it += gridDim.z, ++n) {
+    const auto block = [&](Next &x) {
         // the stage was read by the MMAs of block n - 2, drained one block ago
         char *st = base + (n & 1) * stage;
 #pragma unroll
         for (int k = 0; k < RA; ++k) {
-            const int r = r0 + 16 * k;
+            const int r = r0 + kRows * k;
             if (r >= mi) break;
             uint2 q;
             uint4 u;
             float f[8];
-            memcpy(&q, &qa[k], 8);
+            const Pack<int8_t, 8> qk = x.q[k].get(x.n, x.sh_q);
+            memcpy(&q, &qk, 8);
             code_values4(q.x, f);
             code_values4(q.y, f + 4);
             u.x = pack2<TO>(f[0], f[1]);
@@ -197,15 +281,18 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
         }
 #pragma unroll
         for (int k = 0; k < RB; ++k) {
-            const int r = r0 + 16 * k;
+            const int r = r0 + kRows * k;
             if (r >= no) break;
             char *dst = st + tile_a + (c8 >> 6) * chunk_b + sw_off16(r, c8 & 63);
+            const Pack<T, 8> yk = x.y[k].get(x.n, x.sh_y);
             float f[8];
+            if (NT > 1 || !ones)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = Storage<T>::load(&yb[k].v[j]);
-            bias[k] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                for (int j = 0; j < 8; ++j) f[j] = Storage<T>::load(&yk.v[j]);
+            if (!ones)
+                bias[k] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
             if constexpr (NT == 1) {
-                *reinterpret_cast<Pack<T, 8> *>(dst) = yb[k];
+                *reinterpret_cast<Pack<T, 8> *>(dst) = yk;
             } else {
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
@@ -219,8 +306,8 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
             }
         }
         const float s_prev = sc;
-        sc = sc_next;
-        if (it + gridDim.z < items) load(it + gridDim.z);
+        sc = x.scale;
+        load(x);
         fence_async_smem();
         __syncthreads();
         if (tid == 0) {
@@ -235,21 +322,31 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
             mma_commit(&bar[n & 1]);
         }
         if (n > 0) drain(n - 1, s_prev);
+        ++n;
+    };
+    const int blocks = (int)((items - blockIdx.z + gridDim.z - 1) / gridDim.z);
+    load(next[0]);
+    load(next[1]);
+    while (n < blocks) {
+        block(next[0]);
+        if (n < blocks) block(next[1]);
     }
     if (n > 0) drain(n - 1, sc);
     float *out = part + (int64_t)blockIdx.z * cout * (cin + 1);
 #pragma unroll
-    for (int k = 0; k < kMaxN<T> / 2; ++k) {
-        const int o = o0 + half + k;
-        if (k < hn && half + k < no && row_i < cin) out[(int64_t)o * (cin + 1) + row_i] = acc[k];
+    for (int k = 0; k < NC; ++k) {
+        const int o = o0 + c0 + k;
+        if (k >= hn || c0 + k >= no) break;
+        if (row_i < i0 + mi) out[(int64_t)o * (cin + 1) + row_i] = acc[k];
+        else if (ones && i0 == 0 && row_i == mi) out[(int64_t)o * (cin + 1) + cin] = acc[k];
     }
-    if (i0 == 0)
+    if (!ones && i0 == 0)
 #pragma unroll
         for (int k = 0; k < RB; ++k) {
             float b = bias[k];
 #pragma unroll
             for (int m = 8; m; m >>= 1) b += __shfl_xor_sync(0xffffffffu, b, m);
-            const int r = r0 + 16 * k;
+            const int r = r0 + kRows * k;
             if ((tid & 15) == 0 && r < no) out[(int64_t)(o0 + r) * (cin + 1) + cin] = b;
         }
     __syncthreads();
@@ -259,7 +356,7 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
 }
 
 // The shares of 32 elements added by 8 warps, then across the warps in order.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(256)
 k_linear_grad_sum(const float *__restrict__ part, float *__restrict__ dw, float *__restrict__ db,
                   int cin, int cout, int splits) {
     __shared__ float sm[8][32];
@@ -354,15 +451,19 @@ fno_status_t fno_linear_grad(fno_linear_grad_t p, const void *dy, const int8_t *
     st = with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
         const size_t smem = part_smem<T>(p->cout);
-        if (raise_smem_limit(k_linear_grad_part<T>, smem) != cudaSuccess) return FNO_ERR_CUDA;
-        k_linear_grad_part<T><<<grid, kThreads, smem, s>>>(
-            static_cast<const T *>(dy), codes, scales, part, p->batch, p->points, p->cin, p->cout,
-            groups, p->dev_err);
-        return launched();
+        const auto run = [&](auto kernel) {
+            if (raise_smem_limit(kernel, smem) != cudaSuccess) return FNO_ERR_CUDA;
+            kernel<<<grid, kThreads, smem, s>>>(static_cast<const T *>(dy), codes, scales, part,
+                                                p->batch, p->points, p->cin, p->cout, groups,
+                                                p->dev_err);
+            return launched();
+        };
+        return p->points % 8 == 0 ? run(k_linear_grad_part<T, true>)
+                                  : run(k_linear_grad_part<T, false>);
     });
     if (st != FNO_OK) return st;
     const int64_t n = (int64_t)p->cout * (p->cin + 1);
-    k_linear_grad_sum<<<(unsigned)ceil_div(n, 32), kThreads, 0, s>>>(part, dw, db, p->cin,
+    k_linear_grad_sum<<<(unsigned)ceil_div(n, 32), 256, 0, s>>>(part, dw, db, p->cin,
                                                                      p->cout, p->splits);
     return launched();
 }
