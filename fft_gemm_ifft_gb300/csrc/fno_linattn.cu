@@ -136,9 +136,6 @@ struct ChunkArgs {
     float scale_p;             // of a chunk's weights
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
@@ -171,15 +168,10 @@ __device__ __forceinline__ float2 term_value(uint32_t u) {
 template <typename T> constexpr int kTerms = std::is_same<T, float>::value ? 3
                                              : std::is_same<T, __half>::value ? 2 : 1;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool have) {
+// 16 bytes, or zeros
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool have) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Rows t0 .. t0 + m - 1 (in scan order), w columns, of a (length, heads, full)
@@ -199,7 +191,7 @@ __device__ __forceinline__ void load_rows(__nv_bfloat16 *dst, const T *src, int6
             const int r = i / vecs, c = (i - r * vecs) * 8;
             const bool have = r < m && c < w;
             const T *at = have ? src + (REV ? n - 1 - (t0 + r) : t0 + r) * stride + c : src;
-            cp_async16(smem_u32(dst + r * (W + 8) + c), at, have);
+            cp_async16_or_zero(smem_u32(dst + r * (W + 8) + c), at, have);
         }
         return;
     }

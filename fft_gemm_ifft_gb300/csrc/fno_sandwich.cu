@@ -22,9 +22,9 @@ using namespace fno::ops;
 // How a call runs: by tiles (grid layout), by rows (tokens), or by the kernels
 // for any size.  vec: elements of a thread's loads; per: a thread's channels
 // (tiles) or runs (rows); warps: of a CTA; group: warps of a row.
-enum { kAny = 0, kTiles = 1, kRows = 2 };
+enum { kAny = 0, kTiles = 1, kRows = 2, kStaged = 3 };
 struct Way {
-    int kind, vec, per, warps, group;
+    int kind, vec, per, warps, group;    // (group of kStaged: its stages)
 };
 
 struct fno_sandwich_s {
@@ -771,6 +771,344 @@ k_sandwich_bwd_grid(Args a) {
 }
 
 // ---------------------------------------------------------------------------
+// Backward on tiles of 64 points by every channel (up to 128), for even point
+// counts.  The fields' tiles come to shared memory asynchronously, the next
+// tile's over the work on this one where two fit; warp w takes the 8 channels
+// w, w + warps, ..., lane l the points 2 l and 2 l + 1, and all arithmetic is on
+// the pair (f32x2): what bounds the kernel next to the bytes is the number of
+// instructions, so sums are taken in two rounds (both norms' moments and
+// sum d, sum d N in the first, sum e, sum e M in the second), and a normalised
+// value is one subtraction and one multiply-add wherever it is needed.
+//
+// Moments.  A thread sums x - x0 and (x - x0)^2 over its channels, x0 its first
+// channel; sum (x - mean)^2 = S2 - S1^2 / n loses at most a factor n + 1 of the
+// digits, because x0's own deviation is part of it.  The warps' means are then
+// joined relative to channel 0 of the point, so that a large mean cancels in
+// exact differences.
+// ---------------------------------------------------------------------------
+constexpr int kTileP = 64, kTileC = 8;
+
+template <typename T> __device__ __forceinline__ float2 load_pair(const T *p) {
+    return Storage<T>::load2(p);
+}
+template <typename T> __device__ __forceinline__ void store_pair(T *p, float2 v);
+template <> __device__ __forceinline__ void store_pair<float>(float *p, float2 v) {
+    *reinterpret_cast<float2 *>(p) = v;
+}
+template <> __device__ __forceinline__ void store_pair<__half>(__half *p, float2 v) {
+    *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(v.x, v.y);
+}
+template <> __device__ __forceinline__ void store_pair<__nv_bfloat16>(__nv_bfloat16 *p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+__device__ __forceinline__ float2 code_pair(const int8_t *p) {
+    const uint32_t w = (uint32_t)*reinterpret_cast<const uint16_t *>(p) ^ 0x8080u;
+    return add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)),
+                            __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441))),
+                f2(-8388736.0f));
+}
+
+// bytes of a stage (the fields' tiles and the codes' scales) and of the rest
+__host__ __device__ inline int tile_stage(int channels, int elem, bool f8, bool du, bool dy,
+                                          bool block, bool full) {
+    const int n = channels * kTileP;
+    return n * elem * ((du ? 2 : 0) + dy + full + (block && !f8)) +
+           (f8 ? n + (channels * 4 + 15) / 16 * 16 : 0);
+}
+__host__ __device__ inline int tile_rest(int channels, int warps) {
+    return channels * 16 + 8 * warps * kTileP * 4 + 8 * kTileP * 4;
+}
+
+template <typename T, bool LAYER, bool F8>
+__global__ void __launch_bounds__(512)
+k_sandwich_bwd_tile(Args a, int stages) {
+    extern __shared__ float4 sm[];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int C = a.channels, mine = (C - w + warps - 1) / warps;
+    const bool block = F8 || a.f != nullptr, full = block && a.gate_kind == FNO_GATE_FULL;
+    const bool has_du = a.du != nullptr, has_dy = a.dy != nullptr;
+    float4 *par = sm;            // s a w2, s a, s b2, w1 (a of a gate per channel, else 1)
+    float *rows = reinterpret_cast<float *>(sm + C);
+    float *fin = rows + 8 * warps * kTileP;
+    char *buf = reinterpret_cast<char *>(fin + 8 * kTileP);
+    const int tile_n = C * kTileP, stage = tile_stage(C, sizeof(T), F8, has_du, has_dy, block, full);
+    // offsets of the fields in a stage
+    const int oy = 0, ou = oy + (has_du ? tile_n * (int)sizeof(T) : 0),
+              og = ou + (has_du ? tile_n * (int)sizeof(T) : 0),
+              oa = og + (has_dy ? tile_n * (int)sizeof(T) : 0),
+              of = oa + (full ? tile_n * (int)sizeof(T) : 0), os = of + tile_n;
+    const int64_t tiles = (a.points + kTileP - 1) / kTileP, seg_tiles = a.batch / gridDim.y * tiles;
+    const int64_t groups = (a.points + kGroup - 1) / kGroup;
+    const float inv = 1.0f / (float)C;
+    const bool wide = a.points % (16 / sizeof(T)) == 0, wide8 = a.points % 16 == 0;
+    for (int c = threadIdx.x; c < C; c += blockDim.x) {
+        float sa = block ? a.s[c] : 0.0f;
+        const float sb = block && LAYER ? sa * a.b2[c] : 0.0f;
+        if (block && a.gate_kind == FNO_GATE_CHANNEL)      // one sample a segment
+            sa *= gate_value(static_cast<const float *>(a.gate)[blockIdx.y * C + c], a.sigmoid);
+        par[c] = make_float4(block ? sa * a.w2[c] : 0.0f, sa, sb, has_du ? a.w1[c] : 0.0f);
+    }
+    // a field's tile, 64 points of every channel (what lies past the row's end is
+    // left as it is: those points are worked on and not stored)
+    const auto fetch_field = [&](const void *src, int elem, bool by16, uint32_t dst, int64_t base,
+                                 int np) {
+        const char *s = static_cast<const char *>(src);
+        const int row = kTileP * elem, piece = by16 ? 16 : 4, per = row / piece;
+        const int sh = 31 - __clz(per);                    // (a power of two)
+        for (int i = threadIdx.x; i < C * per; i += blockDim.x) {
+            const int c = i >> sh, o = (i & (per - 1)) * piece;
+            if (o >= np * elem) continue;
+            const char *at = s + (base + (int64_t)c * a.points) * elem + o;
+            if (by16) cp_async16(dst + c * row + o, at);
+            else if (elem > 1 || np * elem - o >= 4) cp_async4(dst + c * row + o, at);
+        }
+    };
+    const auto fetch = [&](int64_t t, int k) {
+        const int64_t tt = blockIdx.y * seg_tiles + t, b = tt / tiles, p = (tt - b * tiles) * kTileP;
+        const int64_t base = b * C * a.points + p;
+        const int np = (int)min((int64_t)kTileP, a.points - p);
+        char *st = buf + k * stage;
+        const uint32_t u = smem_u32(st);
+        if (has_du) {
+            fetch_field(a.x, sizeof(T), wide, u + oy, base, np);
+            fetch_field(a.du, sizeof(T), wide, u + ou, base, np);
+        }
+        if (has_dy) fetch_field(a.dy, sizeof(T), wide, u + og, base, np);
+        if (full) fetch_field(a.gate, sizeof(T), wide, u + oa, base, np);
+        if (F8) {
+            // rows of an even length start on 2 bytes: 4-byte copies need 4
+            if (a.points % 4 == 0) {
+                fetch_field(a.f8, 1, wide8, u + of, base, np);
+            } else {
+                for (int i = threadIdx.x; i < C * (kTileP / 2); i += blockDim.x) {
+                    const int c = i / (kTileP / 2), o = i % (kTileP / 2) * 2;
+                    if (o < np)
+                        *reinterpret_cast<uint16_t *>(st + of + c * kTileP + o) =
+                            *reinterpret_cast<const uint16_t *>(a.f8 + base +
+                                                                (int64_t)c * a.points + o);
+                }
+            }
+            for (int c = threadIdx.x; c < C; c += blockDim.x)
+                cp_async4(u + os + c * 4, a.f8_scale + (b * C + c) * groups + p / kGroup);
+        } else if (block) {
+            fetch_field(a.f, sizeof(T), wide, u + of, base, np);
+        }
+    };
+    float acc[kSums][kTileC] = {};
+    int k = 0;
+    if (blockIdx.x < seg_tiles) fetch(blockIdx.x, 0);
+    cp_async_commit();
+    for (int64_t t = blockIdx.x; t < seg_tiles; t += gridDim.x) {
+        const int64_t tt = blockIdx.y * seg_tiles + t, b = tt / tiles;
+        const int64_t p = (tt - b * tiles) * kTileP + lane * 2;
+        const bool on = p < a.points;
+        const int64_t at = (b * C + w) * a.points + p, step = warps * a.points;
+        if (stages > 1) {
+            if (t + gridDim.x < seg_tiles) fetch(t + gridDim.x, k ^ 1);
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
+        __syncthreads();
+        const char *st = buf + k * stage;
+        const int first = w * kTileP + lane * 2, hop = warps * kTileP;
+        const T *sy = reinterpret_cast<const T *>(st + oy) + first;
+        const T *su = reinterpret_cast<const T *>(st + ou) + first;
+        const T *sg = reinterpret_cast<const T *>(st + og) + first;
+        const T *sa = reinterpret_cast<const T *>(st + oa) + first;
+        const auto f_at = [&](int j) {
+            if constexpr (F8) {
+                const float s = reinterpret_cast<const float *>(st + os)[w + j * warps];
+                return mul2(code_pair(reinterpret_cast<const int8_t *>(st + of) + first + j * hop),
+                            f2(s));
+            } else {
+                return load_pair(reinterpret_cast<const T *>(st + of) + first + j * hop);
+            }
+        };
+        // round 1: each warp's moments of y and f, sum d and sum d (y - y0)
+        {
+            float2 y0 = f2(0.0f), y1 = y0, y2 = y0, g0 = y0, g1 = y0, f0 = y0, f1 = y0, fq = y0;
+#pragma unroll
+            for (int j = 0; j < kTileC; ++j) {
+                if (j >= mine) break;
+                if (has_du) {
+                    const float2 y = load_pair(sy + j * hop);
+                    if (j == 0 && LAYER) y0 = y;
+                    const float2 v = LAYER ? sub2(y, y0) : y;
+                    const float2 d = mul2(load_pair(su + j * hop), f2(par[w + j * warps].w));
+                    if (LAYER) y1 = add2(y1, v);
+                    y2 = fma2(v, v, y2);
+                    g0 = add2(g0, d);
+                    g1 = fma2(d, v, g1);
+                }
+                if (block) {
+                    const float2 f = f_at(j);
+                    if (j == 0 && LAYER) f0 = f;
+                    const float2 v = LAYER ? sub2(f, f0) : f;
+                    if (LAYER) f1 = add2(f1, v);
+                    fq = fma2(v, v, fq);
+                }
+            }
+            float *r = rows + w * kTileP + lane * 2;
+            const int line = warps * kTileP;
+            if (has_du) {
+                if (LAYER) {
+                    *reinterpret_cast<float2 *>(r) = y0;
+                    *reinterpret_cast<float2 *>(r + line) = y1;
+                }
+                *reinterpret_cast<float2 *>(r + 2 * line) = y2;
+                *reinterpret_cast<float2 *>(r + 3 * line) = g0;
+                *reinterpret_cast<float2 *>(r + 4 * line) = g1;
+            }
+            if (block) {
+                if (LAYER) {
+                    *reinterpret_cast<float2 *>(r + 5 * line) = f0;
+                    *reinterpret_cast<float2 *>(r + 6 * line) = f1;
+                }
+                *reinterpret_cast<float2 *>(r + 7 * line) = fq;
+            }
+        }
+        __syncthreads();
+        // joined by one thread for each (point, norm)
+        for (int i = threadIdx.x; i < 2 * kTileP; i += blockDim.x) {
+            const int q = i & (kTileP - 1), line = warps * kTileP;
+            const bool second = i >= kTileP;
+            if (second ? !block : !has_du) continue;
+            const float *r = rows + q + (second ? 5 * line : 0);
+            const int base = C / warps, more = C - base * warps;
+            float ref = 0.0f, mean = 0.0f, ss = 0.0f, e0 = 0.0f, e1 = 0.0f;
+            if (LAYER) {
+                ref = r[0];
+#pragma unroll 4
+                for (int v = 0; v < warps; ++v)
+                    mean += fmaf((float)(base + (v < more)), r[v * kTileP] - ref,
+                                 r[line + v * kTileP]);
+                mean *= inv;
+            }
+#pragma unroll 4
+            for (int v = 0; v < warps; ++v) {
+                ss += r[2 * line + v * kTileP];
+                float off = 0.0f;
+                if (LAYER) {
+                    const float nv = (float)(base + (v < more)), s1 = r[line + v * kTileP];
+                    off = r[v * kTileP] - ref;
+                    const float m = __fdividef(s1, nv), d = off + m - mean;
+                    ss += nv * d * d - m * s1;
+                }
+                if (!second) {
+                    e0 += r[3 * line + v * kTileP];
+                    e1 += fmaf(off, r[3 * line + v * kTileP], r[4 * line + v * kTileP]);
+                }
+            }
+            const float rr = rsqrtf(fmaf(fmaxf(ss, 0.0f), inv, a.eps));
+            float *o = fin + q + (second ? 5 * kTileP : 0);
+            o[0] = ref;
+            o[kTileP] = -mean * rr;
+            o[2 * kTileP] = rr;
+            if (!second) {
+                o[3 * kTileP] = LAYER ? -e0 * inv : 0.0f;
+                o[4 * kTileP] = -rr * (e1 - mean * e0) * inv;
+            }
+        }
+        __syncthreads();
+        const auto fin_at = [&](int i) {
+            return *reinterpret_cast<const float2 *>(fin + i * kTileP + lane * 2);
+        };
+        // round 2: dY and dx, the channels' sums, sum e and sum e M
+        const float2 ref1 = fin_at(0), mr1 = fin_at(1), r1 = fin_at(2), d0 = fin_at(3),
+                     d1 = fin_at(4), ref2 = fin_at(5), mr2 = fin_at(6), r2 = fin_at(7);
+        const auto m_at = [&](int j) {
+            const float2 f = f_at(j);
+            return fma2(LAYER ? sub2(f, ref2) : f, r2, mr2);
+        };
+        float2 e[kTileC], e0 = f2(0.0f), e1 = e0;
+#pragma unroll
+        for (int j = 0; j < kTileC; ++j) {
+            if (j >= mine) break;
+            const float4 q = par[w + j * warps];
+            float2 g = has_dy ? load_pair(sg + j * hop) : f2(0.0f);
+            if (has_du) {
+                const float2 y = load_pair(sy + j * hop), u = load_pair(su + j * hop);
+                const float2 n = fma2(LAYER ? sub2(y, ref1) : y, r1, mr1);
+                float2 d = mul2(u, f2(q.w));
+                if (LAYER) d = add2(d, d0);
+                g = fma2(fma2(n, d1, d), r1, g);
+                const float2 un = mul2(u, n);
+                if (on) {
+                    acc[2][j] += un.x + un.y;
+                    if (LAYER) acc[3][j] += u.x + u.y;
+                }
+            }
+            if (on) store_pair(static_cast<T *>(a.dx) + at + j * step, g);
+            if (block) {
+                const float2 m = m_at(j);
+                if (full) {
+                    const float2 gate = load_pair(sa + j * hop);
+                    const float ax = gate_value(gate.x, a.sigmoid), ay = gate_value(gate.y, a.sigmoid);
+                    if (a.dgate && on)
+                        store_pair(static_cast<T *>(a.dgate) + at + j * step,
+                                   mul2(mul2(g, fma2(m, f2(q.x), f2(q.z))),
+                                        make_float2(gate_slope(ax, a.sigmoid),
+                                                    gate_slope(ay, a.sigmoid))));
+                    g = mul2(g, make_float2(ax, ay));
+                }
+                const float2 gm = mul2(g, m);
+                if (on) {
+                    acc[0][j] += gm.x + gm.y;
+                    if (LAYER) acc[1][j] += g.x + g.y;
+                }
+                e[j] = mul2(g, f2(q.x));
+                e0 = add2(e0, e[j]);
+                e1 = fma2(e[j], m, e1);
+            }
+        }
+        if (block) {
+            float *r = rows + w * kTileP + lane * 2;
+            const int line = warps * kTileP;
+            if (LAYER) *reinterpret_cast<float2 *>(r) = e0;
+            *reinterpret_cast<float2 *>(r + line) = e1;
+            __syncthreads();
+            e0 = e1 = f2(0.0f);
+#pragma unroll 4
+            for (int v = 0; v < warps; ++v) {
+                const float *s = rows + v * kTileP + lane * 2;
+                if (LAYER) e0 = add2(e0, *reinterpret_cast<const float2 *>(s));
+                e1 = add2(e1, *reinterpret_cast<const float2 *>(s + line));
+            }
+            e0 = mul2(e0, f2(-inv));
+            e1 = mul2(e1, f2(-inv));
+#pragma unroll
+            for (int j = 0; j < kTileC; ++j) {
+                if (j >= mine || !on) break;
+                float2 v = LAYER ? add2(e[j], e0) : e[j];
+                v = mul2(fma2(m_at(j), e1, v), r2);
+                store_pair(static_cast<T *>(a.df) + at + j * step, v);
+            }
+        }
+        __syncthreads();         // the next tile reuses the rows and the stage
+        if (stages > 1) {
+            k ^= 1;
+        } else {
+            if (t + gridDim.x < seg_tiles) fetch(t + gridDim.x, 0);
+            cp_async_commit();
+        }
+    }
+    float *out = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kSums * C;
+#pragma unroll
+    for (int j = 0; j < kTileC; ++j) {
+        if (j >= mine) break;
+#pragma unroll
+        for (int q = 0; q < kSums; ++q) {
+            float v = acc[q][j];
+#pragma unroll
+            for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+            if (lane == 0) out[q * C + w + j * warps] = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Token layout: G warps hold a row in registers, each thread J runs of V
 // consecutive channels; a CTA of R = warps / G rows.
 // ---------------------------------------------------------------------------
@@ -1193,6 +1531,8 @@ void with_layout(const fno_sandwich_s &p, F &&f) {
     });
 }
 
+constexpr int kSmemPerSm = 228 * 1024;
+
 // The variant for a shape.  Vectors need the last axis (where every row
 // starts) to be a multiple of them; registers bound a thread's elements (32 of
 // each field forward, 16 to 32 of up to four backward), and with 16 warps a
@@ -1205,7 +1545,14 @@ Way choose_way(const fno_sandwich_desc_t &d, bool backward) {
             return Way{kTiles, vec, per, (int)ceil_div(c, per), 0};
         };
         if (backward) {
-            if (c <= 128) return tiles(d.points % 2 == 0 ? 2 : 1, 8);
+            if (c <= 128 && d.points % 2 == 0) {
+                const int warps = (int)ceil_div(c, kTileC);
+                const int stage = tile_stage(c, (int)elem_bytes(d.dtype), false, true, true, true,
+                                             d.gate == FNO_GATE_FULL);
+                const int most = (kSmemPerSm / 2 - 1024 - tile_rest(c, warps)) / stage;
+                return Way{kStaged, 2, kTileC, warps, most >= 2 ? 2 : 1};
+            }
+            if (c <= 128) return tiles(1, 8);
             if (c <= 256) return tiles(1, 16);
         } else {
             if (c <= 128) return tiles(d.points % 4 == 0 ? 4 : 1, 8);
@@ -1229,7 +1576,7 @@ void with_tiles(const fno_sandwich_s &p, const Way &way, F &&f) {
             if (p.d.norm == FNO_NORM_LAYER) f(t, v, per, std::true_type());
             else f(t, v, per, std::false_type());
         };
-        constexpr std::integral_constant<int, BACKWARD ? 2 : 4> wide;
+        constexpr std::integral_constant<int, BACKWARD ? 1 : 4> wide;
         constexpr std::integral_constant<int, 1> one;
         constexpr std::integral_constant<int, 2> two;
         constexpr std::integral_constant<int, 8> few;
@@ -1257,7 +1604,16 @@ void with_rows(const fno_sandwich_s &p, const Way &way, F &&f) {
 // The backward kernel of a plan as a function for Args, by its way.
 template <class F>
 void with_backward(const fno_sandwich_s &p, bool f8, F &&f) {
-    if (p.bwd.kind == kTiles) {
+    if (p.bwd.kind == kStaged) {
+        with_storage(p.d.dtype, [&](auto t) {
+            using T = decltype(t);
+            const bool layer = p.d.norm == FNO_NORM_LAYER;
+            if (layer && f8) f(k_sandwich_bwd_tile<T, true, true>);
+            else if (layer) f(k_sandwich_bwd_tile<T, true, false>);
+            else if (f8) f(k_sandwich_bwd_tile<T, false, true>);
+            else f(k_sandwich_bwd_tile<T, false, false>);
+        });
+    } else if (p.bwd.kind == kTiles) {
         with_tiles<true>(p, p.bwd, [&](auto t, auto v, auto per, auto layer) {
             using T = decltype(t);
             constexpr int V = decltype(v)::value, CPT = decltype(per)::value;
@@ -1274,22 +1630,31 @@ void with_backward(const fno_sandwich_s &p, bool f8, F &&f) {
     }
 }
 
-// (with_backward's kernels take Args, and the rows' also the warps of a row)
-void launch_tiles(void (*k)(Args), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                  const Args &a) {
-    k<<<grid, threads, smem, s>>>(a);
+// (with_backward's kernels take Args and, but for kTiles, the way's `group`)
+fno_status_t launch_backward(void (*k)(Args), dim3 grid, const Way &way, size_t smem,
+                             cudaStream_t s, const Args &a) {
+    k<<<grid, way.warps * 32, smem, s>>>(a);
+    return launched();
 }
-void launch_tiles(void (*)(Args, int), dim3, int, size_t, cudaStream_t, const Args &) {}
-void launch_rows(void (*k)(Args, int), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                 const Args &a, int group) {
-    k<<<grid, threads, smem, s>>>(a, group);
+fno_status_t launch_backward(void (*k)(Args, int), dim3 grid, const Way &way, size_t smem,
+                             cudaStream_t s, const Args &a) {
+    if (raise_smem_limit(k, smem) != cudaSuccess) return FNO_ERR_CUDA;
+    k<<<grid, way.warps * 32, smem, s>>>(a, way.group);
+    return launched();
 }
-void launch_rows(void (*)(Args), dim3, int, size_t, cudaStream_t, const Args &, int) {}
 
-size_t backward_smem(const fno_sandwich_s &p) {
-    if (p.bwd.kind == kTiles) return grid_smem(p.d.channels, p.bwd.vec, p.bwd.warps, 3);
-    const int rows = p.bwd.warps / p.bwd.group;
-    return rows > 1 ? (size_t)rows * p.d.channels * 4 : 0;
+// Shared memory of a call (of the largest call, for a plan: every operand there).
+size_t backward_smem(const fno_sandwich_s &p, bool f8 = false, bool du = true, bool dy = true,
+                     bool block = true) {
+    const Way &way = p.bwd;
+    const int c = p.d.channels;
+    if (way.kind == kStaged)
+        return tile_rest(c, way.warps) +
+               (size_t)way.group * tile_stage(c, (int)elem_bytes(p.d.dtype), f8, du, dy, block,
+                                              block && p.d.gate == FNO_GATE_FULL);
+    if (way.kind == kTiles) return grid_smem(c, way.vec, way.warps, 3);
+    const int rows = way.warps / way.group;
+    return rows > 1 ? (size_t)rows * c * 4 : 0;
 }
 
 int team_blocks(const fno_sandwich_s &p) {
@@ -1351,8 +1716,10 @@ fno_status_t fno_sandwich_plan(fno_sandwich_t *out, const fno_sandwich_desc_t *d
         int ctas = 1;
         cudaError_t e = cudaSuccess;
         with_backward(*p, false, [&](auto kernel) {
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, p->bwd.warps * 32,
-                                                              backward_smem(*p));
+            e = raise_smem_limit(kernel, backward_smem(*p));
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                    &ctas, kernel, p->bwd.warps * 32, backward_smem(*p));
         });
         if (e != cudaSuccess || ctas < 1) {
             cudaGetLastError();
@@ -1361,9 +1728,8 @@ fno_status_t fno_sandwich_plan(fno_sandwich_t *out, const fno_sandwich_desc_t *d
         }
         want = (int64_t)p->sms * ctas / p->segs;
         if (want < 1) want = 1;
-        most = p->bwd.kind == kTiles
-                   ? d->batch / p->segs * ceil_div(d->points, 32 * p->bwd.vec)
-                   : ceil_div(p->seg_points, p->bwd.warps / p->bwd.group);
+        most = p->bwd.kind == kRows ? ceil_div(p->seg_points, p->bwd.warps / p->bwd.group)
+                                    : d->batch / p->segs * ceil_div(d->points, 32 * p->bwd.vec);
     }
     p->splits = (int)(want < most ? want : most);
     p->workspace = p->part_off + (size_t)p->segs * p->splits * kSums * d->channels * 4;
@@ -1492,12 +1858,12 @@ fno_status_t fno_sandwich_backward(fno_sandwich_t p, const void *y, const void *
     } else {
         const dim3 shares((unsigned)p->splits, (unsigned)p->segs);
         with_backward(*p, f8 != nullptr, [&](auto kernel) {
-            if (p->bwd.kind == kTiles)
-                launch_tiles(kernel, shares, p->bwd.warps * 32, backward_smem(*p), cs, a);
-            else
-                launch_rows(kernel, shares, p->bwd.warps * 32, backward_smem(*p), cs, a,
-                            p->bwd.group);
+            st = launch_backward(kernel, shares, p->bwd,
+                                 backward_smem(*p, f8 != nullptr, du != nullptr, dy != nullptr,
+                                               block),
+                                 cs, a);
         });
+        if (st != FNO_OK) return st;
     }
     const bool per_channel = block && p->d.gate == FNO_GATE_CHANNEL;
     k_sandwich_params<<<(unsigned)ceil_div(a.channels, 32), 1024, 0, cs>>>(
