@@ -819,14 +819,17 @@ __host__ __device__ inline int tile_rest(int channels, int warps) {
     return channels * 16 + 8 * warps * kTileP * 4 + 8 * kTileP * 4;
 }
 
-template <typename T, bool LAYER, bool F8>
+// WHOLE: every operand is there but a full gate, the points are a multiple of
+// 64 and the channels of 8, so that no element needs a check.
+template <typename T, bool LAYER, bool F8, bool WHOLE>
 __global__ void __launch_bounds__(512)
 k_sandwich_bwd_tile(Args a, int stages) {
     extern __shared__ float4 sm[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int C = a.channels, mine = (C - w + warps - 1) / warps;
-    const bool block = F8 || a.f != nullptr, full = block && a.gate_kind == FNO_GATE_FULL;
-    const bool has_du = a.du != nullptr, has_dy = a.dy != nullptr;
+    const int C = a.channels, mine = WHOLE ? kTileC : (C - w + warps - 1) / warps;
+    const bool block = F8 || WHOLE || a.f != nullptr;
+    const bool full = !WHOLE && block && a.gate_kind == FNO_GATE_FULL;
+    const bool has_du = WHOLE || a.du != nullptr, has_dy = WHOLE || a.dy != nullptr;
     float4 *par = sm;            // s a w2, s a, s b2, w1 (a of a gate per channel, else 1)
     float *rows = reinterpret_cast<float *>(sm + C);
     float *fin = rows + 8 * warps * kTileP;
@@ -840,7 +843,8 @@ k_sandwich_bwd_tile(Args a, int stages) {
     const int64_t tiles = (a.points + kTileP - 1) / kTileP, seg_tiles = a.batch / gridDim.y * tiles;
     const int64_t groups = (a.points + kGroup - 1) / kGroup;
     const float inv = 1.0f / (float)C;
-    const bool wide = a.points % (16 / sizeof(T)) == 0, wide8 = a.points % 16 == 0;
+    const bool wide = WHOLE || a.points % (16 / sizeof(T)) == 0;
+    const bool wide8 = WHOLE || a.points % 16 == 0;
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
         float sa = block ? a.s[c] : 0.0f;
         const float sb = block && LAYER ? sa * a.b2[c] : 0.0f;
@@ -853,6 +857,18 @@ k_sandwich_bwd_tile(Args a, int stages) {
     const auto fetch_field = [&](const void *src, int elem, bool by16, uint32_t dst, int64_t base,
                                  int np) {
         const char *s = static_cast<const char *>(src);
+        if (WHOLE) {             // 16 warps at most: a thread's pieces are some rows apart
+            const int per = kTileP * elem / 16, c = threadIdx.x / per;
+            const int o = threadIdx.x % per * 16, hop = blockDim.x / per;
+            const char *at = s + (base + (int64_t)c * a.points) * elem + o;
+            const int64_t step = (int64_t)hop * a.points * elem;
+            dst += c * kTileP * elem + o;
+            const int n = C * per / blockDim.x;          // (C = 8 warps: 1, 2, 4 pieces)
+#pragma unroll 4
+            for (int i = 0; i < n; ++i, at += step, dst += hop * kTileP * elem)
+                cp_async16(dst, at);
+            return;
+        }
         const int row = kTileP * elem, piece = by16 ? 16 : 4, per = row / piece;
         const int sh = 31 - __clz(per);                    // (a power of two)
         for (int i = threadIdx.x; i < C * per; i += blockDim.x) {
@@ -877,7 +893,7 @@ k_sandwich_bwd_tile(Args a, int stages) {
         if (full) fetch_field(a.gate, sizeof(T), wide, u + oa, base, np);
         if (F8) {
             // rows of an even length start on 2 bytes: 4-byte copies need 4
-            if (a.points % 4 == 0) {
+            if (WHOLE || a.points % 4 == 0) {
                 fetch_field(a.f8, 1, wide8, u + of, base, np);
             } else {
                 for (int i = threadIdx.x; i < C * (kTileP / 2); i += blockDim.x) {
@@ -901,7 +917,7 @@ k_sandwich_bwd_tile(Args a, int stages) {
     for (int64_t t = blockIdx.x; t < seg_tiles; t += gridDim.x) {
         const int64_t tt = blockIdx.y * seg_tiles + t, b = tt / tiles;
         const int64_t p = (tt - b * tiles) * kTileP + lane * 2;
-        const bool on = p < a.points;
+        const bool on = WHOLE || p < a.points;
         const int64_t at = (b * C + w) * a.points + p, step = warps * a.points;
         if (stages > 1) {
             if (t + gridDim.x < seg_tiles) fetch(t + gridDim.x, k ^ 1);
@@ -926,6 +942,7 @@ k_sandwich_bwd_tile(Args a, int stages) {
                 return load_pair(reinterpret_cast<const T *>(st + of) + first + j * hop);
             }
         };
+        float2 fv[kTileC];       // f
         // round 1: each warp's moments of y and f, sum d and sum d (y - y0)
         {
             float2 y0 = f2(0.0f), y1 = y0, y2 = y0, g0 = y0, g1 = y0, f0 = y0, f1 = y0, fq = y0;
@@ -943,9 +960,9 @@ k_sandwich_bwd_tile(Args a, int stages) {
                     g1 = fma2(d, v, g1);
                 }
                 if (block) {
-                    const float2 f = f_at(j);
-                    if (j == 0 && LAYER) f0 = f;
-                    const float2 v = LAYER ? sub2(f, f0) : f;
+                    fv[j] = f_at(j);
+                    if (j == 0 && LAYER) f0 = fv[j];
+                    const float2 v = LAYER ? sub2(fv[j], f0) : fv[j];
                     if (LAYER) f1 = add2(f1, v);
                     fq = fma2(v, v, fq);
                 }
@@ -1018,11 +1035,8 @@ k_sandwich_bwd_tile(Args a, int stages) {
         // round 2: dY and dx, the channels' sums, sum e and sum e M
         const float2 ref1 = fin_at(0), mr1 = fin_at(1), r1 = fin_at(2), d0 = fin_at(3),
                      d1 = fin_at(4), ref2 = fin_at(5), mr2 = fin_at(6), r2 = fin_at(7);
-        const auto m_at = [&](int j) {
-            const float2 f = f_at(j);
-            return fma2(LAYER ? sub2(f, ref2) : f, r2, mr2);
-        };
         float2 e[kTileC], e0 = f2(0.0f), e1 = e0;
+        T *dx = static_cast<T *>(a.dx) + at, *df = static_cast<T *>(a.df) + at;
 #pragma unroll
         for (int j = 0; j < kTileC; ++j) {
             if (j >= mine) break;
@@ -1040,9 +1054,11 @@ k_sandwich_bwd_tile(Args a, int stages) {
                     if (LAYER) acc[3][j] += u.x + u.y;
                 }
             }
-            if (on) store_pair(static_cast<T *>(a.dx) + at + j * step, g);
+            if (on) store_pair(dx, g);
+            dx += step;
             if (block) {
-                const float2 m = m_at(j);
+                const float2 m = fma2(LAYER ? sub2(fv[j], ref2) : fv[j], r2, mr2);
+                fv[j] = m;       // M from here on
                 if (full) {
                     const float2 gate = load_pair(sa + j * hop);
                     const float ax = gate_value(gate.x, a.sigmoid), ay = gate_value(gate.y, a.sigmoid);
@@ -1082,8 +1098,9 @@ k_sandwich_bwd_tile(Args a, int stages) {
             for (int j = 0; j < kTileC; ++j) {
                 if (j >= mine || !on) break;
                 float2 v = LAYER ? add2(e[j], e0) : e[j];
-                v = mul2(fma2(m_at(j), e1, v), r2);
-                store_pair(static_cast<T *>(a.df) + at + j * step, v);
+                v = mul2(fma2(fv[j], e1, v), r2);
+                store_pair(df, v);
+                df += step;
             }
         }
         __syncthreads();         // the next tile reuses the rows and the stage
@@ -1603,15 +1620,20 @@ void with_rows(const fno_sandwich_s &p, const Way &way, F &&f) {
 
 // The backward kernel of a plan as a function for Args, by its way.
 template <class F>
-void with_backward(const fno_sandwich_s &p, bool f8, F &&f) {
+void with_backward(const fno_sandwich_s &p, bool f8, bool whole, F &&f) {
     if (p.bwd.kind == kStaged) {
         with_storage(p.d.dtype, [&](auto t) {
             using T = decltype(t);
             const bool layer = p.d.norm == FNO_NORM_LAYER;
-            if (layer && f8) f(k_sandwich_bwd_tile<T, true, true>);
-            else if (layer) f(k_sandwich_bwd_tile<T, true, false>);
-            else if (f8) f(k_sandwich_bwd_tile<T, false, true>);
-            else f(k_sandwich_bwd_tile<T, false, false>);
+            const auto pick = [&](auto l, auto q) {
+                constexpr bool L = decltype(l)::value, Q = decltype(q)::value;
+                if (whole) f(k_sandwich_bwd_tile<T, L, Q, true>);
+                else f(k_sandwich_bwd_tile<T, L, Q, false>);
+            };
+            if (layer && f8) pick(std::true_type(), std::true_type());
+            else if (layer) pick(std::true_type(), std::false_type());
+            else if (f8) pick(std::false_type(), std::true_type());
+            else pick(std::false_type(), std::false_type());
         });
     } else if (p.bwd.kind == kTiles) {
         with_tiles<true>(p, p.bwd, [&](auto t, auto v, auto per, auto layer) {
@@ -1715,7 +1737,7 @@ fno_status_t fno_sandwich_plan(fno_sandwich_t *out, const fno_sandwich_desc_t *d
     } else {
         int ctas = 1;
         cudaError_t e = cudaSuccess;
-        with_backward(*p, false, [&](auto kernel) {
+        with_backward(*p, false, false, [&](auto kernel) {
             e = raise_smem_limit(kernel, backward_smem(*p));
             if (e == cudaSuccess)
                 e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
@@ -1857,7 +1879,9 @@ fno_status_t fno_sandwich_backward(fno_sandwich_t p, const void *y, const void *
         });
     } else {
         const dim3 shares((unsigned)p->splits, (unsigned)p->segs);
-        with_backward(*p, f8 != nullptr, [&](auto kernel) {
+        const bool whole = block && du && dy && p->d.gate != FNO_GATE_FULL &&
+                           p->d.points % kTileP == 0 && p->d.channels % kTileC == 0;
+        with_backward(*p, f8 != nullptr, whole, [&](auto kernel) {
             st = launch_backward(kernel, shares, p->bwd,
                                  backward_smem(*p, f8 != nullptr, du != nullptr, dy != nullptr,
                                                block),
