@@ -1,0 +1,429 @@
+// fno_sandwich_rows.cu -- the sandwich norm on token rows, forward up to 8192
+// channels and backward up to 4096.
+#include "fno_sandwich.h"
+
+using namespace fno;
+using namespace fno::ops;
+using namespace fno::sandwich;
+
+namespace {
+
+constexpr int kMaxWarps = 16;
+
+// ---------------------------------------------------------------------------
+// Token layout: G warps hold a row in registers, each thread J runs of V
+// consecutive channels; a CTA of R = warps / G rows.
+// ---------------------------------------------------------------------------
+// the sum of N values over the G warps of a row
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int G, float (*red)[kMaxWarps]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+    if (G == 1) return;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();             // the last sum's readers are done
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < N; ++k) red[k][w] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        v[k] = lane < G ? red[k][w / G * G + lane] : 0.0f;
+#pragma unroll
+        for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+    }
+}
+
+// mean and r of a row whose values less the shift are x[.]; entries beyond the
+// row's channels are excluded by `have`.
+template <int N, bool LAYER, class Have>
+__device__ __forceinline__ void row_norm(const float (&x)[N], Have &&have, int channels, float eps,
+                                         int G, float (*red)[kMaxWarps], float &mean, float &r) {
+    const float inv = 1.0f / (float)channels;
+    mean = 0.0f;
+    if (LAYER) {
+        float s[1] = {};
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[0] += x[i];          // absent entries are 0
+        row_sum<1>(s, G, red);
+        mean = s[0] * inv;
+    }
+    float q[1] = {};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float d = have(i) ? x[i] - mean : 0.0f;
+        q[0] = fmaf(d, d, q[0]);
+    }
+    row_sum<1>(q, G, red);
+    r = rsqrtf(fmaf(q[0], inv, eps));
+}
+
+template <typename T, int V, int J, bool LAYER>
+__global__ void __launch_bounds__(512)
+k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
+    constexpr int N = V * J;
+    __shared__ float red[1][kMaxWarps];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
+    const int64_t rows = a.batch * a.points;
+    const int64_t row = (int64_t)blockIdx.x * R + w / G;
+    const bool on = row < rows;
+    const int c0 = ((w % G) * 32 + lane) * V, cs = G * 32 * V;     // run j at c0 + j cs
+    const int64_t base = row * a.channels;
+    const auto have = [&](int i) { return c0 + i / V * cs < a.channels; };
+    const bool block = a.f != nullptr;
+    Pack<T, V> xs[J] = {};
+    float v[N];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        if (on && have(j * V))
+            xs[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.x) + base + c0 +
+                                                          j * cs);
+    if (block) {
+        Pack<T, V> fs[J] = {};
+        float shift = 0.0f, mean, r;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (on && have(j * V))
+                fs[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.f) + base +
+                                                              c0 + j * cs);
+        if (LAYER && on) shift = Storage<T>::load(static_cast<const T *>(a.f) + base);
+        if (f8) {
+            // a group is V L lanes' runs: 32 lanes for V = 4, 16 for 8; for V = 1
+            // four runs of 32 lanes (G = 1 run j, or neighbouring warps): then
+            // the caller packs by itself
+            constexpr int L = V > 1 ? kGroup / V : 32;
+            const uint32_t mask = L == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) m = max(m, abs_bits(Storage<T>::load(&fs[j].v[i])));
+                m = __reduce_max_sync(mask, m);
+                const Group8 s = group8(m);
+                Pack<int8_t, V> q;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    q.v[i] = (int8_t)code8(Storage<T>::load(&fs[j].v[i]), s.inv);
+                if (on && have(j * V)) {
+                    const int c = c0 + j * cs;
+                    *reinterpret_cast<Pack<int8_t, V> *>(f8 + base + c) = q;
+                    if (lane % L == 0)
+                        f8_scale[row * ((a.channels + kGroup - 1) / kGroup) + c / kGroup] = s.scale;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = have(i) ? Storage<T>::load(&fs[i / V].v[i % V]) - shift : 0.0f;
+        row_norm<N, LAYER>(v, have, a.channels, a.eps, G, red, mean, r);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!on || !have(j * V)) continue;
+            const int c = c0 + j * cs;
+            const auto s = *reinterpret_cast<const Pack<float, V> *>(a.s + c);
+            const auto w2 = *reinterpret_cast<const Pack<float, V> *>(a.w2 + c);
+            Pack<float, V> b2 = {}, gf = {};
+            Pack<T, V> gs = {}, ys;
+            if (LAYER) b2 = *reinterpret_cast<const Pack<float, V> *>(a.b2 + c);
+            if (a.gate_kind == FNO_GATE_FULL)
+                gs = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.gate) + base + c);
+            if (a.gate_kind == FNO_GATE_CHANNEL)
+                gf = *reinterpret_cast<const Pack<float, V> *>(
+                    static_cast<const float *>(a.gate) + row / a.points * a.channels + c);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float g = 1.0f;
+                if (a.gate_kind != FNO_GATE_NONE)
+                    g = gate_value(a.gate_kind == FNO_GATE_FULL ? Storage<T>::load(&gs.v[i])
+                                                                : gf.v[i], a.sigmoid);
+                const float m = (v[j * V + i] - mean) * r;
+                const float z = LAYER ? fmaf(m, w2.v[i], b2.v[i]) : m * w2.v[i];
+                v[j * V + i] = fmaf(s.v[i] * g, z, Storage<T>::load(&xs[j].v[i]));
+                Storage<T>::store(&ys.v[i], v[j * V + i]);
+            }
+            *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.y) + base + c) = ys;
+        }
+        if (!a.u) return;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = have(i) ? Storage<T>::load(&xs[i / V].v[i % V]) : 0.0f;
+    }
+    float mean, r;
+    if (LAYER) {                 // shift by the row's channel 0
+        __shared__ float first[kMaxWarps];
+        if (w % G == 0 && lane == 0) first[w / G] = v[0];
+        __syncthreads();
+        const float shift = first[w / G];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = have(i) ? v[i] - shift : 0.0f;
+    }
+    row_norm<N, LAYER>(v, have, a.channels, a.eps, G, red, mean, r);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        if (!on || !have(j * V)) continue;
+        const int c = c0 + j * cs;
+        const auto w1 = *reinterpret_cast<const Pack<float, V> *>(a.w1 + c);
+        Pack<float, V> b1 = {};
+        if (LAYER) b1 = *reinterpret_cast<const Pack<float, V> *>(a.b1 + c);
+        Pack<T, V> us;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float n = (v[j * V + i] - mean) * r;
+            Storage<T>::store(&us.v[i], LAYER ? fmaf(n, w1.v[i], b1.v[i]) : n * w1.v[i]);
+        }
+        *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.u) + base + c) = us;
+    }
+}
+
+template <typename T, int V, int J, bool LAYER, bool F8>
+__global__ void __launch_bounds__(512)
+k_sandwich_bwd_rows(Args a, int G) {
+    constexpr int N = V * J;
+    using TF = typename std::conditional<F8, int8_t, T>::type;
+    __shared__ float red[2][kMaxWarps];
+    extern __shared__ float4 sm[];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
+    const int c0 = ((w % G) * 32 + lane) * V, cs = G * 32 * V;
+    const auto have = [&](int i) { return c0 + i / V * cs < a.channels; };
+    const bool block = F8 || a.f != nullptr;
+    const float inv = 1.0f / (float)a.channels;
+    const int64_t groups = (a.channels + kGroup - 1) / kGroup;
+    float acc[kSums][N] = {};
+    for (int64_t t = (int64_t)blockIdx.x * R; t < a.seg_points; t += (int64_t)gridDim.x * R) {
+        const bool on = t + w / G < a.seg_points;
+        const int64_t row = blockIdx.y * a.seg_points + t + w / G, base = row * a.channels;
+        Pack<T, V> ys[J] = {}, us[J] = {}, gs[J] = {}, gates[J] = {};
+        Pack<TF, V> fs[J] = {};
+        float fsc[F8 ? J : 1] = {};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!on || !have(j * V)) continue;
+            const int64_t e = base + c0 + j * cs;
+            if (a.du) {
+                ys[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.x) + e);
+                us[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.du) + e);
+            }
+            if (a.dy) gs[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.dy) + e);
+            if (F8) {
+                fs[j] = *reinterpret_cast<const Pack<TF, V> *>(a.f8 + e);
+                fsc[j] = a.f8_scale[row * groups + (c0 + j * cs) / kGroup];
+            } else if (block) {
+                fs[j] = *reinterpret_cast<const Pack<TF, V> *>(static_cast<const TF *>(a.f) + e);
+            }
+            if (a.gate_kind == FNO_GATE_FULL && block)
+                gates[j] =
+                    *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.gate) + e);
+        }
+        float n1[N], m2[N], dY[N], mean, r1 = 0.0f, r2 = 0.0f, d[2] = {};
+        if (a.du) {
+            const float shift = LAYER && on ? Storage<T>::load(static_cast<const T *>(a.x) + base)
+                                            : 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                n1[i] = have(i) ? Storage<T>::load(&ys[i / V].v[i % V]) - shift : 0.0f;
+            row_norm<N, LAYER>(n1, have, a.channels, a.eps, G, red, mean, r1);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                Pack<float, V> w1 = {};
+                if (have(j * V)) w1 = *reinterpret_cast<const Pack<float, V> *>(a.w1 + c0 + j * cs);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int k = j * V + i;
+                    n1[k] = have(k) ? (n1[k] - mean) * r1 : 0.0f;
+                    const float du = Storage<T>::load(&us[j].v[i]);
+                    acc[2][k] = fmaf(du, n1[k], acc[2][k]);
+                    acc[3][k] += du;
+                    dY[k] = weighted(du, w1.v[i]);
+                    d[0] += dY[k];
+                    d[1] = fmaf(dY[k], n1[k], d[1]);
+                }
+            }
+            row_sum<2>(d, G, red);
+            d[0] = LAYER ? d[0] * inv : 0.0f;
+            d[1] *= inv;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            Pack<T, V> xs;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int k = j * V + i;
+                float g = Storage<T>::load(&gs[j].v[i]);
+                if (a.du) g = fmaf(r1, dY[k] - d[0] - n1[k] * d[1], g);
+                dY[k] = have(k) ? g : 0.0f;
+                Storage<T>::store(&xs.v[i], g);
+            }
+            if (on && have(j * V))
+                *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dx) + base + c0 + j * cs) = xs;
+        }
+        if (!block) continue;
+        float shift = 0.0f;
+        if constexpr (F8) {
+            if (LAYER && on) shift = (float)a.f8[base] * a.f8_scale[row * groups];
+        } else {
+            if (LAYER && on) shift = Storage<T>::load(static_cast<const T *>(a.f) + base);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float f;
+            if constexpr (F8) f = (float)fs[i / V].v[i % V] * fsc[i / V];
+            else f = Storage<T>::load(&fs[i / V].v[i % V]);
+            m2[i] = have(i) ? f - shift : 0.0f;
+        }
+        row_norm<N, LAYER>(m2, have, a.channels, a.eps, G, red, mean, r2);
+        float e[2] = {}, ev[N];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c = c0 + j * cs;
+            Pack<float, V> s = {}, w2 = {}, b2 = {}, gf = {};
+            Pack<T, V> dg;
+            if (have(j * V)) {
+                s = *reinterpret_cast<const Pack<float, V> *>(a.s + c);
+                w2 = *reinterpret_cast<const Pack<float, V> *>(a.w2 + c);
+                if (LAYER) b2 = *reinterpret_cast<const Pack<float, V> *>(a.b2 + c);
+                if (a.gate_kind == FNO_GATE_CHANNEL)
+                    gf = *reinterpret_cast<const Pack<float, V> *>(
+                        static_cast<const float *>(a.gate) + blockIdx.y * a.channels + c);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int k = j * V + i;
+                m2[k] = have(k) ? (m2[k] - mean) * r2 : 0.0f;
+                float av = 1.0f;
+                if (a.gate_kind != FNO_GATE_NONE)
+                    av = gate_value(a.gate_kind == FNO_GATE_FULL ? Storage<T>::load(&gates[j].v[i])
+                                                                 : gf.v[i], a.sigmoid);
+                const float ga = a.gate_kind == FNO_GATE_FULL ? dY[k] * av : dY[k];
+                acc[0][k] = fmaf(ga, m2[k], acc[0][k]);
+                acc[1][k] += ga;
+                const float ts = dY[k] * s.v[i];
+                Storage<T>::store(&dg.v[i], ts * (LAYER ? fmaf(m2[k], w2.v[i], b2.v[i])
+                                                        : m2[k] * w2.v[i]) *
+                                                gate_slope(av, a.sigmoid));
+                ev[k] = weighted(ts * av, w2.v[i]);
+                e[0] += ev[k];
+                e[1] = fmaf(ev[k], m2[k], e[1]);
+            }
+            if (a.dgate && on && have(j * V))
+                *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dgate) + base + c) = dg;
+        }
+        row_sum<2>(e, G, red);
+        e[0] = LAYER ? e[0] * inv : 0.0f;
+        e[1] *= inv;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!on || !have(j * V)) continue;
+            Pack<T, V> out;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int k = j * V + i;
+                Storage<T>::store(&out.v[i], r2 * (ev[k] - e[0] - m2[k] * e[1]));
+            }
+            *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.df) + base + c0 + j * cs) = out;
+        }
+    }
+    // the CTA's rows joined in order, one of the four sums at a time
+    float *join = reinterpret_cast<float *>(sm);        // [R][channels]
+    float *out = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kSums * a.channels;
+#pragma unroll
+    for (int q = 0; q < kSums; ++q) {
+        if (R > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (have(i)) join[(w / G) * a.channels + c0 + i / V * cs + i % V] = acc[q][i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.channels; c += blockDim.x) {
+                float t = 0.0f;
+                for (int k = 0; k < R; ++k) t += join[k * a.channels + c];
+                out[q * a.channels + c] = t;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (have(i)) out[q * a.channels + c0 + i / V * cs + i % V] = acc[q][i];
+        }
+    }
+}
+
+template <int EACH, class F>
+void with_rows(const fno_sandwich_s &p, const Way &way, F &&f) {
+    using std::integral_constant;
+    with_storage(p.d.dtype, [&](auto t) {
+        const auto layer = [&](auto v, auto j) {
+            if (p.d.norm == FNO_NORM_LAYER) f(t, v, j, std::true_type());
+            else f(t, v, j, std::false_type());
+        };
+        constexpr int V = kVec<decltype(t)>;
+        if (way.vec > 1) layer(integral_constant<int, V>(), integral_constant<int, EACH / V>());
+        else layer(integral_constant<int, 1>(), integral_constant<int, EACH>());
+    });
+}
+
+// Calls f with the backward kernel.
+template <class F>
+void with_kernel(const fno_sandwich_s &p, bool f8, F &&f) {
+    with_rows<8>(p, p.bwd, [&](auto t, auto v, auto j, auto layer) {
+        using T = decltype(t);
+        constexpr int V = decltype(v)::value, J = decltype(j)::value;
+        if (f8) f(k_sandwich_bwd_rows<T, V, J, decltype(layer)::value, true>);
+        else f(k_sandwich_bwd_rows<T, V, J, decltype(layer)::value, false>);
+    });
+}
+// the rows' sums joined in shared memory
+size_t smem_of(const fno_sandwich_s &p) {
+    const int rows = p.bwd.warps / p.bwd.group;
+    return rows > 1 ? (size_t)rows * p.d.channels * 4 : 0;
+}
+
+}  // namespace
+
+namespace fno {
+namespace sandwich {
+
+// Vectors need the channel count (where every row starts) to be a multiple of
+// them; registers bound a thread's elements (16 forward, 8 backward), and 16
+// warps a row.
+Way rows_way(const fno_sandwich_desc_t &d, bool backward) {
+    const int c = d.channels, big = d.dtype == FNO_F32 ? 4 : 8;
+    const int vec = c % big == 0 ? big : 1, each = backward ? 8 : 16;
+    int group = 1;
+    while (group <= 16 && group * 32 * each < c) group *= 2;
+    if (group > 16) return Way{kAny, 0, 0, 0, 0};
+    return Way{kRows, vec, each / vec, group > 8 ? group : 8, group};
+}
+
+fno_status_t rows_forward(const fno_sandwich_s &p, const Args &a, int8_t *f8, float *f8_scale,
+                          bool *packed, cudaStream_t s) {
+    const Way &way = p.fwd;
+    *packed = f8 && way.vec > 1;         // a group lies within a warp's loads
+    int8_t *q = *packed ? f8 : nullptr;
+    with_rows<16>(p, way, [&](auto t, auto v, auto j, auto layer) {
+        k_sandwich_fwd_rows<decltype(t), decltype(v)::value, decltype(j)::value,
+                            decltype(layer)::value>
+            <<<(unsigned)ceil_div(p.d.batch * p.d.points, way.warps / way.group), way.warps * 32,
+               0, s>>>(a, way.group, q, f8_scale);
+    });
+    return launched();
+}
+
+fno_status_t rows_shares(const fno_sandwich_s &p, int *ctas, int64_t *most) {
+    *most = ceil_div(p.seg_points, p.bwd.warps / p.bwd.group);
+    fno_status_t st = FNO_OK;
+    with_kernel(p, false,
+                [&](auto k) { st = occupancy(k, p.bwd.warps * 32, smem_of(p), ctas); });
+    return st;
+}
+
+fno_status_t rows_backward(const fno_sandwich_s &p, const Args &a, cudaStream_t s) {
+    with_kernel(p, a.f8 != nullptr, [&](auto k) {
+        k<<<dim3((unsigned)p.splits, (unsigned)p.segs), p.bwd.warps * 32, smem_of(p), s>>>(
+            a, p.bwd.group);
+    });
+    return launched();
+}
+
+}  // namespace sandwich
+}  // namespace fno
