@@ -22,7 +22,8 @@ def __getattr__(name):
     # the sequence operators, loaded at first use (their module imports torch)
     if name in _SEQUENCE:
         from . import sequence
-        return getattr(sequence, name)
+        globals().update({n: getattr(sequence, n) for n in _SEQUENCE})
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

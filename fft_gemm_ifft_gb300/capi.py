@@ -113,6 +113,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libfno.so (raises if it is missing; there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()

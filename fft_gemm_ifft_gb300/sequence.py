@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import torch
 
-from . import FnoError, _require, _stream_handle, capi, check  # noqa: F401
+from . import _require, _stream_handle, capi, check
 
 _DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 _CODES = {torch.float32: capi.FNO_F32, torch.float16: capi.FNO_F16,
@@ -24,12 +24,26 @@ _CODES = {torch.float32: capi.FNO_F32, torch.float16: capi.FNO_F16,
 GROUP = capi.FNO_ACT8_GROUP
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, t):
+    """The handle of ``stream``, or of the current stream of t's device (by the
+    raw query where torch has it: the call is most of a small operator's cost)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return _stream_handle(stream)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
 def _field(t, dtype, shape, name):
-    _require(t, dtype, shape, name)
+    """t's pointer, once its type, shape and layout are those wanted."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _require(t, dtype, shape, name)
     return t.data_ptr()
 
 
@@ -44,9 +58,9 @@ class PackedActivation:
     def __init__(self, codes, scales, dtype):
         if dtype not in _CODES:
             raise TypeError(f"dtype must be one of {list(_CODES)}, got {dtype}")
-        _require(codes, torch.int8, codes.shape, "codes")
-        _require(scales, torch.float32, codes.shape[:-1] + (-(-codes.shape[-1] // GROUP),),
-                 "scales")
+        _field(codes, torch.int8, codes.shape, "codes")
+        _field(scales, torch.float32, codes.shape[:-1] + (-(-codes.shape[-1] // GROUP),),
+               "scales")
         self.codes, self.scales, self.dtype = codes, scales, dtype
         self.shape = codes.shape
 
@@ -58,31 +72,33 @@ class PackedActivation:
         """The values that the codes stand for, in the storage type."""
         if out is None:
             out = torch.empty(self.shape, dtype=self.dtype, device=self.codes.device)
-        _require(out, self.dtype, self.shape, "out")
+        ptr = _field(out, self.dtype, self.shape, "out")
         rows, cols = self._rows()
         check(capi.fno_act8_unpack(rows, cols, _CODES[self.dtype], self.codes.data_ptr(),
-                                   self.scales.data_ptr(), out.data_ptr(),
-                                   _stream_handle(stream)), "fno_act8_unpack")
+                                   self.scales.data_ptr(), ptr, _stream(stream, out)),
+              "fno_act8_unpack")
         return out
 
     def gelu_backward(self, dy, out=None, stream=None):
         """dy * GELU'(values); ``out`` may be dy."""
-        _require(dy, self.dtype, self.shape, "dy")
+        dyp = _field(dy, self.dtype, self.shape, "dy")
         if out is None:
             out = torch.empty_like(dy)
-        _require(out, self.dtype, self.shape, "out")
+        ptr = _field(out, self.dtype, self.shape, "out")
         rows, cols = self._rows()
         check(capi.fno_act8_gelu_backward(rows, cols, _CODES[self.dtype], self.codes.data_ptr(),
-                                          self.scales.data_ptr(), dy.data_ptr(), out.data_ptr(),
-                                          _stream_handle(stream)), "fno_act8_gelu_backward")
+                                          self.scales.data_ptr(), dyp, ptr,
+                                          _stream(stream, dy)), "fno_act8_gelu_backward")
         return out
 
 
 def _empty_packed(shape, dtype, device):
-    codes = torch.empty(shape, dtype=torch.int8, device=device)
-    scales = torch.empty(tuple(shape[:-1]) + (-(-shape[-1] // GROUP),), dtype=torch.float32,
-                         device=device)
-    return PackedActivation(codes, scales, dtype)
+    p = PackedActivation.__new__(PackedActivation)
+    p.codes = torch.empty(shape, dtype=torch.int8, device=device)
+    p.scales = torch.empty((*shape[:-1], -(-shape[-1] // GROUP)), dtype=torch.float32,
+                           device=device)
+    p.dtype, p.shape = dtype, p.codes.shape
+    return p
 
 
 def pack_activation(x, stream=None) -> PackedActivation:
@@ -91,11 +107,11 @@ def pack_activation(x, stream=None) -> PackedActivation:
         raise TypeError("x must be a float32, float16 or bfloat16 CUDA tensor")
     if x.dim() < 1 or x.numel() < 1:
         raise ValueError("x must have at least one element")
-    _require(x, x.dtype, x.shape, "x")
+    ptr = _field(x, x.dtype, x.shape, "x")
     p = _empty_packed(x.shape, x.dtype, x.device)
     rows, cols = p._rows()
-    check(capi.fno_act8_pack(rows, cols, _CODES[x.dtype], x.data_ptr(), p.codes.data_ptr(),
-                             p.scales.data_ptr(), _stream_handle(stream)), "fno_act8_pack")
+    check(capi.fno_act8_pack(rows, cols, _CODES[x.dtype], ptr, p.codes.data_ptr(),
+                             p.scales.data_ptr(), _stream(stream, x)), "fno_act8_pack")
     return p
 
 
@@ -190,7 +206,7 @@ class SandwichNorm(_Plan):
         check(capi.fno_sandwich_forward(self.handle, xp, None, None, None, None, None,
                                         self._vec(params, "w1"),
                                         self._vec(params, "b1", self.layer), None, u.data_ptr(),
-                                        None, None, _stream_handle(stream)),
+                                        None, None, _stream(stream, x)),
               "fno_sandwich_forward")
         return u
 
@@ -211,7 +227,7 @@ class SandwichNorm(_Plan):
             self._vec(params, "b2", layer), self._vec(params, "w1", want_u),
             self._vec(params, "b1", layer and want_u), y.data_ptr(), _ptr(u),
             f8.codes.data_ptr() if save8 else None, f8.scales.data_ptr() if save8 else None,
-            _stream_handle(stream)), "fno_sandwich_forward")
+            _stream(stream, x)), "fno_sandwich_forward")
         return y, u, f8
 
     __call__ = forward
@@ -248,7 +264,7 @@ class SandwichNorm(_Plan):
             self._vec(params, "w2", block), self._vec(params, "b2", block and layer),
             self._vec(params, "w1", du is not None), dyp, dup, ptr["dx"], ptr.get("df"),
             ptr.get("dgate"), ptr.get("ds"), ptr.get("dw2"), ptr.get("db2"), ptr.get("dw1"),
-            ptr.get("db1"), self._workspace(), _stream_handle(stream)), "fno_sandwich_backward")
+            ptr.get("db1"), self._workspace(), _stream(stream, y)), "fno_sandwich_backward")
         return out
 
 
@@ -274,7 +290,7 @@ class LinearGrad(_Plan):
         db = torch.empty((cout,), dtype=torch.float32, device=dy.device)
         check(capi.fno_linear_grad(self.handle, dyp, x8.codes.data_ptr(), x8.scales.data_ptr(),
                                    dw.data_ptr(), db.data_ptr(), self._workspace(),
-                                   _stream_handle(stream)), "fno_linear_grad")
+                                   _stream(stream, dy)), "fno_linear_grad")
         return dw, db
 
     __call__ = backward
@@ -297,13 +313,13 @@ class LinearAttention(_Plan):
         self.q_shape, self.k_shape = (b, t, h, self.dk), (b, t, g, self.dk)
         self.v_shape, self.o_shape = (b, t, g, self.dv), (b, t, h, self.dv)
         self.state_shape = (b, h, self.dk, self.dv)
+        self._shapes = (self.q_shape, self.k_shape, self.v_shape)
+        self._step_shapes = tuple(s[:1] + s[2:] for s in self._shapes)
 
-    def _qkv(self, q, k, v, log_decay, cut=slice(None)):
-        def shape(s):
-            return s if cut == slice(None) else s[:1] + s[2:]
+    def _qkv(self, q, k, v, log_decay, shapes):
         dt = self.torch_dtype
-        return (_field(q, dt, shape(self.q_shape), "q"), _field(k, dt, shape(self.k_shape), "k"),
-                _field(v, dt, shape(self.v_shape), "v"),
+        return (_field(q, dt, shapes[0], "q"), _field(k, dt, shapes[1], "k"),
+                _field(v, dt, shapes[2], "v"),
                 _field(log_decay, torch.float32, (self.heads,), "log_decay"))
 
     def _scale(self, scale):
@@ -313,17 +329,17 @@ class LinearAttention(_Plan):
                 out=None, stream=None):
         """(o, final state or None).  ``lengths`` int32 (batch,): tokens of each
         sequence; ``state``: the initial state (None: zero)."""
-        ptrs = self._qkv(q, k, v, log_decay)
+        ptrs = self._qkv(q, k, v, log_decay, self._shapes)
         lp = _maybe(lengths, torch.int32, (self.batch,), "lengths")
         sp = _maybe(state, torch.float32, self.state_shape, "state")
         if out is None:
             out = torch.empty(self.o_shape, dtype=self.torch_dtype, device=q.device)
-        _require(out, self.torch_dtype, self.o_shape, "out")
+        op = _field(out, self.torch_dtype, self.o_shape, "out")
         final = (torch.empty(self.state_shape, dtype=torch.float32, device=q.device)
                  if want_state else None)
         check(capi.fno_linattn_forward(self.handle, *ptrs, self._scale(scale), lp, sp,
-                                       out.data_ptr(), _ptr(final), self._workspace(),
-                                       _stream_handle(stream)), "fno_linattn_forward")
+                                       op, _ptr(final), self._workspace(),
+                                       _stream(stream, q)), "fno_linattn_forward")
         return out, final
 
     __call__ = forward
@@ -332,7 +348,7 @@ class LinearAttention(_Plan):
                  stream=None):
         """(dq, dk, dv, gradient of the initial state or None).  ``dstate`` is
         the gradient of the final state (None: zero)."""
-        ptrs = self._qkv(q, k, v, log_decay)
+        ptrs = self._qkv(q, k, v, log_decay, self._shapes)
         lp = _maybe(lengths, torch.int32, (self.batch,), "lengths")
         sp = _maybe(state, torch.float32, self.state_shape, "state")
         dop = _field(do, self.torch_dtype, self.o_shape, "do")
@@ -341,7 +357,7 @@ class LinearAttention(_Plan):
         ds0 = torch.empty_like(state) if state is not None else None
         check(capi.fno_linattn_backward(self.handle, *ptrs, self._scale(scale), lp, sp, dop, dsp,
                                         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0),
-                                        self._workspace(), _stream_handle(stream)),
+                                        self._workspace(), _stream(stream, q)),
               "fno_linattn_backward")
         return dq, dk, dv, ds0
 
@@ -351,7 +367,7 @@ class LinearAttention(_Plan):
         kv_heads, ...) -> o (batch, heads, dv).  ``state`` (slots, heads, dk,
         dv) is updated in place unless ``new_state`` is given; ``slots`` int32
         (batch,) says which state a row has (outside: the row is idle)."""
-        ptrs = self._qkv(q, k, v, log_decay, cut=None)
+        ptrs = self._qkv(q, k, v, log_decay, self._step_shapes)
         n = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() else 0
         sp = _field(state, torch.float32, (n,) + self.state_shape[1:], "state")
         tp = _maybe(slots, torch.int32, (self.batch,), "slots")
@@ -360,7 +376,7 @@ class LinearAttention(_Plan):
         shape = (self.batch, self.heads, self.dv)
         if out is None:
             out = torch.empty(shape, dtype=self.torch_dtype, device=q.device)
-        _require(out, self.torch_dtype, shape, "out")
+        op = _field(out, self.torch_dtype, shape, "out")
         check(capi.fno_linattn_step(self.handle, *ptrs, self._scale(scale), tp, n, sp, np_,
-                                    out.data_ptr(), _stream_handle(stream)), "fno_linattn_step")
+                                    op, _stream(stream, q)), "fno_linattn_step")
         return out
