@@ -26,8 +26,30 @@ FNO_LINATTN_EXTERN(__nv_bfloat16)
 
 namespace {
 
+// local states -> the states in front of the segments, in place
+__global__ void k_linattn_prefix(ScanArgs p, float *states, int segments, int64_t seg_len,
+                                 int64_t n_states) {
+    const int64_t size = (int64_t)p.dk * p.dv;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n_states * size) return;
+    const int64_t bh = i / size, at = i - bh * size;
+    const int e = (int)(at / p.dk), a = (int)(at - (int64_t)e * p.dk);
+    int64_t n = p.length;
+    if (p.lengths) n = max((int64_t)0, min((int64_t)p.lengths[bh / p.heads], n));
+    const float ld = p.log_decay[bh % p.heads];
+    float z = p.s0 ? p.s0[bh * size + (p.s_transposed ? at : (int64_t)a * p.dv + e)] : 0.0f;
+    float *s = states + bh * segments * size + at;
+    for (int k = 0; k < segments; ++k) {
+        const int64_t len = max((int64_t)0, min(seg_len, n - k * seg_len));
+        const float local = k + 1 < segments && len > 0 ? s[k * size] : 0.0f;
+        s[k * size] = z;
+        if (len > 0) z = fmaf(z, expf(ld * (float)len), local);
+    }
+}
+
 fno_status_t scan(const fno_linattn_s &p, const ScanArgs &a, bool rev, bool wide_out,
                   float *states, float scale_p, cudaStream_t s) {
+    if (tc_applies(p)) return tc_scan(p, a, rev, wide_out, states, scale_p, s);
     return with_storage(p.dtype, [&](auto t) {
         return scan_of<decltype(t)>(p, a, rev, wide_out, states, scale_p, s);
     });
@@ -83,6 +105,24 @@ k_linattn_step(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
     }
 }
 
+}  // namespace
+
+namespace fno {
+namespace linattn {
+
+fno_status_t segment_states(const fno_linattn_s &p, const ScanArgs &a, float *states,
+                            cudaStream_t s) {
+    const int64_t bh = p.batch * a.heads, n = bh * a.dk * a.dv;
+    k_linattn_prefix<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a, states, p.segments, p.seg_len,
+                                                                bh);
+    return launched();
+}
+
+}  // namespace linattn
+}  // namespace fno
+
+namespace {
+
 struct Sizes {
     size_t q, k, v, o, s;    // bytes
 };
@@ -127,17 +167,22 @@ fno_status_t fno_linattn_plan(fno_linattn_t *out, int64_t batch, int64_t length,
     // and segments of 4 chunks at least (a segment costs a second pass over k
     // and v)
     int per_sm = 1;
-    if (dk <= kChunkWidth) st = with_storage(dtype,
-                                             [&](auto t) { return chunk_occupancy_of<decltype(t)>(*p, &per_sm); });
+    const bool tc = tc_applies(*p);
+    const int step = tc ? 128 : kC;          // tokens of a chunk
+    if (tc)
+        per_sm = tc_ctas(*p);
+    else if (dk <= kChunkWidth)
+        st = with_storage(dtype,
+                          [&](auto t) { return chunk_occupancy_of<decltype(t)>(*p, &per_sm); });
     if (st != FNO_OK) {
         fno_linattn_destroy(p);
         return st;
     }
     const int64_t ctas = batch * heads * ceil_div(dv, 128);
     int64_t segs = (int64_t)per_sm * p->sms / ctas;
-    const int64_t most = ceil_div(length, 4 * kC);
+    const int64_t most = ceil_div(length, 4 * step);
     segs = segs < 1 ? 1 : segs < most ? segs : most;
-    p->seg_len = ceil_div(ceil_div(length, segs), kC) * kC;
+    p->seg_len = ceil_div(ceil_div(length, segs), step) * step;
     p->segments = (int)ceil_div(length, p->seg_len);
     size_t at = 0;
     if (p->segments > 1) at = (size_t)batch * heads * p->segments * dk * dv * 4;

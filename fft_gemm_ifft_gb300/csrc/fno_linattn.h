@@ -45,6 +45,16 @@ struct ScanArgs {
 template <typename T>
 fno_status_t scan_of(const fno_linattn_s &p, const ScanArgs &a, bool rev, bool wide_out,
                      float *states, float scale_p, cudaStream_t s);
+// The states in front of the segments from their local ones, in place (and from
+// a.s0).
+fno_status_t segment_states(const fno_linattn_s &p, const ScanArgs &a, float *states,
+                            cudaStream_t s);
+// The bfloat16 scans on tcgen05: whether a plan's widths allow them, the CTAs an
+// SM holds, and the scan.
+bool tc_applies(const fno_linattn_s &p);
+int tc_ctas(const fno_linattn_s &p);
+fno_status_t tc_scan(const fno_linattn_s &p, const ScanArgs &a, bool rev, bool wide_out,
+                     float *states, float scale_p, cudaStream_t s);
 // CTAs of the chunked kernel that an SM holds.
 template <typename T> fno_status_t chunk_occupancy_of(const fno_linattn_s &p, int *ctas);
 

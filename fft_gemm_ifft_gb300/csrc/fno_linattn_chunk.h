@@ -488,27 +488,6 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
         }
 }
 
-// local states -> the states in front of the segments, in place
-static __global__ void k_linattn_prefix(ChunkArgs ca, int64_t n_states) {
-    const ScanArgs &p = ca.s;
-    const int64_t size = (int64_t)p.dk * p.dv;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n_states * size) return;
-    const int64_t bh = i / size, at = i - bh * size;
-    const int e = (int)(at / p.dk), a = (int)(at - (int64_t)e * p.dk);
-    int64_t n = p.length;
-    if (p.lengths) n = max((int64_t)0, min((int64_t)p.lengths[bh / p.heads], n));
-    const float ld = p.log_decay[bh % p.heads];
-    float z = p.s0 ? p.s0[bh * size + (p.s_transposed ? at : (int64_t)a * p.dv + e)] : 0.0f;
-    float *s = ca.states + bh * ca.segments * size + at;
-    for (int k = 0; k < ca.segments; ++k) {
-        const int64_t len = max((int64_t)0, min(ca.seg_len, n - k * ca.seg_len));
-        const float local = k + 1 < ca.segments && len > 0 ? s[k * size] : 0.0f;
-        s[k * size] = z;
-        if (len > 0) z = fmaf(z, expf(ld * (float)len), local);
-    }
-}
-
 template <typename T>
 size_t chunk_smem(int AP, int warps, bool outputs) {
     const int NT = kTerms<T>, bufs = NT == 1 ? 2 : 1;
@@ -553,8 +532,8 @@ fno_status_t scan(const fno_linattn_s &p, const ScanArgs &a, float *states, floa
         if (p.segments > 1) {
             fno_status_t st = run(k_linattn_chunk<T, T, AP, REV, false, 3>, false);
             if (st != FNO_OK) return st;
-            const int64_t n = bh * a.dk * a.dv;
-            k_linattn_prefix<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(ca, bh);
+            st = segment_states(p, a, states, s);
+            if (st != FNO_OK) return st;
         }
         return run(k_linattn_chunk<T, TO, AP, REV, true, 3>, true);
     });

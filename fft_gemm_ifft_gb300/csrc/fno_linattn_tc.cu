@@ -1,0 +1,441 @@
+// fno_linattn_tc.cu -- the linear attention's scans for bfloat16 on the 5th
+// generation tensor cores, key and value widths up to 128 (multiples of 8).
+//
+// The same chunked form as fno_linattn_chunk.h, with chunks of 128 tokens, one
+// tcgen05 tile: with Z the state in front of the chunk and g_i = gamma^i,
+//   S = Q K^T,  P = S * [i >= j] g_{i-j}            (tensor memory, in place)
+//   O = diag(g_{i+1}) Q Z + P V
+//   Z <- g_m Z + W^T K (transposed),  W_j = g_{m-1-j} v_j, as KT bfloat16 terms
+// All five operands lie in shared memory in one layout, rows of 64 elements
+// under the 128-byte swizzle: Q and K are read along their rows for S and Q Z,
+// and V, W and K across them (the tokens being summed over) for the others.  P
+// is the left operand straight from tensor memory.  A CTA walks one segment of
+// one (sequence, head); two warpgroups share the work on a chunk:
+//   threads 0-127   a token row each: weights from S to P, the output's rows
+//   threads 128-255 W from V, then a value column each of Z^T: the float32 state
+//                   stays in registers, its bfloat16 copy goes to shared memory
+// and one thread of each issues the MMAs that its half feeds.
+//
+// Numbers as in fno_linattn_chunk.h: P and the state's copy are rounded to
+// bfloat16, as the output is; the state is float32, and W has two terms, or
+// three where a float32 state is the result.
+#include "fno_linattn.h"
+#include "fno_tc.cuh"
+
+namespace fno {
+namespace linattn {
+
+using namespace ops;
+using namespace tcu;
+
+namespace {
+
+constexpr int kT = 128;                          // tokens of a chunk
+constexpr uint32_t kPanel = kT * 128;            // 128 tokens x 64 elements
+
+struct TcArgs {
+    ScanArgs s;
+    float *states;             // [b, h, segment][e][a]: local, then initial states
+    int segments;
+    int64_t seg_len;
+    float scale_p;
+    int *err;
+};
+
+// operand read across its rows: 64-element panels `panel` bytes apart, groups of
+// 8 rows 1024 bytes apart
+__device__ __forceinline__ uint64_t desc_across(uint32_t addr, uint32_t panel) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(panel >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+constexpr uint32_t kAcrossA = 1u << 15, kAcrossB = 1u << 16;     // instruction descriptor bits
+// D += A (tensor memory) B
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,"
+                 "%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                   "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+                   "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+}
+__device__ __forceinline__ void half_sync(int which) {       // the 128 threads of a half
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + which) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+// bytes of the operands: W first, so that what an MMA of 128 rows reads past a
+// 64-row panel of it lies within them
+template <int D, bool O, int KT>
+constexpr uint32_t operand_bytes() {
+    return (D / 64) * kPanel * (KT + 2 + (O ? 1 : 0)) + (O ? (D / 64) * D * 128 : 0);
+}
+
+// O: outputs (else only the segment's local state); KT: terms of W.
+template <typename TO, int D, bool REV, bool O, int KT>
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) {
+    using T = __nv_bfloat16;
+    constexpr int NP = D / 64;
+    constexpr uint32_t kW = 0, kK = KT * NP * kPanel, kV = kK + NP * kPanel, kQ = kV + NP * kPanel,
+                       kZ = kQ + NP * kPanel;
+    // tensor memory: S / P, the output, Q Z (its own columns where they fit), W^T K
+    constexpr uint32_t cS = 0, cO = 128, cQZ = D == 128 ? 256 : 128, cD = O ? cQZ + D : 0;
+    constexpr uint32_t kCols = !O ? D : D == 128 ? 512 : 256;
+    extern __shared__ char smem_raw[];
+    char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                          ~static_cast<uintptr_t>(1023));
+    __shared__ __align__(8) uint64_t bar_s, bar_o, bar_d;
+    __shared__ uint32_t s_tmem;
+    __shared__ float pw[kT + 2];
+    const ScanArgs &p = ca.s;
+    const int tid = threadIdx.x, warp = tid >> 5, half = tid >> 7, row = tid & 127;
+    const int seg = blockIdx.x % ca.segments;
+    if (!O && seg == ca.segments - 1) return;      // no segment starts from its state
+    const int64_t bh = blockIdx.x / ca.segments;
+    const int h = (int)(bh % p.heads);
+    const int64_t b = bh / p.heads;
+    int64_t n = p.length;
+    if (p.lengths) n = max((int64_t)0, min((int64_t)p.lengths[b], n));
+    const int64_t first = seg * ca.seg_len, last = min(n, first + ca.seg_len);
+    const int nq = p.heads / p.gq, nk = p.heads / p.gk, nv = p.heads / p.gv;
+    const T *q = static_cast<const T *>(p.q) + (b * p.length * nq + h / p.gq) * p.dk;
+    const T *k = static_cast<const T *>(p.k) + (b * p.length * nk + h / p.gk) * p.dk;
+    const T *v = static_cast<const T *>(p.v) + (b * p.length * nv + h / p.gv) * p.dv;
+    if (tid == 0) {
+        for (uint64_t *x : {&bar_s, &bar_o, &bar_d})
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(tc_smem_addr(x)));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(tc_smem_addr(&s_tmem)), "r"(kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    {
+        const float ld = p.log_decay[h];
+        for (int i = tid; i < kT + 2; i += 256) pw[i] = i ? expf(ld * (float)i) : 1.0f;
+    }
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = s_tmem, sb = tc_smem_addr(base), lanes = (uint32_t)(warp & 3) << 21;
+
+    // a tensor's rows of the chunk at t0 (zeros past the sequence and the width)
+    const auto load = [&](uint32_t dst, const T *src, int64_t stride, int w, int64_t t0, int at,
+                          int threads) {
+        const int m = (int)min((int64_t)kT, last - t0);
+#pragma unroll
+        for (int i = 0; i < kT * (D / 8) / 256; ++i) {
+            for (int u = 0; u < 256 / threads; ++u) {
+                const int x = at + (i * (256 / threads) + u) * threads;
+                const int r = x / (D / 8), c = x % (D / 8);
+                const bool have = r < m && c * 8 < w;
+                const int64_t t = REV ? n - 1 - (t0 + r) : t0 + r;
+                cp_async16_or_zero(sb + dst + (c >> 3) * kPanel + sw_off16(r, (c & 7) * 8),
+                                   have ? src + t * stride + c * 8 : src, have);
+            }
+        }
+    };
+    const int64_t sk = (int64_t)nk * p.dk, sv = (int64_t)nv * p.dv, sq = (int64_t)nq * p.dk;
+    if (first < last) {
+        load(kK, k, sk, p.dk, first, tid, 256);
+        load(kV, v, sv, p.dv, first, tid, 256);
+        if (O) load(kQ, q, sq, p.dk, first, tid, 256);
+    }
+    // the state: thread 128 + e has row e of Z^T
+    const int64_t sbase = bh * (int64_t)p.dk * p.dv;
+    float *seg_state = ca.states + (bh * ca.segments + seg) * (int64_t)p.dk * p.dv;
+    const bool mine = half == 1 && row < D, stored = mine && row < p.dv;
+    const auto caller = [&](int a) {
+        return sbase + (p.s_transposed ? (int64_t)row * p.dk + a : (int64_t)a * p.dv + row);
+    };
+    float z[D];
+    const bool from_seg = O && ca.segments > 1, has_state = from_seg || (O && p.s0);
+#pragma unroll
+    for (int a = 0; a < D; ++a) {
+        z[a] = 0.0f;
+        if (stored && has_state && a < p.dk)
+            z[a] = from_seg ? seg_state[(int64_t)row * p.dk + a] : p.s0[caller(a)];
+    }
+    // its bfloat16 copy, the right operand of Q Z
+    const auto publish = [&]() {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            uint4 u;
+            u.x = pack_bf16(z[8 * c], z[8 * c + 1]);
+            u.y = pack_bf16(z[8 * c + 2], z[8 * c + 3]);
+            u.z = pack_bf16(z[8 * c + 4], z[8 * c + 5]);
+            u.w = pack_bf16(z[8 * c + 6], z[8 * c + 7]);
+            *reinterpret_cast<uint4 *>(base + kZ + (c >> 3) * (D * 128) +
+                                       sw_off16(row, (c & 7) * 8)) = u;
+        }
+    };
+    if (O && mine && has_state) publish();
+    bool zero = !has_state;
+    int chunk = 0;
+    for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
+        const int m = (int)min((int64_t)kT, last - t0);
+        const bool more = t0 + kT < last;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        tc_before_sync();
+        __syncthreads();
+        tc_after_sync();
+        if (O && tid == 0) {
+            const uint32_t id = idesc_f16(kT, true), idz = idesc_f16(D, true);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t at = (i >> 2) * kPanel + (i & 3) * 32;
+                mma_f16(tmem + cS, desc_sw128(sb + kQ + at), desc_sw128(sb + kK + at), id, i > 0);
+            }
+            if (!zero)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    mma_f16(tmem + cQZ, desc_sw128(sb + kQ + (i >> 2) * kPanel + (i & 3) * 32),
+                            desc_sw128(sb + kZ + (i >> 2) * (D * 128) + (i & 3) * 32), idz, i > 0);
+            mma_commit(&bar_s);
+        }
+        // W: a token row a thread (half of it where all threads work on it)
+        if (!O || half == 1) {
+            const float f = pw[max(0, m - 1 - row + REV)] * p.scale_k;
+            constexpr int NC = O ? D / 8 : D / 16;
+            const int c0 = O ? 0 : half * NC;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = c0 + i;
+                char *at = base + (c >> 3) * kPanel + sw_off16(row, (c & 7) * 8);
+                const uint4 u = *reinterpret_cast<uint4 *>(at + kV);
+                float x[8];
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[2 * j] = __uint_as_float(w[j] << 16) * f;
+                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * f;
+                }
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                        x[2 * j] -= __uint_as_float(y[j] << 16);
+                        x[2 * j + 1] -= __uint_as_float(y[j] & 0xffff0000u);
+                    }
+                    *reinterpret_cast<uint4 *>(at + kW + t * NP * kPanel) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            fence_async_smem();
+            if (O) half_sync(1);
+            else __syncthreads();
+            if (tid == 128) {
+                const uint32_t id = idesc_f16(D, true) | kAcrossA | kAcrossB;
+                for (int t = KT - 1; t >= 0; --t)          // the small terms first
+#pragma unroll
+                    for (int i = 0; i < kT / 16; ++i)
+                        mma_f16(tmem + cD,
+                                desc_across(sb + kW + t * NP * kPanel + i * 2048, kPanel),
+                                desc_across(sb + kK + i * 2048, kPanel), id,
+                                t < KT - 1 || i > 0);
+                mma_commit(&bar_d);
+            }
+        }
+        if (O && half == 0) {
+            float qz[D == 64 ? D : 1];
+            mbar_wait(&bar_s, chunk, ca.err);
+            tc_after_sync();
+            if (more) load(kQ, q, sq, p.dk, t0 + kT, row, 128);
+            const float fz = pw[row + !REV];
+            if (D == 64 && !zero) {                        // before the output takes its columns
+                float x[32];
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    tmem_ld32(tmem + cQZ + c + lanes, x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) qz[D == 64 ? c + j : 0] = x[j] * fz;
+                }
+            }
+            // row `row` of P over the columns of S that were read before
+#pragma unroll
+            for (int c = 0; c < kT; c += 32) {
+                uint32_t y[16] = {};
+                if (c <= (warp & 3) * 32) {
+                    float x[32];
+                    tmem_ld32(tmem + cS + c + lanes, x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int d = row - (c + j);
+                        x[j] = d >= 0 ? x[j] * (pw[max(d, 0)] * ca.scale_p) : 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                }
+                tmem_st16u(tmem + cS + c / 2 + lanes, y);
+            }
+            tmem_st_wait();
+            tc_before_sync();
+            half_sync(0);
+            if (tid == 0) {
+                tc_after_sync();
+                const uint32_t id = idesc_f16(D, true) | kAcrossB;
+#pragma unroll
+                for (int i = 0; i < kT / 16; ++i)
+                    mma_f16_ts(tmem + cO, tmem + cS + i * 8,
+                               desc_across(sb + kV + i * 2048, kPanel), id, i > 0);
+                mma_commit(&bar_o);
+            }
+            mbar_wait(&bar_o, chunk, ca.err);
+            tc_after_sync();
+            const int64_t t = REV ? n - 1 - (t0 + row) : t0 + row;
+            TO *o = static_cast<TO *>(p.o) + ((b * p.length + t) * p.heads + h) * p.dv;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float x[32];
+                tmem_ld32(tmem + cO + c + lanes, x);
+                if (!zero) {
+                    if constexpr (D == 64) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] += qz[c + j];
+                    } else {
+                        float y[32];
+                        tmem_ld32(tmem + cQZ + c + lanes, y);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = fmaf(y[j], fz, x[j]);
+                    }
+                }
+                if (row < m) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (c + j >= p.dv) break;
+                        Pack<TO, 8> y;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            Storage<TO>::store(&y.v[i], p.scale_o * x[j + i]);
+                        *reinterpret_cast<Pack<TO, 8> *>(o + c + j) = y;
+                    }
+                }
+            }
+        } else {
+            mbar_wait(&bar_d, chunk, ca.err);
+            if (O) mbar_wait(&bar_s, chunk, ca.err);       // K and the state's copy were read
+            tc_after_sync();
+            if (more) load(kK, k, sk, p.dk, t0 + kT, O ? row : tid, O ? 128 : 256);
+            if (!O && more) load(kV, v, sv, p.dv, t0 + kT, tid, 256);
+            const float carry = pw[m];
+            if (half == 1)
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    if ((warp & 3) * 32 >= D) break;       // (a warp's rows exist together)
+                    float x[32];
+                    tmem_ld32(tmem + cD + c + lanes, x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[c + j] = fmaf(z[c + j], carry, x[j]);
+                }
+            if (O) {
+                if (mine && more) publish();
+                mbar_wait(&bar_o, chunk, ca.err);
+                tc_after_sync();
+                if (more) load(kV, v, sv, p.dv, t0 + kT, row, 128);
+            }
+        }
+        zero = false;
+    }
+    if (O) {
+        TO *o = static_cast<TO *>(p.o) + (b * p.length * p.heads + h) * p.dv;
+        const int64_t from = max(n, first), to = min(p.length, first + ca.seg_len);
+        for (int64_t t = from + warp; t < to; t += 8)
+            for (int e = tid & 31; e < p.dv; e += 32)
+                Storage<TO>::store(o + t * p.heads * p.dv + e, 0.0f);
+    }
+    const bool ends = n > first ? n <= first + ca.seg_len : n == 0 && seg == 0;
+    if (stored && (!O || (p.sT && ends))) {
+#pragma unroll
+        for (int a = 0; a < D; ++a)
+            if (a < p.dk) {
+                if (O) p.sT[caller(a)] = z[a];
+                else seg_state[(int64_t)row * p.dk + a] = z[a];
+            }
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kCols));
+}
+
+template <typename TO, int D, bool REV, int KT>
+fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
+    const int64_t bh = p.batch * ca.s.heads;
+    const auto go = [&](auto kernel, size_t smem) {
+        smem += 1024;
+        if (raise_smem_limit(kernel, smem) != cudaSuccess) return FNO_ERR_CUDA;
+        kernel<<<(unsigned)(bh * ca.segments), 256, smem, s>>>(ca);
+        return launched();
+    };
+    if (ca.segments > 1) {
+        fno_status_t st = go(k_linattn_tc<__nv_bfloat16, D, REV, false, KT>,
+                             operand_bytes<D, false, KT>());
+        if (st == FNO_OK) st = segment_states(p, ca.s, ca.states, s);
+        if (st != FNO_OK) return st;
+    }
+    return go(k_linattn_tc<TO, D, REV, true, KT>, operand_bytes<D, true, KT>());
+}
+
+}  // namespace
+
+bool tc_applies(const fno_linattn_s &p) {
+    return p.dtype == FNO_BF16 && p.dk <= 128 && p.dv <= 128 && p.dk % 8 == 0 && p.dv % 8 == 0;
+}
+
+// CTAs an SM holds (tensor memory and shared memory): two of the 64-wide kernel
+int tc_ctas(const fno_linattn_s &p) { return p.dk <= 64 && p.dv <= 64 ? 2 : 1; }
+
+fno_status_t tc_scan(const fno_linattn_s &p, const ScanArgs &a, bool rev, bool wide_out,
+                     float *states, float scale_p, cudaStream_t s) {
+    const TcArgs ca{a, states, p.segments, p.seg_len, scale_p, p.dev_err};
+    const auto width = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        const auto terms = [&](auto kt) {
+            constexpr int KT = decltype(kt)::value;
+            if (!rev) return run<__nv_bfloat16, D, false, KT>(p, ca, s);
+            if (wide_out) return run<float, D, true, KT>(p, ca, s);
+            return run<__nv_bfloat16, D, true, KT>(p, ca, s);
+        };
+        return a.sT ? terms(std::integral_constant<int, 3>())
+                    : terms(std::integral_constant<int, 2>());
+    };
+    return a.dk <= 64 && a.dv <= 64 ? width(std::integral_constant<int, 64>())
+                                    : width(std::integral_constant<int, 128>());
+}
+
+}  // namespace linattn
+}  // namespace fno
