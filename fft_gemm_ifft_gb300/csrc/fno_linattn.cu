@@ -26,24 +26,34 @@ FNO_LINATTN_EXTERN(__nv_bfloat16)
 
 namespace {
 
-// local states -> the states in front of the segments, in place
-__global__ void k_linattn_prefix(ScanArgs p, float *states, int segments, int64_t seg_len,
-                                 int64_t n_states) {
-    const int64_t size = (int64_t)p.dk * p.dv;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n_states * size) return;
-    const int64_t bh = i / size, at = i - bh * size;
-    const int e = (int)(at / p.dk), a = (int)(at - (int64_t)e * p.dk);
+// local states -> the states in front of the segments, in place: a CTA for 256
+// elements of one (sequence, head), the segments' local values loaded eight at a
+// time ahead of the chain.
+__global__ void __launch_bounds__(256)
+k_linattn_prefix(ScanArgs p, float *__restrict__ states, int segments, int64_t seg_len) {
+    const int size = p.dk * p.dv, at = blockIdx.y * 256 + threadIdx.x;
+    const int64_t bh = blockIdx.x;
+    if (at >= size) return;
     int64_t n = p.length;
     if (p.lengths) n = max((int64_t)0, min((int64_t)p.lengths[bh / p.heads], n));
     const float ld = p.log_decay[bh % p.heads];
-    float z = p.s0 ? p.s0[bh * size + (p.s_transposed ? at : (int64_t)a * p.dv + e)] : 0.0f;
+    const float whole = expf(ld * (float)seg_len);
+    float z = 0.0f;
+    if (p.s0)
+        z = p.s0[bh * size + (p.s_transposed ? at : (at % p.dk) * p.dv + at / p.dk)];
     float *s = states + bh * segments * size + at;
-    for (int k = 0; k < segments; ++k) {
-        const int64_t len = max((int64_t)0, min(seg_len, n - k * seg_len));
-        const float local = k + 1 < segments && len > 0 ? s[k * size] : 0.0f;
-        s[k * size] = z;
-        if (len > 0) z = fmaf(z, expf(ld * (float)len), local);
+    for (int k0 = 0; k0 < segments; k0 += 8) {
+        float local[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            local[k] = k0 + k + 1 < segments ? s[(int64_t)(k0 + k) * size] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k0 + k >= segments) break;
+            s[(int64_t)(k0 + k) * size] = z;
+            const int64_t len = min(seg_len, n - (k0 + k) * seg_len);
+            if (len > 0) z = fmaf(z, len == seg_len ? whole : expf(ld * (float)len), local[k]);
+        }
     }
 }
 
@@ -55,17 +65,33 @@ fno_status_t scan(const fno_linattn_s &p, const ScanArgs &a, bool rev, bool wide
     });
 }
 
-// sum of the `g` query heads' float32 gradients of each shared head
-template <typename T>
-__global__ void k_linattn_group_sum(const float *__restrict__ in, T *__restrict__ out, int64_t n,
-                                    int g, int d) {
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-        const int64_t row = i / d;
-        float s = 0.0f;
-        for (int j = 0; j < g; ++j) s += in[(row * g + j) * d + (i - row * d)];
-        Storage<T>::store(out + i, s);
+// sum of the `g` query heads' float32 gradients of each shared head; V elements
+// a thread (4 where the width allows)
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+k_linattn_group_sum(const float *__restrict__ in, T *__restrict__ out, int64_t n, int g, int d) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+    if (i >= n) return;
+    const int64_t row = n <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)d) : i / d;
+    const float *at = in + row * (g - 1) * d + i;        // (row g) d + (i - row d)
+    Pack<float, V> s = *reinterpret_cast<const Pack<float, V> *>(at);
+#pragma unroll 4
+    for (int j = 1; j < g; ++j) {
+        const Pack<float, V> x = *reinterpret_cast<const Pack<float, V> *>(at + (int64_t)j * d);
+#pragma unroll
+        for (int k = 0; k < V; ++k) s.v[k] += x.v[k];
     }
+    Pack<T, V> r;
+#pragma unroll
+    for (int k = 0; k < V; ++k) Storage<T>::store(&r.v[k], s.v[k]);
+    *reinterpret_cast<Pack<T, V> *>(out + i) = r;
+}
+template <typename T>
+void group_sum(const float *in, T *out, int64_t n, int g, int d, cudaStream_t s) {
+    if (d % 4 == 0)
+        k_linattn_group_sum<T, 4><<<(unsigned)ceil_div(n, 1024), 256, 0, s>>>(in, out, n, g, d);
+    else
+        k_linattn_group_sum<T, 1><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(in, out, n, g, d);
 }
 
 // One token: a CTA per (row, head, slice of value columns), the key rows over
@@ -112,9 +138,8 @@ namespace linattn {
 
 fno_status_t segment_states(const fno_linattn_s &p, const ScanArgs &a, float *states,
                             cudaStream_t s) {
-    const int64_t bh = p.batch * a.heads, n = bh * a.dk * a.dv;
-    k_linattn_prefix<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a, states, p.segments, p.seg_len,
-                                                                bh);
+    const dim3 grid((unsigned)(p.batch * a.heads), (unsigned)ceil_div(a.dk * a.dv, 256));
+    k_linattn_prefix<<<grid, 256, 0, s>>>(a, states, p.segments, p.seg_len);
     return launched();
 }
 
@@ -260,10 +285,8 @@ fno_status_t fno_linattn_backward(fno_linattn_t p, const void *q, const void *k,
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
         const int64_t rows = p->batch * p->length * p->kv_heads;
-        k_linattn_group_sum<T><<<p->sms * 4, 256, 0, s>>>(gk, static_cast<T *>(dk), rows * p->dk,
-                                                          g, p->dk);
-        k_linattn_group_sum<T><<<p->sms * 4, 256, 0, s>>>(gv, static_cast<T *>(dv), rows * p->dv,
-                                                          g, p->dv);
+        group_sum(gk, static_cast<T *>(dk), rows * p->dk, g, p->dk, s);
+        group_sum(gv, static_cast<T *>(dv), rows * p->dv, g, p->dv, s);
         return launched();
     });
 }

@@ -10,10 +10,10 @@
 // under the 128-byte swizzle: Q and K are read along their rows for S and Q Z,
 // and V, W and K across them (the tokens being summed over) for the others.  P
 // is the left operand straight from tensor memory.  A CTA walks one segment of
-// one (sequence, head); two warpgroups share the work on a chunk:
-//   threads 0-127   a token row each: weights from S to P, the output's rows
-//   threads 128-255 W from V, then a value column each of Z^T: the float32 state
-//                   stays in registers, its bfloat16 copy goes to shared memory
+// one (sequence, head); two halves of 256 threads share the work on a chunk:
+//   half 0  half a token row a thread: weights from S to P, the output's rows
+//   half 1  W from V, then half a value column of Z^T a thread: the float32
+//           state stays in registers, its bfloat16 copy goes to shared memory
 // and one thread of each issues the MMAs that its half feeds.
 //
 // Numbers as in fno_linattn_chunk.h: P and the state's copy are rounded to
@@ -56,21 +56,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
                  ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&v)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,"
                  "%10,%11,%12,%13,%14,%15,%16};"
@@ -85,8 +70,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     memcpy(&u, &h, 4);
     return u;
 }
-__device__ __forceinline__ void half_sync(int which) {       // the 128 threads of a half
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + which) : "memory");
+__device__ __forceinline__ void half_sync(int which) {       // the 256 threads of a half
+    asm volatile("bar.sync %0, 256;" ::"r"(1 + which) : "memory");
 }
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool have) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -102,13 +87,15 @@ constexpr uint32_t operand_bytes() {
 
 // O: outputs (else only the segment's local state); KT: terms of W.
 template <typename TO, int D, bool REV, bool O, int KT>
-__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) {
+__global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn_tc(TcArgs ca) {
     using T = __nv_bfloat16;
-    constexpr int NP = D / 64;
+    constexpr int NP = D / 64, DH = D / 2;
     constexpr uint32_t kW = 0, kK = KT * NP * kPanel, kV = kK + NP * kPanel, kQ = kV + NP * kPanel,
                        kZ = kQ + NP * kPanel;
-    // tensor memory: S / P, the output, Q Z (its own columns where they fit), W^T K
-    constexpr uint32_t cS = 0, cO = 128, cQZ = D == 128 ? 256 : 128, cD = O ? cQZ + D : 0;
+    // tensor memory: S / P, the output, Q Z (the 64-wide one in the half of S that
+    // P leaves free), W^T K
+    constexpr uint32_t cS = 0, cO = 128, cQZ = D == 128 ? 256 : 64,
+                       cD = !O ? 0 : D == 128 ? 384 : 192;
     constexpr uint32_t kCols = !O ? D : D == 128 ? 512 : 256;
     extern __shared__ char smem_raw[];
     char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -116,8 +103,10 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
     __shared__ __align__(8) uint64_t bar_s, bar_o, bar_d;
     __shared__ uint32_t s_tmem;
     __shared__ float pw[kT + 2];
+    __shared__ float4 down[8];                     // gamma^31 .. gamma^0
     const ScanArgs &p = ca.s;
-    const int tid = threadIdx.x, warp = tid >> 5, half = tid >> 7, row = tid & 127;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int half = O ? tid >> 8 : 1, t8 = tid & 255, row = tid & 127, sub = t8 >> 7;
     const int seg = blockIdx.x % ca.segments;
     if (!O && seg == ca.segments - 1) return;      // no segment starts from its state
     const int64_t bh = blockIdx.x / ca.segments;
@@ -127,9 +116,6 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
     if (p.lengths) n = max((int64_t)0, min((int64_t)p.lengths[b], n));
     const int64_t first = seg * ca.seg_len, last = min(n, first + ca.seg_len);
     const int nq = p.heads / p.gq, nk = p.heads / p.gk, nv = p.heads / p.gv;
-    const T *q = static_cast<const T *>(p.q) + (b * p.length * nq + h / p.gq) * p.dk;
-    const T *k = static_cast<const T *>(p.k) + (b * p.length * nk + h / p.gk) * p.dk;
-    const T *v = static_cast<const T *>(p.v) + (b * p.length * nv + h / p.gv) * p.dv;
     if (tid == 0) {
         for (uint64_t *x : {&bar_s, &bar_o, &bar_d})
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(tc_smem_addr(x)));
@@ -142,64 +128,88 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
     }
     {
         const float ld = p.log_decay[h];
-        for (int i = tid; i < kT + 2; i += 256) pw[i] = i ? expf(ld * (float)i) : 1.0f;
+        for (int i = tid; i < kT + 2; i += blockDim.x) pw[i] = i ? expf(ld * (float)i) : 1.0f;
+        if (tid < 32) reinterpret_cast<float *>(down)[tid] = tid < 31 ? expf(ld * (31 - tid)) : 1.0f;
     }
-    tc_before_sync();
-    __syncthreads();
-    tc_after_sync();
-    const uint32_t tmem = s_tmem, sb = tc_smem_addr(base), lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t sb = tc_smem_addr(base), lanes = (uint32_t)(warp & 3) << 21;
 
-    // a tensor's rows of the chunk at t0 (zeros past the sequence and the width)
-    const auto load = [&](uint32_t dst, const T *src, int64_t stride, int w, int64_t t0, int at,
-                          int threads) {
-        const int m = (int)min((int64_t)kT, last - t0);
-#pragma unroll
-        for (int i = 0; i < kT * (D / 8) / 256; ++i) {
-            for (int u = 0; u < 256 / threads; ++u) {
-                const int x = at + (i * (256 / threads) + u) * threads;
-                const int r = x / (D / 8), c = x % (D / 8);
-                const bool have = r < m && c * 8 < w;
-                const int64_t t = REV ? n - 1 - (t0 + r) : t0 + r;
-                cp_async16_or_zero(sb + dst + (c >> 3) * kPanel + sw_off16(r, (c & 7) * 8),
-                                   have ? src + t * stride + c * 8 : src, have);
-            }
-        }
+    // A tensor's rows of a chunk, zeros past the sequence and the width: thread t8
+    // of a half takes the 16-byte piece `pc` of the rows r0, r0 + RS, ...
+    constexpr int RS = 256 / (D / 8);
+    const int r0 = t8 / (D / 8), pc = t8 % (D / 8);
+    const uint32_t piece = (pc >> 3) * kPanel + sw_off16(r0, (pc & 7) * 8);
+    struct Source {
+        const T *at;               // this thread's piece of its first row of the next chunk
+        int64_t row, chunk;        // steps, in elements
+        bool have;                 // the piece lies within the width
     };
-    const int64_t sk = (int64_t)nk * p.dk, sv = (int64_t)nv * p.dv, sq = (int64_t)nq * p.dk;
+    const auto source = [&](const void *x, int heads, int shared, int w) {
+        const int64_t stride = (int64_t)heads * w, t = first + r0;
+        const T *at = static_cast<const T *>(x) + (b * p.length * heads + h / shared) * w +
+                      (REV ? n - 1 - t : t) * stride + pc * 8;
+        return Source{at, (REV ? -RS : RS) * stride, (REV ? -kT : kT) * stride, pc * 8 < w};
+    };
+    const auto load = [&](uint32_t dst, Source &x, int64_t t0) {
+        const int m = (int)min((int64_t)kT, last - t0) - r0;
+        const T *at = x.at;
+#pragma unroll
+        for (int i = 0; i < kT / RS; ++i, at += x.row) {
+            const bool have = x.have && i * RS < m;
+            cp_async16_or_zero(sb + dst + piece + i * RS * 128, have ? at : p.q, have);
+        }
+        x.at += x.chunk;
+    };
+    Source q = source(p.q, nq, p.gq, p.dk), k = source(p.k, nk, p.gk, p.dk),
+           v = source(p.v, nv, p.gv, p.dv);
     if (first < last) {
-        load(kK, k, sk, p.dk, first, tid, 256);
-        load(kV, v, sv, p.dv, first, tid, 256);
-        if (O) load(kQ, q, sq, p.dk, first, tid, 256);
+        if (O && half == 0) load(kQ, q, first);
+        if (half == 1) {
+            load(kK, k, first);
+            load(kV, v, first);
+        }
     }
-    // the state: thread 128 + e has row e of Z^T
+    // the state: row `row` of Z^T, half of its columns a thread of half 1
     const int64_t sbase = bh * (int64_t)p.dk * p.dv;
     float *seg_state = ca.states + (bh * ca.segments + seg) * (int64_t)p.dk * p.dv;
     const bool mine = half == 1 && row < D, stored = mine && row < p.dv;
+    const int a0 = sub * DH;
     const auto caller = [&](int a) {
         return sbase + (p.s_transposed ? (int64_t)row * p.dk + a : (int64_t)a * p.dv + row);
     };
-    float z[D];
+    float z[DH];
     const bool from_seg = O && ca.segments > 1, has_state = from_seg || (O && p.s0);
 #pragma unroll
-    for (int a = 0; a < D; ++a) {
+    for (int a = 0; a < DH; ++a) {
         z[a] = 0.0f;
-        if (stored && has_state && a < p.dk)
-            z[a] = from_seg ? seg_state[(int64_t)row * p.dk + a] : p.s0[caller(a)];
+        if (stored && has_state && a0 + a < p.dk)
+            z[a] = from_seg ? seg_state[(int64_t)row * p.dk + a0 + a] : p.s0[caller(a0 + a)];
     }
     // its bfloat16 copy, the right operand of Q Z
     const auto publish = [&]() {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < DH / 8; ++c) {
             uint4 u;
             u.x = pack_bf16(z[8 * c], z[8 * c + 1]);
             u.y = pack_bf16(z[8 * c + 2], z[8 * c + 3]);
             u.z = pack_bf16(z[8 * c + 4], z[8 * c + 5]);
             u.w = pack_bf16(z[8 * c + 6], z[8 * c + 7]);
-            *reinterpret_cast<uint4 *>(base + kZ + (c >> 3) * (D * 128) +
-                                       sw_off16(row, (c & 7) * 8)) = u;
+            const int at = a0 / 8 + c;
+            *reinterpret_cast<uint4 *>(base + kZ + (at >> 3) * (D * 128) +
+                                       sw_off16(row, (at & 7) * 8)) = u;
         }
     };
     if (O && mine && has_state) publish();
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = s_tmem;
+    const auto mma_qz = [&]() {
+        const uint32_t id = idesc_f16(D, true);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            mma_f16(tmem + cQZ, desc_sw128(sb + kQ + (i >> 2) * kPanel + (i & 3) * 32),
+                    desc_sw128(sb + kZ + (i >> 2) * (D * 128) + (i & 3) * 32), id, i > 0);
+    };
     bool zero = !has_state;
     int chunk = 0;
     for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
@@ -211,27 +221,21 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
         __syncthreads();
         tc_after_sync();
         if (O && tid == 0) {
-            const uint32_t id = idesc_f16(kT, true), idz = idesc_f16(D, true);
+            const uint32_t id = idesc_f16(kT, true);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 const uint32_t at = (i >> 2) * kPanel + (i & 3) * 32;
                 mma_f16(tmem + cS, desc_sw128(sb + kQ + at), desc_sw128(sb + kK + at), id, i > 0);
             }
-            if (!zero)
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    mma_f16(tmem + cQZ, desc_sw128(sb + kQ + (i >> 2) * kPanel + (i & 3) * 32),
-                            desc_sw128(sb + kZ + (i >> 2) * (D * 128) + (i & 3) * 32), idz, i > 0);
             mma_commit(&bar_s);
+            if (D == 128 && !zero) mma_qz();       // (completes with P V)
         }
-        // W: a token row a thread (half of it where all threads work on it)
-        if (!O || half == 1) {
+        if (half == 1) {
+            // W: half of a token row a thread
             const float f = pw[max(0, m - 1 - row + REV)] * p.scale_k;
-            constexpr int NC = O ? D / 8 : D / 16;
-            const int c0 = O ? 0 : half * NC;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int c = c0 + i;
+            for (int i = 0; i < DH / 8; ++i) {
+                const int c = a0 / 8 + i;
                 char *at = base + (c >> 3) * kPanel + sw_off16(row, (c & 7) * 8);
                 const uint4 u = *reinterpret_cast<uint4 *>(at + kV);
                 float x[8];
@@ -255,9 +259,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
                 }
             }
             fence_async_smem();
-            if (O) half_sync(1);
-            else __syncthreads();
-            if (tid == 128) {
+            half_sync(1);
+            if (t8 == 0) {
                 const uint32_t id = idesc_f16(D, true) | kAcrossA | kAcrossB;
                 for (int t = KT - 1; t >= 0; --t)          // the small terms first
 #pragma unroll
@@ -268,45 +271,79 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
                                 t < KT - 1 || i > 0);
                 mma_commit(&bar_d);
             }
-        }
-        if (O && half == 0) {
-            float qz[D == 64 ? D : 1];
+            mbar_wait(&bar_d, chunk, ca.err);
+            if (O) mbar_wait(&bar_s, chunk, ca.err);
+            tc_after_sync();
+            if (more) load(kK, k, t0 + kT);
+            if (!O && more) load(kV, v, t0 + kT);
+            const float carry = pw[m];
+            if ((warp & 3) * 32 < D)                       // (a warp's rows exist together)
+#pragma unroll
+                for (int c = 0; c < DH; c += 16) {
+                    float x[16];
+                    tmem_ld16(tmem + cD + a0 + c + lanes, x);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) z[c + j] = fmaf(z[c + j], carry, x[j]);
+                }
+            if (O) {
+                mbar_wait(&bar_o, chunk, ca.err);          // V and the state's copy were read
+                tc_after_sync();
+                if (more) {
+                    load(kV, v, t0 + kT);
+                    if (mine) publish();
+                }
+            }
+        } else {
             mbar_wait(&bar_s, chunk, ca.err);
             tc_after_sync();
-            if (more) load(kQ, q, sq, p.dk, t0 + kT, row, 128);
-            const float fz = pw[row + !REV];
-            if (D == 64 && !zero) {                        // before the output takes its columns
-                float x[32];
+            // row `row` of P, every other 32 columns a thread; it replaces columns
+            // of S that other threads read, so all read first
+            const int diag = (warp & 3) * 32;
+            uint32_t y[2][16];
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    tmem_ld32(tmem + cQZ + c + lanes, x);
+            for (int i = 0; i < 2; ++i) {
+                const int c = (2 * i + sub) * 32;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) qz[D == 64 ? c + j : 0] = x[j] * fz;
-                }
-            }
-            // row `row` of P over the columns of S that were read before
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    if (c > diag) {                        // above the diagonal
 #pragma unroll
-            for (int c = 0; c < kT; c += 32) {
-                uint32_t y[16] = {};
-                if (c <= (warp & 3) * 32) {
-                    float x[32];
-                    tmem_ld32(tmem + cS + c + lanes, x);
+                        for (int j = 0; j < 8; ++j) y[i][8 * k2 + j] = 0;
+                        continue;
+                    }
+                    float x[16];
+                    tmem_ld16(tmem + cS + c + 16 * k2 + lanes, x);
+                    if (c == diag) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int d = row - (c + j);
-                        x[j] = d >= 0 ? x[j] * (pw[max(d, 0)] * ca.scale_p) : 0.0f;
+                        for (int j = 0; j < 16; ++j) {
+                            const int d = row - (c + 16 * k2 + j);
+                            x[j] = d >= 0 ? x[j] * (pw[max(d, 0)] * ca.scale_p) : 0.0f;
+                        }
+                    } else {                               // gamma^(row - c - 31) gamma^(31 - j)
+                        const float f = pw[max(row - c - 31, 0)] * ca.scale_p;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 g = down[4 * k2 + j / 4];
+                            x[j] *= f * g.x;
+                            x[j + 1] *= f * g.y;
+                            x[j + 2] *= f * g.z;
+                            x[j + 3] *= f * g.w;
+                        }
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                    for (int j = 0; j < 8; ++j) y[i][8 * k2 + j] = pack_bf16(x[2 * j], x[2 * j + 1]);
                 }
-                tmem_st16u(tmem + cS + c / 2 + lanes, y);
             }
+            half_sync(0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                tmem_st16u(tmem + cS + (2 * i + sub) * 16 + lanes, y[i]);
             tmem_st_wait();
             tc_before_sync();
             half_sync(0);
             if (tid == 0) {
                 tc_after_sync();
                 const uint32_t id = idesc_f16(D, true) | kAcrossB;
+                if (D == 64 && !zero) mma_qz();
 #pragma unroll
                 for (int i = 0; i < kT / 16; ++i)
                     mma_f16_ts(tmem + cO, tmem + cS + i * 8,
@@ -315,74 +352,52 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
             }
             mbar_wait(&bar_o, chunk, ca.err);
             tc_after_sync();
+            if (more) load(kQ, q, t0 + kT);
+            const float fz = pw[row + !REV] * p.scale_o;
             const int64_t t = REV ? n - 1 - (t0 + row) : t0 + row;
-            TO *o = static_cast<TO *>(p.o) + ((b * p.length + t) * p.heads + h) * p.dv;
+            TO *o = static_cast<TO *>(p.o) + ((b * p.length + t) * p.heads + h) * p.dv + a0;
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float x[32];
-                tmem_ld32(tmem + cO + c + lanes, x);
+            for (int c = 0; c < DH; c += 16) {
+                float x[16];
+                tmem_ld16(tmem + cO + a0 + c + lanes, x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] *= p.scale_o;
                 if (!zero) {
-                    if constexpr (D == 64) {
+                    float y2[16];
+                    tmem_ld16(tmem + cQZ + a0 + c + lanes, y2);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] += qz[c + j];
-                    } else {
-                        float y[32];
-                        tmem_ld32(tmem + cQZ + c + lanes, y);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = fmaf(y[j], fz, x[j]);
-                    }
+                    for (int j = 0; j < 16; ++j) x[j] = fmaf(y2[j], fz, x[j]);
                 }
                 if (row < m) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        if (c + j >= p.dv) break;
-                        Pack<TO, 8> y;
+                    for (int j = 0; j < 16; j += 8) {
+                        if (a0 + c + j >= p.dv) break;
+                        Pack<TO, 8> u;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            Storage<TO>::store(&y.v[i], p.scale_o * x[j + i]);
-                        *reinterpret_cast<Pack<TO, 8> *>(o + c + j) = y;
+                        for (int i = 0; i < 8; ++i) Storage<TO>::store(&u.v[i], x[j + i]);
+                        *reinterpret_cast<Pack<TO, 8> *>(o + c + j) = u;
                     }
                 }
-            }
-        } else {
-            mbar_wait(&bar_d, chunk, ca.err);
-            if (O) mbar_wait(&bar_s, chunk, ca.err);       // K and the state's copy were read
-            tc_after_sync();
-            if (more) load(kK, k, sk, p.dk, t0 + kT, O ? row : tid, O ? 128 : 256);
-            if (!O && more) load(kV, v, sv, p.dv, t0 + kT, tid, 256);
-            const float carry = pw[m];
-            if (half == 1)
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    if ((warp & 3) * 32 >= D) break;       // (a warp's rows exist together)
-                    float x[32];
-                    tmem_ld32(tmem + cD + c + lanes, x);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) z[c + j] = fmaf(z[c + j], carry, x[j]);
-                }
-            if (O) {
-                if (mine && more) publish();
-                mbar_wait(&bar_o, chunk, ca.err);
-                tc_after_sync();
-                if (more) load(kV, v, sv, p.dv, t0 + kT, row, 128);
             }
         }
         zero = false;
     }
     if (O) {
+        // zeros past the sequence, in this segment's rows
         TO *o = static_cast<TO *>(p.o) + (b * p.length * p.heads + h) * p.dv;
         const int64_t from = max(n, first), to = min(p.length, first + ca.seg_len);
-        for (int64_t t = from + warp; t < to; t += 8)
-            for (int e = tid & 31; e < p.dv; e += 32)
-                Storage<TO>::store(o + t * p.heads * p.dv + e, 0.0f);
+        const Pack<TO, 8> none = {};
+        for (int64_t t = from + r0 + (half ? RS : 0); t < to; t += 2 * RS)
+            if (pc * 8 < p.dv)
+                *reinterpret_cast<Pack<TO, 8> *>(o + t * p.heads * p.dv + pc * 8) = none;
     }
     const bool ends = n > first ? n <= first + ca.seg_len : n == 0 && seg == 0;
     if (stored && (!O || (p.sT && ends))) {
 #pragma unroll
-        for (int a = 0; a < D; ++a)
-            if (a < p.dk) {
-                if (O) p.sT[caller(a)] = z[a];
-                else seg_state[(int64_t)row * p.dk + a] = z[a];
+        for (int a = 0; a < DH; ++a)
+            if (a0 + a < p.dk) {
+                if (O) p.sT[caller(a0 + a)] = z[a];
+                else seg_state[(int64_t)row * p.dk + a0 + a] = z[a];
             }
     }
     tc_before_sync();
@@ -395,19 +410,19 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) k_linattn_tc(TcArgs ca) 
 template <typename TO, int D, bool REV, int KT>
 fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
     const int64_t bh = p.batch * ca.s.heads;
-    const auto go = [&](auto kernel, size_t smem) {
+    const auto go = [&](auto kernel, int threads, size_t smem) {
         smem += 1024;
         if (raise_smem_limit(kernel, smem) != cudaSuccess) return FNO_ERR_CUDA;
-        kernel<<<(unsigned)(bh * ca.segments), 256, smem, s>>>(ca);
+        kernel<<<(unsigned)(bh * ca.segments), threads, smem, s>>>(ca);
         return launched();
     };
     if (ca.segments > 1) {
-        fno_status_t st = go(k_linattn_tc<__nv_bfloat16, D, REV, false, KT>,
+        fno_status_t st = go(k_linattn_tc<__nv_bfloat16, D, REV, false, KT>, 256,
                              operand_bytes<D, false, KT>());
         if (st == FNO_OK) st = segment_states(p, ca.s, ca.states, s);
         if (st != FNO_OK) return st;
     }
-    return go(k_linattn_tc<TO, D, REV, true, KT>, operand_bytes<D, true, KT>());
+    return go(k_linattn_tc<TO, D, REV, true, KT>, 512, operand_bytes<D, true, KT>());
 }
 
 }  // namespace
