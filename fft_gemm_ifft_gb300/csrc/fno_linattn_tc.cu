@@ -78,11 +78,20 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
                  ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
 
+// An output row on its way out: 16 bytes more than it has, against bank conflicts.
+template <typename TO, int D> constexpr uint32_t kStageRow = D * sizeof(TO) + 16;
+// bytes of W, whose place also takes the output tile
+template <typename TO, int D, bool O, int KT>
+constexpr uint32_t w_bytes() {
+    const uint32_t w = KT * (D / 64) * kPanel, stage = (kT * kStageRow<TO, D> + 1023) / 1024 * 1024;
+    return O && stage > w ? stage : w;
+}
 // bytes of the operands: W first, so that what an MMA of 128 rows reads past a
 // 64-row panel of it lies within them
-template <int D, bool O, int KT>
+template <typename TO, int D, bool O, int KT>
 constexpr uint32_t operand_bytes() {
-    return (D / 64) * kPanel * (KT + 2 + (O ? 1 : 0)) + (O ? (D / 64) * D * 128 : 0);
+    return w_bytes<TO, D, O, KT>() + (D / 64) * kPanel * (2 + (O ? 1 : 0)) +
+           (O ? (D / 64) * D * 128 : 0);
 }
 
 // O: outputs (else only the segment's local state); KT: terms of W.
@@ -90,7 +99,7 @@ template <typename TO, int D, bool REV, bool O, int KT>
 __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn_tc(TcArgs ca) {
     using T = __nv_bfloat16;
     constexpr int NP = D / 64, DH = D / 2;
-    constexpr uint32_t kW = 0, kK = KT * NP * kPanel, kV = kK + NP * kPanel, kQ = kV + NP * kPanel,
+    constexpr uint32_t kW = 0, kK = w_bytes<TO, D, O, KT>(), kV = kK + NP * kPanel, kQ = kV + NP * kPanel,
                        kZ = kQ + NP * kPanel;
     // tensor memory: S / P, the output, Q Z (the 64-wide one in the half of S that
     // P leaves free), W^T K
@@ -131,7 +140,10 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
         for (int i = tid; i < kT + 2; i += blockDim.x) pw[i] = i ? expf(ld * (float)i) : 1.0f;
         if (tid < 32) reinterpret_cast<float *>(down)[tid] = tid < 31 ? expf(ld * (31 - tid)) : 1.0f;
     }
-    const uint32_t sb = tc_smem_addr(base), lanes = (uint32_t)(warp & 3) << 21;
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t sb = tc_smem_addr(base), tmem = s_tmem, lanes = (uint32_t)(warp & 3) << 21;
 
     // A tensor's rows of a chunk, zeros past the sequence and the width: thread t8
     // of a half takes the 16-byte piece `pc` of the rows r0, r0 + RS, ...
@@ -168,69 +180,52 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             load(kV, v, first);
         }
     }
-    // the state: row `row` of Z^T, half of its columns a thread of half 1
-    const int64_t sbase = bh * (int64_t)p.dk * p.dv;
-    float *seg_state = ca.states + (bh * ca.segments + seg) * (int64_t)p.dk * p.dv;
-    const bool mine = half == 1 && row < D, stored = mine && row < p.dv;
-    const int a0 = sub * DH;
-    const auto caller = [&](int a) {
-        return sbase + (p.s_transposed ? (int64_t)row * p.dk + a : (int64_t)a * p.dv + row);
-    };
-    float z[DH];
-    const bool from_seg = O && ca.segments > 1, has_state = from_seg || (O && p.s0);
-#pragma unroll
-    for (int a = 0; a < DH; ++a) {
-        z[a] = 0.0f;
-        if (stored && has_state && a0 + a < p.dk)
-            z[a] = from_seg ? seg_state[(int64_t)row * p.dk + a0 + a] : p.s0[caller(a0 + a)];
-    }
-    // its bfloat16 copy, the right operand of Q Z
-    const auto publish = [&]() {
-#pragma unroll
-        for (int c = 0; c < DH / 8; ++c) {
-            uint4 u;
-            u.x = pack_bf16(z[8 * c], z[8 * c + 1]);
-            u.y = pack_bf16(z[8 * c + 2], z[8 * c + 3]);
-            u.z = pack_bf16(z[8 * c + 4], z[8 * c + 5]);
-            u.w = pack_bf16(z[8 * c + 6], z[8 * c + 7]);
-            const int at = a0 / 8 + c;
-            *reinterpret_cast<uint4 *>(base + kZ + (at >> 3) * (D * 128) +
-                                       sw_off16(row, (at & 7) * 8)) = u;
-        }
-    };
-    if (O && mine && has_state) publish();
-    tc_before_sync();
-    __syncthreads();
-    tc_after_sync();
-    const uint32_t tmem = s_tmem;
-    const auto mma_qz = [&]() {
-        const uint32_t id = idesc_f16(D, true);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-            mma_f16(tmem + cQZ, desc_sw128(sb + kQ + (i >> 2) * kPanel + (i & 3) * 32),
-                    desc_sw128(sb + kZ + (i >> 2) * (D * 128) + (i & 3) * 32), id, i > 0);
-    };
-    bool zero = !has_state;
-    int chunk = 0;
-    for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
-        const int m = (int)min((int64_t)kT, last - t0);
-        const bool more = t0 + kT < last;
+    // all threads, once a chunk: the operands are there
+    const auto meet = [&]() {
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_async_smem();
         tc_before_sync();
-        __syncthreads();
+        asm volatile("bar.sync 0, %0;" ::"n"(O ? 512 : 256) : "memory");
         tc_after_sync();
-        if (O && tid == 0) {
-            const uint32_t id = idesc_f16(kT, true);
+    };
+    const bool has_state = O && (ca.segments > 1 || p.s0);
+    if (half == 1) {
+        // the state: row `row` of Z^T, half of its columns a thread
+        const int64_t sbase = bh * (int64_t)p.dk * p.dv;
+        float *seg_state =
+            ca.states + (bh * ca.segments + seg) * (int64_t)p.dk * p.dv + (int64_t)row * p.dk;
+        const bool mine = row < D, stored = mine && row < p.dv;
+        const int a0 = sub * DH;
+        const auto caller = [&](int a) {
+            return sbase + (p.s_transposed ? (int64_t)row * p.dk + a : (int64_t)a * p.dv + row);
+        };
+        float z[DH];
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint32_t at = (i >> 2) * kPanel + (i & 3) * 32;
-                mma_f16(tmem + cS, desc_sw128(sb + kQ + at), desc_sw128(sb + kK + at), id, i > 0);
-            }
-            mma_commit(&bar_s);
-            if (D == 128 && !zero) mma_qz();       // (completes with P V)
+        for (int a = 0; a < DH; ++a) {
+            z[a] = 0.0f;
+            if (stored && has_state && a0 + a < p.dk)
+                z[a] = ca.segments > 1 ? seg_state[a0 + a] : p.s0[caller(a0 + a)];
         }
-        if (half == 1) {
+        // its bfloat16 copy, the right operand of Q Z
+        const auto publish = [&]() {
+#pragma unroll
+            for (int c = 0; c < DH / 8; ++c) {
+                uint4 u;
+                u.x = pack_bf16(z[8 * c], z[8 * c + 1]);
+                u.y = pack_bf16(z[8 * c + 2], z[8 * c + 3]);
+                u.z = pack_bf16(z[8 * c + 4], z[8 * c + 5]);
+                u.w = pack_bf16(z[8 * c + 6], z[8 * c + 7]);
+                const int at = a0 / 8 + c;
+                *reinterpret_cast<uint4 *>(base + kZ + (at >> 3) * (D * 128) +
+                                           sw_off16(row, (at & 7) * 8)) = u;
+            }
+        };
+        if (mine && has_state) publish();
+        int chunk = 0;
+        for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
+            const int m = (int)min((int64_t)kT, last - t0);
+            const bool more = t0 + kT < last;
+            meet();
             // W: half of a token row a thread
             const float f = pw[max(0, m - 1 - row + REV)] * p.scale_k;
 #pragma unroll
@@ -293,50 +288,88 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                     if (mine) publish();
                 }
             }
-        } else {
+        }
+        const bool ends = n > first ? n <= first + ca.seg_len : n == 0 && seg == 0;
+        if (stored && (!O || (p.sT && ends))) {
+#pragma unroll
+            for (int a = 0; a < DH; ++a)
+                if (a0 + a < p.dk) {
+                    if (O) p.sT[caller(a0 + a)] = z[a];
+                    else seg_state[a0 + a] = z[a];
+                }
+        }
+    }
+    if (O && half == 0) {
+        const auto mma_qz = [&]() {
+            const uint32_t id = idesc_f16(D, true);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                mma_f16(tmem + cQZ, desc_sw128(sb + kQ + (i >> 2) * kPanel + (i & 3) * 32),
+                        desc_sw128(sb + kZ + (i >> 2) * (D * 128) + (i & 3) * 32), id, i > 0);
+        };
+        const int diag = (warp & 3) * 32, a0 = sub * DH;
+        const float fz = pw[row + !REV] * p.scale_o;
+        bool zero = !has_state;
+        int chunk = 0;
+        for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
+            const int m = (int)min((int64_t)kT, last - t0);
+            meet();
+            if (tid == 0) {
+                const uint32_t id = idesc_f16(kT, true);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t at = (i >> 2) * kPanel + (i & 3) * 32;
+                    mma_f16(tmem + cS, desc_sw128(sb + kQ + at), desc_sw128(sb + kK + at), id,
+                            i > 0);
+                }
+                mma_commit(&bar_s);
+                if (D == 128 && !zero) mma_qz();           // (completes with P V)
+            }
             mbar_wait(&bar_s, chunk, ca.err);
             tc_after_sync();
-            // row `row` of P, every other 32 columns a thread; it replaces columns
-            // of S that other threads read, so all read first
-            const int diag = (warp & 3) * 32;
-            uint32_t y[2][16];
+            // row `row` of P, the 32 columns of S at 32 sub, then at 64 + 32 sub.  P's
+            // columns 0 .. 63 take the place of S's, which the first of them are
+            // read from: all threads read those before any writes
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = (2 * i + sub) * 32;
+                uint32_t y[16];
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) {
                     if (c > diag) {                        // above the diagonal
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) y[i][8 * k2 + j] = 0;
+                        for (int j = 0; j < 8; ++j) y[8 * k2 + j] = 0;
                         continue;
                     }
-                    float x[16];
-                    tmem_ld16(tmem + cS + c + 16 * k2 + lanes, x);
+                    // the factors first: a load under each element's condition
+                    // would be 16 branches (5000 cycles a block, not 300)
+                    float x[16], f[16];
                     if (c == diag) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int d = row - (c + 16 * k2 + j);
-                            x[j] = d >= 0 ? x[j] * (pw[max(d, 0)] * ca.scale_p) : 0.0f;
-                        }
+                        for (int j = 0; j < 16; ++j) f[j] = pw[max(row - (c + 16 * k2 + j), 0)];
                     } else {                               // gamma^(row - c - 31) gamma^(31 - j)
-                        const float f = pw[max(row - c - 31, 0)] * ca.scale_p;
+                        const float f0 = pw[max(row - c - 31, 0)];
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 g = down[4 * k2 + j / 4];
-                            x[j] *= f * g.x;
-                            x[j + 1] *= f * g.y;
-                            x[j + 2] *= f * g.z;
-                            x[j + 3] *= f * g.w;
+                            f[j] = f0 * g.x;
+                            f[j + 1] = f0 * g.y;
+                            f[j + 2] = f0 * g.z;
+                            f[j + 3] = f0 * g.w;
                         }
                     }
+                    tmem_ld16(tmem + cS + c + 16 * k2 + lanes, x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[i][8 * k2 + j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) {
+                        x[j] *= f[j] * ca.scale_p;
+                        x[j] = row < c + 16 * k2 + j ? 0.0f : x[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[8 * k2 + j] = pack_bf16(x[2 * j], x[2 * j + 1]);
                 }
+                if (i == 0) half_sync(0);
+                tmem_st16u(tmem + cS + c / 2 + lanes, y);
             }
-            half_sync(0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                tmem_st16u(tmem + cS + (2 * i + sub) * 16 + lanes, y[i]);
             tmem_st_wait();
             tc_before_sync();
             half_sync(0);
@@ -351,11 +384,12 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                 mma_commit(&bar_o);
             }
             mbar_wait(&bar_o, chunk, ca.err);
+            mbar_wait(&bar_d, chunk, ca.err);
             tc_after_sync();
-            if (more) load(kQ, q, t0 + kT);
-            const float fz = pw[row + !REV] * p.scale_o;
-            const int64_t t = REV ? n - 1 - (t0 + row) : t0 + row;
-            TO *o = static_cast<TO *>(p.o) + ((b * p.length + t) * p.heads + h) * p.dv + a0;
+            if (t0 + kT < last) load(kQ, q, t0 + kT);
+            // the tile by way of W's place (W was read), a row a bulk copy: a
+            // thread's own 16-byte stores would each touch 32 rows
+            char *stage = base + row * kStageRow<TO, D>;
 #pragma unroll
             for (int c = 0; c < DH; c += 16) {
                 float x[16];
@@ -368,19 +402,29 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
 #pragma unroll
                     for (int j = 0; j < 16; ++j) x[j] = fmaf(y2[j], fz, x[j]);
                 }
-                if (row < m) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        if (a0 + c + j >= p.dv) break;
-                        Pack<TO, 8> u;
+                for (int j = 0; j < 16; j += 8) {
+                    Pack<TO, 8> u;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) Storage<TO>::store(&u.v[i], x[j + i]);
-                        *reinterpret_cast<Pack<TO, 8> *>(o + c + j) = u;
-                    }
+                    for (int i = 0; i < 8; ++i) Storage<TO>::store(&u.v[i], x[j + i]);
+                    *reinterpret_cast<Pack<TO, 8> *>(stage + (a0 + c + j) * sizeof(TO)) = u;
                 }
             }
+            fence_async_smem();
+            half_sync(0);
+            if (sub == 0) {
+                if (row < m) {
+                    const int64_t t = REV ? n - 1 - (t0 + row) : t0 + row;
+                    TO *o = static_cast<TO *>(p.o) + ((b * p.length + t) * p.heads + h) * p.dv;
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                                 ::"l"(o), "r"(sb + row * kStageRow<TO, D>),
+                                   "r"((uint32_t)(p.dv * sizeof(TO))) : "memory");
+                }
+                bulk_commit();
+                bulk_wait_read();                          // W is rewritten after this chunk
+            }
+            zero = false;
         }
-        zero = false;
     }
     if (O) {
         // zeros past the sequence, in this segment's rows
@@ -391,15 +435,7 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             if (pc * 8 < p.dv)
                 *reinterpret_cast<Pack<TO, 8> *>(o + t * p.heads * p.dv + pc * 8) = none;
     }
-    const bool ends = n > first ? n <= first + ca.seg_len : n == 0 && seg == 0;
-    if (stored && (!O || (p.sT && ends))) {
-#pragma unroll
-        for (int a = 0; a < DH; ++a)
-            if (a0 + a < p.dk) {
-                if (O) p.sT[caller(a0 + a)] = z[a];
-                else seg_state[(int64_t)row * p.dk + a0 + a] = z[a];
-            }
-    }
+    if (O) bulk_wait_all();
     tc_before_sync();
     __syncthreads();
     if (warp == 0)
@@ -418,11 +454,11 @@ fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
     };
     if (ca.segments > 1) {
         fno_status_t st = go(k_linattn_tc<__nv_bfloat16, D, REV, false, KT>, 256,
-                             operand_bytes<D, false, KT>());
+                             operand_bytes<__nv_bfloat16, D, false, KT>());
         if (st == FNO_OK) st = segment_states(p, ca.s, ca.states, s);
         if (st != FNO_OK) return st;
     }
-    return go(k_linattn_tc<TO, D, REV, true, KT>, 512, operand_bytes<D, true, KT>());
+    return go(k_linattn_tc<TO, D, REV, true, KT>, 512, operand_bytes<TO, D, true, KT>());
 }
 
 }  // namespace
