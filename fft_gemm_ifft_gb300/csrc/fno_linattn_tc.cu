@@ -33,6 +33,11 @@ namespace {
 constexpr int kT = 128;                          // tokens of a chunk
 constexpr uint32_t kPanel = kT * 128;            // 128 tokens x 64 elements
 
+// Up to so many segments each adds up its earlier ones' local states itself (its
+// prologue reads them all at once); more are joined by a kernel in between, which
+// reads each once but costs its launch and a trip through memory.
+constexpr int kFold = 8;
+
 struct TcArgs {
     ScanArgs s;
     float *states;             // [b, h, segment][e][a]: local, then initial states
@@ -192,19 +197,36 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
     if (half == 1) {
         // the state: row `row` of Z^T, half of its columns a thread
         const int64_t sbase = bh * (int64_t)p.dk * p.dv;
-        float *seg_state =
-            ca.states + (bh * ca.segments + seg) * (int64_t)p.dk * p.dv + (int64_t)row * p.dk;
+        const int64_t size = (int64_t)p.dk * p.dv;
+        float *seg_state = ca.states + (bh * ca.segments + seg) * size + (int64_t)row * p.dk;
         const bool mine = row < D, stored = mine && row < p.dv;
         const int a0 = sub * DH;
         const auto caller = [&](int a) {
             return sbase + (p.s_transposed ? (int64_t)row * p.dk + a : (int64_t)a * p.dv + row);
         };
         float z[DH];
+        const bool ready = ca.segments > kFold;            // seg_state is the initial state
 #pragma unroll
         for (int a = 0; a < DH; ++a) {
             z[a] = 0.0f;
-            if (stored && has_state && a0 + a < p.dk)
-                z[a] = ca.segments > 1 ? seg_state[a0 + a] : p.s0[caller(a0 + a)];
+            if (stored && has_state && a0 + a < p.dk) {
+                if (ready) z[a] = seg_state[a0 + a];
+                else if (p.s0) z[a] = p.s0[caller(a0 + a)];
+            }
+        }
+        if (O && !ready && stored) {                       // the earlier segments' local states
+            const float whole = expf(p.log_decay[h] * (float)ca.seg_len);
+            const float *at = seg_state - seg * size + a0;
+            for (int j = 0; j < seg; ++j, at += size)
+#pragma unroll
+                for (int a = 0; a < DH; a += 4)            // (dk is a multiple of 8)
+                    if (a0 + a < p.dk) {
+                        const float4 x = *reinterpret_cast<const float4 *>(at + a);
+                        z[a] = fmaf(z[a], whole, x.x);
+                        z[a + 1] = fmaf(z[a + 1], whole, x.y);
+                        z[a + 2] = fmaf(z[a + 2], whole, x.z);
+                        z[a + 3] = fmaf(z[a + 3], whole, x.w);
+                    }
         }
         // its bfloat16 copy, the right operand of Q Z
         const auto publish = [&]() {
@@ -455,7 +477,7 @@ fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
     if (ca.segments > 1) {
         fno_status_t st = go(k_linattn_tc<__nv_bfloat16, D, REV, false, KT>, 256,
                              operand_bytes<__nv_bfloat16, D, false, KT>());
-        if (st == FNO_OK) st = segment_states(p, ca.s, ca.states, s);
+        if (st == FNO_OK && ca.segments > kFold) st = segment_states(p, ca.s, ca.states, s);
         if (st != FNO_OK) return st;
     }
     return go(k_linattn_tc<TO, D, REV, true, KT>, 512, operand_bytes<TO, D, true, KT>());
