@@ -69,6 +69,30 @@ __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&v)[16])
                    "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
                  : "memory");
 }
+// One lane of a warp, chosen where control flow is uniform: the MMAs' operands then
+// stay in uniform registers (issued under a thread index they cost 90 cycles each).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(e));
+    return e != 0;
+}
+// all 32 columns of a thread's lane, one wait
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     uint32_t u;
@@ -117,10 +141,11 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
     __shared__ __align__(8) uint64_t bar_s, bar_o, bar_d;
     __shared__ uint32_t s_tmem;
     __shared__ float pw[kT + 2];
+    __shared__ float up[O ? 2 * kT : 1];           // scale_p gamma^(i - kT), 0 for i < kT
     __shared__ float4 down[8];                     // gamma^31 .. gamma^0
     const ScanArgs &p = ca.s;
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int half = O ? tid >> 8 : 1, t8 = tid & 255, row = tid & 127, sub = t8 >> 7;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int half = O ? warp >> 3 : 1, t8 = tid & 255, row = tid & 127, sub = t8 >> 7;
     const int seg = blockIdx.x % ca.segments;
     if (!O && seg == ca.segments - 1) return;      // no segment starts from its state
     const int64_t bh = blockIdx.x / ca.segments;
@@ -143,12 +168,14 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
     {
         const float ld = p.log_decay[h];
         for (int i = tid; i < kT + 2; i += blockDim.x) pw[i] = i ? expf(ld * (float)i) : 1.0f;
+        if (O && tid < 2 * kT)
+            up[tid] = tid < kT ? 0.0f : ca.scale_p * (tid > kT ? expf(ld * (tid - kT)) : 1.0f);
         if (tid < 32) reinterpret_cast<float *>(down)[tid] = tid < 31 ? expf(ld * (31 - tid)) : 1.0f;
     }
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    const uint32_t sb = tc_smem_addr(base), tmem = s_tmem, lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t sb = tc_smem_addr(base), tmem = __shfl_sync(0xffffffffu, s_tmem, 0), lanes = (uint32_t)(warp & 3) << 21;
 
     // A tensor's rows of a chunk, zeros past the sequence and the width: thread t8
     // of a half takes the 16-byte piece `pc` of the rows r0, r0 + RS, ...
@@ -277,7 +304,7 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             }
             fence_async_smem();
             half_sync(1);
-            if (t8 == 0) {
+            if (warp == (O ? 8 : 0) && elect_one()) {
                 const uint32_t id = idesc_f16(D, true) | kAcrossA | kAcrossB;
                 for (int t = KT - 1; t >= 0; --t)          // the small terms first
 #pragma unroll
@@ -336,7 +363,7 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
         for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
             const int m = (int)min((int64_t)kT, last - t0);
             meet();
-            if (tid == 0) {
+            if (warp == 0 && elect_one()) {
                 const uint32_t id = idesc_f16(kT, true);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -356,38 +383,37 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             for (int i = 0; i < 2; ++i) {
                 const int c = (2 * i + sub) * 32;
                 uint32_t y[16];
+                if (c > diag) {                            // above the diagonal
 #pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2) {
-                    if (c > diag) {                        // above the diagonal
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) y[8 * k2 + j] = 0;
-                        continue;
-                    }
-                    // the factors first: a load under each element's condition
-                    // would be 16 branches (5000 cycles a block, not 300)
-                    float x[16], f[16];
+                    for (int j = 0; j < 16; ++j) y[j] = 0;
+                } else {
+                    float x[32];
+                    tmem_ld32(tmem + cS + c + lanes, x);
                     if (c == diag) {
+                        // (the factor read whatever the condition: read under it, each
+                        // element is a branch, 5000 cycles a block)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] = pw[max(row - (c + 16 * k2 + j), 0)];
+                        for (int j = 0; j < 32; ++j) {
+                            x[j] *= up[row - (c + j) + kT];
+                            x[j] = row < c + j ? 0.0f : x[j];
+                        }
                     } else {                               // gamma^(row - c - 31) gamma^(31 - j)
-                        const float f0 = pw[max(row - c - 31, 0)];
+                        const float2 f = f2(up[row - c - 31 + kT]);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 g = down[4 * k2 + j / 4];
-                            f[j] = f0 * g.x;
-                            f[j + 1] = f0 * g.y;
-                            f[j + 2] = f0 * g.z;
-                            f[j + 3] = f0 * g.w;
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 g = down[j / 4];
+                            const float2 lo = mul2(make_float2(x[j], x[j + 1]),
+                                                   mul2(f, make_float2(g.x, g.y)));
+                            const float2 hi = mul2(make_float2(x[j + 2], x[j + 3]),
+                                                   mul2(f, make_float2(g.z, g.w)));
+                            x[j] = lo.x;
+                            x[j + 1] = lo.y;
+                            x[j + 2] = hi.x;
+                            x[j + 3] = hi.y;
                         }
                     }
-                    tmem_ld16(tmem + cS + c + 16 * k2 + lanes, x);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        x[j] *= f[j] * ca.scale_p;
-                        x[j] = row < c + 16 * k2 + j ? 0.0f : x[j];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[8 * k2 + j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) y[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
                 }
                 if (i == 0) half_sync(0);
                 tmem_st16u(tmem + cS + c / 2 + lanes, y);
@@ -395,7 +421,7 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             tmem_st_wait();
             tc_before_sync();
             half_sync(0);
-            if (tid == 0) {
+            if (warp == 0 && elect_one()) {
                 tc_after_sync();
                 const uint32_t id = idesc_f16(D, true) | kAcrossB;
                 if (D == 64 && !zero) mma_qz();
@@ -409,8 +435,8 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             mbar_wait(&bar_d, chunk, ca.err);
             tc_after_sync();
             if (t0 + kT < last) load(kQ, q, t0 + kT);
-            // the tile by way of W's place (W was read), a row a bulk copy: a
-            // thread's own 16-byte stores would each touch 32 rows
+            // the tile by way of W's place (W was read): a thread's own 16-byte stores
+            // would each touch 32 rows
             char *stage = base + row * kStageRow<TO, D>;
 #pragma unroll
             for (int c = 0; c < DH; c += 16) {
@@ -432,18 +458,18 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                     *reinterpret_cast<Pack<TO, 8> *>(stage + (a0 + c + j) * sizeof(TO)) = u;
                 }
             }
-            fence_async_smem();
             half_sync(0);
-            if (sub == 0) {
-                if (row < m) {
-                    const int64_t t = REV ? n - 1 - (t0 + row) : t0 + row;
-                    TO *o = static_cast<TO *>(p.o) + ((b * p.length + t) * p.heads + h) * p.dv;
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                                 ::"l"(o), "r"(sb + row * kStageRow<TO, D>),
-                                   "r"((uint32_t)(p.dv * sizeof(TO))) : "memory");
-                }
-                bulk_commit();
-                bulk_wait_read();                          // W is rewritten after this chunk
+            // ... and out by 16-byte pieces, a row's side by side
+            constexpr int E = 16 / (int)sizeof(TO), PR = D / E;
+#pragma unroll 4
+            for (int i = t8; i < kT * PR; i += 256) {
+                const int r = i / PR, c = i % PR * E;
+                if (r >= m || c >= p.dv) continue;
+                const int64_t t = REV ? n - 1 - (t0 + r) : t0 + r;
+                *reinterpret_cast<uint4 *>(static_cast<TO *>(p.o) +
+                                           ((b * p.length + t) * p.heads + h) * p.dv + c) =
+                    *reinterpret_cast<const uint4 *>(base + r * kStageRow<TO, D> +
+                                                     c * sizeof(TO));
             }
             zero = false;
         }
@@ -457,7 +483,6 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             if (pc * 8 < p.dv)
                 *reinterpret_cast<Pack<TO, 8> *>(o + t * p.heads * p.dv + pc * 8) = none;
     }
-    if (O) bulk_wait_all();
     tc_before_sync();
     __syncthreads();
     if (warp == 0)
