@@ -37,6 +37,10 @@ struct ScanArgs {
     int dk, dv;
     float scale_o, scale_k;        // of the output, of each k v^T added to the state
     bool s_transposed;             // s0 and sT are stored (dv, dk)
+    // tcgen05 scans: the segments' states are those that the scan before left, of
+    // the same sums with keys and values exchanged; the states are wanted to
+    // float32's digits although this scan returns none
+    bool states_t, exact;
 };
 
 // One scan: in chunks up to 128 key columns, token by token beyond.  rev: from the

@@ -99,6 +99,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     memcpy(&u, &h, 4);
     return u;
 }
+__device__ __forceinline__ float2 bf16_pair(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ void half_sync(int which) {       // the 256 threads of a half
     asm volatile("bar.sync %0, 256;" ::"r"(1 + which) : "memory");
 }
@@ -115,11 +118,11 @@ constexpr uint32_t w_bytes() {
     const uint32_t w = KT * (D / 64) * kPanel, stage = (kT * kStageRow<TO, D> + 1023) / 1024 * 1024;
     return O && stage > w ? stage : w;
 }
-// bytes of the operands: W first, so that what an MMA of 128 rows reads past a
+// bytes of the operands (K, V and Q, or two of K and V): W first, so that what an MMA of 128 rows reads past a
 // 64-row panel of it lies within them
 template <typename TO, int D, bool O, int KT>
 constexpr uint32_t operand_bytes() {
-    return w_bytes<TO, D, O, KT>() + (D / 64) * kPanel * (2 + (O ? 1 : 0)) +
+    return w_bytes<TO, D, O, KT>() + (D / 64) * kPanel * (O ? 3 : 4) +
            (O ? (D / 64) * D * 128 : 0);
 }
 
@@ -127,7 +130,8 @@ constexpr uint32_t operand_bytes() {
 template <typename TO, int D, bool REV, bool O, int KT>
 __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn_tc(TcArgs ca) {
     using T = __nv_bfloat16;
-    constexpr int NP = D / 64, DH = D / 2;
+    constexpr uint32_t kKV = 2 * (D / 64) * kPanel;
+    constexpr int NP = D / 64, DH = D / 2, NB = D == 64 && O ? 2 : 4;
     constexpr uint32_t kW = 0, kK = w_bytes<TO, D, O, KT>(), kV = kK + NP * kPanel, kQ = kV + NP * kPanel,
                        kZ = kQ + NP * kPanel;
     // tensor memory: S / P, the output, Q Z (the 64-wide one in the half of S that
@@ -241,7 +245,18 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                 else if (p.s0) z[a] = p.s0[caller(a0 + a)];
             }
         }
-        if (O && !ready && stored) {                       // the earlier segments' local states
+        if (O && stored && p.states_t) {                   // another scan's, transposed
+            const float *at = ca.states + (bh * ca.segments + (ready ? seg : 0)) * size +
+                              (int64_t)a0 * p.dv + row;
+            const float whole = expf(p.log_decay[h] * (float)ca.seg_len);
+            for (int j = ready ? seg : 0; j < (ready ? seg + 1 : seg); ++j, at += size)
+#pragma unroll
+                for (int a = 0; a < DH; ++a)
+                    if (a0 + a < p.dk) {
+                        const float x = at[(int64_t)a * p.dv];
+                        z[a] = ready ? x : fmaf(z[a], whole, x);
+                    }
+        } else if (O && !ready && stored) {                // the earlier segments' local states
             const float whole = expf(p.log_decay[h] * (float)ca.seg_len);
             const float *at = seg_state - seg * size + a0;
             for (int j = 0; j < seg; ++j, at += size)
@@ -275,31 +290,43 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             const int m = (int)min((int64_t)kT, last - t0);
             const bool more = t0 + kT < last;
             meet();
-            // W: half of a token row a thread
-            const float f = pw[max(0, m - 1 - row + REV)] * p.scale_k;
+            // without outputs there is room for the next chunk's K and V
+            const uint32_t at_kv = O ? 0 : (chunk & 1) * kKV;
+            if (!O && more) {
+                load(kK + (kKV - at_kv), k, t0 + kT);
+                load(kV + (kKV - at_kv), v, t0 + kT);
+            }
+            // W: half of a token row a thread, NB pieces read before the first of their
+            // terms is written
+            const float2 f = f2(pw[max(0, m - 1 - row + REV)] * p.scale_k);
 #pragma unroll
-            for (int i = 0; i < DH / 8; ++i) {
-                const int c = a0 / 8 + i;
-                char *at = base + (c >> 3) * kPanel + sw_off16(row, (c & 7) * 8);
-                const uint4 u = *reinterpret_cast<uint4 *>(at + kV);
-                float x[8];
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int i0 = 0; i0 < DH / 8; i0 += NB) {
+                uint4 u[NB];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[2 * j] = __uint_as_float(w[j] << 16) * f;
-                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * f;
+                for (int i = 0; i < NB; ++i) {
+                    const int c = a0 / 8 + i0 + i;
+                    u[i] = *reinterpret_cast<uint4 *>(base + kV + at_kv + (c >> 3) * kPanel +
+                                                      sw_off16(row, (c & 7) * 8));
                 }
 #pragma unroll
-                for (int t = 0; t < KT; ++t) {
-                    uint32_t y[4];
+                for (int i = 0; i < NB; ++i) {
+                    const int c = a0 / 8 + i0 + i;
+                    char *at = base + kW + (c >> 3) * kPanel + sw_off16(row, (c & 7) * 8);
+                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    float2 x[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-                        x[2 * j] -= __uint_as_float(y[j] << 16);
-                        x[2 * j + 1] -= __uint_as_float(y[j] & 0xffff0000u);
+                    for (int j = 0; j < 4; ++j) x[j] = mul2(bf16_pair(w[j]), f);
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            y[j] = pack_bf16(x[j].x, x[j].y);
+                            if (t + 1 < KT) x[j] = sub2(x[j], bf16_pair(y[j]));
+                        }
+                        *reinterpret_cast<uint4 *>(at + t * NP * kPanel) =
+                            make_uint4(y[0], y[1], y[2], y[3]);
                     }
-                    *reinterpret_cast<uint4 *>(at + kW + t * NP * kPanel) =
-                        make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
             fence_async_smem();
@@ -311,15 +338,19 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                     for (int i = 0; i < kT / 16; ++i)
                         mma_f16(tmem + cD,
                                 desc_across(sb + kW + t * NP * kPanel + i * 2048, kPanel),
-                                desc_across(sb + kK + i * 2048, kPanel), id,
+                                desc_across(sb + kK + at_kv + i * 2048, kPanel), id,
                                 t < KT - 1 || i > 0);
                 mma_commit(&bar_d);
             }
             mbar_wait(&bar_d, chunk, ca.err);
             if (O) mbar_wait(&bar_s, chunk, ca.err);
             tc_after_sync();
-            if (more) load(kK, k, t0 + kT);
-            if (!O && more) load(kV, v, t0 + kT);
+            if (O) {
+                if (more) load(kK, k, t0 + kT);
+                mbar_wait(&bar_o, chunk, ca.err);          // V and the state's copy were read
+                if (more) load(kV, v, t0 + kT);
+                tc_after_sync();
+            }
             const float carry = pw[m];
             if ((warp & 3) * 32 < D)                       // (a warp's rows exist together)
 #pragma unroll
@@ -329,14 +360,7 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
 #pragma unroll
                     for (int j = 0; j < 16; ++j) z[c + j] = fmaf(z[c + j], carry, x[j]);
                 }
-            if (O) {
-                mbar_wait(&bar_o, chunk, ca.err);          // V and the state's copy were read
-                tc_after_sync();
-                if (more) {
-                    load(kV, v, t0 + kT);
-                    if (mine) publish();
-                }
-            }
+            if (O && more && mine) publish();
         }
         const bool ends = n > first ? n <= first + ca.seg_len : n == 0 && seg == 0;
         if (stored && (!O || (p.sT && ends))) {
@@ -460,17 +484,18 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             }
             half_sync(0);
             // ... and out by 16-byte pieces, a row's side by side
-            constexpr int E = 16 / (int)sizeof(TO), PR = D / E;
-#pragma unroll 4
-            for (int i = t8; i < kT * PR; i += 256) {
-                const int r = i / PR, c = i % PR * E;
-                if (r >= m || c >= p.dv) continue;
-                const int64_t t = REV ? n - 1 - (t0 + r) : t0 + r;
-                *reinterpret_cast<uint4 *>(static_cast<TO *>(p.o) +
-                                           ((b * p.length + t) * p.heads + h) * p.dv + c) =
-                    *reinterpret_cast<const uint4 *>(base + r * kStageRow<TO, D> +
-                                                     c * sizeof(TO));
-            }
+            constexpr int E = 16 / (int)sizeof(TO), PR = D / E, RO = 256 / PR;
+            const int ro = t8 / PR, co = t8 % PR * E;
+            const int64_t t = REV ? n - 1 - (t0 + ro) : t0 + ro;
+            const int64_t hop = (int64_t)p.heads * p.dv * (REV ? -RO : RO);
+            TO *o = static_cast<TO *>(p.o) + ((b * p.length + t) * p.heads + h) * p.dv + co;
+            const char *from = base + ro * kStageRow<TO, D> + co * sizeof(TO);
+            const int rows = co < p.dv ? m - ro : 0;
+#pragma unroll
+            for (int i = 0; i < kT / RO; ++i, o += hop)
+                if (i * RO < rows)
+                    *reinterpret_cast<uint4 *>(o) =
+                        *reinterpret_cast<const uint4 *>(from + i * RO * kStageRow<TO, D>);
             zero = false;
         }
     }
@@ -499,7 +524,7 @@ fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
         kernel<<<(unsigned)(bh * ca.segments), threads, smem, s>>>(ca);
         return launched();
     };
-    if (ca.segments > 1) {
+    if (ca.segments > 1 && !ca.s.states_t) {
         fno_status_t st = go(k_linattn_tc<__nv_bfloat16, D, REV, false, KT>, 256,
                              operand_bytes<__nv_bfloat16, D, false, KT>());
         if (st == FNO_OK && ca.segments > kFold) st = segment_states(p, ca.s, ca.states, s);
@@ -528,7 +553,7 @@ fno_status_t tc_scan(const fno_linattn_s &p, const ScanArgs &a, bool rev, bool w
             if (wide_out) return run<float, D, true, KT>(p, ca, s);
             return run<__nv_bfloat16, D, true, KT>(p, ca, s);
         };
-        return a.sT ? terms(std::integral_constant<int, 3>())
+        return a.sT || a.exact ? terms(std::integral_constant<int, 3>())
                     : terms(std::integral_constant<int, 2>());
     };
     return a.dk <= 64 && a.dv <= 64 ? width(std::integral_constant<int, 64>())
