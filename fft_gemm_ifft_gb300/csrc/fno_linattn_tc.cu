@@ -69,14 +69,6 @@ __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t (&v)[16])
                    "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
                  : "memory");
 }
-// One lane of a warp, chosen where control flow is uniform: the MMAs' operands then
-// stay in uniform registers (issued under a thread index they cost 90 cycles each).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(e));
-    return e != 0;
-}
 // all 32 columns of a thread's lane, one wait
 __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
     uint32_t r[32];

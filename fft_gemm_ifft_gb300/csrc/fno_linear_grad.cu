@@ -164,7 +164,7 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
                                           ~static_cast<uintptr_t>(1023));
     __shared__ __align__(8) uint64_t bar[2];
     __shared__ uint32_t s_tmem;
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int i0 = blockIdx.x * kM, o0 = blockIdx.y * kMaxN<T>;
     const int mi = min(kM, cin - i0), no = min(kMaxN<T>, cout - o0), N = (no + 15) / 16 * 16;
     const uint32_t chunk_b = N * 128, tile_a = 2 * kChunkA, stage = tile_a + NT * 2 * chunk_b;
@@ -192,7 +192,7 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    const uint32_t tmem = s_tmem, sb = tc_smem_addr(base);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0), sb = tc_smem_addr(base);
     const int64_t items = batch * groups;
     const int r0 = tid >> 4, c8 = (tid & 15) * 8;        // rows r0 + 32 k, points c8 .. c8 + 7
     const int row_i = i0 + (w & 3) * 32 + lane;          // this thread's accumulator row
@@ -310,11 +310,13 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
         load(x);
         fence_async_smem();
         __syncthreads();
-        if (tid == 0) {
+        if (w == 0 && elect_one()) {
             tc_after_sync();
             const uint32_t a = sb + (n & 1) * stage, d = tmem + (n & 1) * kMaxN<T>;
             const uint32_t id = idesc_f16(N, !std::is_same<TO, __half>::value);
+#pragma unroll
             for (int x = NT - 1; x >= 0; --x)            // the small terms first
+#pragma unroll
                 for (int k = 0; k < kGroup / 16; ++k)
                     mma_f16(d, desc_sw128(a + (k >> 2) * kChunkA + (k & 3) * 32),
                             desc_sw128(a + tile_a + (2 * x + (k >> 2)) * chunk_b + (k & 3) * 32),

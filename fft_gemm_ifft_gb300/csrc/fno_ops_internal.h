@@ -163,6 +163,14 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// One lane of a warp, chosen where control flow is uniform: the MMAs' operands then
+// stay in uniform registers (issued under a thread index they cost 90 cycles each).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(e));
+    return e != 0;
+}
 // The values of four codes: the biased byte under the exponent of 2^23, less
 // 2^23 + 128 (two instructions a code at full rate; a conversion runs at a
 // quarter of it or less).
