@@ -159,6 +159,7 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
     constexpr int NT = kTerms<T>;
     constexpr int RA = kM / kRows, RB = kMaxN<T> / kRows;   // rows of a thread: codes, dy
     constexpr int NC = kMaxN<T> / 4;                     // accumulators of a thread
+    constexpr uint32_t kCols = 2 * kMaxN<T>;             // two of D
     extern __shared__ char smem_raw[];
     char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                           ~static_cast<uintptr_t>(1023));
@@ -175,7 +176,7 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
     }
     if (w == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(tc_smem_addr(&s_tmem)), "r"(2u * kMaxN<T>));
+                     ::"r"(tc_smem_addr(&s_tmem)), "r"(kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     // rows past the channels are never written: zero, once
@@ -207,41 +208,62 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
     } next[2] = {};
     float sc = 0.0f, acc[NC] = {}, bias[RB] = {};
     // the loads run over this CTA's blocks in order: (b, g) is the next one
+    // (and where its rows start, kept up with it)
     int64_t it = blockIdx.z, b = it / groups, g = it - b * groups;
     const int64_t row_step = (int64_t)kRows * points;
+    const int8_t *q_row, *q_at;
+    const T *y_row, *y_at;
+    const float *s_row;
+    const auto sample = [&]() {
+        q_row = codes + (b * cin + i0 + r0) * points + c8;
+        y_row = dy + (b * cout + o0 + r0) * points + c8;
+        s_row = scales + (b * cin + row_i) * groups;
+    };
+    sample();
+    q_at = q_row + g * kGroup;
+    y_at = y_row + g * kGroup;
     const auto load = [&](Next &x) {
         if (it >= items) return;
-        const int64_t p = g * kGroup + c8;
-        x.n = (int)max((int64_t)0, min((int64_t)8, points - p));
-        const int8_t *q = codes + (b * cin + i0 + r0) * points + p;
-        const T *y = dy + (b * cout + o0 + r0) * points + p;
+        x.n = (int)max((int64_t)0, min((int64_t)8, points - g * kGroup - c8));
         if (!VEC) {
-            x.sh_q = (int)(reinterpret_cast<uintptr_t>(q) & 3) * 8;
-            x.sh_y = (int)(reinterpret_cast<uintptr_t>(y) & 3) * 8;
+            x.sh_q = (int)(reinterpret_cast<uintptr_t>(q_at) & 3) * 8;
+            x.sh_y = (int)(reinterpret_cast<uintptr_t>(y_at) & 3) * 8;
         }
         // words reach up to 4 bytes past the wanted elements: there are as many in
         // the tensor when 4 blocks follow, each of an element a row at least
         if (VEC || it + 4 < items) {
 #pragma unroll
-            for (int k = 0; k < RA; ++k)
-                x.q[k].load(q + k * row_step, r0 + kRows * k < mi ? x.n : 0);
+            for (int k = 0; k < RA; ++k) {
+                if (kRows * k >= mi) break;
+                x.q[k].load(q_at + k * row_step, r0 + kRows * k < mi ? x.n : 0);
+            }
 #pragma unroll
-            for (int k = 0; k < RB; ++k)
-                x.y[k].load(y + k * row_step, r0 + kRows * k < no ? x.n : 0);
+            for (int k = 0; k < RB; ++k) {
+                if (kRows * k >= no) break;
+                x.y[k].load(y_at + k * row_step, r0 + kRows * k < no ? x.n : 0);
+            }
         } else {                                         // near the tensors' ends
 #pragma unroll
             for (int k = 0; k < RA; ++k)
-                x.q[k].load_exact(q + k * row_step, r0 + kRows * k < mi ? x.n : 0);
+                x.q[k].load_exact(q_at + k * row_step, r0 + kRows * k < mi ? x.n : 0);
 #pragma unroll
             for (int k = 0; k < RB; ++k)
-                x.y[k].load_exact(y + k * row_step, r0 + kRows * k < no ? x.n : 0);
+                x.y[k].load_exact(y_at + k * row_step, r0 + kRows * k < no ? x.n : 0);
         }
-        x.scale = row_i < i0 + mi ? scales[(b * cin + row_i) * groups + g] : 1.0f;
+        x.scale = row_i < i0 + mi ? s_row[g] : 1.0f;
         it += gridDim.z;
         g += gridDim.z;
-        while (g >= groups) {
-            g -= groups;
-            ++b;
+        if (g < groups) {
+            q_at += (int)gridDim.z * kGroup;
+            y_at += (int)gridDim.z * kGroup;
+        } else {
+            do {
+                g -= groups;
+                ++b;
+            } while (g >= groups);
+            sample();
+            q_at = q_row + g * kGroup;
+            y_at = y_row + g * kGroup;
         }
     };
     const auto drain = [&](int n, float s) {             // D of block n, times the scales
@@ -354,7 +376,7 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
     __syncthreads();
     if (w == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(2u * kMaxN<T>));
+                     "r"(kCols));
 }
 
 // The shares of 32 elements added by 8 warps, then across the warps in order.
