@@ -121,17 +121,40 @@ k_act8_pack_any(const T *__restrict__ x, int8_t *__restrict__ codes, float *__re
 // 1 - erf is Abramowitz & Stegun 7.1.26, poly(t) e^{-x^2} with x = |v| / sqrt 2
 // (absolute error 1.5e-7, as in fno_gelu.cuh), whose exponential is also the
 // density's: one exponential and one reciprocal an element, where erfcf and
-// expf would make the arithmetic cost more than the bytes.
-__device__ __forceinline__ float gelu_slope(float v) {
+// expf would make the arithmetic cost more than the bytes.  Two elements at a
+// time: 15 instructions an element.
+__device__ __forceinline__ float2 gelu_slope2(float2 v) {
     constexpr float p = 0.3275911f * 0.70710678118654752f;
     constexpr float a1 = 0.254829592f, a2 = -0.284496736f, a3 = 1.421413741f,
                     a4 = -1.453152027f, a5 = 1.061405429f;
-    const float m = fabsf(v);
-    const float t = __fdividef(1.0f, fmaf(p, m, 1.0f));
-    const float e = __expf(-0.5f * m * m);
-    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, a5, a4), a3), a2), a1);
-    const float half = 0.5f * q * e;                   // Phi(-|v|)
-    return fmaf(v * 0.3989422804014327f, e, v < 0.0f ? half : 1.0f - half);
+    const float2 d = fma2(f2(p), make_float2(fabsf(v.x), fabsf(v.y)), f2(1.0f));
+    const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
+    const float2 w = mul2(mul2(v, v), f2(-0.5f));
+    const float2 e = make_float2(__expf(w.x), __expf(w.y));
+    float2 q = fma2(t, f2(a5), f2(a4));
+    q = fma2(t, q, f2(a3));
+    q = fma2(t, q, f2(a2));
+    q = fma2(t, q, f2(a1));
+    // Phi(-|v|) = q t e / 2, and Phi(v) = 1/2 + sign(v) (1/2 - Phi(-|v|))
+    const float2 r = fma2(mul2(mul2(q, t), e), f2(-0.5f), f2(0.5f));
+    const float2 phi = add2(make_float2(copysignf(r.x, v.x), copysignf(r.y, v.y)), f2(0.5f));
+    return fma2(mul2(v, f2(0.3989422804014327f)), e, phi);
+}
+// of a pair's values and gradients, or the values themselves
+template <bool GELU>
+__device__ __forceinline__ float2 result2(float2 v, float2 dy) {
+    return GELU ? mul2(dy, gelu_slope2(v)) : v;
+}
+
+// the scale of the element after column c
+template <typename I>
+__device__ __forceinline__ float step_scale(const float *scales, I cols, I &c, I &at, float s) {
+    ++c;
+    if (c == cols) {
+        c = 0;
+        return scales[++at];           // a row's first group follows the last row's last
+    }
+    return c % kGroup == 0 ? scales[++at] : s;
 }
 
 // out = value, or dy * GELU'(value).  The tensors are walked as flat arrays by
@@ -154,13 +177,6 @@ k_act8_read(const int8_t *__restrict__ codes, const float *__restrict__ scales, 
         if (first[k] < n && n - first[k] >= V) {
             q[k] = *reinterpret_cast<const Pack<int8_t, V> *>(codes + first[k]);
             if (GELU) d[k] = *reinterpret_cast<const Pack<T, V> *>(dy + first[k]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (first[k] < n && (I)i < n - first[k]) {
-                    q[k].v[i] = codes[first[k] + i];
-                    if (GELU) d[k].v[i] = dy[first[k] + i];
-                }
         }
     }
 #pragma unroll
@@ -168,31 +184,42 @@ k_act8_read(const int8_t *__restrict__ codes, const float *__restrict__ scales, 
         if (first[k] >= n) continue;
         const I row = first[k] / cols, col = first[k] - row * cols;
         const bool one = cols - col >= V && col % kGroup <= kGroup - V;
-        const bool whole = n - first[k] >= V;
         I at = row * groups_per_row + col / kGroup;
-        float s = scales[at];
-        I c = col;
+        if (n - first[k] >= V) {
+            float f[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (!one && i > 0 && (whole || (I)i < n - first[k])) {
-                ++c;
-                if (c == cols) {
-                    c = 0;
-                    s = scales[++at];          // a row's first group follows the last row's last
-                } else if (c % kGroup == 0) {
-                    s = scales[++at];
-                }
+            for (int i = 0; i < V; i += 4) {
+                uint32_t u;
+                memcpy(&u, &q[k].v[i], 4);
+                code_values4(u, f + i);
             }
-            const float v = (float)q[k].v[i] * s;
-            const float r = GELU ? Storage<T>::load(&d[k].v[i]) * gelu_slope(v) : v;
-            Storage<T>::store(&d[k].v[i], r);
-        }
-        if (whole) {
+            float s = scales[at], t = s;
+            I c = col;
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                if (!one) {                    // scales element by element
+                    if (i > 0) s = step_scale(scales, cols, c, at, s);
+                    t = step_scale(scales, cols, c, at, s);
+                }
+                const float2 v = mul2(make_float2(f[i], f[i + 1]), make_float2(s, t));
+                const float2 dv = GELU ? make_float2(Storage<T>::load(&d[k].v[i]),
+                                                     Storage<T>::load(&d[k].v[i + 1]))
+                                       : v;
+                const float2 r = result2<GELU>(v, dv);
+                Storage<T>::store(&d[k].v[i], r.x);
+                Storage<T>::store(&d[k].v[i + 1], r.y);
+                s = t;
+            }
             *reinterpret_cast<Pack<T, V> *>(out + first[k]) = d[k];
         } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if ((I)i < n - first[k]) out[first[k] + i] = d[k].v[i];
+            float s = scales[at];
+            I c = col;
+            for (int i = 0; (I)i < n - first[k]; ++i) {
+                if (i > 0) s = step_scale(scales, cols, c, at, s);
+                const float v = (float)codes[first[k] + i] * s;
+                const float dv = GELU ? Storage<T>::load(dy + first[k] + i) : v;
+                Storage<T>::store(out + first[k] + i, result2<GELU>(f2(v), f2(dv)).x);
+            }
         }
     }
 }

@@ -94,40 +94,71 @@ void group_sum(const float *in, T *out, int64_t n, int g, int d, cudaStream_t s)
         k_linattn_group_sum<T, 1><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(in, out, n, g, d);
 }
 
-// One token: a CTA per (row, head, slice of value columns), the key rows over
-// the warps.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// One token: a CTA per (row, head).  V value columns a thread (4 where the width
+// allows), the key rows over the threads that are left; eight rows' loads are in
+// flight at a time, for the state read and written once is all that it costs.
+constexpr int kStepThreads = 128;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kStepThreads)
 k_linattn_step(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
                const float *__restrict__ log_decay, float scale, const int32_t *__restrict__ slots,
                int64_t num_slots, const float *state, float *new_state, T *__restrict__ o,
                int heads, int group, int dk, int dv) {
-    __shared__ float sum[8][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int h = blockIdx.x % heads, e = blockIdx.y * 32 + lane;
+    __shared__ float sum[kStepThreads * V], sq[kMaxWidth], sk[kMaxWidth];
+    const int h = blockIdx.x % heads;
     const int64_t b = blockIdx.x / heads;
     const int64_t slot = slots ? (int64_t)slots[b] : b;
     const bool live = slot >= 0 && slot < num_slots;
-    float s = 0.0f;
-    if (live && e < dv) {
-        const float gm1 = expm1f(log_decay[h]);
-        const int64_t base = (slot * heads + h) * (int64_t)dk * dv + e;
-        const int64_t kv = b * (heads / group) + h / group;
-        const float ve = Storage<T>::load(v + kv * dv + e);
-        for (int d = w; d < dk; d += 8) {
-            const float z0 = state[base + (int64_t)d * dv];
-            const float z = fmaf(Storage<T>::load(k + kv * dk + d), ve, fmaf(z0, gm1, z0));
-            new_state[base + (int64_t)d * dv] = z;
-            s = fmaf(Storage<T>::load(q + (b * heads + h) * dk + d), z, s);
-        }
+    const int64_t kv = b * (heads / group) + h / group;
+    for (int d = threadIdx.x; d < dk; d += kStepThreads) {
+        sq[d] = Storage<T>::load(q + (b * heads + h) * dk + d);
+        sk[d] = Storage<T>::load(k + kv * dk + d);
     }
-    sum[w][lane] = s;
     __syncthreads();
-    if (w == 0 && e < dv) {
-        float t = 0.0f;
+    const float gm1 = expm1f(log_decay[h]);
+    // columns in rounds of the threads (dv up to 256), rows over what is left
+    const int lanes = (dv + V - 1) / V, across = lanes < kStepThreads ? lanes : kStepThreads;
+    const int down = kStepThreads / across, mine = threadIdx.x % across, part = threadIdx.x / across;
+    for (int e0 = mine * V; e0 < (dv + V - 1) / V * V; e0 += across * V) {
+        Pack<float, V> s = {};
+        if (live && part < down && e0 < dv) {
+            const int64_t base = (slot * heads + h) * (int64_t)dk * dv + e0;
+            Pack<float, V> ve;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t += sum[j][lane];
-        Storage<T>::store(o + (b * heads + h) * dv + e, scale * t);
+            for (int i = 0; i < V; ++i) ve.v[i] = Storage<T>::load(v + kv * dv + e0 + i);
+            for (int d0 = part; d0 < dk; d0 += 8 * down) {
+                Pack<float, V> z[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (d0 + r * down < dk)
+                        z[r] = *reinterpret_cast<const Pack<float, V> *>(
+                            state + base + (int64_t)(d0 + r * down) * dv);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int d = d0 + r * down;
+                    if (d >= dk) break;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        z[r].v[i] = fmaf(sk[d], ve.v[i], fmaf(z[r].v[i], gm1, z[r].v[i]));
+                        s.v[i] = fmaf(sq[d], z[r].v[i], s.v[i]);
+                    }
+                    *reinterpret_cast<Pack<float, V> *>(new_state + base + (int64_t)d * dv) = z[r];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[threadIdx.x * V + i] = s.v[i];
+        __syncthreads();
+        if (part == 0 && e0 < dv) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float t = 0.0f;
+                for (int r = 0; r < down; ++r) t += sum[(r * across + mine) * V + i];
+                Storage<T>::store(o + (b * heads + h) * dv + e0 + i, scale * t);
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -309,13 +340,17 @@ fno_status_t fno_linattn_step(fno_linattn_t p, const void *q, const void *k, con
          {state, sb, false}, {new_state, sb, true, state}, {o, n.o, true}});
     if (st != FNO_OK) return st;
     if (inject("launch")) return FNO_ERR_CUDA;
-    const dim3 grid((unsigned)(p->batch * p->heads), (unsigned)ceil_div(p->dv, 32));
     with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
-        k_linattn_step<T><<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-            static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v),
-            log_decay, scale, slots, num_slots, state, new_state, static_cast<T *>(o), p->heads,
-            p->heads / p->kv_heads, p->dk, p->dv);
+        const auto run = [&](auto kernel) {
+            kernel<<<(unsigned)(p->batch * p->heads), kStepThreads, 0,
+                     reinterpret_cast<cudaStream_t>(stream)>>>(
+                static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v),
+                log_decay, scale, slots, num_slots, state, new_state, static_cast<T *>(o),
+                p->heads, p->heads / p->kv_heads, p->dk, p->dv);
+        };
+        if (p->dv % 4 == 0) run(k_linattn_step<T, 4>);
+        else run(k_linattn_step<T, 1>);
     });
     return launched();
 }

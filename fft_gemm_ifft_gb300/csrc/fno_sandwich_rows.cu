@@ -14,25 +14,25 @@ constexpr int kMaxWarps = 16;
 // Token layout: G warps hold a row in registers, each thread J runs of V
 // consecutive channels; a CTA of R = warps / G rows.
 // ---------------------------------------------------------------------------
-// the sum of N values over the G warps of a row
+// The sums of N values over the G warps of a row.  `buf` ([N][kMaxWarps]) is this
+// sum's own: a buffer may be used again once another sum came in between, whose
+// barrier every reader of this one has passed.
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int G, float (*red)[kMaxWarps]) {
+__device__ __forceinline__ void row_sum(float (&v)[N], int G, float (*buf)[kMaxWarps]) {
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
     if (G == 1) return;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();             // the last sum's readers are done
-    if (lane == 0)
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int k = 0; k < N; ++k) red[k][w] = v[k];
+        for (int k = 0; k < N; ++k) buf[k][w] = v[k];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        v[k] = lane < G ? red[k][w / G * G + lane] : 0.0f;
-#pragma unroll
-        for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+        v[k] = 0.0f;
+        for (int i = 0; i < G; ++i) v[k] += buf[k][w / G * G + i];
     }
 }
 
@@ -40,14 +40,15 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int G, float (*red)[kMaxW
 // row's channels are excluded by `have`.
 template <int N, bool LAYER, class Have>
 __device__ __forceinline__ void row_norm(const float (&x)[N], Have &&have, int channels, float eps,
-                                         int G, float (*red)[kMaxWarps], float &mean, float &r) {
+                                         int G, float (*red)[1][kMaxWarps], float &mean,
+                                         float &r) {
     const float inv = 1.0f / (float)channels;
     mean = 0.0f;
     if (LAYER) {
         float s[1] = {};
 #pragma unroll
         for (int i = 0; i < N; ++i) s[0] += x[i];          // absent entries are 0
-        row_sum<1>(s, G, red);
+        row_sum<1>(s, G, red[0]);
         mean = s[0] * inv;
     }
     float q[1] = {};
@@ -56,7 +57,7 @@ __device__ __forceinline__ void row_norm(const float (&x)[N], Have &&have, int c
         const float d = have(i) ? x[i] - mean : 0.0f;
         q[0] = fmaf(d, d, q[0]);
     }
-    row_sum<1>(q, G, red);
+    row_sum<1>(q, G, red[1]);
     r = rsqrtf(fmaf(q[0], inv, eps));
 }
 
@@ -64,7 +65,7 @@ template <typename T, int V, int J, bool LAYER>
 __global__ void __launch_bounds__(512)
 k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
     constexpr int N = V * J;
-    __shared__ float red[1][kMaxWarps];
+    __shared__ float red[4][1][kMaxWarps];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
     const int64_t rows = a.batch * a.points;
     const int64_t row = (int64_t)blockIdx.x * R + w / G;
@@ -159,7 +160,7 @@ k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = have(i) ? v[i] - shift : 0.0f;
     }
-    row_norm<N, LAYER>(v, have, a.channels, a.eps, G, red, mean, r);
+    row_norm<N, LAYER>(v, have, a.channels, a.eps, G, red + 2, mean, r);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         if (!on || !have(j * V)) continue;
@@ -182,7 +183,9 @@ __global__ void __launch_bounds__(512)
 k_sandwich_bwd_rows(Args a, int G) {
     constexpr int N = V * J;
     using TF = typename std::conditional<F8, int8_t, T>::type;
-    __shared__ float red[2][kMaxWarps];
+    // three rounds of sums a row: the means; the squared deviations, sum d and
+    // sum d N; sum e and sum e M
+    __shared__ float red1[2][kMaxWarps], red2[4][kMaxWarps], red3[2][kMaxWarps];
     extern __shared__ float4 sm[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
     const int c0 = ((w % G) * 32 + lane) * V, cs = G * 32 * V;
@@ -216,34 +219,54 @@ k_sandwich_bwd_rows(Args a, int G) {
                 gates[j] =
                     *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.gate) + e);
         }
-        float n1[N], m2[N], dY[N], mean, r1 = 0.0f, r2 = 0.0f, d[2] = {};
-        if (a.du) {
-            const float shift = LAYER && on ? Storage<T>::load(static_cast<const T *>(a.x) + base)
-                                            : 0.0f;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                n1[i] = have(i) ? Storage<T>::load(&ys[i / V].v[i % V]) - shift : 0.0f;
-            row_norm<N, LAYER>(n1, have, a.channels, a.eps, G, red, mean, r1);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                Pack<float, V> w1 = {};
-                if (have(j * V)) w1 = *reinterpret_cast<const Pack<float, V> *>(a.w1 + c0 + j * cs);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int k = j * V + i;
-                    n1[k] = have(k) ? (n1[k] - mean) * r1 : 0.0f;
-                    const float du = Storage<T>::load(&us[j].v[i]);
-                    acc[2][k] = fmaf(du, n1[k], acc[2][k]);
-                    acc[3][k] += du;
-                    dY[k] = weighted(du, w1.v[i]);
-                    d[0] += dY[k];
-                    d[1] = fmaf(dY[k], n1[k], d[1]);
-                }
+        float n1[N], m2[N], dY[N], mean[2] = {}, q[4] = {}, shift1 = 0.0f, shift2 = 0.0f;
+        if (LAYER && on) {
+            if (a.du) shift1 = Storage<T>::load(static_cast<const T *>(a.x) + base);
+            if constexpr (F8) {
+                shift2 = (float)a.f8[base] * a.f8_scale[row * groups];
+            } else {
+                if (block) shift2 = Storage<T>::load(static_cast<const T *>(a.f) + base);
             }
-            row_sum<2>(d, G, red);
-            d[0] = LAYER ? d[0] * inv : 0.0f;
-            d[1] *= inv;
         }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float f;
+            if constexpr (F8) f = (float)fs[i / V].v[i % V] * fsc[i / V];
+            else f = Storage<T>::load(&fs[i / V].v[i % V]);
+            n1[i] = have(i) ? Storage<T>::load(&ys[i / V].v[i % V]) - shift1 : 0.0f;
+            m2[i] = have(i) ? f - shift2 : 0.0f;
+            mean[0] += n1[i];
+            mean[1] += m2[i];
+        }
+        if (LAYER) {
+            row_sum<2>(mean, G, red1);
+            mean[0] *= inv;
+            mean[1] *= inv;
+        } else {
+            mean[0] = mean[1] = 0.0f;
+        }
+        // q: sum (y - mean)^2, sum (f - mean)^2, sum d, sum d (y - mean)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            Pack<float, V> w1 = {};
+            if (a.du && have(j * V))
+                w1 = *reinterpret_cast<const Pack<float, V> *>(a.w1 + c0 + j * cs);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int k = j * V + i;
+                n1[k] = have(k) ? n1[k] - mean[0] : 0.0f;
+                m2[k] = have(k) ? m2[k] - mean[1] : 0.0f;
+                dY[k] = weighted(Storage<T>::load(&us[j].v[i]), w1.v[i]);
+                q[0] = fmaf(n1[k], n1[k], q[0]);
+                q[1] = fmaf(m2[k], m2[k], q[1]);
+                q[2] += dY[k];
+                q[3] = fmaf(dY[k], n1[k], q[3]);
+            }
+        }
+        row_sum<4>(q, G, red2);
+        const float r1 = on && a.du ? rsqrtf(fmaf(q[0], inv, a.eps)) : 0.0f;
+        const float r2 = on ? rsqrtf(fmaf(q[1], inv, a.eps)) : 0.0f;
+        const float d0 = LAYER ? q[2] * inv : 0.0f, d1 = q[3] * r1 * inv;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             Pack<T, V> xs;
@@ -251,7 +274,13 @@ k_sandwich_bwd_rows(Args a, int G) {
             for (int i = 0; i < V; ++i) {
                 const int k = j * V + i;
                 float g = Storage<T>::load(&gs[j].v[i]);
-                if (a.du) g = fmaf(r1, dY[k] - d[0] - n1[k] * d[1], g);
+                if (a.du) {
+                    const float du = Storage<T>::load(&us[j].v[i]);
+                    n1[k] *= r1;
+                    acc[2][k] = fmaf(du, n1[k], acc[2][k]);
+                    if (LAYER) acc[3][k] += du;
+                    g = fmaf(r1, dY[k] - d0 - n1[k] * d1, g);
+                }
                 dY[k] = have(k) ? g : 0.0f;
                 Storage<T>::store(&xs.v[i], g);
             }
@@ -259,20 +288,6 @@ k_sandwich_bwd_rows(Args a, int G) {
                 *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dx) + base + c0 + j * cs) = xs;
         }
         if (!block) continue;
-        float shift = 0.0f;
-        if constexpr (F8) {
-            if (LAYER && on) shift = (float)a.f8[base] * a.f8_scale[row * groups];
-        } else {
-            if (LAYER && on) shift = Storage<T>::load(static_cast<const T *>(a.f) + base);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float f;
-            if constexpr (F8) f = (float)fs[i / V].v[i % V] * fsc[i / V];
-            else f = Storage<T>::load(&fs[i / V].v[i % V]);
-            m2[i] = have(i) ? f - shift : 0.0f;
-        }
-        row_norm<N, LAYER>(m2, have, a.channels, a.eps, G, red, mean, r2);
         float e[2] = {}, ev[N];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -290,14 +305,14 @@ k_sandwich_bwd_rows(Args a, int G) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int k = j * V + i;
-                m2[k] = have(k) ? (m2[k] - mean) * r2 : 0.0f;
+                m2[k] *= r2;
                 float av = 1.0f;
                 if (a.gate_kind != FNO_GATE_NONE)
                     av = gate_value(a.gate_kind == FNO_GATE_FULL ? Storage<T>::load(&gates[j].v[i])
                                                                  : gf.v[i], a.sigmoid);
                 const float ga = a.gate_kind == FNO_GATE_FULL ? dY[k] * av : dY[k];
                 acc[0][k] = fmaf(ga, m2[k], acc[0][k]);
-                acc[1][k] += ga;
+                if (LAYER) acc[1][k] += ga;
                 const float ts = dY[k] * s.v[i];
                 Storage<T>::store(&dg.v[i], ts * (LAYER ? fmaf(m2[k], w2.v[i], b2.v[i])
                                                         : m2[k] * w2.v[i]) *
@@ -309,7 +324,7 @@ k_sandwich_bwd_rows(Args a, int G) {
             if (a.dgate && on && have(j * V))
                 *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dgate) + base + c) = dg;
         }
-        row_sum<2>(e, G, red);
+        row_sum<2>(e, G, red3);
         e[0] = LAYER ? e[0] * inv : 0.0f;
         e[1] *= inv;
 #pragma unroll
