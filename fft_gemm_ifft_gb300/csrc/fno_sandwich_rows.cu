@@ -178,10 +178,31 @@ k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
     }
 }
 
+// The pair of elements 2 k, 2 k + 1 of a thread's runs.
+template <typename T, int V, int J>
+__device__ __forceinline__ float2 pair_of(const Pack<T, V> (&x)[J], int k) {
+    return make_float2(Storage<T>::load(&x[2 * k / V].v[2 * k % V]),
+                       Storage<T>::load(&x[(2 * k + 1) / V].v[(2 * k + 1) % V]));
+}
+template <int V, int J>
+__device__ __forceinline__ float2 pair_of(const Pack<int8_t, V> (&x)[J], const float (&scale)[J],
+                                          int k) {
+    return make_float2((float)x[2 * k / V].v[2 * k % V] * scale[2 * k / V],
+                       (float)x[(2 * k + 1) / V].v[(2 * k + 1) % V] * scale[(2 * k + 1) / V]);
+}
+template <typename T, int V, int J>
+__device__ __forceinline__ void set_pair(Pack<T, V> (&x)[J], int k, float2 v) {
+    Storage<T>::store(&x[2 * k / V].v[2 * k % V], v.x);
+    Storage<T>::store(&x[(2 * k + 1) / V].v[(2 * k + 1) % V], v.y);
+}
+
+// Backward: G warps walk the rows of a share, and keep their channels' sums in
+// registers.  The arithmetic is on pairs of elements (f32x2): the instructions an
+// element bound it next to the bytes.
 template <typename T, int V, int J, bool LAYER, bool F8>
 __global__ void __launch_bounds__(512)
 k_sandwich_bwd_rows(Args a, int G) {
-    constexpr int N = V * J;
+    constexpr int N = V * J, H = N / 2;
     using TF = typename std::conditional<F8, int8_t, T>::type;
     // three rounds of sums a row: the means; the squared deviations, sum d and
     // sum d N; sum e and sum e M
@@ -189,176 +210,202 @@ k_sandwich_bwd_rows(Args a, int G) {
     extern __shared__ float4 sm[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
     const int c0 = ((w % G) * 32 + lane) * V, cs = G * 32 * V;
-    const auto have = [&](int i) { return c0 + i / V * cs < a.channels; };
-    const bool block = F8 || a.f != nullptr;
+    const bool block = F8 || a.f != nullptr, full = block && a.gate_kind == FNO_GATE_FULL;
+    const bool has_du = a.du != nullptr, has_dy = a.dy != nullptr;
     const float inv = 1.0f / (float)a.channels;
     const int64_t groups = (a.channels + kGroup - 1) / kGroup;
-    float acc[kSums][N] = {};
+    bool have[J];
+    float one[J];                // 1 for a run within the row, else 0
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        have[j] = c0 + j * cs < a.channels;
+        one[j] = have[j] ? 1.0f : 0.0f;
+    }
+    const auto ones = [&](int k) { return make_float2(one[2 * k / V], one[(2 * k + 1) / V]); };
+    float2 acc[kSums][H] = {};
     for (int64_t t = (int64_t)blockIdx.x * R; t < a.seg_points; t += (int64_t)gridDim.x * R) {
         const bool on = t + w / G < a.seg_points;
-        const int64_t row = blockIdx.y * a.seg_points + t + w / G, base = row * a.channels;
-        Pack<T, V> ys[J] = {}, us[J] = {}, gs[J] = {}, gates[J] = {};
+        const int64_t row = blockIdx.y * a.seg_points + t + w / G, base = row * a.channels + c0;
+        Pack<T, V> ys[J] = {}, us[J] = {}, gs[J] = {}, gates[J] = {}, out[J], out2[J];
         Pack<TF, V> fs[J] = {};
-        float fsc[F8 ? J : 1] = {};
+        float fsc[J] = {};
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            if (!on || !have(j * V)) continue;
-            const int64_t e = base + c0 + j * cs;
-            if (a.du) {
+            if (!on || !have[j]) continue;
+            const int64_t e = base + j * cs;
+            if (has_du) {
                 ys[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.x) + e);
                 us[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.du) + e);
             }
-            if (a.dy) gs[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.dy) + e);
+            if (has_dy)
+                gs[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.dy) + e);
             if (F8) {
                 fs[j] = *reinterpret_cast<const Pack<TF, V> *>(a.f8 + e);
                 fsc[j] = a.f8_scale[row * groups + (c0 + j * cs) / kGroup];
             } else if (block) {
                 fs[j] = *reinterpret_cast<const Pack<TF, V> *>(static_cast<const TF *>(a.f) + e);
             }
-            if (a.gate_kind == FNO_GATE_FULL && block)
+            if (full)
                 gates[j] =
                     *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.gate) + e);
         }
-        float n1[N], m2[N], dY[N], mean[2] = {}, q[4] = {}, shift1 = 0.0f, shift2 = 0.0f;
+        float mean[2] = {}, q[4] = {}, shift1 = 0.0f, shift2 = 0.0f;
         if (LAYER && on) {
-            if (a.du) shift1 = Storage<T>::load(static_cast<const T *>(a.x) + base);
+            if (has_du) shift1 = Storage<T>::load(static_cast<const T *>(a.x) + base - c0);
             if constexpr (F8) {
-                shift2 = (float)a.f8[base] * a.f8_scale[row * groups];
+                shift2 = (float)a.f8[base - c0] * a.f8_scale[row * groups];
             } else {
-                if (block) shift2 = Storage<T>::load(static_cast<const T *>(a.f) + base);
+                if (block) shift2 = Storage<T>::load(static_cast<const T *>(a.f) + base - c0);
             }
         }
+        float2 n[H], m[H], dY[H];
+        {
+            float2 s1 = f2(0.0f), s2 = s1;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float f;
-            if constexpr (F8) f = (float)fs[i / V].v[i % V] * fsc[i / V];
-            else f = Storage<T>::load(&fs[i / V].v[i % V]);
-            n1[i] = have(i) ? Storage<T>::load(&ys[i / V].v[i % V]) - shift1 : 0.0f;
-            m2[i] = have(i) ? f - shift2 : 0.0f;
-            mean[0] += n1[i];
-            mean[1] += m2[i];
+            for (int k = 0; k < H; ++k) {
+                n[k] = pair_of<T, V, J>(ys, k);
+                if constexpr (F8) m[k] = pair_of<V, J>(fs, fsc, k);
+                else m[k] = pair_of<T, V, J>(fs, k);
+                if (LAYER) {
+                    n[k] = fma2(ones(k), f2(-shift1), n[k]);
+                    m[k] = fma2(ones(k), f2(-shift2), m[k]);
+                    s1 = add2(s1, n[k]);
+                    s2 = add2(s2, m[k]);
+                }
+            }
+            mean[0] = s1.x + s1.y;
+            mean[1] = s2.x + s2.y;
         }
         if (LAYER) {
             row_sum<2>(mean, G, red1);
-            mean[0] *= inv;
-            mean[1] *= inv;
-        } else {
-            mean[0] = mean[1] = 0.0f;
+            mean[0] *= -inv;
+            mean[1] *= -inv;
         }
         // q: sum (y - mean)^2, sum (f - mean)^2, sum d, sum d (y - mean)
+        {
+            Pack<float, V> w1[J] = {};
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            Pack<float, V> w1 = {};
-            if (a.du && have(j * V))
-                w1 = *reinterpret_cast<const Pack<float, V> *>(a.w1 + c0 + j * cs);
+            for (int j = 0; j < J; ++j)
+                if (has_du && have[j])
+                    w1[j] = *reinterpret_cast<const Pack<float, V> *>(a.w1 + c0 + j * cs);
+            float2 q0 = f2(0.0f), q1 = q0, q2 = q0, q3 = q0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int k = j * V + i;
-                n1[k] = have(k) ? n1[k] - mean[0] : 0.0f;
-                m2[k] = have(k) ? m2[k] - mean[1] : 0.0f;
-                dY[k] = weighted(Storage<T>::load(&us[j].v[i]), w1.v[i]);
-                q[0] = fmaf(n1[k], n1[k], q[0]);
-                q[1] = fmaf(m2[k], m2[k], q[1]);
-                q[2] += dY[k];
-                q[3] = fmaf(dY[k], n1[k], q[3]);
+            for (int k = 0; k < H; ++k) {
+                if (LAYER) {
+                    n[k] = fma2(ones(k), f2(mean[0]), n[k]);
+                    m[k] = fma2(ones(k), f2(mean[1]), m[k]);
+                }
+                const float2 u = pair_of<T, V, J>(us, k), wk = pair_of<float, V, J>(w1, k);
+                dY[k] = make_float2(weighted(u.x, wk.x), weighted(u.y, wk.y));
+                q0 = fma2(n[k], n[k], q0);
+                q1 = fma2(m[k], m[k], q1);
+                q2 = add2(q2, dY[k]);
+                q3 = fma2(dY[k], n[k], q3);
             }
+            q[0] = q0.x + q0.y;
+            q[1] = q1.x + q1.y;
+            q[2] = q2.x + q2.y;
+            q[3] = q3.x + q3.y;
         }
         row_sum<4>(q, G, red2);
-        const float r1 = on && a.du ? rsqrtf(fmaf(q[0], inv, a.eps)) : 0.0f;
+        const float r1 = on && has_du ? rsqrtf(fmaf(q[0], inv, a.eps)) : 0.0f;
         const float r2 = on ? rsqrtf(fmaf(q[1], inv, a.eps)) : 0.0f;
-        const float d0 = LAYER ? q[2] * inv : 0.0f, d1 = q[3] * r1 * inv;
+        const float2 d0 = f2(LAYER ? -q[2] * inv : 0.0f), d1 = f2(-q[3] * r1 * inv);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            Pack<T, V> xs;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int k = j * V + i;
-                float g = Storage<T>::load(&gs[j].v[i]);
-                if (a.du) {
-                    const float du = Storage<T>::load(&us[j].v[i]);
-                    n1[k] *= r1;
-                    acc[2][k] = fmaf(du, n1[k], acc[2][k]);
-                    if (LAYER) acc[3][k] += du;
-                    g = fmaf(r1, dY[k] - d0 - n1[k] * d1, g);
-                }
-                dY[k] = have(k) ? g : 0.0f;
-                Storage<T>::store(&xs.v[i], g);
+        for (int k = 0; k < H; ++k) {
+            float2 g = pair_of<T, V, J>(gs, k);
+            if (has_du) {
+                const float2 u = pair_of<T, V, J>(us, k);
+                n[k] = mul2(n[k], f2(r1));
+                acc[2][k] = fma2(u, n[k], acc[2][k]);
+                if (LAYER) acc[3][k] = add2(acc[3][k], u);
+                const float2 d = LAYER ? add2(dY[k], d0) : dY[k];
+                g = fma2(fma2(n[k], d1, d), f2(r1), g);
             }
-            if (on && have(j * V))
-                *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dx) + base + c0 + j * cs) = xs;
+            set_pair<T, V, J>(out, k, g);
+            dY[k] = mul2(g, ones(k));
         }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (on && have[j])
+                *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dx) + base + j * cs) = out[j];
         if (!block) continue;
-        float e[2] = {}, ev[N];
+        // dY becomes e
+        Pack<float, V> s[J] = {}, w2[J] = {}, b2[J] = {}, gf[J] = {};
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int c = c0 + j * cs;
-            Pack<float, V> s = {}, w2 = {}, b2 = {}, gf = {};
-            Pack<T, V> dg;
-            if (have(j * V)) {
-                s = *reinterpret_cast<const Pack<float, V> *>(a.s + c);
-                w2 = *reinterpret_cast<const Pack<float, V> *>(a.w2 + c);
-                if (LAYER) b2 = *reinterpret_cast<const Pack<float, V> *>(a.b2 + c);
-                if (a.gate_kind == FNO_GATE_CHANNEL)
-                    gf = *reinterpret_cast<const Pack<float, V> *>(
-                        static_cast<const float *>(a.gate) + blockIdx.y * a.channels + c);
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int k = j * V + i;
-                m2[k] *= r2;
-                float av = 1.0f;
-                if (a.gate_kind != FNO_GATE_NONE)
-                    av = gate_value(a.gate_kind == FNO_GATE_FULL ? Storage<T>::load(&gates[j].v[i])
-                                                                 : gf.v[i], a.sigmoid);
-                const float ga = a.gate_kind == FNO_GATE_FULL ? dY[k] * av : dY[k];
-                acc[0][k] = fmaf(ga, m2[k], acc[0][k]);
-                if (LAYER) acc[1][k] += ga;
-                const float ts = dY[k] * s.v[i];
-                Storage<T>::store(&dg.v[i], ts * (LAYER ? fmaf(m2[k], w2.v[i], b2.v[i])
-                                                        : m2[k] * w2.v[i]) *
-                                                gate_slope(av, a.sigmoid));
-                ev[k] = weighted(ts * av, w2.v[i]);
-                e[0] += ev[k];
-                e[1] = fmaf(ev[k], m2[k], e[1]);
-            }
-            if (a.dgate && on && have(j * V))
-                *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dgate) + base + c) = dg;
+            if (!have[j]) continue;
+            s[j] = *reinterpret_cast<const Pack<float, V> *>(a.s + c);
+            w2[j] = *reinterpret_cast<const Pack<float, V> *>(a.w2 + c);
+            if (LAYER && full) b2[j] = *reinterpret_cast<const Pack<float, V> *>(a.b2 + c);
+            if (a.gate_kind == FNO_GATE_CHANNEL)
+                gf[j] = *reinterpret_cast<const Pack<float, V> *>(
+                    static_cast<const float *>(a.gate) + blockIdx.y * a.channels + c);
         }
+        float2 e0 = f2(0.0f), e1 = e0;
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            m[k] = mul2(m[k], f2(r2));
+            const float2 w2k = pair_of<float, V, J>(w2, k);
+            float2 ts = mul2(dY[k], pair_of<float, V, J>(s, k));
+            if (full) {
+                const float2 gate = pair_of<T, V, J>(gates, k);
+                const float2 av = make_float2(gate_value(gate.x, a.sigmoid),
+                                              gate_value(gate.y, a.sigmoid));
+                const float2 slope = make_float2(gate_slope(av.x, a.sigmoid),
+                                                 gate_slope(av.y, a.sigmoid));
+                const float2 z = LAYER ? fma2(m[k], w2k, pair_of<float, V, J>(b2, k))
+                                       : mul2(m[k], w2k);
+                set_pair<T, V, J>(out2, k, mul2(mul2(ts, z), slope));
+                ts = mul2(ts, av);
+                dY[k] = mul2(dY[k], av);
+            } else if (a.gate_kind == FNO_GATE_CHANNEL) {
+                const float2 gate = pair_of<float, V, J>(gf, k);
+                ts = mul2(ts, make_float2(gate_value(gate.x, a.sigmoid),
+                                          gate_value(gate.y, a.sigmoid)));
+            }
+            acc[0][k] = fma2(dY[k], m[k], acc[0][k]);
+            if (LAYER) acc[1][k] = add2(acc[1][k], dY[k]);
+            dY[k] = make_float2(weighted(ts.x, w2k.x), weighted(ts.y, w2k.y));
+            e0 = add2(e0, dY[k]);
+            e1 = fma2(dY[k], m[k], e1);
+        }
+        float e[2] = {e0.x + e0.y, e1.x + e1.y};
         row_sum<2>(e, G, red3);
-        e[0] = LAYER ? e[0] * inv : 0.0f;
-        e[1] *= inv;
+        e0 = f2(LAYER ? -e[0] * inv : 0.0f);
+        e1 = f2(-e[1] * inv);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            const float2 d = LAYER ? add2(dY[k], e0) : dY[k];
+            set_pair<T, V, J>(out, k, mul2(fma2(m[k], e1, d), f2(r2)));
+        }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            if (!on || !have(j * V)) continue;
-            Pack<T, V> out;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int k = j * V + i;
-                Storage<T>::store(&out.v[i], r2 * (ev[k] - e[0] - m2[k] * e[1]));
-            }
-            *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.df) + base + c0 + j * cs) = out;
+            if (!on || !have[j]) continue;
+            *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.df) + base + j * cs) = out[j];
+            if (a.dgate)
+                *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dgate) + base + j * cs) =
+                    out2[j];
         }
     }
     // the CTA's rows joined in order, one of the four sums at a time
     float *join = reinterpret_cast<float *>(sm);        // [R][channels]
-    float *out = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kSums * a.channels;
+    float *part = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kSums * a.channels;
 #pragma unroll
     for (int q = 0; q < kSums; ++q) {
+        float *to = R > 1 ? join + (w / G) * a.channels : part + q * a.channels;
+        if (R > 1) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (have[i / V]) to[c0 + i / V * cs + i % V] = i % 2 ? acc[q][i / 2].y : acc[q][i / 2].x;
         if (R > 1) {
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (have(i)) join[(w / G) * a.channels + c0 + i / V * cs + i % V] = acc[q][i];
-            __syncthreads();
             for (int c = threadIdx.x; c < a.channels; c += blockDim.x) {
-                float t = 0.0f;
-                for (int k = 0; k < R; ++k) t += join[k * a.channels + c];
-                out[q * a.channels + c] = t;
+                float v = 0.0f;
+                for (int k = 0; k < R; ++k) v += join[k * a.channels + c];
+                part[q * a.channels + c] = v;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (have(i)) out[q * a.channels + c0 + i / V * cs + i % V] = acc[q][i];
         }
     }
 }
