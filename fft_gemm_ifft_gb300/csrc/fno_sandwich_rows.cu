@@ -24,16 +24,27 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int G, float (*buf)[kMaxW
 #pragma unroll
         for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
     if (G == 1) return;
-    const int w = threadIdx.x >> 5;
+    const int w = threadIdx.x >> 5, w0 = w & -G;           // (G is a power of two)
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
         for (int k = 0; k < N; ++k) buf[k][w] = v[k];
     __syncthreads();
+    if (G == 2) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        v[k] = 0.0f;
-        for (int i = 0; i < G; ++i) v[k] += buf[k][w / G * G + i];
+        for (int k = 0; k < N; ++k) {
+            const float2 x = *reinterpret_cast<const float2 *>(&buf[k][w0]);
+            v[k] = x.x + x.y;
+        }
+        return;
     }
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = 0.0f;
+    for (int i = 0; i < G; i += 4)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(&buf[k][w0 + i]);
+            v[k] += (x.x + x.y) + (x.z + x.w);
+        }
 }
 
 // mean and r of a row whose values less the shift are x[.]; entries beyond the
@@ -65,7 +76,7 @@ template <typename T, int V, int J, bool LAYER>
 __global__ void __launch_bounds__(512)
 k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
     constexpr int N = V * J;
-    __shared__ float red[4][1][kMaxWarps];
+    __shared__ alignas(16) float red[4][1][kMaxWarps];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
     const int64_t rows = a.batch * a.points;
     const int64_t row = (int64_t)blockIdx.x * R + w / G;
@@ -206,7 +217,7 @@ k_sandwich_bwd_rows(Args a, int G) {
     using TF = typename std::conditional<F8, int8_t, T>::type;
     // three rounds of sums a row: the means; the squared deviations, sum d and
     // sum d N; sum e and sum e M
-    __shared__ float red1[2][kMaxWarps], red2[4][kMaxWarps], red3[2][kMaxWarps];
+    __shared__ alignas(16) float red1[2][kMaxWarps], red2[4][kMaxWarps], red3[2][kMaxWarps];
     extern __shared__ float4 sm[];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
     const int c0 = ((w % G) * 32 + lane) * V, cs = G * 32 * V;
@@ -223,15 +234,101 @@ k_sandwich_bwd_rows(Args a, int G) {
     }
     const auto ones = [&](int k) { return make_float2(one[2 * k / V], one[(2 * k + 1) / V]); };
     float2 acc[kSums][H] = {};
-    for (int64_t t = (int64_t)blockIdx.x * R; t < a.seg_points; t += (int64_t)gridDim.x * R) {
+    // The next row's vectors are on their way over the work on this one: each
+    // thread copies its own into its own slots of shared memory (two rows' worth),
+    // which takes no registers and no barrier.
+    constexpr bool AHEAD = V > 1;
+    constexpr int kFields = F8 ? 4 : 5;                    // y, du, dy, gate, (f)
+    char *slots = reinterpret_cast<char *>(sm) + (size_t)(R > 1 ? R : 0) * a.channels * 4 +
+                  threadIdx.x * 16;
+    const int slot = blockDim.x * 16, stage = (kFields * J + (F8 ? 1 : 0)) * slot;
+    const int64_t hop = (int64_t)gridDim.x * R;
+    // the next row's channel 0, as stored (a conversion would wait for the load)
+    T next1 = T(0.0f);
+    TF next2 = TF(0);
+    float next_scale = 0.0f;
+    const auto ahead = [&](int64_t t, int k) {
+        const int64_t row = blockIdx.y * a.seg_points + t + w / G, base = row * a.channels + c0;
+        if (t + w / G < a.seg_points) {
+            char *at = slots + k * stage;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!have[j]) continue;
+                const int64_t e = base + j * cs;
+                const auto fetch = [&](int f, const void *src) {
+                    cp_async16(smem_u32(at + (f * J + j) * slot),
+                               static_cast<const T *>(src) + e);
+                };
+                if (has_du) {
+                    fetch(0, a.x);
+                    fetch(1, a.du);
+                }
+                if (has_dy) fetch(2, a.dy);
+                if (full) fetch(3, a.gate);
+                if (F8) {
+                    // codes at the front of the slots of J runs, their scales behind
+                    const uint32_t to = smem_u32(at + kFields * J * slot + j * 8);
+                    if (V == 8) cp_async8(to, a.f8 + e);
+                    else cp_async4(to, a.f8 + e);
+                } else if (block) {
+                    fetch(4, a.f);
+                }
+            }
+            if (LAYER) {
+                if (has_du) next1 = static_cast<const T *>(a.x)[base - c0];
+                if (F8) {
+                    next2 = static_cast<const TF *>(static_cast<const void *>(a.f8))[base - c0];
+                    next_scale = a.f8_scale[row * groups];
+                } else if (block) {
+                    next2 = static_cast<const TF *>(a.f)[base - c0];
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    int k = 0;
+    if (AHEAD) ahead((int64_t)blockIdx.x * R, 0);
+    for (int64_t t = (int64_t)blockIdx.x * R; t < a.seg_points; t += hop, k ^= 1) {
         const bool on = t + w / G < a.seg_points;
         const int64_t row = blockIdx.y * a.seg_points + t + w / G, base = row * a.channels + c0;
         Pack<T, V> ys[J] = {}, us[J] = {}, gs[J] = {}, gates[J] = {}, out[J], out2[J];
         Pack<TF, V> fs[J] = {};
         float fsc[J] = {};
+        float mean[2] = {}, q[4] = {}, shift1 = 0.0f, shift2 = 0.0f;
+        if (AHEAD) {
+            if (LAYER) {
+                shift1 = Storage<T>::load(&next1);
+                if constexpr (F8) shift2 = (float)next2 * next_scale;
+                else shift2 = Storage<T>::load(&next2);
+            }
+            if (F8)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (on && have[j]) fsc[j] = a.f8_scale[row * groups + (c0 + j * cs) / kGroup];
+            ahead(t + hop, k ^ 1);
+            cp_async_wait<1>();
+            const char *at = slots + k * stage;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!on || !have[j]) continue;
+                const auto get = [&](int f) {
+                    return *reinterpret_cast<const Pack<T, V> *>(at + (f * J + j) * slot);
+                };
+                if (has_du) {
+                    ys[j] = get(0);
+                    us[j] = get(1);
+                }
+                if (has_dy) gs[j] = get(2);
+                if (full) gates[j] = get(3);
+                if constexpr (F8)
+                    fs[j] = *reinterpret_cast<const Pack<TF, V> *>(at + kFields * J * slot + j * 8);
+                else if (block)
+                    fs[j] = get(4);
+            }
+        }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            if (!on || !have[j]) continue;
+            if (AHEAD || !on || !have[j]) continue;
             const int64_t e = base + j * cs;
             if (has_du) {
                 ys[j] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.x) + e);
@@ -249,8 +346,8 @@ k_sandwich_bwd_rows(Args a, int G) {
                 gates[j] =
                     *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.gate) + e);
         }
-        float mean[2] = {}, q[4] = {}, shift1 = 0.0f, shift2 = 0.0f;
-        if (LAYER && on) {
+        if (!on) shift1 = shift2 = 0.0f;
+        if (!AHEAD && LAYER && on) {
             if (has_du) shift1 = Storage<T>::load(static_cast<const T *>(a.x) + base - c0);
             if constexpr (F8) {
                 shift2 = (float)a.f8[base - c0] * a.f8_scale[row * groups];
@@ -434,10 +531,12 @@ void with_kernel(const fno_sandwich_s &p, bool f8, F &&f) {
         else f(k_sandwich_bwd_rows<T, V, J, decltype(layer)::value, false>);
     });
 }
-// the rows' sums joined in shared memory
+// the rows' sums joined in shared memory, and two rows' vectors (as many as the
+// float32 codes' case takes: y, du, dy, gate, f)
 size_t smem_of(const fno_sandwich_s &p) {
     const int rows = p.bwd.warps / p.bwd.group;
-    return rows > 1 ? (size_t)rows * p.d.channels * 4 : 0;
+    const size_t join = rows > 1 ? (size_t)rows * p.d.channels * 4 : 0;
+    return join + (p.bwd.vec > 1 ? (size_t)2 * 5 * p.bwd.per * p.bwd.warps * 32 * 16 : 0);
 }
 
 }  // namespace
@@ -480,11 +579,17 @@ fno_status_t rows_shares(const fno_sandwich_s &p, int *ctas, int64_t *most) {
 }
 
 fno_status_t rows_backward(const fno_sandwich_s &p, const Args &a, cudaStream_t s) {
+    fno_status_t st = FNO_OK;
     with_kernel(p, a.f8 != nullptr, [&](auto k) {
+        if (raise_smem_limit(k, smem_of(p)) != cudaSuccess) {
+            st = FNO_ERR_CUDA;
+            return;
+        }
         k<<<dim3((unsigned)p.splits, (unsigned)p.segs), p.bwd.warps * 32, smem_of(p), s>>>(
             a, p.bwd.group);
+        st = launched();
     });
-    return launched();
+    return st;
 }
 
 }  // namespace sandwich
