@@ -94,6 +94,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float2 bf16_pair(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
+// the next bfloat16 term of a pair, which keeps what it leaves (unless it is the last)
+__device__ __forceinline__ uint32_t take_term(float2 &v, bool rest) {
+    const uint32_t u = pack_bf16(v.x, v.y);
+    if (rest) v = sub2(v, bf16_pair(u));
+    return u;
+}
 __device__ __forceinline__ void half_sync(int which) {       // the 256 threads of a half
     asm volatile("bar.sync %0, 256;" ::"r"(1 + which) : "memory");
 }
@@ -104,33 +110,41 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
 
 // An output row on its way out: 16 bytes more than it has, against bank conflicts.
 template <typename TO, int D> constexpr uint32_t kStageRow = D * sizeof(TO) + 16;
+template <typename T> constexpr int kTerms = std::is_same<T, float>::value ? 3
+                                             : std::is_same<T, __half>::value ? 2 : 1;
 // bytes of W, whose place also takes the output tile
 template <typename TO, int D, bool O, int KT>
 constexpr uint32_t w_bytes() {
     const uint32_t w = KT * (D / 64) * kPanel, stage = (kT * kStageRow<TO, D> + 1023) / 1024 * 1024;
     return O && stage > w ? stage : w;
 }
-// bytes of the operands (K, V and Q, or two of K and V): W first, so that what an MMA of 128 rows reads past a
+// bytes of the operands (K, V and Q, or K and V, twice where they fit): W first, so that what an MMA of 128 rows reads past a
 // 64-row panel of it lies within them
-template <typename TO, int D, bool O, int KT>
+template <typename T, typename TO, int D, bool O, int KT>
 constexpr uint32_t operand_bytes() {
-    return w_bytes<TO, D, O, KT>() + (D / 64) * kPanel * (O ? 3 : 4) +
-           (O ? (D / 64) * D * 128 : 0);
+    return w_bytes<TO, D, O, KT>() +
+           kTerms<T> * (D / 64) * (kPanel * (O ? 3 : kTerms<T> == 1 ? 4 : 2) + (O ? D * 128 : 0));
 }
 
 // O: outputs (else only the segment's local state); KT: terms of W.
-template <typename TO, int D, bool REV, bool O, int KT>
-__global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn_tc(TcArgs ca) {
-    using T = __nv_bfloat16;
-    constexpr uint32_t kKV = 2 * (D / 64) * kPanel;
-    constexpr int NP = D / 64, DH = D / 2, NB = D == 64 && O ? 2 : 4;
-    constexpr uint32_t kW = 0, kK = w_bytes<TO, D, O, KT>(), kV = kK + NP * kPanel, kQ = kV + NP * kPanel,
-                       kZ = kQ + NP * kPanel;
-    // tensor memory: S / P, the output, Q Z (the 64-wide one in the half of S that
-    // P leaves free), W^T K
-    constexpr uint32_t cS = 0, cO = 128, cQZ = D == 128 ? 256 : 64,
-                       cD = !O ? 0 : D == 128 ? 384 : 192;
-    constexpr uint32_t kCols = !O ? D : D == 128 ? 512 : 256;
+template <typename T, typename TO, int D, bool REV, bool O, int KT>
+__global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O && kTerms<T> == 1 ? 2 : 1)
+k_linattn_tc(TcArgs ca) {
+    constexpr int NT = kTerms<T>, NP = D / 64, DH = D / 2, NB = NT > 1 ? 1 : D == 64 && O ? 2 : 4;
+    static_assert(NT == 1 || D == 64, "the terms of 128 columns do not fit");
+    constexpr uint32_t kPlane = NP * kPanel, kOp = NT * kPlane, kZPlane = NP * D * 128;
+    constexpr bool TWICE = !O && NT == 1;                  // two of K and V
+    constexpr uint32_t kKV = 2 * kOp;
+    constexpr uint32_t kW = 0, kK = w_bytes<TO, D, O, KT>(), kV = kK + kOp, kQ = kV + kOp,
+                       kZ = kQ + kOp;
+    // tensor memory: S / P, the output, Q Z, W^T K.  The 64-wide Q Z of one term
+    // has the half of S that P leaves free, and is made when S has been read; the
+    // other terms of P lie behind S
+    constexpr bool EARLY = D == 128 || NT > 1;             // Q Z has columns of its own
+    constexpr uint32_t cS = 0, cP = 128, cO = NT > 1 ? 256 : 128,
+                       cQZ = NT > 1 ? 320 : D == 128 ? 256 : 64,
+                       cD = !O ? 0 : EARLY ? 384 : 192;
+    constexpr uint32_t kCols = !O ? D : EARLY ? 512 : 256;
     extern __shared__ char smem_raw[];
     char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                           ~static_cast<uintptr_t>(1023));
@@ -189,23 +203,60 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                       (REV ? n - 1 - t : t) * stride + pc * 8;
         return Source{at, (REV ? -RS : RS) * stride, (REV ? -kT : kT) * stride, pc * 8 < w};
     };
-    const auto load = [&](uint32_t dst, Source &x, int64_t t0) {
+    // One-term rows are copied asynchronously.  Rows of more terms come into
+    // registers (`fetch`), early, and are split into their planes (`put`) when the
+    // last chunk's are no longer read.
+    struct Rows {
+        Pack<T, 8> x[NT == 1 ? 1 : kT / RS];
+    };
+    const auto fetch = [&](uint32_t dst, Source &x, int64_t t0, Rows &to) {
         const int m = (int)min((int64_t)kT, last - t0) - r0;
         const T *at = x.at;
 #pragma unroll
         for (int i = 0; i < kT / RS; ++i, at += x.row) {
             const bool have = x.have && i * RS < m;
-            cp_async16_or_zero(sb + dst + piece + i * RS * 128, have ? at : p.q, have);
+            if constexpr (NT == 1) {
+                cp_async16_or_zero(sb + dst + piece + i * RS * 128, have ? at : p.q, have);
+            } else {
+                to.x[i] = Pack<T, 8>{};
+                if (have) to.x[i] = *reinterpret_cast<const Pack<T, 8> *>(at);
+            }
         }
         x.at += x.chunk;
     };
+    const auto put = [&](uint32_t dst, const Rows &from) {
+        if constexpr (NT > 1) {
+#pragma unroll
+            for (int i = 0; i < kT / RS; ++i) {
+                float2 f[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    f[j] = make_float2(Storage<T>::load(&from.x[i].v[2 * j]),
+                                       Storage<T>::load(&from.x[i].v[2 * j + 1]));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = take_term(f[j], t + 1 < NT);
+                    *reinterpret_cast<uint4 *>(base + dst + t * kPlane + piece + i * RS * 128) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+        }
+    };
     Source q = source(p.q, nq, p.gq, p.dk), k = source(p.k, nk, p.gk, p.dk),
            v = source(p.v, nv, p.gv, p.dv);
+    Rows rq, rk, rv;
     if (first < last) {
-        if (O && half == 0) load(kQ, q, first);
+        if (O && half == 0) {
+            fetch(kQ, q, first, rq);
+            put(kQ, rq);
+        }
         if (half == 1) {
-            load(kK, k, first);
-            load(kV, v, first);
+            fetch(kK, k, first, rk);
+            fetch(kV, v, first, rv);
+            put(kK, rk);
+            put(kV, rv);
         }
     }
     // all threads, once a chunk: the operands are there
@@ -262,18 +313,23 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                         z[a + 3] = fmaf(z[a + 3], whole, x.w);
                     }
         }
-        // its bfloat16 copy, the right operand of Q Z
+        // its bfloat16 terms, the right operands of Q Z
         const auto publish = [&]() {
 #pragma unroll
             for (int c = 0; c < DH / 8; ++c) {
-                uint4 u;
-                u.x = pack_bf16(z[8 * c], z[8 * c + 1]);
-                u.y = pack_bf16(z[8 * c + 2], z[8 * c + 3]);
-                u.z = pack_bf16(z[8 * c + 4], z[8 * c + 5]);
-                u.w = pack_bf16(z[8 * c + 6], z[8 * c + 7]);
+                float2 f[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = make_float2(z[8 * c + 2 * j], z[8 * c + 2 * j + 1]);
                 const int at = a0 / 8 + c;
-                *reinterpret_cast<uint4 *>(base + kZ + (at >> 3) * (D * 128) +
-                                           sw_off16(row, (at & 7) * 8)) = u;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = take_term(f[j], t + 1 < NT);
+                    *reinterpret_cast<uint4 *>(base + kZ + t * kZPlane + (at >> 3) * (D * 128) +
+                                               sw_off16(row, (at & 7) * 8)) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
+                }
             }
         };
         if (mine && has_state) publish();
@@ -282,41 +338,47 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             const int m = (int)min((int64_t)kT, last - t0);
             const bool more = t0 + kT < last;
             meet();
-            // without outputs there is room for the next chunk's K and V
-            const uint32_t at_kv = O ? 0 : (chunk & 1) * kKV;
-            if (!O && more) {
-                load(kK + (kKV - at_kv), k, t0 + kT);
-                load(kV + (kKV - at_kv), v, t0 + kT);
+            // (one term without outputs: there is room for the next chunk's K and V)
+            const uint32_t at_kv = TWICE ? (chunk & 1) * kKV : 0;
+            if (TWICE && more) {
+                fetch(kK + (kKV - at_kv), k, t0 + kT, rk);
+                fetch(kV + (kKV - at_kv), v, t0 + kT, rv);
             }
             // W: half of a token row a thread, NB pieces read before the first of their
             // terms is written
             const float2 f = f2(pw[max(0, m - 1 - row + REV)] * p.scale_k);
 #pragma unroll
             for (int i0 = 0; i0 < DH / 8; i0 += NB) {
-                uint4 u[NB];
+                uint4 u[NB][NT];
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int c = a0 / 8 + i0 + i;
-                    u[i] = *reinterpret_cast<uint4 *>(base + kV + at_kv + (c >> 3) * kPanel +
-                                                      sw_off16(row, (c & 7) * 8));
-                }
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const int c = a0 / 8 + i0 + i;
+                        u[i][t] = *reinterpret_cast<uint4 *>(base + kV + at_kv + t * kPlane +
+                                                             (c >> 3) * kPanel +
+                                                             sw_off16(row, (c & 7) * 8));
+                    }
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     const int c = a0 / 8 + i0 + i;
                     char *at = base + kW + (c >> 3) * kPanel + sw_off16(row, (c & 7) * 8);
-                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                    float2 x[4];
+                    float2 x[4] = {};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = mul2(bf16_pair(w[j]), f);
+                    for (int t = NT - 1; t >= 0; --t) {
+                        const uint32_t w[4] = {u[i][t].x, u[i][t].y, u[i][t].z, u[i][t].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[j] = t == NT - 1 ? bf16_pair(w[j]) : add2(x[j], bf16_pair(w[j]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], f);
 #pragma unroll
                     for (int t = 0; t < KT; ++t) {
                         uint32_t y[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            y[j] = pack_bf16(x[j].x, x[j].y);
-                            if (t + 1 < KT) x[j] = sub2(x[j], bf16_pair(y[j]));
-                        }
-                        *reinterpret_cast<uint4 *>(at + t * NP * kPanel) =
+                        for (int j = 0; j < 4; ++j) y[j] = take_term(x[j], t + 1 < KT);
+                        *reinterpret_cast<uint4 *>(at + t * kPlane) =
                             make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
@@ -325,22 +387,36 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             half_sync(1);
             if (warp == (O ? 8 : 0) && elect_one()) {
                 const uint32_t id = idesc_f16(D, true) | kAcrossA | kAcrossB;
-                for (int t = KT - 1; t >= 0; --t)          // the small terms first
+                bool add = false;
 #pragma unroll
-                    for (int i = 0; i < kT / 16; ++i)
-                        mma_f16(tmem + cD,
-                                desc_across(sb + kW + t * NP * kPanel + i * 2048, kPanel),
-                                desc_across(sb + kK + at_kv + i * 2048, kPanel), id,
-                                t < KT - 1 || i > 0);
+                for (int sum = KT - 1; sum >= 0; --sum)    // the small products first
+#pragma unroll
+                    for (int t = 0; t <= sum; ++t) {
+                        if (sum - t >= NT) continue;
+#pragma unroll
+                        for (int i = 0; i < kT / 16; ++i) {
+                            mma_f16(tmem + cD,
+                                    desc_across(sb + kW + t * kPlane + i * 2048, kPanel),
+                                    desc_across(sb + kK + at_kv + (sum - t) * kPlane + i * 2048,
+                                                kPanel), id, add);
+                            add = true;
+                        }
+                    }
                 mma_commit(&bar_d);
+            }
+            if (NT > 1 && more) {                          // on their way over the MMAs
+                fetch(kK, k, t0 + kT, rk);
+                fetch(kV, v, t0 + kT, rv);
             }
             mbar_wait(&bar_d, chunk, ca.err);
             if (O) mbar_wait(&bar_s, chunk, ca.err);
             tc_after_sync();
-            if (O) {
-                if (more) load(kK, k, t0 + kT);
-                mbar_wait(&bar_o, chunk, ca.err);          // V and the state's copy were read
-                if (more) load(kV, v, t0 + kT);
+            if (!TWICE) {
+                if (NT == 1 && more) fetch(kK, k, t0 + kT, rk);
+                if (more) put(kK, rk);
+                if (O) mbar_wait(&bar_o, chunk, ca.err);   // V and the state's copy were read
+                if (NT == 1 && more) fetch(kV, v, t0 + kT, rv);
+                if (more) put(kV, rv);
                 tc_after_sync();
             }
             const float carry = pw[m];
@@ -367,10 +443,19 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
     if (O && half == 0) {
         const auto mma_qz = [&]() {
             const uint32_t id = idesc_f16(D, true);
+            bool add = false;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                mma_f16(tmem + cQZ, desc_sw128(sb + kQ + (i >> 2) * kPanel + (i & 3) * 32),
-                        desc_sw128(sb + kZ + (i >> 2) * (D * 128) + (i & 3) * 32), id, i > 0);
+            for (int sum = NT - 1; sum >= 0; --sum)        // the small products first
+#pragma unroll
+                for (int x = 0; x <= sum; ++x)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        mma_f16(tmem + cQZ,
+                                desc_sw128(sb + kQ + x * kPlane + (i >> 2) * kPanel + (i & 3) * 32),
+                                desc_sw128(sb + kZ + (sum - x) * kZPlane + (i >> 2) * (D * 128) +
+                                           (i & 3) * 32), id, add);
+                        add = true;
+                    }
         };
         const int diag = (warp & 3) * 32, a0 = sub * DH;
         const float fz = pw[row + !REV] * p.scale_o;
@@ -381,14 +466,20 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             meet();
             if (warp == 0 && elect_one()) {
                 const uint32_t id = idesc_f16(kT, true);
+                bool add = false;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t at = (i >> 2) * kPanel + (i & 3) * 32;
-                    mma_f16(tmem + cS, desc_sw128(sb + kQ + at), desc_sw128(sb + kK + at), id,
-                            i > 0);
-                }
+                for (int sum = NT - 1; sum >= 0; --sum)
+#pragma unroll
+                    for (int x = 0; x <= sum; ++x)
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t at = (i >> 2) * kPanel + (i & 3) * 32;
+                            mma_f16(tmem + cS, desc_sw128(sb + kQ + x * kPlane + at),
+                                    desc_sw128(sb + kK + (sum - x) * kPlane + at), id, add);
+                            add = true;
+                        }
                 mma_commit(&bar_s);
-                if (D == 128 && !zero) mma_qz();           // (completes with P V)
+                if (EARLY && !zero) mma_qz();              // (completes with P V)
             }
             mbar_wait(&bar_s, chunk, ca.err);
             tc_after_sync();
@@ -399,11 +490,11 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             for (int i = 0; i < 2; ++i) {
                 const int c = (2 * i + sub) * 32;
                 uint32_t y[16];
+                float x[32];
                 if (c > diag) {                            // above the diagonal
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = 0;
+                    for (int j = 0; j < 32; ++j) x[j] = 0.0f;
                 } else {
-                    float x[32];
                     tmem_ld32(tmem + cS + c + lanes, x);
                     if (c == diag) {
                         // (the factor read whatever the condition: read under it, each
@@ -428,11 +519,19 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                             x[j + 3] = hi.y;
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
                 }
-                if (i == 0) half_sync(0);
-                tmem_st16u(tmem + cS + c / 2 + lanes, y);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float2 v = make_float2(x[2 * j], x[2 * j + 1]);
+                        y[j] = take_term(v, t + 1 < NT);
+                        x[2 * j] = v.x;
+                        x[2 * j + 1] = v.y;
+                    }
+                    if (i == 0 && t == 0) half_sync(0);
+                    tmem_st16u(tmem + (t ? cP + 64 * (t - 1) : cS) + c / 2 + lanes, y);
+                }
             }
             tmem_st_wait();
             tc_before_sync();
@@ -440,17 +539,27 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
             if (warp == 0 && elect_one()) {
                 tc_after_sync();
                 const uint32_t id = idesc_f16(D, true) | kAcrossB;
-                if (D == 64 && !zero) mma_qz();
+                if (!EARLY && !zero) mma_qz();
+                bool add = false;
 #pragma unroll
-                for (int i = 0; i < kT / 16; ++i)
-                    mma_f16_ts(tmem + cO, tmem + cS + i * 8,
-                               desc_across(sb + kV + i * 2048, kPanel), id, i > 0);
+                for (int sum = NT - 1; sum >= 0; --sum)
+#pragma unroll
+                    for (int t = 0; t <= sum; ++t)
+#pragma unroll
+                        for (int i = 0; i < kT / 16; ++i) {
+                            mma_f16_ts(tmem + cO, tmem + (t ? cP + 64 * (t - 1) : cS) + i * 8,
+                                       desc_across(sb + kV + (sum - t) * kPlane + i * 2048, kPanel),
+                                       id, add);
+                            add = true;
+                        }
                 mma_commit(&bar_o);
             }
+            if (NT > 1 && t0 + kT < last) fetch(kQ, q, t0 + kT, rq);
             mbar_wait(&bar_o, chunk, ca.err);
             mbar_wait(&bar_d, chunk, ca.err);
             tc_after_sync();
-            if (t0 + kT < last) load(kQ, q, t0 + kT);
+            if (NT == 1 && t0 + kT < last) fetch(kQ, q, t0 + kT, rq);
+            if (t0 + kT < last) put(kQ, rq);
             // the tile by way of W's place (W was read): a thread's own 16-byte stores
             // would each touch 32 rows
             char *stage = base + row * kStageRow<TO, D>;
@@ -507,7 +616,7 @@ __global__ void __launch_bounds__(O ? 512 : 256, D == 64 && O ? 2 : 1) k_linattn
                      "r"(kCols));
 }
 
-template <typename TO, int D, bool REV, int KT>
+template <typename T, typename TO, int D, bool REV, int KT>
 fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
     const int64_t bh = p.batch * ca.s.heads;
     const auto go = [&](auto kernel, int threads, size_t smem) {
@@ -517,39 +626,47 @@ fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
         return launched();
     };
     if (ca.segments > 1 && !ca.s.states_t) {
-        fno_status_t st = go(k_linattn_tc<__nv_bfloat16, D, REV, false, KT>, 256,
-                             operand_bytes<__nv_bfloat16, D, false, KT>());
+        fno_status_t st = go(k_linattn_tc<T, T, D, REV, false, KT>, 256,
+                             operand_bytes<T, T, D, false, KT>());
         if (st == FNO_OK && ca.segments > kFold) st = segment_states(p, ca.s, ca.states, s);
         if (st != FNO_OK) return st;
     }
-    return go(k_linattn_tc<TO, D, REV, true, KT>, 512, operand_bytes<TO, D, true, KT>());
+    return go(k_linattn_tc<T, TO, D, REV, true, KT>, 512, operand_bytes<T, TO, D, true, KT>());
+}
+
+template <typename T, int D, int KT>
+fno_status_t directions(const fno_linattn_s &p, const TcArgs &ca, bool rev, bool wide_out,
+                        cudaStream_t s) {
+    if (!rev) return run<T, T, D, false, KT>(p, ca, s);
+    if (wide_out) return run<T, float, D, true, KT>(p, ca, s);
+    return run<T, T, D, true, KT>(p, ca, s);
 }
 
 }  // namespace
 
+// Rows of whole 16-byte pieces; bfloat16 up to 128 columns, float32 and fp16, whose
+// terms take three and two times the room, up to 64.
 bool tc_applies(const fno_linattn_s &p) {
-    return p.dtype == FNO_BF16 && p.dk <= 128 && p.dv <= 128 && p.dk % 8 == 0 && p.dv % 8 == 0;
+    const int most = p.dtype == FNO_BF16 ? 128 : 64;
+    return p.dk <= most && p.dv <= most && p.dk % 8 == 0 && p.dv % 8 == 0;
 }
 
-// CTAs an SM holds (tensor memory and shared memory): two of the 64-wide kernel
-int tc_ctas(const fno_linattn_s &p) { return p.dk <= 64 && p.dv <= 64 ? 2 : 1; }
+// CTAs an SM holds (tensor memory and shared memory): two of the 64-wide bfloat16
+int tc_ctas(const fno_linattn_s &p) {
+    return p.dtype == FNO_BF16 && p.dk <= 64 && p.dv <= 64 ? 2 : 1;
+}
 
 fno_status_t tc_scan(const fno_linattn_s &p, const ScanArgs &a, bool rev, bool wide_out,
                      float *states, float scale_p, cudaStream_t s) {
     const TcArgs ca{a, states, p.segments, p.seg_len, scale_p, p.dev_err};
-    const auto width = [&](auto d) {
-        constexpr int D = decltype(d)::value;
-        const auto terms = [&](auto kt) {
-            constexpr int KT = decltype(kt)::value;
-            if (!rev) return run<__nv_bfloat16, D, false, KT>(p, ca, s);
-            if (wide_out) return run<float, D, true, KT>(p, ca, s);
-            return run<__nv_bfloat16, D, true, KT>(p, ca, s);
-        };
-        return a.sT || a.exact ? terms(std::integral_constant<int, 3>())
-                    : terms(std::integral_constant<int, 2>());
-    };
-    return a.dk <= 64 && a.dv <= 64 ? width(std::integral_constant<int, 64>())
-                                    : width(std::integral_constant<int, 128>());
+    if (p.dtype == FNO_F32) return directions<float, 64, 3>(p, ca, rev, wide_out, s);
+    if (p.dtype == FNO_F16) return directions<__half, 64, 3>(p, ca, rev, wide_out, s);
+    const bool exact = a.sT || a.exact;
+    if (a.dk <= 64 && a.dv <= 64)
+        return exact ? directions<__nv_bfloat16, 64, 3>(p, ca, rev, wide_out, s)
+                     : directions<__nv_bfloat16, 64, 2>(p, ca, rev, wide_out, s);
+    return exact ? directions<__nv_bfloat16, 128, 3>(p, ca, rev, wide_out, s)
+                 : directions<__nv_bfloat16, 128, 2>(p, ca, rev, wide_out, s);
 }
 
 }  // namespace linattn
