@@ -96,7 +96,9 @@ void group_sum(const float *in, T *out, int64_t n, int g, int d, cudaStream_t s)
 
 // One token: a CTA per (row, head).  V value columns a thread (4 where the width
 // allows), the key rows over the threads that are left; eight rows' loads are in
-// flight at a time, for the state read and written once is all that it costs.
+// flight at a time, for the state read and written once is all that it costs: 64 of
+// 96 slots, 16 heads, 64 x 64: 34 MB in 9.4 us, most of it latency; 128 x 128: 26 us,
+// 5.2 TB/s.
 constexpr int kStepThreads = 128;
 
 template <typename T, int V>

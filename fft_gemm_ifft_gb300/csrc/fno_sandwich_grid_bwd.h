@@ -29,6 +29,12 @@ template <typename T> fno_status_t grid_shares_of(const fno_sandwich_s &p, int *
 // digits, because x0's own deviation is part of it.  The warps' means are then
 // joined relative to channel 0 of the point, so that a large mean cancels in
 // exact differences.
+//
+// Measured for 32 x 64 x 256^2 bfloat16 from the 8-bit checkpoint (1.48 GB): 470 us,
+// 3.2 TB/s (float32 5.0 TB/s); with the checks of ragged tiles 784 us, with the
+// fields held in registers and six rounds of sums 1892 us, reading each field for
+// each sum 4225 us.  1400 warp instructions a tile and warp are what is left
+// over the bytes.
 // ---------------------------------------------------------------------------
 constexpr int kTileP = 64, kTileC = 8;
 constexpr int kSmemPerSm = 228 * 1024;
@@ -440,7 +446,9 @@ __device__ __forceinline__ float lanes_sum4(const float (&s)[kSums]) {
 // The same two rounds for any point count and up to kWideC channels, where the
 // channels of a tile do not fit registers: 32 V points a tile (V = 2 for even
 // counts), each round reads the fields again (from L1 or L2), and the channels'
-// sums are kept in shared memory by the warp that owns the channel.
+// sums are kept in shared memory by the warp that owns the channel.  2 x 1023 x
+// 256^2 bfloat16: 0.3 to 0.5 TB/s, where the point-by-point kernels take twice the
+// time; 2 x 512 x 256^2 takes the staged tiles at 0.7 TB/s.
 constexpr int kWideWarps = 16, kWideC = 4096;
 
 template <typename T, bool LAYER, bool F8, int V>

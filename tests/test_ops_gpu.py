@@ -33,6 +33,9 @@ def rand(g, shape, dtype="f32", scale=1.0, mean=0.0):
 SHAPES = [  # batch, points, channels
     (1, 1, 1), (2, 1, 33), (1, 3, 512), (3, 257, 7), (2, 130, 64), (1, 513, 96), (2, 64, 1000),
     (1, 40, 2056), (2, 1024, 128), (5, 9, 4099),
+    # the tiles of half and quarter warps, the tiles read again with an odd point
+    # count, and rows past every kernel that holds them
+    (2, 70, 200), (1, 77, 130), (1, 33, 700), (1, 3, 9000),
 ]
 
 
