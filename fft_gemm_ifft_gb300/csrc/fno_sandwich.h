@@ -12,9 +12,9 @@ namespace sandwich {
 enum { kAny = 0, kTiles = 1, kRows = 2, kStaged = 3, kWide = 4 };
 // vec: elements of a thread's loads, parts of a warp for kStaged; per: a thread's
 // channels (tiles) or runs (rows); warps: of a CTA; group: warps of a row, stages
-// of kStaged.
+// of kStaged; lanes: of a row within one warp.
 struct Way {
-    int kind, vec, per, warps, group;
+    int kind, vec, per, warps, group, lanes;
 };
 }  // namespace sandwich
 }  // namespace fno

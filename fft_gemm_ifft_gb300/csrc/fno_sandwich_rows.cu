@@ -11,55 +11,81 @@ namespace {
 constexpr int kMaxWarps = 16;
 
 // ---------------------------------------------------------------------------
-// Token layout: G warps hold a row in registers, each thread J runs of V
-// consecutive channels; a CTA of R = warps / G rows.
+// Token layout: a row lies in registers, with G whole warps or (SMALL) with 2^k
+// lanes of one; each thread holds J runs of V consecutive channels.
 // ---------------------------------------------------------------------------
-// The sums of N values over the G warps of a row.  `buf` ([N][kMaxWarps]) is this
-// sum's own: a buffer may be used again once another sum came in between, whose
-// barrier every reader of this one has passed.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int G, float (*buf)[kMaxWarps]) {
+template <bool SMALL>
+struct Team {
+    int lanes, warps;        // of a row
+    int row, rows;           // this thread's among the CTA's
+    int member;              // this thread's place in its row
+    int first, slot;         // the row's and this warp's entries of a buffer of sums
+    __device__ __forceinline__ Team(int G, int L) {
+        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        lanes = SMALL ? L : 32;
+        warps = SMALL ? 1 : G;
+        row = SMALL ? (int)threadIdx.x / L : w / G;
+        rows = SMALL ? (int)blockDim.x / L : (int)(blockDim.x >> 5) / G;
+        member = SMALL ? lane & (L - 1) : w % G * 32 + lane;
+        first = w / G * (G > 2 ? (G + 3) & ~3 : G);
+        slot = first + w % G;
+    }
+    // the entries behind a row's last, for its sums' vector reads
+    template <int N> __device__ __forceinline__ void clear(float (*buf)[kMaxWarps]) const {
+        if constexpr (!SMALL)
+            if (warps > 2 && member == 32 * warps - 1)
+                for (int i = slot + 1; i & 3; ++i)
+                    for (int k = 0; k < N; ++k) buf[k][i] = 0.0f;
+    }
+};
+
+// The sums of N values over a row.  `buf` ([N][kMaxWarps]) is this sum's own: a
+// buffer may be used again once another sum came in between, whose barrier every
+// reader of this one has passed.
+template <int N, bool SMALL>
+__device__ __forceinline__ void row_sum(float (&v)[N], const Team<SMALL> &team,
+                                        float (*buf)[kMaxWarps]) {
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+    for (int m = 16; m; m >>= 1)
+        if (!SMALL || m < team.lanes)
 #pragma unroll
-        for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
-    if (G == 1) return;
-    const int w = threadIdx.x >> 5, w0 = w & -G;           // (G is a power of two)
+            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
+    if (SMALL || team.warps == 1) return;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int k = 0; k < N; ++k) buf[k][w] = v[k];
+        for (int k = 0; k < N; ++k) buf[k][team.slot] = v[k];
     __syncthreads();
-    if (G == 2) {
+    if (team.warps == 2) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const float2 x = *reinterpret_cast<const float2 *>(&buf[k][w0]);
+            const float2 x = *reinterpret_cast<const float2 *>(&buf[k][team.first]);
             v[k] = x.x + x.y;
         }
         return;
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = 0.0f;
-    for (int i = 0; i < G; i += 4)
+    for (int i = 0; i < team.warps; i += 4)
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const float4 x = *reinterpret_cast<const float4 *>(&buf[k][w0 + i]);
+            const float4 x = *reinterpret_cast<const float4 *>(&buf[k][team.first + i]);
             v[k] += (x.x + x.y) + (x.z + x.w);
         }
 }
 
 // mean and r of a row whose values less the shift are x[.]; entries beyond the
 // row's channels are excluded by `have`.
-template <int N, bool LAYER, class Have>
+template <int N, bool LAYER, bool SMALL, class Have>
 __device__ __forceinline__ void row_norm(const float (&x)[N], Have &&have, int channels, float eps,
-                                         int G, float (*red)[1][kMaxWarps], float &mean,
-                                         float &r) {
+                                         const Team<SMALL> &team, float (*red)[1][kMaxWarps],
+                                         float &mean, float &r) {
     const float inv = 1.0f / (float)channels;
     mean = 0.0f;
     if (LAYER) {
         float s[1] = {};
 #pragma unroll
         for (int i = 0; i < N; ++i) s[0] += x[i];          // absent entries are 0
-        row_sum<1>(s, G, red[0]);
+        row_sum<1, SMALL>(s, team, red[0]);
         mean = s[0] * inv;
     }
     float q[1] = {};
@@ -68,20 +94,25 @@ __device__ __forceinline__ void row_norm(const float (&x)[N], Have &&have, int c
         const float d = have(i) ? x[i] - mean : 0.0f;
         q[0] = fmaf(d, d, q[0]);
     }
-    row_sum<1>(q, G, red[1]);
+    row_sum<1, SMALL>(q, team, red[1]);
     r = rsqrtf(fmaf(q[0], inv, eps));
 }
 
-template <typename T, int V, int J, bool LAYER>
-__global__ void __launch_bounds__(512)
-k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
+template <typename T, int V, int J, bool LAYER, bool SMALL>
+// (80 registers, three CTAs of 8 warps an SM: 3 x 10922 x 1024 fp16 with a sigmoid gate
+// an element 123 us, with as many as it takes 159)
+__global__ void __maxnreg__(80)
+k_sandwich_fwd_rows(Args a, int G, int L, int8_t *f8, float *f8_scale) {
     constexpr int N = V * J;
     __shared__ alignas(16) float red[4][1][kMaxWarps];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
+    const Team<SMALL> team(G, L);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) team.clear<1>(red[k]);
+    const int lane = threadIdx.x & 31;
     const int64_t rows = a.batch * a.points;
-    const int64_t row = (int64_t)blockIdx.x * R + w / G;
+    const int64_t row = (int64_t)blockIdx.x * team.rows + team.row;
     const bool on = row < rows;
-    const int c0 = ((w % G) * 32 + lane) * V, cs = G * 32 * V;     // run j at c0 + j cs
+    const int c0 = team.member * V, cs = (SMALL ? L : G * 32) * V;                // run j at c0 + j cs
     const int64_t base = row * a.channels;
     const auto have = [&](int i) { return c0 + i / V * cs < a.channels; };
     const bool block = a.f != nullptr;
@@ -102,11 +133,10 @@ k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
                                                               c0 + j * cs);
         if (LAYER && on) shift = Storage<T>::load(static_cast<const T *>(a.f) + base);
         if (f8) {
-            // a group is V L lanes' runs: 32 lanes for V = 4, 16 for 8; for V = 1
-            // four runs of 32 lanes (G = 1 run j, or neighbouring warps): then
-            // the caller packs by itself
-            constexpr int L = V > 1 ? kGroup / V : 32;
-            const uint32_t mask = L == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
+            // a group is 128 / V lanes' runs, which are the row's lanes or fewer
+            // (for V <= 2 the caller packs by itself)
+            constexpr int S = V > 2 ? kGroup / V : 32;
+            const uint32_t mask = S == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 uint32_t m = 0;
@@ -121,7 +151,7 @@ k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
                 if (on && have(j * V)) {
                     const int c = c0 + j * cs;
                     *reinterpret_cast<Pack<int8_t, V> *>(f8 + base + c) = q;
-                    if (lane % L == 0)
+                    if (lane % S == 0)
                         f8_scale[row * ((a.channels + kGroup - 1) / kGroup) + c / kGroup] = s.scale;
                 }
             }
@@ -129,7 +159,7 @@ k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             v[i] = have(i) ? Storage<T>::load(&fs[i / V].v[i % V]) - shift : 0.0f;
-        row_norm<N, LAYER>(v, have, a.channels, a.eps, G, red, mean, r);
+        row_norm<N, LAYER, SMALL>(v, have, a.channels, a.eps, team, red, mean, r);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             if (!on || !have(j * V)) continue;
@@ -165,13 +195,16 @@ k_sandwich_fwd_rows(Args a, int G, int8_t *f8, float *f8_scale) {
     float mean, r;
     if (LAYER) {                 // shift by the row's channel 0
         __shared__ float first[kMaxWarps];
-        if (w % G == 0 && lane == 0) first[w / G] = v[0];
-        __syncthreads();
-        const float shift = first[w / G];
+        float shift = __shfl_sync(0xffffffffu, v[0], SMALL ? lane & -L : 0);
+        if (!SMALL && G > 1) {
+            if (team.member == 0) first[team.row] = shift;
+            __syncthreads();
+            shift = first[team.row];
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = have(i) ? v[i] - shift : 0.0f;
     }
-    row_norm<N, LAYER>(v, have, a.channels, a.eps, G, red + 2, mean, r);
+    row_norm<N, LAYER, SMALL>(v, have, a.channels, a.eps, team, red + 2, mean, r);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         if (!on || !have(j * V)) continue;
@@ -208,19 +241,25 @@ __device__ __forceinline__ void set_pair(Pack<T, V> (&x)[J], int k, float2 v) {
 }
 
 // Backward: G warps walk the rows of a share, and keep their channels' sums in
-// registers.  The arithmetic is on pairs of elements (f32x2): the instructions an
-// element bound it next to the bytes.
-template <typename T, int V, int J, bool LAYER, bool F8>
+// registers.  The arithmetic is on pairs of elements (f32x2).  3 x 4099 x 1024 fp16
+// with a sigmoid gate an element (201 MB): 72 us, of which the three rounds of
+// row sums with their barriers are a third; 106 us with six rounds and the row's
+// loads at its start, 593 us reading each field for each sum.  A row in the lanes that
+// it needs: 3 x 174762 x 64 fp16 131 us, with a warp to a row 484.
+template <typename T, int V, int J, bool LAYER, bool F8, bool SMALL>
 __global__ void __launch_bounds__(512)
-k_sandwich_bwd_rows(Args a, int G) {
+k_sandwich_bwd_rows(Args a, int G, int L) {
     constexpr int N = V * J, H = N / 2;
     using TF = typename std::conditional<F8, int8_t, T>::type;
     // three rounds of sums a row: the means; the squared deviations, sum d and
     // sum d N; sum e and sum e M
     __shared__ alignas(16) float red1[2][kMaxWarps], red2[4][kMaxWarps], red3[2][kMaxWarps];
     extern __shared__ float4 sm[];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, R = (blockDim.x >> 5) / G;
-    const int c0 = ((w % G) * 32 + lane) * V, cs = G * 32 * V;
+    const Team<SMALL> team(G, L);
+    team.clear<2>(red1);
+    team.clear<4>(red2);
+    team.clear<2>(red3);
+    const int R = team.rows, c0 = team.member * V, cs = (SMALL ? L : G * 32) * V;
     const bool block = F8 || a.f != nullptr, full = block && a.gate_kind == FNO_GATE_FULL;
     const bool has_du = a.du != nullptr, has_dy = a.dy != nullptr;
     const float inv = 1.0f / (float)a.channels;
@@ -236,28 +275,34 @@ k_sandwich_bwd_rows(Args a, int G) {
     float2 acc[kSums][H] = {};
     // The next row's vectors are on their way over the work on this one: each
     // thread copies its own into its own slots of shared memory (two rows' worth),
-    // which takes no registers and no barrier.
-    constexpr bool AHEAD = V > 1;
+    // which takes no registers and no barrier.  (Pairs of
+    // fp16 so, 3 x 21592 x 518: 391 us, loaded when they are needed 611; but single
+    // float32, 3 x 21760 x 257: 297 us, loaded 243.)
+    constexpr int kPiece = V * (int)sizeof(T);
+    constexpr bool AHEAD = V > 1 && (!F8 || V >= 4);
     constexpr int kFields = F8 ? 4 : 5;                    // y, du, dy, gate, (f)
     char *slots = reinterpret_cast<char *>(sm) + (size_t)(R > 1 ? R : 0) * a.channels * 4 +
-                  threadIdx.x * 16;
-    const int slot = blockDim.x * 16, stage = (kFields * J + (F8 ? 1 : 0)) * slot;
+                  threadIdx.x * kPiece;
+    const int slot = blockDim.x * kPiece, stage = (kFields * J + (F8 ? 1 : 0)) * slot;
     const int64_t hop = (int64_t)gridDim.x * R;
     // the next row's channel 0, as stored (a conversion would wait for the load)
     T next1 = T(0.0f);
     TF next2 = TF(0);
     float next_scale = 0.0f;
     const auto ahead = [&](int64_t t, int k) {
-        const int64_t row = blockIdx.y * a.seg_points + t + w / G, base = row * a.channels + c0;
-        if (t + w / G < a.seg_points) {
+        const int64_t row = blockIdx.y * a.seg_points + t + team.row, base = row * a.channels + c0;
+        if (t + team.row < a.seg_points) {
             char *at = slots + k * stage;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!have[j]) continue;
                 const int64_t e = base + j * cs;
                 const auto fetch = [&](int f, const void *src) {
-                    cp_async16(smem_u32(at + (f * J + j) * slot),
-                               static_cast<const T *>(src) + e);
+                    const uint32_t to = smem_u32(at + (f * J + j) * slot);
+                    const T *from = static_cast<const T *>(src) + e;
+                    if constexpr (kPiece == 16) cp_async16(to, from);
+                    else if constexpr (kPiece == 8) cp_async8(to, from);
+                    else cp_async4(to, from);
                 };
                 if (has_du) {
                     fetch(0, a.x);
@@ -289,8 +334,8 @@ k_sandwich_bwd_rows(Args a, int G) {
     int k = 0;
     if (AHEAD) ahead((int64_t)blockIdx.x * R, 0);
     for (int64_t t = (int64_t)blockIdx.x * R; t < a.seg_points; t += hop, k ^= 1) {
-        const bool on = t + w / G < a.seg_points;
-        const int64_t row = blockIdx.y * a.seg_points + t + w / G, base = row * a.channels + c0;
+        const bool on = t + team.row < a.seg_points;
+        const int64_t row = blockIdx.y * a.seg_points + t + team.row, base = row * a.channels + c0;
         Pack<T, V> ys[J] = {}, us[J] = {}, gs[J] = {}, gates[J] = {}, out[J], out2[J];
         Pack<TF, V> fs[J] = {};
         float fsc[J] = {};
@@ -374,7 +419,7 @@ k_sandwich_bwd_rows(Args a, int G) {
             mean[1] = s2.x + s2.y;
         }
         if (LAYER) {
-            row_sum<2>(mean, G, red1);
+            row_sum<2, SMALL>(mean, team, red1);
             mean[0] *= -inv;
             mean[1] *= -inv;
         }
@@ -404,7 +449,7 @@ k_sandwich_bwd_rows(Args a, int G) {
             q[2] = q2.x + q2.y;
             q[3] = q3.x + q3.y;
         }
-        row_sum<4>(q, G, red2);
+        row_sum<4, SMALL>(q, team, red2);
         const float r1 = on && has_du ? rsqrtf(fmaf(q[0], inv, a.eps)) : 0.0f;
         const float r2 = on ? rsqrtf(fmaf(q[1], inv, a.eps)) : 0.0f;
         const float2 d0 = f2(LAYER ? -q[2] * inv : 0.0f), d1 = f2(-q[3] * r1 * inv);
@@ -469,7 +514,7 @@ k_sandwich_bwd_rows(Args a, int G) {
             e1 = fma2(dY[k], m[k], e1);
         }
         float e[2] = {e0.x + e0.y, e1.x + e1.y};
-        row_sum<2>(e, G, red3);
+        row_sum<2, SMALL>(e, team, red3);
         e0 = f2(LAYER ? -e[0] * inv : 0.0f);
         e1 = f2(-e[1] * inv);
 #pragma unroll
@@ -491,7 +536,7 @@ k_sandwich_bwd_rows(Args a, int G) {
     float *part = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kSums * a.channels;
 #pragma unroll
     for (int q = 0; q < kSums; ++q) {
-        float *to = R > 1 ? join + (w / G) * a.channels : part + q * a.channels;
+        float *to = R > 1 ? join + team.row * a.channels : part + q * a.channels;
         if (R > 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -507,36 +552,43 @@ k_sandwich_bwd_rows(Args a, int G) {
     }
 }
 
+// Calls f with the storage type, the variant's constants, and whether a row has
+// less than a warp.
 template <int EACH, class F>
 void with_rows(const fno_sandwich_s &p, const Way &way, F &&f) {
     using std::integral_constant;
     with_storage(p.d.dtype, [&](auto t) {
-        const auto layer = [&](auto v, auto j) {
-            if (p.d.norm == FNO_NORM_LAYER) f(t, v, j, std::true_type());
-            else f(t, v, j, std::false_type());
+        const auto rows = [&](auto v, auto j) {
+            with_bools(p.d.norm == FNO_NORM_LAYER, way.lanes < 32,
+                       [&](auto layer, auto small) { f(t, v, j, layer, small); });
         };
         constexpr int V = kVec<decltype(t)>;
-        if (way.vec > 1) layer(integral_constant<int, V>(), integral_constant<int, EACH / V>());
-        else layer(integral_constant<int, 1>(), integral_constant<int, EACH>());
+        if (way.vec > 2) rows(integral_constant<int, V>(), integral_constant<int, EACH / V>());
+        else if (way.vec == 2) rows(integral_constant<int, 2>(), integral_constant<int, EACH / 2>());
+        else rows(integral_constant<int, 1>(), integral_constant<int, EACH>());
     });
 }
 
 // Calls f with the backward kernel.
 template <class F>
 void with_kernel(const fno_sandwich_s &p, bool f8, F &&f) {
-    with_rows<8>(p, p.bwd, [&](auto t, auto v, auto j, auto layer) {
+    with_rows<8>(p, p.bwd, [&](auto t, auto v, auto j, auto layer, auto small) {
         using T = decltype(t);
         constexpr int V = decltype(v)::value, J = decltype(j)::value;
-        if (f8) f(k_sandwich_bwd_rows<T, V, J, decltype(layer)::value, true>);
-        else f(k_sandwich_bwd_rows<T, V, J, decltype(layer)::value, false>);
+        constexpr bool LAYER = decltype(layer)::value, SMALL = decltype(small)::value;
+        if (f8) f(k_sandwich_bwd_rows<T, V, J, LAYER, true, SMALL>);
+        else f(k_sandwich_bwd_rows<T, V, J, LAYER, false, SMALL>);
     });
 }
-// the rows' sums joined in shared memory, and two rows' vectors (as many as the
+int rows_of(const Way &way) { return way.warps / way.group * (32 / way.lanes); }
+
+// the rows' sums joined in shared memory, and two rows' pieces (as many as the
 // float32 codes' case takes: y, du, dy, gate, f)
 size_t smem_of(const fno_sandwich_s &p) {
-    const int rows = p.bwd.warps / p.bwd.group;
+    const int rows = rows_of(p.bwd);
     const size_t join = rows > 1 ? (size_t)rows * p.d.channels * 4 : 0;
-    return join + (p.bwd.vec > 1 ? (size_t)2 * 5 * p.bwd.per * p.bwd.warps * 32 * 16 : 0);
+    const size_t piece = p.bwd.vec * elem_bytes(p.d.dtype);
+    return join + (p.bwd.vec > 1 ? 2 * 5 * piece * p.bwd.per * p.bwd.warps * 32 : 0);
 }
 
 }  // namespace
@@ -546,32 +598,35 @@ namespace sandwich {
 
 // Vectors need the channel count (where every row starts) to be a multiple of
 // them; registers bound a thread's elements (16 forward, 8 backward), and 16
-// warps a row.
+// warps a row.  A row has the fewest lanes that hold it, or warps if it is longer,
+// so that few lie beyond its end.
 Way rows_way(const fno_sandwich_desc_t &d, bool backward) {
     const int c = d.channels, big = d.dtype == FNO_F32 ? 4 : 8;
-    const int vec = c % big == 0 ? big : 1, each = backward ? 8 : 16;
-    int group = 1;
-    while (group <= 16 && group * 32 * each < c) group *= 2;
-    if (group > 16) return Way{kAny, 0, 0, 0, 0};
-    return Way{kRows, vec, each / vec, group > 8 ? group : 8, group};
+    const int vec = c % big == 0 ? big : c % 2 == 0 ? 2 : 1, each = backward ? 8 : 16;
+    const int group = (int)ceil_div(c, 32 * each);
+    if (group > kMaxWarps) return Way{kAny, 0, 0, 0, 0};
+    int lanes = 32;
+    while (group == 1 && lanes > 1 && lanes / 2 * each >= c) lanes /= 2;
+    return Way{kRows, vec, each / vec, group * (group < 8 ? 8 / group : 1), group, lanes};
 }
 
 fno_status_t rows_forward(const fno_sandwich_s &p, const Args &a, int8_t *f8, float *f8_scale,
                           bool *packed, cudaStream_t s) {
-    const Way &way = p.fwd;
-    *packed = f8 && way.vec > 1;         // a group lies within a warp's loads
+    Way way = p.fwd;
+    *packed = f8 && way.vec > 2;         // a group lies within a warp's loads
     int8_t *q = *packed ? f8 : nullptr;
-    with_rows<16>(p, way, [&](auto t, auto v, auto j, auto layer) {
+    if (q && way.lanes < kGroup / way.vec) way.lanes = kGroup / way.vec;
+    with_rows<16>(p, way, [&](auto t, auto v, auto j, auto layer, auto small) {
         k_sandwich_fwd_rows<decltype(t), decltype(v)::value, decltype(j)::value,
-                            decltype(layer)::value>
-            <<<(unsigned)ceil_div(p.d.batch * p.d.points, way.warps / way.group), way.warps * 32,
-               0, s>>>(a, way.group, q, f8_scale);
+                            decltype(layer)::value, decltype(small)::value>
+            <<<(unsigned)ceil_div(p.d.batch * p.d.points, rows_of(way)), way.warps * 32,
+               0, s>>>(a, way.group, way.lanes, q, f8_scale);
     });
     return launched();
 }
 
 fno_status_t rows_shares(const fno_sandwich_s &p, int *ctas, int64_t *most) {
-    *most = ceil_div(p.seg_points, p.bwd.warps / p.bwd.group);
+    *most = ceil_div(p.seg_points, rows_of(p.bwd));
     fno_status_t st = FNO_OK;
     with_kernel(p, false,
                 [&](auto k) { st = occupancy(k, p.bwd.warps * 32, smem_of(p), ctas); });
@@ -586,7 +641,7 @@ fno_status_t rows_backward(const fno_sandwich_s &p, const Args &a, cudaStream_t 
             return;
         }
         k<<<dim3((unsigned)p.splits, (unsigned)p.segs), p.bwd.warps * 32, smem_of(p), s>>>(
-            a, p.bwd.group);
+            a, p.bwd.group, p.bwd.lanes);
         st = launched();
     });
     return st;
