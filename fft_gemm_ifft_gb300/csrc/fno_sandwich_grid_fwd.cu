@@ -13,8 +13,8 @@ namespace {
 // channel in registers, so that each field is read once.  Warp w takes the
 // channels w, w + warps, ... (CPT of them at most), lane l the V consecutive
 // points l V ...; a norm's sums go over a thread's channels in registers and
-// over the warps through shared memory.  Bound by bytes: 66 us for 16 x 64 x 128^2
-// float32 with the 8-bit checkpoint (302 MB, 4.6 TB/s; the kernel that reads each
+// over the warps through shared memory.  Bound by bytes: 60 us for 16 x 64 x 128^2
+// float32 with the 8-bit checkpoint (302 MB, 5.0 TB/s; the kernel that reads each
 // field for each sum 297 us); the rest is the two norms' barriers.
 // ---------------------------------------------------------------------------
 
@@ -82,14 +82,24 @@ __device__ __forceinline__ void tile_norm(X &&x, int mine, int channels, float e
     }
 }
 
+// TIGHT keeps to 80 registers, so that an SM holds more CTAs of up to 12 warps: 17 x
+// 289 x 6560 fp16 314 us against 505, 79 x 64 x 6560 fp16 127 against 142.  With more
+// warps only the spills are left (500 channels 390 us against 350), and the float32
+// tiles of 4 points spill most (84 against 83).  Those of one point and 8 channels
+// always keep to 64, for two CTAs of 16 warps (39 x 128 x 6557 fp16 221 us against 397).
+constexpr int kTightWarps = 12;
+template <typename T, int V, int CPT>
+constexpr bool tight_pays = !(V == 4 && sizeof(T) == 4) && V * CPT > 8;
+
 // Shared memory of a grid kernel: per channel (s w2, s b2, w1, b1), then the
 // sums' rows, then the norms' results.
 size_t grid_smem(int channels, int V, int warps) {
     return (size_t)channels * 16 + (size_t)(2 * warps + 4) * 32 * V * 4;
 }
 
-template <typename T, int V, int CPT, bool LAYER>
-__global__ void __launch_bounds__(512)
+template <typename T, int V, int CPT, bool LAYER, bool TIGHT>
+__global__ void __launch_bounds__(TIGHT ? kTightWarps * 32 : 512,
+                                  TIGHT || V * CPT == 8 ? 2 : 1)
 k_sandwich_fwd_grid(Args a, int8_t *f8, float *f8_scale) {
     constexpr int PT = 32 * V;
     extern __shared__ float4 sm[];
@@ -229,7 +239,8 @@ void with_tiles(const fno_sandwich_s &p, const Way &way, F &&f) {
         };
         constexpr std::integral_constant<int, 1> one;
         constexpr std::integral_constant<int, 8> few;
-        if (way.per == 8 && way.vec > 1) layer(std::integral_constant<int, 4>(), few);
+        if (way.per == 8 && way.vec == 4) layer(std::integral_constant<int, 4>(), few);
+        else if (way.per == 8 && way.vec == 2) layer(std::integral_constant<int, 2>(), few);
         else if (way.per == 8) layer(one, few);
         else if (way.vec == 1) layer(one, std::integral_constant<int, 32>());
         else layer(std::integral_constant<int, 2>(), std::integral_constant<int, 16>());
@@ -248,7 +259,9 @@ Way grid_forward_way(const fno_sandwich_desc_t &d) {
     const auto tiles = [&](int vec, int per) {
         return Way{kTiles, vec, per, (int)ceil_div(c, per), 0};
     };
-    if (c <= 128) return tiles(d.points % 4 == 0 ? 4 : 1, 8);
+    if (c <= 128 && d.points % 4 == 0) return tiles(4, 8);
+    if (c <= 8 * kTightWarps && d.points % 2 == 0) return tiles(2, 8);
+    if (c <= 128) return tiles(1, 8);
     if (c <= 256 && d.points % 2 == 0) return tiles(2, 16);
     if (c <= 512) return tiles(1, 32);
     return Way{kAny, 0, 0, 0, 0};
@@ -260,10 +273,18 @@ fno_status_t grid_forward(const fno_sandwich_s &p, const Args &a, int8_t *f8, fl
     *packed = f8 && way.vec == 4;        // a warp's 128 points are one group
     int8_t *q = *packed ? f8 : nullptr;
     with_tiles(p, way, [&](auto t, auto v, auto per, auto layer) {
+        using T = decltype(t);
         constexpr int V = decltype(v)::value, CPT = decltype(per)::value;
-        k_sandwich_fwd_grid<decltype(t), V, CPT, decltype(layer)::value>
-            <<<(unsigned)(p.d.batch * ceil_div(p.d.points, 32 * V)), way.warps * 32,
-               grid_smem(a.channels, V, way.warps), s>>>(a, q, f8_scale);
+        constexpr bool LAYER = decltype(layer)::value;
+        const auto run = [&](auto kernel) {
+            kernel<<<(unsigned)(p.d.batch * ceil_div(p.d.points, 32 * V)), way.warps * 32,
+                     grid_smem(a.channels, V, way.warps), s>>>(a, q, f8_scale);
+        };
+        if constexpr (tight_pays<T, V, CPT>) {
+            if (way.warps <= kTightWarps)
+                return run(k_sandwich_fwd_grid<T, V, CPT, LAYER, true>);
+        }
+        run(k_sandwich_fwd_grid<T, V, CPT, LAYER, false>);
     });
     return launched();
 }
