@@ -188,6 +188,8 @@ fno_status_t fno_linear_grad_destroy(fno_linear_grad_t plan);
  *   lengths (batch) int32 or NULL: sequence b has max(0, min(lengths[b],
  *     length)) tokens; o and the gradients beyond are 0 and q, k, v beyond are
  *     not looked at; a sequence of no tokens returns its initial state
+ * Up to 128 tokens are worked on together: an infinity or a NaN in one of a
+ * sequence's tokens may reach the outputs of that many before it in its head.
  * ------------------------------------------------------------------------- */
 typedef struct fno_linattn_s *fno_linattn_t;
 
