@@ -118,6 +118,23 @@ def test_norm(pkg, layout, dtype, i):
     check_norm(pkg, layout, *SHAPES[i], dtype, kinds[k % 2], gates[k % 3], k % 4 == 1, k % 5 < 2)
 
 
+# rows of some lanes, of three to fourteen warps, by pairs and single elements, with
+# row counts that leave a CTA's last rows out; tiles of every part of a warp, whose
+# rows start on 8, 4 and fewer bytes
+EDGES = [("tokens", 2, 67, c) for c in (3, 22, 40, 63, 300, 518, 1300, 2303, 3500)] + \
+        [("tokens", 1, 5, 6150)] + \
+        [("grid", 2, 100, 300), ("grid", 1, 101, 400), ("grid", 2, 66, 40), ("grid", 1, 67, 20),
+         ("grid", 1, 131, 97), ("grid", 1, 134, 160), ("grid", 1, 65, 289)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("i", range(len(EDGES)))
+def test_norm_edges(pkg, dtype, i):
+    layout, B, P, C = EDGES[i]
+    check_norm(pkg, layout, B, P, C, dtype, "layer", "full", True, dtype != "f16")
+    check_norm(pkg, layout, B, P, C, dtype, "rms", "channel", False, dtype == "f16")
+
+
 @pytest.mark.parametrize("layout,kind,gate,sigmoid,packed", [
     c for c in itertools.product(["grid", "tokens"], ["rms", "layer"], ["none", "channel", "full"],
                                  [False, True], [False, True]) if c[2] != "none" or not c[3]])
