@@ -255,8 +255,8 @@ class SandwichNorm(_Plan):
             if gp is not None:
                 out["dgate"] = torch.empty(self.gate_shape, dtype=self.gate_dtype,
                                            device=y.device)
-        for n, row in zip(names, vecs):
-            out["d" + n] = row[:C]
+        for n, row in zip(names, vecs.narrow(1, 0, C).unbind(0)):      # (one view, not five)
+            out["d" + n] = row
         ptr = {n: t.data_ptr() for n, t in out.items()}
         check(capi.fno_sandwich_backward(
             self.handle, yp, fp, f.codes.data_ptr() if packed else None,
