@@ -82,9 +82,8 @@ __global__ void __launch_bounds__(256) k_linattn_scan(ScanArgs a) {
 // Numbers.  Operands are sums of bfloat16 terms: 1 for bfloat16 inputs, 2 for
 // fp16 (exact: 11 bits in 16), 3 for float32 (24 bits), and products of terms
 // below the result's own rounding are left out (i + j > L).  All sums are
-// float32.  For bfloat16 the chunk's weights and the state in front of it are
-// rounded to one term (the size of the output's own rounding); the state itself
-// is carried in float32 and its update takes the decayed values in three terms,
+// float32.  For bfloat16 the chunk's weights and the state in front of it are two
+// terms (16 bits, under the output's own 8); the state itself is carried in float32 and its update takes the decayed values in three terms,
 // so that a final state has float32's digits.
 //
 // A warp owns 16 rows of the transposed state Z^T (value columns x key rows) in
@@ -139,6 +138,8 @@ __device__ __forceinline__ float2 term_value(uint32_t u) {
 
 template <typename T> constexpr int kTerms = std::is_same<T, float>::value ? 3
                                              : std::is_same<T, __half>::value ? 2 : 1;
+// of the chunk's weights and of the state in front of it
+template <typename T> constexpr int kInner = kTerms<T> == 1 ? 2 : kTerms<T>;
 
 // 16 bytes, or zeros
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool have) {
@@ -228,14 +229,14 @@ __device__ __forceinline__ void mma_terms(float (&hi)[2][4], float (&lo)[2][4],
 template <typename T, typename TO, int AP, bool REV, bool O, int KT>
 __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
     constexpr int NT = kTerms<T>, LA = AP + 8, PL = kC * LA, LP = kC + 8, PP = kC * LP;
-    constexpr int L = NT - 1;
+    constexpr int PT = kInner<T>, L = PT - 1;
     extern __shared__ __align__(16) char smem_chunk[];
     const ScanArgs &p = ca.s;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int ET = warps * 16, LE = ET + 8, PE = kC * LE;
     // weights, then one (two with asynchronous copies) of k, v, q
     __nv_bfloat16 *sp = reinterpret_cast<__nv_bfloat16 *>(smem_chunk);
-    __nv_bfloat16 *sbuf = sp + (O ? NT * PP : 0);
+    __nv_bfloat16 *sbuf = sp + (O ? PT * PP : 0);
     const int buf = NT * (PL + PE + (O ? PL : 0));
     __shared__ float pw[kC + 2];
     const int seg = blockIdx.x % ca.segments;
@@ -334,11 +335,10 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                     }
                     mma_terms<NT, NT, L>(s, sl, A, B);
                 }
-                if (NT > 1)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) s[y][x] += sl[y][x];
+                    for (int x = 0; x < 4; ++x) s[y][x] += sl[y][x];
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -349,17 +349,17 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                                        ? s[y][2 * x + 1] * (pw[max(0, t - sc - 1)] * ca.scale_p)
                                        : 0.0f;
 #pragma unroll
-                        for (int z = 0; z < NT; ++z)
+                        for (int z = 0; z < PT; ++z)
                             *reinterpret_cast<uint32_t *>(sp + z * PP + t * LP + sc) =
                                 take_term(f0, f1);
                     }
             }
             __syncthreads();
-            float acc[kC / 16][2][4] = {}, acl[NT > 1 ? kC / 16 : 1][2][4] = {};
+            float acc[kC / 16][2][4] = {}, acl[kC / 16][2][4] = {};
             if (!zero) {
 #pragma unroll
                 for (int kk = 0; kk < AP / 16; ++kk) {
-                    uint32_t A[NT][4];
+                    uint32_t A[PT][4];
                     float z[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                         z[4 + i] = Z[2 * kk + 1][i];
                     }
 #pragma unroll
-                    for (int x = 0; x < NT; ++x)
+                    for (int x = 0; x < PT; ++x)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) A[x][i] = take_term(z[2 * i], z[2 * i + 1]);
 #pragma unroll
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
 #pragma unroll
                         for (int x = 0; x < NT; ++x)
                             ldsm4(B[x], uq + 2 * (x * PL + (tb * 16 + rb) * LA + kk * 16 + kb));
-                        mma_terms<NT, NT, L>(acc[tb], acl[NT > 1 ? tb : 0], A, B);
+                        mma_terms<PT, NT, L>(acc[tb], acl[tb], A, B);
                     }
                 }
 #pragma unroll
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                     for (int i = 0; i < 4; ++i) {
                         const float f = pw[j * 8 + c2 + (i & 1) + !REV];
                         acc[j / 2][j % 2][i] *= f;
-                        if (NT > 1) acl[NT > 1 ? j / 2 : 0][j % 2][i] *= f;
+                        acl[j / 2][j % 2][i] *= f;
                     }
             }
 #pragma unroll
@@ -405,11 +405,11 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
 #pragma unroll
                 for (int tb = 0; tb < kC / 16; ++tb) {
                     if (tb < sb || tb >= blocks) continue;
-                    uint32_t B[NT][4];
+                    uint32_t B[PT][4];
 #pragma unroll
-                    for (int x = 0; x < NT; ++x)
+                    for (int x = 0; x < PT; ++x)
                         ldsm4(B[x], up + 2 * (x * PP + (tb * 16 + rb) * LP + sb * 16 + kb));
-                    mma_terms<NT, NT, L>(acc[tb], acl[NT > 1 ? tb : 0], A, B);
+                    mma_terms<NT, PT, L>(acc[tb], acl[tb], A, B);
                 }
             }
             TO *o = static_cast<TO *>(p.o) + (b * p.length * p.heads + h) * p.dv + e0;
@@ -421,9 +421,7 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
                     if (r < m && e < ew)
                         Storage<TO>::store(
                             o + (REV ? n - 1 - (t0 + r) : t0 + r) * p.heads * p.dv + e,
-                            p.scale_o * (NT > 1 ? acc[j / 2][j % 2][i] +
-                                                      acl[NT > 1 ? j / 2 : 0][j % 2][i]
-                                                : acc[j / 2][j % 2][i]));
+                            p.scale_o * (acc[j / 2][j % 2][i] + acl[j / 2][j % 2][i]));
                 }
         }
         // the state after the chunk: the chunk's own sum is made apart and added
@@ -498,8 +496,8 @@ __global__ void __launch_bounds__(256) k_linattn_chunk(ChunkArgs ca) {
 template <typename T>
 size_t chunk_smem(int AP, int warps, bool outputs) {
     const int NT = kTerms<T>, bufs = NT == 1 ? 2 : 1;
-    return (size_t)NT * kC * 2 * (bufs * ((outputs ? 2 : 1) * (AP + 8) + warps * 16 + 8) +
-                                  (outputs ? kC + 8 : 0));
+    return (size_t)kC * 2 * (NT * bufs * ((outputs ? 2 : 1) * (AP + 8) + warps * 16 + 8) +
+                             (outputs ? kInner<T> * (kC + 8) : 0));
 }
 inline int chunk_warps(int dv) {
     const int w = (dv + 15) / 16;

@@ -18,9 +18,12 @@
 // and one thread of each issues the MMAs that its half feeds.
 //
 // Numbers as in fno_linattn_chunk.h: float32 and fp16 operands are three and two
-// bfloat16 terms, a plane each.  For bfloat16, P and the state's copy are rounded
-// to one term, as the output is; the state is float32, and W has two terms, or
-// three where a float32 state is the result.
+// bfloat16 terms, a plane each.  For bfloat16, P and the state's copy have two terms
+// (16 bits, under the output's own 8; with one term each, the outputs' relative error
+// was 2.35e-3 where their own rounding gives 1.66e-3).  The
+// two of the state's copy share one place: the second is written when Q Z has read the
+// first.  The state is float32, and W has two terms, or three where a float32 state is
+// the result.
 //
 // Measured: 2 x 8192 tokens, 16 heads, 128 wide, bfloat16 (4 segments a head): 72 us
 // a pass over q, k, v with outputs, 45 us for the segments' states (the kernel of
@@ -146,18 +149,23 @@ k_linattn_tc(TcArgs ca) {
     constexpr uint32_t kKV = 2 * kOp;
     constexpr uint32_t kW = 0, kK = w_bytes<TO, D, O, KT>(), kV = kK + kOp, kQ = kV + kOp,
                        kZ = kQ + kOp;
-    // tensor memory: S / P, the output, Q Z, W^T K.  The 64-wide Q Z of one term
-    // has the half of S that P leaves free, and is made when S has been read; the
-    // other terms of P lie behind S
-    constexpr bool EARLY = D == 128 || NT > 1;             // Q Z has columns of its own
-    constexpr uint32_t cS = 0, cP = 128, cO = NT > 1 ? 256 : 128,
-                       cQZ = NT > 1 ? 320 : D == 128 ? 256 : 64,
-                       cD = !O ? 0 : EARLY ? 384 : 192;
-    constexpr uint32_t kCols = !O ? D : EARLY ? 512 : 256;
+    // terms of P and of the state's copy
+    constexpr int PT = NT == 1 ? 2 : NT;
+    // tensor memory: S / P, the output, W^T K.  bfloat16: each half of S gives its 64
+    // columns to both terms of P, and Q Z is made where the output goes, and scaled
+    // there before P V is added.  Others: P's terms past the first lie behind S, and
+    // Q Z has columns of its own
+    constexpr uint32_t cS = 0, cP = 128, cO = NT > 1 ? 256 : 128, cQZ = NT > 1 ? 320 : cO,
+                       cD = !O ? 0 : NT > 1 ? 384 : cO + D;
+    constexpr uint32_t kCols = !O ? D : D == 128 || NT > 1 ? 512 : 256;
+    const auto p_at = [](int t, int c) -> uint32_t {       // term t of P from token c on
+        return NT == 1 ? cS + (c & 64) + t * 32 + (c & 63) / 2
+                       : (t ? cP + 64 * (t - 1) : cS) + c / 2;
+    };
     extern __shared__ char smem_raw[];
     char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                           ~static_cast<uintptr_t>(1023));
-    __shared__ __align__(8) uint64_t bar_s, bar_o, bar_d;
+    __shared__ __align__(8) uint64_t bar_s, bar_o, bar_d, bar_z, bar_z2;
     __shared__ uint32_t s_tmem;
     __shared__ float pw[kT + 2];
     __shared__ float up[O ? 2 * kT : 1];           // scale_p gamma^(i - kT), 0 for i < kT
@@ -175,7 +183,7 @@ k_linattn_tc(TcArgs ca) {
     const int64_t first = seg * ca.seg_len, last = min(n, first + ca.seg_len);
     const int nq = p.heads / p.gq, nk = p.heads / p.gk, nv = p.heads / p.gv;
     if (tid == 0) {
-        for (uint64_t *x : {&bar_s, &bar_o, &bar_d})
+        for (uint64_t *x : {&bar_s, &bar_o, &bar_d, &bar_z, &bar_z2})
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(tc_smem_addr(x)));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -277,6 +285,23 @@ k_linattn_tc(TcArgs ca) {
         tc_after_sync();
     };
     const bool has_state = O && (ca.segments > 1 || p.s0);
+    // Q Z over the terms of Z that lie in shared memory (bfloat16: one at a time), added
+    // to what is there or not
+    const auto mma_qz = [&](bool add) {
+        const uint32_t id = idesc_f16(D, true);
+#pragma unroll
+        for (int sum = NT - 1; sum >= 0; --sum)            // the small products first
+#pragma unroll
+            for (int x = 0; x <= sum; ++x)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    mma_f16(tmem + cQZ,
+                            desc_sw128(sb + kQ + x * kPlane + (i >> 2) * kPanel + (i & 3) * 32),
+                            desc_sw128(sb + kZ + (sum - x) * kZPlane + (i >> 2) * (D * 128) +
+                                       (i & 3) * 32), id, add);
+                    add = true;
+                }
+    };
     if (half == 1) {
         // the state: row `row` of Z^T, half of its columns a thread
         const int64_t sbase = bh * (int64_t)p.dk * p.dv;
@@ -322,8 +347,9 @@ k_linattn_tc(TcArgs ca) {
                         z[a + 3] = fmaf(z[a + 3], whole, x.w);
                     }
         }
-        // its bfloat16 terms, the right operands of Q Z
-        const auto publish = [&]() {
+        // its bfloat16 terms, the right operands of Q Z: all of them, or for bfloat16
+        // the first, whose place the second takes when it has been read
+        const auto publish = [&](bool second) {
 #pragma unroll
             for (int c = 0; c < DH / 8; ++c) {
                 float2 f[4];
@@ -334,15 +360,19 @@ k_linattn_tc(TcArgs ca) {
                 for (int t = 0; t < NT; ++t) {
                     uint32_t y[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = take_term(f[j], t + 1 < NT);
+                    for (int j = 0; j < 4; ++j) {
+                        y[j] = take_term(f[j], t + 1 < PT);
+                        if (NT == 1 && second) y[j] = take_term(f[j], false);
+                    }
                     *reinterpret_cast<uint4 *>(base + kZ + t * kZPlane + (at >> 3) * (D * 128) +
                                                sw_off16(row, (at & 7) * 8)) =
                         make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
         };
-        if (mine && has_state) publish();
+        if (mine && has_state) publish(false);
         int chunk = 0;
+        uint32_t carried = 0;                              // chunks with a state in front
         for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
             const int m = (int)min((int64_t)kT, last - t0);
             const bool more = t0 + kT < last;
@@ -392,9 +422,20 @@ k_linattn_tc(TcArgs ca) {
                     }
                 }
             }
+            const bool state2 = O && NT == 1 && (has_state || chunk > 0);
+            if (state2) {
+                mbar_wait(&bar_z, carried++, ca.err);
+                tc_after_sync();
+                if (mine) publish(true);
+            }
             fence_async_smem();
             half_sync(1);
             if (warp == (O ? 8 : 0) && elect_one()) {
+                if (state2) {
+                    tc_after_sync();
+                    mma_qz(true);
+                    mma_commit(&bar_z2);
+                }
                 const uint32_t id = idesc_f16(D, true) | kAcrossA | kAcrossB;
                 bool add = false;
 #pragma unroll
@@ -437,7 +478,7 @@ k_linattn_tc(TcArgs ca) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) z[c + j] = fmaf(z[c + j], carry, x[j]);
                 }
-            if (O && more && mine) publish();
+            if (O && more && mine) publish(false);
         }
         const bool ends = n > first ? n <= first + ca.seg_len : n == 0 && seg == 0;
         if (stored && (!O || (p.sT && ends))) {
@@ -450,26 +491,11 @@ k_linattn_tc(TcArgs ca) {
         }
     }
     if (O && half == 0) {
-        const auto mma_qz = [&]() {
-            const uint32_t id = idesc_f16(D, true);
-            bool add = false;
-#pragma unroll
-            for (int sum = NT - 1; sum >= 0; --sum)        // the small products first
-#pragma unroll
-                for (int x = 0; x <= sum; ++x)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        mma_f16(tmem + cQZ,
-                                desc_sw128(sb + kQ + x * kPlane + (i >> 2) * kPanel + (i & 3) * 32),
-                                desc_sw128(sb + kZ + (sum - x) * kZPlane + (i >> 2) * (D * 128) +
-                                           (i & 3) * 32), id, add);
-                        add = true;
-                    }
-        };
         const int diag = (warp & 3) * 32, a0 = sub * DH;
-        const float fz = pw[row + !REV] * p.scale_o;
+        const float fz = pw[row + !REV];
         bool zero = !has_state;
         int chunk = 0;
+        uint32_t carried = 0;
         for (int64_t t0 = first; t0 < last; t0 += kT, ++chunk) {
             const int m = (int)min((int64_t)kT, last - t0);
             meet();
@@ -488,13 +514,14 @@ k_linattn_tc(TcArgs ca) {
                             add = true;
                         }
                 mma_commit(&bar_s);
-                if (EARLY && !zero) mma_qz();              // (completes with P V)
+                if (!zero) mma_qz(false);
+                if (NT == 1 && !zero) mma_commit(&bar_z);  // (others complete with P V)
             }
             mbar_wait(&bar_s, chunk, ca.err);
             tc_after_sync();
-            // row `row` of P, the 32 columns of S at 32 sub, then at 64 + 32 sub.  P's
-            // columns 0 .. 63 take the place of S's, which the first of them are
-            // read from: all threads read those before any writes
+            // row `row` of P, the 32 columns of S at 32 sub, then at 64 + 32 sub.  P takes
+            // the place of the S that it is read from (the first 64 columns, then, for
+            // bfloat16, the others): all threads read those before any writes
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = (2 * i + sub) * 32;
@@ -530,16 +557,28 @@ k_linattn_tc(TcArgs ca) {
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
+                for (int t = 0; t < PT; ++t) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         float2 v = make_float2(x[2 * j], x[2 * j + 1]);
-                        y[j] = take_term(v, t + 1 < NT);
+                        y[j] = take_term(v, t + 1 < PT);
                         x[2 * j] = v.x;
                         x[2 * j + 1] = v.y;
                     }
-                    if (i == 0 && t == 0) half_sync(0);
-                    tmem_st16u(tmem + (t ? cP + 64 * (t - 1) : cS) + c / 2 + lanes, y);
+                    if (t == 0 && (NT == 1 || i == 0)) half_sync(0);
+                    tmem_st16u(tmem + p_at(t, c) + lanes, y);
+                }
+            }
+            if (NT == 1 && !zero) {                        // diag(g) Q Z, both terms of Z
+                mbar_wait(&bar_z2, carried++, ca.err);
+                tc_after_sync();
+#pragma unroll
+                for (int c = 0; c < DH; c += 16) {
+                    float x[16];
+                    tmem_ld16(tmem + cO + a0 + c + lanes, x);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] *= fz;
+                    tmem_st16(tmem + cO + a0 + c + lanes, x);
                 }
             }
             tmem_st_wait();
@@ -548,15 +587,15 @@ k_linattn_tc(TcArgs ca) {
             if (warp == 0 && elect_one()) {
                 tc_after_sync();
                 const uint32_t id = idesc_f16(D, true) | kAcrossB;
-                if (!EARLY && !zero) mma_qz();
-                bool add = false;
+                bool add = NT == 1 && !zero;
 #pragma unroll
-                for (int sum = NT - 1; sum >= 0; --sum)
+                for (int sum = PT - 1; sum >= 0; --sum)
 #pragma unroll
                     for (int t = 0; t <= sum; ++t)
 #pragma unroll
                         for (int i = 0; i < kT / 16; ++i) {
-                            mma_f16_ts(tmem + cO, tmem + (t ? cP + 64 * (t - 1) : cS) + i * 8,
+                            if (sum - t >= NT) continue;
+                            mma_f16_ts(tmem + cO, tmem + p_at(t, i * 16),
                                        desc_across(sb + kV + (sum - t) * kPlane + i * 2048, kPanel),
                                        id, add);
                             add = true;
@@ -578,11 +617,11 @@ k_linattn_tc(TcArgs ca) {
                 tmem_ld16(tmem + cO + a0 + c + lanes, x);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] *= p.scale_o;
-                if (!zero) {
+                if (NT > 1 && !zero) {
                     float y2[16];
                     tmem_ld16(tmem + cQZ + a0 + c + lanes, y2);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = fmaf(y2[j], fz, x[j]);
+                    for (int j = 0; j < 16; ++j) x[j] = fmaf(y2[j], fz * p.scale_o, x[j]);
                 }
 #pragma unroll
                 for (int j = 0; j < 16; j += 8) {
