@@ -83,8 +83,9 @@ __global__ void __launch_bounds__(256) k_linattn_scan(ScanArgs a) {
 // fp16 (exact: 11 bits in 16), 3 for float32 (24 bits), and products of terms
 // below the result's own rounding are left out (i + j > L).  All sums are
 // float32.  For bfloat16 the chunk's weights and the state in front of it are two
-// terms (16 bits, under the output's own 8); the state itself is carried in float32 and its update takes the decayed values in three terms,
-// so that a final state has float32's digits.
+// terms (16 bits, under the output's own 8); the state itself is carried in float32
+// and its update takes the decayed values in three terms, so that a final state has
+// float32's digits.
 //
 // A warp owns 16 rows of the transposed state Z^T (value columns x key rows) in
 // registers, in the accumulator layout, which is also the layout of the left
