@@ -471,7 +471,12 @@ k_sandwich_bwd_rows(Args a, int G, int L) {
         for (int j = 0; j < J; ++j)
             if (on && have[j])
                 *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(a.dx) + base + j * cs) = out[j];
-        if (!block) continue;
+        if (!block) {
+            // red2 is the only sum of such a row without the means' own: every warp of
+            // the row has read it before the next row's is written
+            if (!LAYER && !SMALL && team.warps > 1) __syncthreads();
+            continue;
+        }
         // dY becomes e
         Pack<float, V> s[J] = {}, w2[J] = {}, b2[J] = {}, gf[J] = {};
 #pragma unroll

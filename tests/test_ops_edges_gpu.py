@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import ops_ref as R
-from test_ops_gpu import attn_inputs, cuda, d64
+from test_ops_gpu import attn_inputs, cuda, d64, norm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -13,6 +13,32 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def pkg(fno):
     return fno
+
+
+# ---------------------------------------------------------------------------
+# sandwich norm
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("C", [300, 1024, 2300])
+def test_norm_alone_over_many_rows(pkg, dtype, kind, C):
+    # rows of several warps, several rows for each: the rows' sums follow one another
+    # in the same shared memory
+    P = 4099
+    t, p = norm_inputs("tokens", 1, P, C, dtype, kind, "none")
+    n = pkg.SandwichNorm(C, P, 1, layout="tokens", norm=kind, dtype=dtype)
+    T, PR = cuda(t), cuda(p)
+    p64 = {k: v.double().requires_grad_() for k, v in p.items()}
+    x = d64(t["x"]).requires_grad_()
+    _, ru = R.sandwich(x, None, p64, kind, 1e-5, "tokens")
+    names = ["dx", "dw1"] + ["db1"] * (kind == "layer")
+    want = torch.autograd.grad(ru, [x] + [p64[k[1:]] for k in names[1:]], d64(t["du"]))
+    got = n.backward(T["x"], None, PR, None, T["du"])
+    for k, w in zip(names, want):
+        assert R.rel(got[k], w) < R.tol(dtype if k == "dx" else "f32"), k
+    for _ in range(3):
+        again = n.backward(T["x"], None, PR, None, T["du"])
+        assert all(torch.equal(again[k], got[k]) for k in got)
 
 
 # ---------------------------------------------------------------------------
