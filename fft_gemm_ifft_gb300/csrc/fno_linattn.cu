@@ -277,7 +277,7 @@ fno_status_t fno_linattn_forward(fno_linattn_t p, const void *q, const void *k, 
     if (inject("launch")) return FNO_ERR_CUDA;
     const int g = p->heads / p->kv_heads;
     ScanArgs a{q, k, v, log_decay, lengths, s0, o, sT, p->length, p->heads, 1, g, g,
-               p->dk, p->dv, scale, 1.0f, false, false, false};
+               p->dk, p->dv, scale, 1.0f, false, false, false, sT && sT == s0};
     return scan(*p, a, false, false, static_cast<float *>(workspace), 1.0f,
                 reinterpret_cast<cudaStream_t>(stream));
 }
@@ -303,16 +303,17 @@ fno_status_t fno_linattn_backward(fno_linattn_t p, const void *q, const void *k,
     float *states = static_cast<float *>(workspace);
     float *gk = reinterpret_cast<float *>(static_cast<char *>(workspace) + p->group_off[0]);
     float *gv = reinterpret_cast<float *>(static_cast<char *>(workspace) + p->group_off[1]);
+    const bool in_place = ds0 && ds0 == gsT;
     // dq: queries go, keys v, values k, the state transposed
     const ScanArgs aq{go, v, k, log_decay, lengths, s0, dq, nullptr, p->length, p->heads, 1, g, g,
-                      p->dv, p->dk, scale, 1.0f, true, false, false};
+                      p->dv, p->dk, scale, 1.0f, true, false, false, false};
     // dk: queries v, keys go, values q;  dv: queries k, keys q, values go
     const ScanArgs ak{v, go, q, log_decay, lengths, gsT, g > 1 ? (void *)gk : dk, nullptr,
                       p->length, p->heads, g, 1, 1, p->dv, p->dk, 1.0f, scale, true, false,
-                      ds0 != nullptr};
+                      ds0 != nullptr, in_place};
     const ScanArgs av{k, q, go, log_decay, lengths, gsT, g > 1 ? (void *)gv : dv, ds0,
                       p->length, p->heads, g, 1, 1, p->dk, p->dv, 1.0f, scale, false,
-                      tc_applies(*p) && p->segments > 1, false};
+                      tc_applies(*p) && p->segments > 1, false, in_place};
     st = scan(*p, aq, false, false, states, 1.0f, s);
     if (st == FNO_OK) st = scan(*p, ak, true, g > 1, states, scale, s);
     if (st == FNO_OK) st = scan(*p, av, true, g > 1, states, scale, s);

@@ -41,6 +41,9 @@ struct ScanArgs {
     // the same sums with keys and values exchanged; the states are wanted to
     // float32's digits although this scan returns none
     bool states_t, exact;
+    // tcgen05 scans: s0 may be written by this call (it is sT), so that only a launch
+    // before the outputs' reads it
+    bool joined;
 };
 
 // One scan: in chunks up to 128 key columns, token by token beyond.  rev: from the

@@ -47,7 +47,9 @@ constexpr uint32_t kPanel = kT * 128;            // 128 tokens x 64 elements
 
 // Up to so many segments each adds up its earlier ones' local states itself (its
 // prologue reads them all at once); more are joined by a kernel in between, which
-// reads each once but costs its launch and a trip through memory.
+// reads each once but costs its launch and a trip through memory.  That kernel also
+// joins the segments of a call whose final state replaces the initial one: every
+// segment's prologue would read s0, which the last segment's CTA may have written.
 constexpr int kFold = 8;
 
 struct TcArgs {
@@ -57,6 +59,9 @@ struct TcArgs {
     int64_t seg_len;
     float scale_p;
     int *err;
+    __host__ __device__ bool joined() const {
+        return segments > kFold || (segments > 1 && s.joined);
+    }
 };
 
 // operand read across its rows: 64-element panels `panel` bytes apart, groups of
@@ -313,7 +318,7 @@ k_linattn_tc(TcArgs ca) {
             return sbase + (p.s_transposed ? (int64_t)row * p.dk + a : (int64_t)a * p.dv + row);
         };
         float z[DH];
-        const bool ready = ca.segments > kFold;            // seg_state is the initial state
+        const bool ready = ca.joined();                    // seg_state is the initial state
 #pragma unroll
         for (int a = 0; a < DH; ++a) {
             z[a] = 0.0f;
@@ -676,7 +681,7 @@ fno_status_t run(const fno_linattn_s &p, const TcArgs &ca, cudaStream_t s) {
     if (ca.segments > 1 && !ca.s.states_t) {
         fno_status_t st = go(k_linattn_tc<T, T, D, REV, false, KT>, 256,
                              operand_bytes<T, T, D, false, KT>());
-        if (st == FNO_OK && ca.segments > kFold) st = segment_states(p, ca.s, ca.states, s);
+        if (st == FNO_OK && ca.joined()) st = segment_states(p, ca.s, ca.states, s);
         if (st != FNO_OK) return st;
     }
     return go(k_linattn_tc<T, TO, D, REV, true, KT>, 512, operand_bytes<T, TO, D, true, KT>());

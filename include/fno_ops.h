@@ -211,7 +211,8 @@ fno_status_t fno_linattn_forward(fno_linattn_t plan, const void *q, const void *
 
 /* Gradients of L given go = dL/do and gsT = dL/dS_T (NULL: zero).  dq, dk, dv
  * have the shapes of q, k, v (a shared key/value head sums over its query
- * heads); ds0 NULL: not wanted.  Needs FNO_LINATTN_BACKWARD.                  */
+ * heads); ds0 NULL: not wanted; ds0 may be gsT itself.  Needs
+ * FNO_LINATTN_BACKWARD.                                                       */
 fno_status_t fno_linattn_backward(fno_linattn_t plan, const void *q, const void *k, const void *v,
                                   const float *log_decay, float scale, const int32_t *lengths,
                                   const float *s0, const void *go, const float *gsT, void *dq,

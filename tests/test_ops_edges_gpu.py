@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import ops_ref as R
+from fft_gemm_ifft_gb300 import capi
 from test_ops_gpu import attn_inputs, cuda, d64, norm_inputs
 
 pytestmark = pytest.mark.gpu
@@ -77,4 +78,37 @@ def test_attention_bfloat16_digits(pkg, B, T, H, K, dk, dv, state):
     want, size = run(lambda x: x.clone()), run(torch.abs)
     for got, w, s, name in zip([o, *grads[:3]], want, size, ("o", "dq", "dk", "dv")):
         close(got, w, s, name)
+    assert a.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f16", 128)])
+@pytest.mark.parametrize("T", [200, 1024, 2500, 4096, 9000])     # 1, 2, 5, 8 and more segments
+def test_attention_states_in_place(pkg, dtype, d, T):
+    # sT = s0 and ds0 = gsT (the C ABI allows them): every part of the time axis starts
+    # from the state as it was.  The parts are joined in the same order by either way,
+    # but for the rounding of the initial state's product
+    t = attn_inputs(1, T, 2, 1, d, d, dtype, True)
+    t["log_decay"] = torch.tensor([-1e-4, -2e-3])       # the initial state counts to the end
+    C = cuda(t)
+    a = pkg.LinearAttention(1, T, 2, 1, d, d, dtype=dtype, backward=True)
+    args = (C["q"], C["k"], C["v"], C["log_decay"])
+    o, sT = a.forward(*args, state=C["s0"], want_state=True)
+    grads = a.backward(*args, C["do"], state=C["s0"], dstate=C["dsT"])
+    space = torch.empty(a.workspace_bytes, dtype=torch.uint8, device="cuda")
+    ws = space.data_ptr()
+    p = [x.data_ptr() for x in args] + [d ** -0.5, None]
+    st = torch.cuda.current_stream().cuda_stream
+    for _ in range(3):
+        s, o2 = C["s0"].clone(), torch.empty_like(o)
+        assert capi.fno_linattn_forward(a.handle, *p, s.data_ptr(), o2.data_ptr(), s.data_ptr(),
+                                        ws, st) == capi.FNO_OK
+        assert R.rel(o2, o.cpu()) < (2e-6 if dtype == "f32" else R.HALF_ULP[dtype] / 8)
+        assert R.rel(s, sT.cpu()) < 2e-6
+        ds, g = C["dsT"].clone(), [torch.empty_like(x) for x in grads[:3]]
+        assert capi.fno_linattn_backward(a.handle, *p, C["s0"].data_ptr(), C["do"].data_ptr(),
+                                         ds.data_ptr(), *(x.data_ptr() for x in g),
+                                         ds.data_ptr(), ws, st) == capi.FNO_OK
+        for x, y in zip(g, grads):
+            assert R.rel(x, y.cpu()) < (2e-6 if dtype == "f32" else R.HALF_ULP[dtype] / 8)
+        assert R.rel(ds, grads[3].cpu()) < 2e-6
     assert a.device_error() == 0
