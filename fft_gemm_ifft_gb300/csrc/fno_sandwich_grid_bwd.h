@@ -95,7 +95,8 @@ __device__ __forceinline__ void join_moments(const float *rows, float *fin, int 
             e1 += fmaf(off, r[3 * line + v * pt], r[4 * line + v * pt]);
         }
     }
-    const float rr = rsqrtf(fmaf(fmaxf(ss, 0.0f), inv, eps));
+    // (a NaN stays one; fmaxf would make it 0)
+    const float rr = rsqrtf(fmaf(ss < 0.0f ? 0.0f : ss, inv, eps));
     float *o = fin + q + (second ? 5 * pt : 0);
     o[0] = ref;
     o[pt] = -mean * rr;

@@ -42,6 +42,35 @@ def test_norm_alone_over_many_rows(pkg, dtype, kind, C):
         assert all(torch.equal(again[k], got[k]) for k in got)
 
 
+@pytest.mark.parametrize("layout,C", [("grid", 24), ("grid", 130), ("grid", 700), ("grid", 4099),
+                                      ("tokens", 40), ("tokens", 300), ("tokens", 4099)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("where", ["x", "f", "dy", "du"])
+def test_norm_gradients_of_nan(pkg, layout, C, kind, where):
+    # a NaN of one element is a NaN wherever the definition has one, and nowhere else
+    B, P = 2, 70
+    t, p = norm_inputs(layout, B, P, C, "f32", kind, "none")
+    at = (1, C // 2, 33) if layout == "grid" else (1, 33, C // 2)
+    t[where][at] = float("nan")
+    p64 = {k: v.double().requires_grad_() for k, v in p.items()}
+    y, f = d64(t["x"]).requires_grad_(), d64(t["f"]).requires_grad_()
+    _, ru = R.sandwich(y, None, p64, kind, 1e-5, layout)
+    layer = kind == "layer"
+    g1 = torch.autograd.grad(ru, [y, p64["w1"]] + ([p64["b1"]] if layer else []), d64(t["du"]))
+    dY = g1[0] + d64(t["dy"])
+    ry, _ = R.sandwich(torch.zeros_like(y), f, p64, kind, 1e-5, layout, want_u=False)
+    g2 = torch.autograd.grad(ry, [f, p64["s"], p64["w2"]] + ([p64["b2"]] if layer else []), dY)
+    want = dict(zip(["df", "ds", "dw2", "db2"], g2), dx=dY, dw1=g1[1])
+    if layer:
+        want["db1"] = g1[2]
+    n = pkg.SandwichNorm(C, P, B, layout=layout, norm=kind)
+    T = cuda(t)
+    got = n.backward(T["x"], T["f"], cuda(p), T["dy"], T["du"])
+    assert set(got) == set(want)
+    for k, w in want.items():
+        assert torch.equal(torch.isnan(got[k]).cpu(), torch.isnan(w)), k
+
+
 # ---------------------------------------------------------------------------
 # linear attention
 # ---------------------------------------------------------------------------
