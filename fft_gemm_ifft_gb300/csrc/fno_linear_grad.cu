@@ -45,7 +45,8 @@ template <typename T, bool VEC>
 struct Raw8 {
     static constexpr int kWords = 8 * (int)sizeof(T) / 4 + (VEC || sizeof(T) == 4 ? 0 : 1);
     uint32_t w[kWords];
-    // `n` elements from `at` on are wanted.  Words may reach 4 bytes past them.
+    // `n` elements from `at` on are wanted.  Every word that is read has a wanted byte,
+    // so that none reaches more than 3 bytes past them.
     __device__ __forceinline__ void load(const T *at, int n) {
         if constexpr (VEC) {
             constexpr int B = 8 * (int)sizeof(T);
@@ -70,10 +71,12 @@ struct Raw8 {
         } else {
             const uint32_t *p =
                 reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(3));
+            const int end =
+                n > 0 ? n * (int)sizeof(T) + (int)(reinterpret_cast<uintptr_t>(at) & 3) : 0;
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
                 w[i] = 0;
-                if (n > 0 && i * 4 < n * (int)sizeof(T) + (sizeof(T) == 4 ? 0 : 4)) w[i] = p[i];
+                if (i * 4 < end) w[i] = p[i];
             }
         }
     }
@@ -235,7 +238,7 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
             x.sh_q = (int)(reinterpret_cast<uintptr_t>(q_at) & 3) * 8;
             x.sh_y = (int)(reinterpret_cast<uintptr_t>(y_at) & 3) * 8;
         }
-        // words reach up to 4 bytes past the wanted elements: there are as many in
+        // words reach up to 3 bytes past the wanted elements: there are as many in
         // the tensor when 4 blocks follow, each of an element a row at least
         if (VEC || it + 4 < items) {
 #pragma unroll

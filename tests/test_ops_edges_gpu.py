@@ -6,7 +6,7 @@ import torch
 
 import ops_ref as R
 from fft_gemm_ifft_gb300 import capi
-from test_ops_gpu import attn_inputs, cuda, d64, norm_inputs
+from test_ops_gpu import attn_inputs, cuda, d64, gen, norm_inputs, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -69,6 +69,30 @@ def test_norm_gradients_of_nan(pkg, layout, C, kind, where):
     assert set(got) == set(want)
     for k, w in want.items():
         assert torch.equal(torch.isnan(got[k]).cpu(), torch.isnan(w)), k
+
+
+# ---------------------------------------------------------------------------
+# weight and bias gradient
+# ---------------------------------------------------------------------------
+def check_linear_grad(pkg, B, ci, co, P, dtype):
+    g = gen(B + ci + co + P)
+    x, dy = rand(g, (B, ci, P), dtype), rand(g, (B, co, P), dtype)
+    p = pkg.pack_activation(x.cuda())
+    n = pkg.LinearGrad(B, ci, co, P, dtype=dtype)
+    dw, db = n(dy.cuda(), p)
+    v = R.values(p.codes, p.scales)
+    assert R.rel(dw, torch.einsum("bop,bip->oi", dy.double(), v)) < R.tol("f32")
+    want = dy.double().sum((0, 2))
+    assert ((db.cpu().double() - want).abs() <= 1e-5 * dy.double().abs().sum((0, 2))).all()
+    assert n.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("P", [1, 2, 3, 5, 7, 9, 129, 131])
+def test_linear_grad_of_few_elements(pkg, dtype, P):
+    # rows that end within a word, samples of a row or two
+    for B, ci, co in ((5, 1, 1), (6, 1, 2), (9, 3, 1), (700, 1, 1)):
+        check_linear_grad(pkg, B, ci, co, P, dtype)
 
 
 # ---------------------------------------------------------------------------
