@@ -118,14 +118,15 @@ struct Raw8 {
     }
 };
 
-// two floats as the next bfloat16 term; they keep what it leaves
-__device__ __forceinline__ uint32_t take_term(float &x, float &y) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    const float2 f = __bfloat1622float2(h);
-    x -= f.x;
-    y -= f.y;
+// two floats as the next bfloat16 term; they keep what it leaves.  A term but the last
+// is the largest bfloat16 at most, so that an infinity leaves itself (and no
+// inf - inf) and is the last term.
+__device__ __forceinline__ uint32_t take_term(float &x, float &y, bool last) {
     uint32_t u;
-    memcpy(&u, &h, 4);
+    if (last) asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(u) : "f"(x), "f"(y));
+    else asm("cvt.rn.satfinite.bf16x2.f32 %0, %2, %1;" : "=r"(u) : "f"(x), "f"(y));
+    x -= __uint_as_float(u << 16);
+    y -= __uint_as_float(u & 0xffff0000u);
     return u;
 }
 template <typename T> __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -328,10 +329,10 @@ k_linear_grad_part(const T *__restrict__ dy, const int8_t *__restrict__ codes,
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                     uint4 u;
-                    u.x = take_term(f[0], f[1]);
-                    u.y = take_term(f[2], f[3]);
-                    u.z = take_term(f[4], f[5]);
-                    u.w = take_term(f[6], f[7]);
+                    u.x = take_term(f[0], f[1], x + 1 == NT);
+                    u.y = take_term(f[2], f[3], x + 1 == NT);
+                    u.z = take_term(f[4], f[5], x + 1 == NT);
+                    u.w = take_term(f[6], f[7], x + 1 == NT);
                     *reinterpret_cast<uint4 *>(dst + x * 2 * chunk_b) = u;
                 }
             }

@@ -95,6 +95,33 @@ def test_linear_grad_of_few_elements(pkg, dtype, P):
         check_linear_grad(pkg, B, ci, co, P, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("ci", [40, 128])                # the bias by a row of ones, by threads
+@pytest.mark.parametrize("P", [256, 301])
+def test_linear_grad_of_infinities(pkg, dtype, ci, P):
+    # codes of no element are 0: an infinity in dy is one in every weight of its output,
+    # two of opposite signs are NaN, and no other output sees them
+    B, co = 2, 24
+    g = gen(P + ci)
+    x = rand(g, (B, ci, P), dtype)
+    x = torch.where(x < 0, x - 0.5, x + 0.5)
+    dy = rand(g, (B, co, P), dtype)
+    inf = float("inf")
+    dy[0, 3, 17], dy[1, 5, P - 1], dy[1, 20, 130] = inf, -inf, inf
+    dy[0, 9, 0], dy[1, 9, 0] = inf, -inf
+    dy[1, 11, 200] = float("nan")
+    p = pkg.pack_activation(x.cuda())
+    assert p.codes.bool().all()
+    dw, db = pkg.LinearGrad(B, ci, co, P, dtype=dtype)(dy.cuda(), p)
+    v = R.values(p.codes, p.scales)
+    want = torch.stack([(dy[:, o, None].double() * v).sum((0, 2)) for o in range(co)])
+    for got, w in ((dw.cpu(), want), (db.cpu(), dy.double().sum((0, 2)))):
+        for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+            assert torch.equal(kind(got), kind(w)), kind
+        fine = torch.isfinite(w)
+        assert R.rel(got[fine], w[fine]) < R.tol("f32")
+
+
 # ---------------------------------------------------------------------------
 # linear attention
 # ---------------------------------------------------------------------------
