@@ -253,10 +253,12 @@ namespace sandwich {
 
 // Vectors need the point count (where every channel's row starts) to be a
 // multiple of them; registers bound a thread's elements (32 of each field), and
-// 16 warps a CTA's channels.
+// 16 warps a CTA's channels.  A launch has a CTA a tile: more tiles than a grid has
+// room for (billions of samples of a few points) take the kernel for any size.
 Way grid_forward_way(const fno_sandwich_desc_t &d) {
     const int c = d.channels;
     const auto tiles = [&](int vec, int per) {
+        if (d.batch * ceil_div(d.points, 32 * vec) > 0x7fffffffll) return Way{kAny, 0, 0, 0, 0};
         return Way{kTiles, vec, per, (int)ceil_div(c, per), 0};
     };
     if (c <= 128 && d.points % 4 == 0) return tiles(4, 8);

@@ -71,6 +71,22 @@ def test_norm_gradients_of_nan(pkg, layout, C, kind, where):
         assert torch.equal(torch.isnan(got[k]).cpu(), torch.isnan(w)), k
 
 
+@pytest.mark.parametrize("B", [2 ** 31 + 9, 2 ** 32 + 5])
+def test_norm_of_more_samples_than_a_grid_has_blocks(pkg, B):
+    # one point and channel a sample: 9 to 17 GB
+    x = torch.ones((B, 1, 1), dtype=torch.float16, device="cuda")
+    x[-3:, 0, 0] = torch.tensor([-2.0, 0.0, 0.003], dtype=torch.float16)
+    u = torch.full_like(x, float("nan"))
+    n = pkg.SandwichNorm(1, 1, B, dtype="f16")
+    n.pre(x, {"w1": torch.ones(1, device="cuda")}, u=u)
+    t = x[-4:, 0, 0].double().cpu()
+    want = t / torch.sqrt(t * t + 1e-5)
+    assert (u[-4:, 0, 0].double().cpu() - want).abs().max() < 2.0 ** -11
+    one = u[-4]
+    for i in range(0, B - 3, 1 << 30):
+        assert (u[i:min(i + (1 << 30), B - 3)] == one).all()
+
+
 # ---------------------------------------------------------------------------
 # weight and bias gradient
 # ---------------------------------------------------------------------------
