@@ -31,7 +31,8 @@ inline bool inject(const char *site) {
 }
 
 // An operand of a call: its bytes, whether the call writes it, and an input
-// that it may coincide with exactly (an in-place update).
+// that it may coincide with exactly (an in-place update; no second input may lie
+// there).
 struct Operand {
     const void *p;
     size_t bytes;
@@ -45,8 +46,13 @@ inline fno_status_t check_operands(std::initializer_list<Operand> all) {
         if (!aligned16(a.p)) return FNO_ERR_MISALIGNED;
     for (const Operand &a : all) {
         if (!a.out || !a.p) continue;
+        bool in_place = false;
         for (const Operand &b : all) {
-            if (&a == &b || !b.p || (b.p == a.p && a.same == b.p && !b.out)) continue;
+            if (&a == &b || !b.p) continue;
+            if (b.p == a.p && a.same == b.p && !b.out && !in_place) {
+                in_place = true;
+                continue;
+            }
             const char *pa = static_cast<const char *>(a.p), *pb = static_cast<const char *>(b.p);
             if (pa < pb + b.bytes && pb < pa + a.bytes) return FNO_ERR_ALIASING;
         }

@@ -87,6 +87,20 @@ def test_norm_of_more_samples_than_a_grid_has_blocks(pkg, B):
         assert (u[i:min(i + (1 << 30), B - 3)] == one).all()
 
 
+def test_norm_in_place_over_two_inputs(pkg):
+    # y may be x, but not while x is f as well: f's codes are taken after y is stored
+    n = pkg.SandwichNorm(8, 65, 2)
+    x = torch.randn(2, 8, 65, device="cuda")
+    one = torch.ones(8, device="cuda")
+    w = {"s": one, "w2": one, "w1": one}
+    before = x.clone()
+    with pytest.raises(pkg.FnoError) as e:
+        n.forward(x, x, w, y=x, save8=True)
+    assert e.value.status == capi.FNO_ERR_ALIASING and torch.equal(x, before)
+    y, _, f8 = n.forward(x, x, w, save8=True)               # apart from y: as any f
+    assert torch.equal(f8.codes, pkg.pack_activation(x).codes)
+
+
 # ---------------------------------------------------------------------------
 # weight and bias gradient
 # ---------------------------------------------------------------------------
