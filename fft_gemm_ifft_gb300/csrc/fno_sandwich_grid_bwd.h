@@ -428,16 +428,16 @@ k_sandwich_bwd_tile(Args a, int stages) {
     }
     float *out = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kSums * C;
 #pragma unroll
-    for (int j = 0; j < kTileC; ++j) {
-        if (j >= mine) break;
+    for (int j = 0; j < kTileC; ++j)
 #pragma unroll
         for (int q = 0; q < kSums; ++q) {
+            // every lane of the warp, whose parts need not have as many channels (a
+            // channel that a part has not is a sum of 0)
             float v = acc[q][j];
 #pragma unroll
             for (int m = TL / 2; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-            if (lane == 0) out[q * C + w + j * warps] = v;
+            if (lane == 0 && j < mine) out[q * C + w + j * warps] = v;
         }
-    }
 }
 
 // The sums over the lanes of four values: lanes 0-7, 8-15, 16-23 and 24-31 get
