@@ -122,7 +122,8 @@ k_linattn_step(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
     // columns in rounds of the threads (dv up to 256), rows over what is left
     const int lanes = (dv + V - 1) / V, across = lanes < kStepThreads ? lanes : kStepThreads;
     const int down = kStepThreads / across, mine = threadIdx.x % across, part = threadIdx.x / across;
-    for (int e0 = mine * V; e0 < (dv + V - 1) / V * V; e0 += across * V) {
+    for (int round = 0; round < dv; round += across * V) {          // (every thread's)
+        const int e0 = round + mine * V;
         Pack<float, V> s = {};
         if (live && part < down && e0 < dv) {
             const int64_t base = (slot * heads + h) * (int64_t)dk * dv + e0;

@@ -222,3 +222,17 @@ def test_attention_states_in_place(pkg, dtype, d, T):
             assert R.rel(x, y.cpu()) < (2e-6 if dtype == "f32" else R.HALF_ULP[dtype] / 8)
         assert R.rel(ds, grads[3].cpu()) < 2e-6
     assert a.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 129), (33, 130), (7, 255), (200, 131), (256, 256)])
+def test_attention_step_of_wide_values(pkg, dtype, dk, dv):
+    # more value columns than threads: a second round, which some threads have no column of
+    B, H = 3, 2
+    t = attn_inputs(B, 1, H, 1, dk, dv, dtype, True)
+    C = cuda(t)
+    a = pkg.LinearAttention(B, 1, H, 1, dk, dv, dtype=dtype)
+    ro, rS = R.attention(*(d64(t[x]) for x in ("q", "k", "v")), t["log_decay"], 0.5, state=t["s0"])
+    o = a.step(*(C[x][:, 0].contiguous() for x in ("q", "k", "v")), C["log_decay"], C["s0"],
+               scale=0.5)
+    assert R.rel(o, ro[:, 0]) < R.tol(dtype) and R.rel(C["s0"], rS) < R.tol("f32")
