@@ -58,6 +58,10 @@ class PackedActivation:
     def __init__(self, codes, scales, dtype):
         if dtype not in _CODES:
             raise TypeError(f"dtype must be one of {list(_CODES)}, got {dtype}")
+        if not isinstance(codes, torch.Tensor):
+            raise TypeError("codes must be a CUDA tensor")
+        if codes.dim() < 1 or codes.numel() < 1:
+            raise ValueError("codes must have at least one element")
         _field(codes, torch.int8, codes.shape, "codes")
         _field(scales, torch.float32, codes.shape[:-1] + (-(-codes.shape[-1] // GROUP),),
                "scales")

@@ -101,6 +101,18 @@ def test_norm_in_place_over_two_inputs(pkg):
     assert torch.equal(f8.codes, pkg.pack_activation(x).codes)
 
 
+def test_packed_activation_refusals(pkg):
+    c, s = (torch.zeros((3, 0), dtype=t, device="cuda") for t in (torch.int8, torch.float32))
+    with pytest.raises(TypeError):
+        pkg.PackedActivation(None, s, torch.float32)
+    with pytest.raises(ValueError):
+        pkg.PackedActivation(c, s, torch.float32)               # no element
+    with pytest.raises(ValueError):
+        pkg.PackedActivation(c.new_zeros(()), s.new_zeros(()), torch.float32)
+    with pytest.raises(TypeError):
+        pkg.PackedActivation(c.new_zeros((3, 4)).float(), s.new_zeros((3, 1)), torch.float32)
+
+
 # ---------------------------------------------------------------------------
 # weight and bias gradient
 # ---------------------------------------------------------------------------
