@@ -6,7 +6,7 @@ import torch
 
 import ops_ref as R
 from fft_gemm_ifft_gb300 import capi
-from test_ops_gpu import attn_inputs, cuda, d64, gen, norm_inputs, rand
+from test_ops_gpu import attn_inputs, check_norm, cuda, d64, gen, norm_inputs, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -101,6 +101,49 @@ def test_norm_in_place_over_two_inputs(pkg):
     assert torch.equal(f8.codes, pkg.pack_activation(x).codes)
 
 
+# Rows, tiles and blocks for several turns of every CTA (one wave has 152 SMs' worth),
+# the last of them in part: what is on its way while a CTA works, the buffers' second
+# use, sums over turns.
+TURNS = [("tokens", 1, 4099, 300), ("tokens", 1, 4099, 1024), ("tokens", 3, 21001, 40),
+         ("tokens", 1, 3001, 2500), ("grid", 2, 39999, 64), ("grid", 2, 40000, 64),
+         ("grid", 1, 60000, 20), ("grid", 2, 12010, 200), ("grid", 1, 12003, 300),
+         ("grid", 1, 25002, 600), ("grid", 1, 12001, 520)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("i", range(len(TURNS)))
+def test_norm_of_several_turns(pkg, dtype, i):
+    layout, B, P, C = TURNS[i]
+    kinds, gates = ["rms", "layer"], ["none", "channel", "full"]
+    k = i + ["f32", "f16", "bf16"].index(dtype)
+    check_norm(pkg, layout, B, P, C, dtype, kinds[k % 2], gates[k % 3], k % 4 < 2, False)
+    check_norm(pkg, layout, B, P, C, dtype, kinds[1 - k % 2], gates[(k + 1) % 3], k % 4 > 1, True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("layout,P,C", [("tokens", 4099, 300), ("tokens", 20001, 40),
+                                        ("grid", 39999, 24), ("grid", 12003, 300),
+                                        ("grid", 25002, 520)])
+def test_norm_of_several_turns_is_repeatable(pkg, dtype, layout, P, C):
+    t, p = norm_inputs(layout, 1, P, C, dtype, "layer", "full")
+    n = pkg.SandwichNorm(C, P, 1, layout=layout, norm="layer", gate="full", dtype=dtype)
+    T, PR = cuda(t), cuda(p)
+    for f in (T["f"], pkg.pack_activation(T["f"])):
+        a = n.backward(T["x"], f, PR, T["dy"], T["du"], gate=T["gate"])
+        for _ in range(3):
+            b = n.backward(T["x"], f, PR, T["dy"], T["du"], gate=T["gate"])
+            assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.parametrize("layout,B,P,C", [("tokens", 100, 3, 40), ("grid", 33, 70, 24),
+                                          ("tokens", 3001, 12, 32), ("grid", 1000, 5, 300),
+                                          ("tokens", 65535, 2, 8), ("grid", 65535, 2, 3)])
+def test_norm_gate_of_many_samples(pkg, layout, B, P, C):
+    # a gate per sample and channel, up to the most samples it takes
+    check_norm(pkg, layout, B, P, C, "f32", "layer", "channel", True, False)
+    check_norm(pkg, layout, B, P, C, "bf16", "rms", "channel", False, True)
+
+
 def test_packed_activation_refusals(pkg):
     c, s = (torch.zeros((3, 0), dtype=t, device="cuda") for t in (torch.int8, torch.float32))
     with pytest.raises(TypeError):
@@ -135,6 +178,14 @@ def test_linear_grad_of_few_elements(pkg, dtype, P):
     # rows that end within a word, samples of a row or two
     for B, ci, co in ((5, 1, 1), (6, 1, 2), (9, 3, 1), (700, 1, 1)):
         check_linear_grad(pkg, B, ci, co, P, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,ci,co,P", [(2, 64, 64, 50048), (3, 40, 60, 50001), (1, 128, 33, 99999),
+                                       (2, 130, 200, 40008), (700, 5, 7, 129)])
+def test_linear_grad_of_several_blocks(pkg, dtype, B, ci, co, P):
+    # five blocks and more for every CTA: each stage and accumulator again
+    check_linear_grad(pkg, B, ci, co, P, dtype)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
