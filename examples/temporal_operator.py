@@ -13,6 +13,8 @@ frame's features:
 The training step keeps the spectral layer's output and the head's input and
 pre-activation in 8 bits; every gradient is taken by the library's backward
 calls.  The rollout carries the attention's state instead of the past frames.
+A gate per channel of each point makes every point a sample of the norm over time,
+which takes batch n^2 up to 65535.
 
     python examples/temporal_operator.py
 """

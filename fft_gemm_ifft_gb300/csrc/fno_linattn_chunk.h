@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(256) k_linattn_scan(ScanArgs a) {
 // transposing ldmatrix; the chunk's weights P go through shared memory.
 //
 // These kernels take what fno_linattn_tc.cu does not: fp16 and float32 wider than
-// 64, and widths that are not multiples of 8.  Measured for 4 x 4096 tokens, 16
-// heads, 64 wide, bfloat16: 127 us where the tcgen05 kernels take 62; for 16383
-// tokens, 8 heads, 64 wide, float32: 150 us against 103.  mma.sync peaks at 1024
-// multiply-adds a cycle and SM, and the latency of its chains keeps it at a third
-// of that.
+// 64, and widths that are not multiples of 8.  Measured for 2 x 4096 tokens, 8 heads:
+// 128 wide 234 us in float32 and 195 in fp16 (bfloat16 on tcgen05: 73), keys of 48
+// and values of 80 columns 150 and 114 (49), 50 wide 97, 72 and, in bfloat16, 63.
+// mma.sync peaks at 1024 multiply-adds a cycle and SM, and the latency of its chains
+// keeps it at a third of that.
 // ---------------------------------------------------------------------------
 struct ChunkArgs {
     ScanArgs s;

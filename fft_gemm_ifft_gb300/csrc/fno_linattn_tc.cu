@@ -20,15 +20,15 @@
 // Numbers as in fno_linattn_chunk.h: float32 and fp16 operands are three and two
 // bfloat16 terms, a plane each.  For bfloat16, P and the state's copy have two terms
 // (16 bits, under the output's own 8; with one term each, the outputs' relative error
-// was 2.35e-3 where their own rounding gives 1.66e-3).  The
+// was 2.35e-3 where their own rounding gives 1.66e-3, and this pass took 72 us).  The
 // two of the state's copy share one place: the second is written when Q Z has read the
-// first.  The state is float32, and W has two terms, or three where a float32 state is
-// the result.
+// first.  The state is summed and carried in float32; W, what a chunk adds to it, has
+// two terms, or three where a float32 state is the result.
 //
-// Measured: 2 x 8192 tokens, 16 heads, 128 wide, bfloat16 (4 segments a head): 72 us
-// a pass over q, k, v with outputs, 45 us for the segments' states (the kernel of
-// fno_linattn_chunk.h: 229 us with outputs).  A chunk takes 8400 cycles; an M = 128
-// MMA costs about 100 whatever its N, and a chunk has 40 of them, half of them W^T K.
+// Measured: 2 x 8192 tokens, 16 heads, 128 wide, bfloat16 (4 segments a head): 92 us
+// a pass over q, k, v with outputs, 45 us for the segments' states.  A chunk takes
+// 10 900 cycles; an M = 128 MMA costs about 100 whatever its N, and a chunk has 56 of
+// them: 8 for S, 16 each for Q Z, P V and W^T K.
 // What is left is the order S, P, P V, output within a chunk: its operands fill
 // shared memory, so that the next chunk's loads start when this one's are read.
 #include "fno_linattn.h"

@@ -52,7 +52,8 @@ struct Args {
     int64_t seg_points;
 };
 
-// (the fast quotient, 2 ulp: the exact one is a dozen instructions and a branch)
+// (the fast exponential and quotient, 1e-6 relative for |g| up to 10: the exact
+// quotient alone is a dozen instructions and a branch)
 __device__ __forceinline__ float sigmoid(float g) {
     return __fdividef(1.0f, 1.0f + __expf(-g));
 }

@@ -10,7 +10,10 @@
 
 As in the rest of the package, the classes marshal arguments: a plan, a
 workspace from torch, tensor pointers and the current stream.  A plan object
-holds one workspace, so calls on it have to be ordered (one stream).
+holds one workspace, so calls on it have to be ordered (one stream).  A call with
+``stream=`` is launched there and allocates its results on the current stream:
+that stream has to wait for the current one's work before the call, and the
+current one for it before the results are used or dropped.
 """
 from __future__ import annotations
 
@@ -159,7 +162,7 @@ class SandwichNorm(_Plan):
     ``layout`` "grid": fields (batch, channels, points); "tokens": (batch,
     points, channels).  ``params`` is a dict of float32 (channels,) tensors: s,
     w2, w1, and b2, b1 for norm="layer".  ``gate`` "channel" takes float32
-    (batch, channels), "full" a field.
+    (batch, channels) of up to 65535 samples, "full" a field.
     """
 
     def __init__(self, channels, points, batch, layout="grid", norm="rms", gate="none",

@@ -21,9 +21,10 @@
  * call but the plan calls allocates or waits, so that every other call can be
  * captured in a CUDA graph; an output may not overlap an input, another output
  * or the workspace (FNO_ERR_ALIASING) except where a call says so.  Parameters
- * and their gradients are float32; fields have the storage type; every sum is
- * taken in float32 and results do not depend on the order in which the GPU
- * runs its blocks.  Calls that may run at the same time need their own
+ * and their gradients are float32; fields have the storage type; sums, norms
+ * and states are float32 and results do not depend on the order in which the
+ * GPU runs its blocks.  Where operands or functions have fewer digits than
+ * that, a call says so.  Calls that may run at the same time need their own
  * workspaces; a plan may be shared.
  */
 #ifndef FNO_OPS_H_
@@ -68,14 +69,16 @@ typedef struct fno_sandwich_desc_s {
     fno_layout_t layout;
     fno_norm_t norm;
     fno_gate_t gate;
-    int32_t gate_sigmoid;     /* 0: a = g, 1: a = 1 / (1 + e^-g)                          */
+    int32_t gate_sigmoid;     /* 0: a = g, 1: a = 1 / (1 + e^-g) (1e-6 relative for       */
+                              /* |g| up to 10)                                            */
     float eps;                /* >= 0                                                     */
     fno_dtype_t dtype;        /* storage type of x, f, y, u and a full gate               */
 } fno_sandwich_desc_t;
 
 /* Validate the description and make a plan (host memory only).  *plan is NULL
- * on failure.  Errors: INVALID_ARG, UNSUPPORTED (more than 2^38 elements),
- * OUT_OF_MEMORY, CUDA.                                                        */
+ * on failure.  Errors: INVALID_ARG, UNSUPPORTED (more than 2^38 elements, than
+ * 2^34 - 8 points in all samples, than 65535 samples with FNO_GATE_CHANNEL, for
+ * either direction), OUT_OF_MEMORY, CUDA.                                     */
 fno_status_t fno_sandwich_plan(fno_sandwich_t *plan, const fno_sandwich_desc_t *desc);
 
 /* Device workspace bytes of fno_sandwich_backward (the forward needs none). */
@@ -132,7 +135,8 @@ fno_status_t fno_sandwich_destroy(fno_sandwich_t plan);
  * a code is code * scale, at most m / 254 (and rounding) from x.  A group that
  * holds a NaN or an infinity has that scale, and reads back as NaN.
  * codes: int8, rows x cols.  scales: float32, rows x ceil(cols / GROUP).
- * rows, cols >= 1, at most 2^38 elements (else FNO_ERR_UNSUPPORTED).
+ * rows, cols >= 1, at most 2^38 elements and 2^36 - 32 groups (else
+ * FNO_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 #define FNO_ACT8_GROUP 128
 
@@ -144,7 +148,8 @@ fno_status_t fno_act8_unpack(int64_t rows, int64_t cols, fno_dtype_t dtype, cons
                              const float *scales, void *x, fno_stream_t stream);
 
 /* dx = dy * GELU'(v), v the checkpoint's values, GELU the exact form
- * v/2 (1 + erf(v / sqrt 2)).  dx may be dy itself.                           */
+ * v/2 (1 + erf(v / sqrt 2)), its slope to 3e-7 absolute (erf by a published
+ * polynomial, as in the pointwise layers).  dx may be dy itself.              */
 fno_status_t fno_act8_gelu_backward(int64_t rows, int64_t cols, fno_dtype_t dtype,
                                     const int8_t *codes, const float *scales, const void *dy,
                                     void *dx, fno_stream_t stream);
@@ -189,7 +194,12 @@ fno_status_t fno_linear_grad_destroy(fno_linear_grad_t plan);
  *     length)) tokens; o and the gradients beyond are 0 and q, k, v beyond are
  *     not looked at; a sequence of no tokens returns its initial state
  * Up to 128 tokens are worked on together: an infinity or a NaN in one of a
- * sequence's tokens may reach the outputs of that many before it in its head.
+ * sequence's tokens may reach the outputs of that many before it in its head,
+ * and an infinity may come out as a NaN.
+ * The sums and the state are float32.  With fp16 and float32 all products have
+ * float32's digits; with bfloat16 the products of queries and keys, the state
+ * that a query meets and what a token adds to it have 16 bits or more in front
+ * of the rounding of the result (final states and ds0: float32's digits).
  * ------------------------------------------------------------------------- */
 typedef struct fno_linattn_s *fno_linattn_t;
 
