@@ -101,6 +101,40 @@ def test_norm_in_place_over_two_inputs(pkg):
     assert torch.equal(f8.codes, pkg.pack_activation(x).codes)
 
 
+@pytest.mark.parametrize("layout,P,C", [("grid", 400, 24), ("grid", 401, 40), ("grid", 20001, 40),
+                                        ("grid", 333, 200), ("grid", 130, 300), ("grid", 200, 600),
+                                        ("grid", 33, 4099), ("tokens", 4099, 40),
+                                        ("tokens", 4099, 300), ("tokens", 700, 1025),
+                                        ("tokens", 50, 4099), ("tokens", 9, 9000)])
+@pytest.mark.parametrize("dtype,kind,gate", [("f32", "layer", "full"), ("bf16", "rms", "channel"),
+                                             ("f16", "layer", "none")])
+def test_norm_over_its_operands(pkg, layout, P, C, dtype, kind, gate):
+    # y over x and dx over dy (the C ABI) are what they are apart
+    B = 2
+    t, p = norm_inputs(layout, B, P, C, dtype, kind, gate)
+    n = pkg.SandwichNorm(C, P, B, layout=layout, norm=kind, gate=gate, dtype=dtype)
+    T, PR = cuda(t), cuda(p)
+    y, u, f8 = n.forward(T["x"], T["f"], PR, gate=T["gate"], save8=True)
+    x = T["x"].clone()
+    y2, u2, g8 = n.forward(x, T["f"], PR, gate=T["gate"], save8=True, y=x)
+    assert torch.equal(x, y) and torch.equal(u, u2) and torch.equal(f8.codes, g8.codes)
+    for f in (T["f"], f8):
+        want = n.backward(y, f, PR, T["dy"], T["du"], gate=T["gate"])
+        got = {k: torch.full_like(v, float("nan")) for k, v in want.items()}
+        got["dx"] = T["dy"].clone()
+        packed = f is f8
+        ptr = lambda v: None if v is None else v.data_ptr()
+        assert capi.fno_sandwich_backward(
+            n.handle, ptr(y), None if packed else ptr(f), ptr(f8.codes) if packed else None,
+            ptr(f8.scales) if packed else None, ptr(T["gate"]), ptr(PR["s"]), ptr(PR["w2"]),
+            ptr(PR.get("b2")), ptr(PR["w1"]), ptr(got["dx"]), ptr(T["du"]), ptr(got["dx"]),
+            ptr(got["df"]), ptr(got.get("dgate")), ptr(got["ds"]), ptr(got["dw2"]),
+            ptr(got.get("db2")), ptr(got["dw1"]), ptr(got.get("db1")), n.workspace.data_ptr(),
+            torch.cuda.current_stream().cuda_stream) == capi.FNO_OK
+        for k, w in want.items():
+            assert torch.equal(got[k], w), k
+
+
 # Rows, tiles and blocks for several turns of every CTA (one wave has 152 SMs' worth),
 # the last of them in part: what is on its way while a CTA works, the buffers' second
 # use, sums over turns.
