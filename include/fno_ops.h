@@ -196,10 +196,10 @@ fno_status_t fno_linear_grad_destroy(fno_linear_grad_t plan);
  * Up to 128 tokens are worked on together: an infinity or a NaN in one of a
  * sequence's tokens may reach the outputs of that many before it in its head,
  * and an infinity may come out as a NaN.
- * The sums and the state are float32.  With fp16 and float32 all products have
- * float32's digits; with bfloat16 the products of queries and keys, the state
- * that a query meets and what a token adds to it have 16 bits or more in front
- * of the rounding of the result (final states and ds0: float32's digits).
+ * The sums and the state are float32.  The decayed products of queries and keys,
+ * the state that a query meets and what a token adds to the state keep float32's
+ * digits for float32, and 16 bits or more for fp16 and bfloat16, in front of the
+ * rounding of the result (final states and ds0: float32's digits for all).
  * ------------------------------------------------------------------------- */
 typedef struct fno_linattn_s *fno_linattn_t;
 
