@@ -14,7 +14,7 @@ from .capi import (FNO_BF16, FNO_F16, FNO_F32, FNO_PLAN_DEFAULT,  # noqa: F401
                    FNO_PLAN_UNFUSED, fno_status_string)
 
 _SEQUENCE = ("SandwichNorm", "PackedActivation", "pack_activation", "LinearGrad",
-             "LinearAttention")
+             "LinearAttention", "Rotary", "CausalConv", "SelectiveScan")
 __all__ = ["capi", "FnoError", "SpectralConv", "FnoModel", "check", *_SEQUENCE]
 
 

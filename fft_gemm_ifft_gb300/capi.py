@@ -42,9 +42,14 @@ FNO_PLAN_SPLIT_LAYER = 512
 # include/fno_ops.h
 FNO_ACT8_GROUP = 128
 FNO_LINATTN_BACKWARD = 1
+FNO_CAUSAL_CONV_BACKWARD = 1
+FNO_SCAN_BACKWARD = 1
 LAYOUT_CODES = {"grid": 0, "tokens": 1}
 NORM_CODES = {"rms": 0, "layer": 1}
 GATE_CODES = {"none": 0, "channel": 1, "full": 2}
+ACT_CODES = {"none": 0, "silu": 1}
+ROTARY_LAYOUT_CODES = {"half": 0, "interleaved": 1}
+ROTARY_SCALING_CODES = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 
 # Every symbol include/fno.h and include/fno_ops.h declare.
 EXPORTS = (
@@ -65,6 +70,11 @@ EXPORTS = (
     "fno_linattn_plan", "fno_linattn_workspace_size", "fno_linattn_forward",
     "fno_linattn_backward", "fno_linattn_step", "fno_linattn_get_device_error",
     "fno_linattn_destroy",
+    "fno_rotary_plan", "fno_rotary_apply", "fno_rotary_destroy",
+    "fno_causal_conv_plan", "fno_causal_conv_workspace_size", "fno_causal_conv_forward",
+    "fno_causal_conv_backward", "fno_causal_conv_step", "fno_causal_conv_destroy",
+    "fno_scan_plan", "fno_scan_workspace_size", "fno_scan_forward", "fno_scan_backward",
+    "fno_scan_step", "fno_scan_destroy",
 )
 
 _vp = ctypes.c_void_p
@@ -86,6 +96,23 @@ class fno_sandwich_desc_t(ctypes.Structure):
                 ("norm", ctypes.c_int), ("gate", ctypes.c_int),
                 ("gate_sigmoid", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("dtype", ctypes.c_int)]
+
+
+class fno_rotary_desc_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("length", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original", ctypes.c_double), ("fast", ctypes.c_double),
+                ("slow", ctypes.c_double), ("dtype", ctypes.c_int)]
+
+
+class fno_scan_desc_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("length", ctypes.c_int64),
+                ("channels", ctypes.c_int32), ("states", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("softplus", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("flags", ctypes.c_uint32)]
 
 
 class fno_trace_record_t(ctypes.Structure):
@@ -174,7 +201,19 @@ def lib() -> ctypes.CDLL:
             L.fno_linattn_forward.argtypes = [_vp] * 5 + [f32] + [_vp] * 6
             L.fno_linattn_backward.argtypes = [_vp] * 5 + [f32] + [_vp] * 10
             L.fno_linattn_step.argtypes = [_vp] * 5 + [f32, _vp, i64] + [_vp] * 4
-            for name in ("sandwich", "linear_grad", "linattn"):
+            L.fno_rotary_plan.argtypes = [pvp, ctypes.POINTER(fno_rotary_desc_t)]
+            L.fno_rotary_apply.argtypes = [_vp] * 5 + [i32] + [_vp] * 3
+            L.fno_rotary_destroy.argtypes = [_vp]
+            L.fno_causal_conv_plan.argtypes = [pvp, i64, i64, i32, i32, ctypes.c_int, _st,
+                                               ctypes.c_uint32]
+            L.fno_causal_conv_forward.argtypes = [_vp] * 9
+            L.fno_causal_conv_backward.argtypes = [_vp] * 14
+            L.fno_causal_conv_step.argtypes = [_vp] * 5 + [i64] + [_vp] * 4
+            L.fno_scan_plan.argtypes = [pvp, ctypes.POINTER(fno_scan_desc_t)]
+            L.fno_scan_forward.argtypes = [_vp] * 15
+            L.fno_scan_backward.argtypes = [_vp] * 24
+            L.fno_scan_step.argtypes = [_vp] * 10 + [i64] + [_vp] * 4
+            for name in ("sandwich", "linear_grad", "linattn", "causal_conv", "scan"):
                 getattr(L, f"fno_{name}_workspace_size").argtypes = [_vp, psz]
                 getattr(L, f"fno_{name}_destroy").argtypes = [_vp]
             for name in ("linear_grad", "linattn"):
@@ -416,3 +455,76 @@ def fno_linattn_get_device_error(plan, stream):
 
 def fno_linattn_destroy(plan):
     return lib().fno_linattn_destroy(plan)
+
+
+def fno_rotary_plan(desc: fno_rotary_desc_t):
+    h = _vp(0)
+    st = lib().fno_rotary_plan(ctypes.byref(h), ctypes.byref(desc))
+    return st, h.value
+
+
+def fno_rotary_apply(plan, q_ptr, k_ptr, positions_ptr, offsets_ptr, transpose, qo_ptr, ko_ptr,
+                     stream):
+    return lib().fno_rotary_apply(plan, q_ptr, k_ptr, positions_ptr, offsets_ptr, transpose,
+                                  qo_ptr, ko_ptr, stream)
+
+
+def fno_rotary_destroy(plan):
+    return lib().fno_rotary_destroy(plan)
+
+
+def fno_causal_conv_plan(batch, length, channels, width, act, dtype, flags=0):
+    h = _vp(0)
+    st = lib().fno_causal_conv_plan(ctypes.byref(h), batch, length, channels, width, act, dtype,
+                                    flags)
+    return st, h.value
+
+
+def fno_causal_conv_workspace_size(plan):
+    v = ctypes.c_size_t(0)
+    return lib().fno_causal_conv_workspace_size(plan, ctypes.byref(v)), v.value
+
+
+def fno_causal_conv_forward(plan, *ptrs_and_stream):
+    return lib().fno_causal_conv_forward(plan, *ptrs_and_stream)
+
+
+def fno_causal_conv_backward(plan, *ptrs_and_stream):
+    return lib().fno_causal_conv_backward(plan, *ptrs_and_stream)
+
+
+def fno_causal_conv_step(plan, x_ptr, w_ptr, bias_ptr, slots_ptr, num_slots, state_ptr,
+                         new_state_ptr, y_ptr, stream):
+    return lib().fno_causal_conv_step(plan, x_ptr, w_ptr, bias_ptr, slots_ptr, num_slots,
+                                      state_ptr, new_state_ptr, y_ptr, stream)
+
+
+def fno_causal_conv_destroy(plan):
+    return lib().fno_causal_conv_destroy(plan)
+
+
+def fno_scan_plan(desc: fno_scan_desc_t):
+    h = _vp(0)
+    st = lib().fno_scan_plan(ctypes.byref(h), ctypes.byref(desc))
+    return st, h.value
+
+
+def fno_scan_workspace_size(plan):
+    v = ctypes.c_size_t(0)
+    return lib().fno_scan_workspace_size(plan, ctypes.byref(v)), v.value
+
+
+def fno_scan_forward(plan, *ptrs_and_stream):
+    return lib().fno_scan_forward(plan, *ptrs_and_stream)
+
+
+def fno_scan_backward(plan, *ptrs_and_stream):
+    return lib().fno_scan_backward(plan, *ptrs_and_stream)
+
+
+def fno_scan_step(plan, *args):
+    return lib().fno_scan_step(plan, *args)
+
+
+def fno_scan_destroy(plan):
+    return lib().fno_scan_destroy(plan)

@@ -7,6 +7,10 @@
 ``LinearGrad``        weight and bias gradient of a 1x1 linear from one
 ``LinearAttention``   linear attention with a decay for each head: prompts,
                       single tokens, gradients
+``Rotary``            rotary positions of its queries and keys
+``CausalConv``        short causal convolutions along time, and
+``SelectiveScan``     the selective state space scan behind them: prompts, single
+                      tokens, gradients
 
 As in the rest of the package, the classes marshal arguments: a plan, a
 workspace from torch, tensor pointers and the current stream.  A plan object
@@ -386,4 +390,302 @@ class LinearAttention(_Plan):
         op = _field(out, self.torch_dtype, shape, "out")
         check(capi.fno_linattn_step(self.handle, *ptrs, self._scale(scale), tp, n, sp, np_,
                                     op, _stream(stream, q)), "fno_linattn_step")
+        return out
+
+
+def _int32(v, name):
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits, got {v}")
+    return v
+
+
+def _code(codes, key, name):
+    if key not in codes:
+        raise ValueError(f"{name} must be one of {list(codes)}, got {key!r}")
+    return codes[key]
+
+
+class _DevicePlan(_Plan):
+    """A plan of the device that was current when it was made: its calls take that
+    device's tensors while it is the current one."""
+
+    def _own(self, status, handle, name, workspace=True):
+        check(status, f"fno_{name}_plan")
+        self.handle, self._name = handle, name
+        self.workspace, self.workspace_bytes = None, 0
+        if workspace:
+            st, self.workspace_bytes = getattr(capi, f"fno_{name}_workspace_size")(handle)
+            check(st)
+        self.device = torch.cuda.current_device()
+
+    def device_error(self, stream=None) -> int:
+        """These kernels have no device-side waits or checks to report."""
+        return capi.FNO_OK
+
+    def _at(self, t, dtype, shape, name):
+        """t's pointer, once its type, shape, layout and device are those wanted."""
+        p = _field(t, dtype, shape, name)
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on cuda:{self.device}, got {t.device}")
+        return p
+
+    def _maybe_at(self, t, dtype, shape, name):
+        return None if t is None else self._at(t, dtype, shape, name)
+
+    def _launch_stream(self, stream):
+        if torch.cuda.current_device() != self.device:
+            raise ValueError(f"the plan is of cuda:{self.device}, which is not the current device")
+        if stream is None and _raw_stream is not None:
+            return _raw_stream(self.device)
+        return _stream_handle(stream)
+
+    def _empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _out(self, t, dtype, shape, name):
+        if t is None:
+            t = self._empty(shape, dtype)
+            return t, t.data_ptr()
+        return t, self._at(t, dtype, shape, name)
+
+    def _slots(self, state, new_state, slots, dtype, rest):
+        """(number of slots, pointers of slots, state and new state) of a step."""
+        n = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() else 0
+        sp = self._at(state, dtype, (n,) + rest, "state")
+        if n < 1:
+            raise ValueError("state must have at least one slot")
+        if slots is None and n < self.batch:
+            raise ValueError(f"state must have {self.batch} slots without slots=, got {n}")
+        np_ = sp if new_state is None else self._at(new_state, dtype, (n,) + rest, "new_state")
+        return n, self._maybe_at(slots, torch.int32, (self.batch,), "slots"), sp, np_
+
+
+class Rotary(_DevicePlan):
+    """Rotary positions (``fno_rotary_*``): the pairs in the first ``rotary_dim``
+    elements (default: all) of every head of q (batch, length, heads, dim) and k
+    (batch, length, kv_heads, dim; none for kv_heads=0) turned by position times
+    base ** (-2 i / rotary_dim).  ``layout`` "half" pairs elements i and i +
+    rotary_dim / 2, "interleaved" 2 i and 2 i + 1.  ``scaling`` for contexts longer
+    than those trained on: None, ("linear", factor), ("base", factor) or ("ramp",
+    factor, original length, fast, slow)."""
+
+    def __init__(self, batch, length, heads, kv_heads, dim, rotary_dim=None, layout="half",
+                 base=10000.0, scaling=None, dtype="f32"):
+        d = capi.fno_rotary_desc_t()
+        d.batch, d.length = int(batch), int(length)
+        d.heads, d.kv_heads = _int32(heads, "heads"), _int32(kv_heads, "kv_heads")
+        d.dim = _int32(dim, "dim")
+        d.rotary_dim = d.dim if rotary_dim is None else _int32(rotary_dim, "rotary_dim")
+        d.layout = _code(capi.ROTARY_LAYOUT_CODES, layout, "layout")
+        kind, *values = ("none",) if scaling is None else tuple(scaling)
+        d.scaling = _code(capi.ROTARY_SCALING_CODES, kind, "scaling")
+        names = {"none": (), "linear": ("factor",), "base": ("factor",),
+                 "ramp": ("factor", "original", "fast", "slow")}[kind]
+        if len(values) != len(names):
+            raise ValueError(f"scaling {kind!r} takes {names}, got {tuple(values)}")
+        for name, v in zip(names, values):
+            setattr(d, name, float(v))
+        d.base, d.dtype = float(base), _code(capi.DTYPE_CODES, dtype, "dtype")
+        self._own(*capi.fno_rotary_plan(d), "rotary", workspace=False)
+        self.torch_dtype = _DTYPES[dtype]
+        self.batch, self.length = d.batch, d.length
+        self.q_shape = (d.batch, d.length, d.heads, d.dim)
+        self.k_shape = (d.batch, d.length, d.kv_heads, d.dim) if d.kv_heads else None
+
+    def _apply(self, q, k, positions, offsets, q_out, k_out, transpose, stream):
+        dt = self.torch_dtype
+        qp = self._at(q, dt, self.q_shape, "q")
+        q_out, qop = self._out(q_out, dt, self.q_shape, "q_out")
+        kp = kop = None
+        if self.k_shape is None:
+            if k is not None or k_out is not None:
+                raise ValueError("this plan has no k")
+        else:
+            kp = self._at(k, dt, self.k_shape, "k")
+            k_out, kop = self._out(k_out, dt, self.k_shape, "k_out")
+        if positions is not None and offsets is not None:
+            raise ValueError("positions and offsets exclude each other")
+        pp = self._maybe_at(positions, torch.int32, (self.batch, self.length), "positions")
+        op = self._maybe_at(offsets, torch.int32, (self.batch,), "offsets")
+        check(capi.fno_rotary_apply(self.handle, qp, kp, pp, op, transpose, qop, kop,
+                                    self._launch_stream(stream)), "fno_rotary_apply")
+        return q_out, k_out
+
+    def forward(self, q, k=None, positions=None, offsets=None, q_out=None, k_out=None,
+                stream=None):
+        """(q, k) turned.  Token t of sequence b is at ``positions[b, t]`` (int32), at
+        ``offsets[b]`` + t, or at t.  ``q_out`` and ``k_out`` may be q and k."""
+        return self._apply(q, k, positions, offsets, q_out, k_out, 0, stream)
+
+    __call__ = forward
+
+    def backward(self, dq, dk=None, positions=None, offsets=None, q_out=None, k_out=None,
+                 stream=None):
+        """Gradients of q and k from those of ``forward``'s outputs."""
+        return self._apply(dq, dk, positions, offsets, q_out, k_out, 1, stream)
+
+
+class CausalConv(_DevicePlan):
+    """y_t = act(bias + sum_j w[:, j] x_{t - width + 1 + j}) for each channel of x
+    (batch, length, channels) (``fno_causal_conv_*``).  w (channels, width) and bias
+    (channels,) are float32; ``act`` is "silu" or "none"; states (batch, width - 1,
+    channels) of the storage type hold the last inputs, oldest first.
+    ``backward=True`` prepares the workspace of ``backward``."""
+
+    def __init__(self, batch, length, channels, width, act="silu", dtype="f32", backward=False):
+        self.batch, self.length = int(batch), int(length)
+        self.channels, self.width = _int32(channels, "channels"), _int32(width, "width")
+        self._own(*capi.fno_causal_conv_plan(
+            self.batch, self.length, self.channels, self.width,
+            _code(capi.ACT_CODES, act, "act"), _code(capi.DTYPE_CODES, dtype, "dtype"),
+            capi.FNO_CAUSAL_CONV_BACKWARD if backward else 0), "causal_conv")
+        self.torch_dtype = _DTYPES[dtype]
+        self.x_shape = (self.batch, self.length, self.channels)
+        self.state_shape = (self.batch, self.width - 1, self.channels)
+
+    def _inputs(self, x, w, bias, lengths, state):
+        return (self._at(x, self.torch_dtype, self.x_shape, "x"),
+                self._at(w, torch.float32, (self.channels, self.width), "w"),
+                self._maybe_at(bias, torch.float32, (self.channels,), "bias"),
+                self._maybe_at(lengths, torch.int32, (self.batch,), "lengths"),
+                self._maybe_at(state, self.torch_dtype, self.state_shape, "state"))
+
+    def forward(self, x, w, bias=None, lengths=None, state=None, want_state=False, out=None,
+                stream=None):
+        """(y, final state or None).  ``lengths`` int32 (batch,): tokens of each
+        sequence; ``state``: the inputs in front of the first token (None: zeros)."""
+        ptrs = self._inputs(x, w, bias, lengths, state)
+        out, op = self._out(out, self.torch_dtype, self.x_shape, "out")
+        final = self._empty(self.state_shape, self.torch_dtype) if want_state else None
+        check(capi.fno_causal_conv_forward(self.handle, *ptrs, op, _ptr(final),
+                                           self._launch_stream(stream)),
+              "fno_causal_conv_forward")
+        return out, final
+
+    __call__ = forward
+
+    def backward(self, x, w, dy, bias=None, lengths=None, state=None, dstate=None, stream=None):
+        """(dx, dw, dbias or None, gradient of the initial state or None).  ``dstate`` is
+        the gradient of the final state (None: zero)."""
+        ptrs = self._inputs(x, w, bias, lengths, state)
+        dyp = self._at(dy, self.torch_dtype, self.x_shape, "dy")
+        dsp = self._maybe_at(dstate, self.torch_dtype, self.state_shape, "dstate")
+        dx = self._empty(self.x_shape, self.torch_dtype)
+        dw = self._empty((self.channels, self.width), torch.float32)
+        db = None if bias is None else self._empty((self.channels,), torch.float32)
+        ds0 = None if state is None else self._empty(self.state_shape, self.torch_dtype)
+        check(capi.fno_causal_conv_backward(
+            self.handle, *ptrs, dyp, dsp, dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ds0),
+            self._workspace(), self._launch_stream(stream)), "fno_causal_conv_backward")
+        return dx, dw, db, ds0
+
+    def step(self, x, w, state, bias=None, slots=None, new_state=None, out=None, stream=None):
+        """One token for each row: x (batch, channels) -> y (batch, channels).  ``state``
+        (slots, width - 1, channels) is updated in place unless ``new_state`` is given;
+        ``slots`` int32 (batch,) says which state a row has (outside: the row is idle)."""
+        shape = (self.batch, self.channels)
+        xp = self._at(x, self.torch_dtype, shape, "x")
+        wp = self._at(w, torch.float32, (self.channels, self.width), "w")
+        bp = self._maybe_at(bias, torch.float32, (self.channels,), "bias")
+        n, tp, sp, np_ = self._slots(state, new_state, slots, self.torch_dtype,
+                                     self.state_shape[1:])
+        out, op = self._out(out, self.torch_dtype, shape, "out")
+        check(capi.fno_causal_conv_step(self.handle, xp, wp, bp, tp, n, sp, np_, op,
+                                        self._launch_stream(stream)), "fno_causal_conv_step")
+        return out
+
+
+class SelectiveScan(_DevicePlan):
+    """The selective state space scan (``fno_scan_*``): with d = softplus(dt + dt_bias)
+    (or the sum itself for softplus=False),
+
+        h_t = e^{d_t A} h_{t-1} + d_t x_t B_t,   y_t = (C_t h_t + D x_t) silu(z_t)
+
+    for each channel of x, dt, z (batch, length, channels), whose group shares B and C
+    (batch, length, groups, states).  A (channels, states), D and dt_bias (channels,)
+    are float32, states h (batch, channels, states) float32; D, z, dt_bias may be None.
+    ``backward=True`` prepares the workspace of ``backward``."""
+
+    def __init__(self, batch, length, channels, states, groups=1, softplus=True, dtype="f32",
+                 backward=False):
+        d = capi.fno_scan_desc_t()
+        d.batch, d.length = int(batch), int(length)
+        d.channels, d.states = _int32(channels, "channels"), _int32(states, "states")
+        d.groups, d.softplus = _int32(groups, "groups"), int(bool(softplus))
+        d.dtype = _code(capi.DTYPE_CODES, dtype, "dtype")
+        d.flags = capi.FNO_SCAN_BACKWARD if backward else 0
+        self._own(*capi.fno_scan_plan(d), "scan")
+        self.torch_dtype = _DTYPES[dtype]
+        self.batch, self.length, self.channels = d.batch, d.length, d.channels
+        self.a_shape = (d.channels, d.states)
+        self.x_shape = (d.batch, d.length, d.channels)
+        self.b_shape = (d.batch, d.length, d.groups, d.states)
+        self.state_shape = (d.batch, d.channels, d.states)
+
+    def _inputs(self, x, dt, A, B, C, D, z, dt_bias, row, bc):
+        at, maybe, t = self._at, self._maybe_at, self.torch_dtype
+        f32, c = torch.float32, (self.channels,)
+        return (at(x, t, row, "x"), at(dt, t, row, "dt"), at(A, f32, self.a_shape, "A"),
+                at(B, t, bc, "B"), at(C, t, bc, "C"), maybe(D, f32, c, "D"),
+                maybe(z, t, row, "z"), maybe(dt_bias, f32, c, "dt_bias"))
+
+    def _sequence(self, x, dt, A, B, C, D, z, dt_bias, lengths, state):
+        return (*self._inputs(x, dt, A, B, C, D, z, dt_bias, self.x_shape, self.b_shape),
+                self._maybe_at(lengths, torch.int32, (self.batch,), "lengths"),
+                self._maybe_at(state, torch.float32, self.state_shape, "state"))
+
+    def forward(self, x, dt, A, B, C, D=None, z=None, dt_bias=None, lengths=None, state=None,
+                want_state=False, out=None, stream=None):
+        """(y, final state or None).  ``lengths`` int32 (batch,): tokens of each
+        sequence; ``state``: the initial state (None: zero)."""
+        ptrs = self._sequence(x, dt, A, B, C, D, z, dt_bias, lengths, state)
+        out, op = self._out(out, self.torch_dtype, self.x_shape, "out")
+        final = self._empty(self.state_shape, torch.float32) if want_state else None
+        check(capi.fno_scan_forward(self.handle, *ptrs, op, _ptr(final), self._workspace(),
+                                    self._launch_stream(stream)), "fno_scan_forward")
+        return out, final
+
+    __call__ = forward
+
+    def backward(self, x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, lengths=None, state=None,
+                 dstate=None, stream=None):
+        """Gradients as a dict: dx, ddt, dA, dB, dC, and where their input was given dD,
+        dz, ddt_bias, dstate (of the initial state).  ``dstate=`` is the gradient of the
+        final state (None: zero)."""
+        ptrs = self._sequence(x, dt, A, B, C, D, z, dt_bias, lengths, state)
+        dyp = self._at(dy, self.torch_dtype, self.x_shape, "dy")
+        dsp = self._maybe_at(dstate, torch.float32, self.state_shape, "dstate")
+        t, f32 = self.torch_dtype, torch.float32
+        shapes = {"dx": (self.x_shape, t), "ddt": (self.x_shape, t), "dA": (self.a_shape, f32),
+                  "dB": (self.b_shape, t), "dC": (self.b_shape, t)}
+        if D is not None:
+            shapes["dD"] = ((self.channels,), f32)
+        if z is not None:
+            shapes["dz"] = (self.x_shape, t)
+        if dt_bias is not None:
+            shapes["ddt_bias"] = ((self.channels,), f32)
+        if state is not None:
+            shapes["dstate"] = (self.state_shape, f32)
+        out = {name: self._empty(*s) for name, s in shapes.items()}
+        p = {name: v.data_ptr() for name, v in out.items()}
+        check(capi.fno_scan_backward(
+            self.handle, *ptrs, dyp, dsp, p["dx"], p["ddt"], p["dA"], p["dB"], p["dC"],
+            p.get("dD"), p.get("dz"), p.get("ddt_bias"), p.get("dstate"), self._workspace(),
+            self._launch_stream(stream)), "fno_scan_backward")
+        return out
+
+    def step(self, x, dt, A, B, C, state, D=None, z=None, dt_bias=None, slots=None,
+             new_state=None, out=None, stream=None):
+        """One token for each row: x, dt, z (batch, channels), B, C (batch, groups,
+        states) -> y (batch, channels).  ``state`` (slots, channels, states) is updated in
+        place unless ``new_state`` is given; ``slots`` int32 (batch,) says which state a
+        row has (outside: the row is idle)."""
+        shape = (self.batch, self.channels)
+        ptrs = self._inputs(x, dt, A, B, C, D, z, dt_bias, shape,
+                            (self.batch,) + self.b_shape[2:])
+        n, tp, sp, np_ = self._slots(state, new_state, slots, torch.float32, self.a_shape)
+        out, op = self._out(out, self.torch_dtype, shape, "out")
+        check(capi.fno_scan_step(self.handle, *ptrs, tp, n, sp, np_, op,
+                                 self._launch_stream(stream)), "fno_scan_step")
         return out

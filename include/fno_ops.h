@@ -8,12 +8,16 @@
  *   fno_linear_grad_*  weight and bias gradient of a 1x1 linear from the 8-bit
  *                      checkpoint of its input;
  *   fno_linattn_*      linear attention with a decay for each head: prompts,
- *                      single tokens, gradients.
+ *                      single tokens, gradients;
+ *   fno_rotary_*       rotary positions of its queries and keys;
+ *   fno_causal_conv_*  short causal convolutions along time, and
+ *   fno_scan_*         the selective state space scan behind them: prompts, single
+ *                      tokens, gradients.
  *
  * They surround the spectral layers of fno.h in a deep or time-dependent
  * neural operator: the sandwich norm and the checkpoints work on the layers'
- * channels-first fields as well as on token rows, and the linear attention
- * carries the history of a simulation from frame to frame.
+ * channels-first fields as well as on token rows, and the linear attention or
+ * the scan carries the history of a simulation from frame to frame.
  *
  * The conventions of fno.h hold: fno_status_t from every call, nothing thrown
  * or printed; device pointers are the caller's, 16-byte aligned
@@ -245,6 +249,171 @@ fno_status_t fno_linattn_step(fno_linattn_t plan, const void *q, const void *k, 
  * fno_plan_get_device_error).                                                */
 fno_status_t fno_linattn_get_device_error(fno_linattn_t plan, fno_stream_t stream);
 fno_status_t fno_linattn_destroy(fno_linattn_t plan);
+
+/* -------------------------------------------------------------------------
+ * Rotary positions.
+ * The first `rotary_dim` elements of each head are pairs (a, b), pair i of
+ * rotary_dim / 2: elements i and i + rotary_dim / 2 (FNO_ROTARY_HALF) or 2 i and
+ * 2 i + 1 (FNO_ROTARY_INTERLEAVED).  A token at position p turns pair i to
+ *   m (a cos(p f_i) - b sin(p f_i)),  m (b cos(p f_i) + a sin(p f_i)),
+ *   f_i = base^(-2 i / rotary_dim),  m = 1,
+ * and the rest of the head is copied.  For contexts longer than those trained on
+ * (`factor` times):
+ *   FNO_ROTARY_LINEAR  f_i / factor
+ *   FNO_ROTARY_BASE    base times factor^(rotary_dim / (rotary_dim - 2))  (rotary_dim > 2)
+ *   FNO_ROTARY_RAMP    f_i (k + (1 - k) / factor), where a pair that makes `fast` turns or
+ *                      more over `original` positions has k = 1 (it stays), one that makes
+ *                      `slow` or fewer k = 0, and k is linear in the turns between;
+ *                      m = 1 + 0.1 log(factor)
+ * Angles are exact to 2^-32 of a turn and to what f_i's 53 bits give at any position of
+ * 32 bits; cosines and sines are float32's.
+ * ------------------------------------------------------------------------- */
+typedef enum fno_rotary_layout_e {
+    FNO_ROTARY_HALF = 0, FNO_ROTARY_INTERLEAVED = 1
+} fno_rotary_layout_t;
+
+typedef enum fno_rotary_scaling_e {
+    FNO_ROTARY_NONE = 0, FNO_ROTARY_LINEAR = 1, FNO_ROTARY_BASE = 2, FNO_ROTARY_RAMP = 3
+} fno_rotary_scaling_t;
+
+typedef struct fno_rotary_s *fno_rotary_t;
+
+typedef struct fno_rotary_desc_s {
+    int64_t batch, length;    /* >= 1                                                     */
+    int32_t heads;            /* of q, >= 1                                               */
+    int32_t kv_heads;         /* of k, >= 0 (0: there is no k)                            */
+    int32_t dim;              /* of a head, 1 .. 1024                                     */
+    int32_t rotary_dim;       /* even, 2 .. min(dim, 256)                                 */
+    fno_rotary_layout_t layout;
+    fno_rotary_scaling_t scaling;
+    double base;              /* > 1                                                      */
+    double factor;            /* >= 1 (unless FNO_ROTARY_NONE)                            */
+    double original, fast, slow;    /* FNO_ROTARY_RAMP: > 0, fast > slow >= 0             */
+    fno_dtype_t dtype;        /* storage type of q and k                                  */
+} fno_rotary_desc_t;
+
+/* Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_MEMORY, CUDA. */
+fno_status_t fno_rotary_plan(fno_rotary_t *plan, const fno_rotary_desc_t *desc);
+
+/* q (batch, length, heads, dim), k (batch, length, kv_heads, dim) -> qo, ko, which may be
+ * q and k themselves.  k and ko are NULL for kv_heads = 0.  Token t of sequence b has
+ *   positions  int32 (batch, length): its position, or NULL
+ *   offsets    int32 (batch): position offsets[b] + t, or NULL (at most one of the two)
+ * or, both NULL, position t.  transpose != 0: the gradients of q and k from those of qo and
+ * ko (each pair turned back, times m).                                        */
+fno_status_t fno_rotary_apply(fno_rotary_t plan, const void *q, const void *k,
+                              const int32_t *positions, const int32_t *offsets,
+                              int32_t transpose, void *qo, void *ko, fno_stream_t stream);
+fno_status_t fno_rotary_destroy(fno_rotary_t plan);
+
+/* -------------------------------------------------------------------------
+ * Short causal convolution of each channel along time.
+ *   y_t = act(bias[c] + sum_j w[c, j] x_{t - width + 1 + j}),   j = 0 .. width - 1
+ *   x, y (batch, length, channels): storage type; w (channels, width), bias (channels)
+ *     float32, bias NULL: zero
+ *   act: none, or v / (1 + e^-v) (1e-6 relative for |v| up to 10)
+ *   states (batch, width - 1, channels), storage type: the inputs in front of the first
+ *     token, oldest first
+ *   lengths (batch) int32 or NULL: sequence b has max(0, min(lengths[b], length)) tokens; y
+ *     and dx beyond are 0 and x and dy beyond are not looked at
+ * ------------------------------------------------------------------------- */
+typedef enum fno_act_e { FNO_ACT_NONE = 0, FNO_ACT_SILU = 1 } fno_act_t;
+
+typedef struct fno_causal_conv_s *fno_causal_conv_t;
+
+#define FNO_CAUSAL_CONV_BACKWARD 1u   /* the workspace is that of the backward              */
+
+/* batch, length, channels >= 1; 2 <= width <= 8.  Errors: INVALID_ARG, UNSUPPORTED,
+ * OUT_OF_MEMORY, CUDA.                                                        */
+fno_status_t fno_causal_conv_plan(fno_causal_conv_t *plan, int64_t batch, int64_t length,
+                                  int32_t channels, int32_t width, fno_act_t act,
+                                  fno_dtype_t dtype, uint32_t flags);
+fno_status_t fno_causal_conv_workspace_size(fno_causal_conv_t plan, size_t *bytes);
+
+/* s0 NULL: zeros; sT (the last width - 1 inputs, s0's among them where the sequence is
+ * shorter) NULL: not wanted.  Needs no workspace.                             */
+fno_status_t fno_causal_conv_forward(fno_causal_conv_t plan, const void *x, const float *w,
+                                     const float *bias, const int32_t *lengths, const void *s0,
+                                     void *y, void *sT, fno_stream_t stream);
+
+/* Gradients given dy = dL/dy and dsT = dL/dsT (NULL: zero).  dw (channels, width) and dbias
+ * (channels) float32; dbias, ds0 NULL: not wanted.  Needs FNO_CAUSAL_CONV_BACKWARD. */
+fno_status_t fno_causal_conv_backward(fno_causal_conv_t plan, const void *x, const float *w,
+                                      const float *bias, const int32_t *lengths, const void *s0,
+                                      const void *dy, const void *dsT, void *dx, float *dw,
+                                      float *dbias, void *ds0, void *workspace,
+                                      fno_stream_t stream);
+
+/* One token for each of the plan's `batch` rows: x, y (batch, channels).  state, new_state
+ * (num_slots, width - 1, channels): row b reads state[slots[b]] and writes
+ * new_state[slots[b]] (new_state may be state itself).  slots NULL: row b uses slot b.  A row
+ * whose slot is outside [0, num_slots) is idle: its y is 0 and no state is touched.  Two rows
+ * of one call may not share a slot.                                           */
+fno_status_t fno_causal_conv_step(fno_causal_conv_t plan, const void *x, const float *w,
+                                  const float *bias, const int32_t *slots, int64_t num_slots,
+                                  const void *state, void *new_state, void *y,
+                                  fno_stream_t stream);
+fno_status_t fno_causal_conv_destroy(fno_causal_conv_t plan);
+
+/* -------------------------------------------------------------------------
+ * Selective state space scan.  For each channel c (of group g = c / (channels / groups)) and
+ * state n of a sequence
+ *   d_t = softplus(dt_t[c] + dt_bias[c])   (or dt_t[c] + dt_bias[c])
+ *   h_t[c, n] = e^{d_t A[c, n]} h_{t-1}[c, n] + d_t x_t[c] B_t[g, n]
+ *   y_t[c] = (sum_n C_t[g, n] h_t[c, n] + D[c] x_t[c]) * silu(z_t[c])
+ *   x, dt, z, y (batch, length, channels), B, C (batch, length, groups, states): storage
+ *     type; z NULL: no gate
+ *   A (channels, states), D, dt_bias (channels) float32; D, dt_bias NULL: zero
+ *   states h (batch, channels, states) float32
+ *   lengths (batch) int32 or NULL: sequence b has max(0, min(lengths[b], length)) tokens; y
+ *     and the gradients beyond are 0 and the inputs beyond are not looked at; a sequence of
+ *     no tokens returns its initial state
+ * All arithmetic is float32 on the stored inputs; a decay is good to 2e-7 of itself, softplus
+ * and silu to 1e-6.  An infinity in a token may come out as a NaN.
+ * ------------------------------------------------------------------------- */
+typedef struct fno_scan_s *fno_scan_t;
+
+#define FNO_SCAN_BACKWARD 1u   /* the workspace also covers the backward                    */
+
+typedef struct fno_scan_desc_s {
+    int64_t batch, length;    /* >= 1                                                     */
+    int32_t channels;         /* >= 1, a multiple of groups                               */
+    int32_t states;           /* 1 .. 128                                                 */
+    int32_t groups;           /* >= 1                                                     */
+    int32_t softplus;         /* 0: d = dt + dt_bias                                      */
+    fno_dtype_t dtype;
+    uint32_t flags;
+} fno_scan_desc_t;
+
+/* Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_MEMORY, CUDA. */
+fno_status_t fno_scan_plan(fno_scan_t *plan, const fno_scan_desc_t *desc);
+fno_status_t fno_scan_workspace_size(fno_scan_t plan, size_t *bytes);
+
+/* s0 NULL: zero initial state; sT NULL: final state not wanted. */
+fno_status_t fno_scan_forward(fno_scan_t plan, const void *x, const void *dt, const float *A,
+                              const void *B, const void *C, const float *D, const void *z,
+                              const float *dt_bias, const int32_t *lengths, const float *s0,
+                              void *y, float *sT, void *workspace, fno_stream_t stream);
+
+/* Gradients given dy = dL/dy and dsT = dL/dsT (NULL: zero).  dx, ddt, dz, dB, dC have the
+ * shapes and type of x, dt, z, B, C (of B and C, the sums over a group's channels); dA, dD,
+ * ddt_bias float32.  dz is NULL without z; dD, ddt_bias, ds0 NULL: not wanted.  Needs
+ * FNO_SCAN_BACKWARD.                                                          */
+fno_status_t fno_scan_backward(fno_scan_t plan, const void *x, const void *dt, const float *A,
+                               const void *B, const void *C, const float *D, const void *z,
+                               const float *dt_bias, const int32_t *lengths, const float *s0,
+                               const void *dy, const float *dsT, void *dx, void *ddt, float *dA,
+                               void *dB, void *dC, float *dD, void *dz, float *ddt_bias,
+                               float *ds0, void *workspace, fno_stream_t stream);
+
+/* One token for each of the plan's `batch` rows: x, dt, z, y (batch, channels), B, C (batch,
+ * groups, states).  state, new_state (num_slots, channels, states) float32; slots as for
+ * fno_causal_conv_step.                                                       */
+fno_status_t fno_scan_step(fno_scan_t plan, const void *x, const void *dt, const float *A,
+                           const void *B, const void *C, const float *D, const void *z,
+                           const float *dt_bias, const int32_t *slots, int64_t num_slots,
+                           const float *state, float *new_state, void *y, fno_stream_t stream);
+fno_status_t fno_scan_destroy(fno_scan_t plan);
 
 #ifdef __cplusplus
 }
