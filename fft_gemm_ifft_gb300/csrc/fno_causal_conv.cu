@@ -1,9 +1,11 @@
 // fno_causal_conv.cu -- short causal convolutions of every channel along time, with their
 // activation: whole sequences, gradients, single tokens.
 //
-// 2 width multiply-adds an element: bound by bytes.  A thread takes V channels (one load)
-// of a run of tokens with the last inputs in registers, so that an input is loaded once and
-// the width - 1 in front of a run once more.
+// 2 width multiply-adds an element: bound by bytes.  A thread takes two channels (one, where
+// their number is odd) of a run of tokens with the last inputs in registers, so that an input
+// is loaded once and the width - 1 in front of a run once more.  Two channels and no more:
+// the weights, the window and eight tokens' loads then take few enough registers for the
+// warps that keep enough loads on their way.
 #include "fno_ops_internal.h"
 
 using namespace fno;
@@ -32,8 +34,8 @@ struct Args {
     const int32_t *lengths;
     void *y, *sT, *dx, *ds0;
     float *part;               // per part: dw (width, channels), then dbias
-    int64_t batch, length;
-    int channels, run, parts;
+    int64_t rows;              // runs of all sequences
+    int length, channels, run, across;
     bool silu;
 };
 
@@ -60,7 +62,7 @@ __device__ __forceinline__ void store(T *p, const float *v) {
 
 // Input s of a sequence (s < 0: of its initial state).
 template <typename T, int V, int W>
-__device__ __forceinline__ void input(const Args &p, int64_t b, int64_t s, int c, float *v) {
+__device__ __forceinline__ void input(const Args &p, int64_t b, int s, int c, float *v) {
     if (s >= 0) {
         load<T, V>(static_cast<const T *>(p.x) + (b * p.length + s) * p.channels + c, v);
     } else if (p.s0) {
@@ -70,37 +72,61 @@ __device__ __forceinline__ void input(const Args &p, int64_t b, int64_t s, int c
         for (int i = 0; i < V; ++i) v[i] = 0.0f;
     }
 }
-__device__ __forceinline__ int64_t tokens(const Args &p, int64_t b) {
-    return p.lengths ? max((int64_t)0, min((int64_t)p.lengths[b], p.length)) : p.length;
+__device__ __forceinline__ int tokens(const Args &p, int64_t b) {
+    return p.lengths ? max(0, min(p.lengths[b], p.length)) : p.length;
 }
+// The weights (channels, W) of V channels, tap by tap.
+template <int V, int W>
+__device__ __forceinline__ void load_weights(const Args &p, int c, float (&w)[W][V],
+                                             float (&bias)[V]) {
+    float flat[V * W];
+    const float *from = p.w + (int64_t)c * W;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        const Pack<float, V> a = *reinterpret_cast<const Pack<float, V> *>(from + k * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) flat[k * V + i] = a.v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = flat[i * W + j];
+        bias[i] = p.bias ? p.bias[c + i] : 0.0f;
+    }
+}
+// A block: `across` threads over channels (all blockIdx.y make), the rest over runs.  Which
+// run of which sequence:
+struct Run {
+    int64_t b;
+    int t0, t1;
+    __device__ Run(const Args &p, int64_t row) {
+        const int runs = (p.length + p.run - 1) / p.run;
+        b = row <= 0xffffffffll ? (int64_t)((uint32_t)row / (uint32_t)runs) : row / runs;
+        t0 = (int)(row - b * runs) * p.run;
+        t1 = min(t0 + p.run, p.length);
+    }
+};
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads)
 k_conv(const Args p) {
     constexpr int U = 8;                       // tokens whose loads are in flight
-    const int cols = p.channels / V;
-    const int64_t runs = (p.length + p.run - 1) / p.run;
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t row = id / cols;
-    if (row >= p.batch * runs) return;
-    const int c = (int)(id - row * cols) * V;
-    const int64_t b = row / runs, t0 = (row - b * runs) * p.run;
-    const int64_t t1 = min(t0 + p.run, p.length), n = tokens(p, b);
+    const int lane = threadIdx.x % p.across, rank = threadIdx.x / p.across;
+    const int c = (blockIdx.y * p.across + lane) * V;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / p.across) + rank;
+    if (row >= p.rows || c >= p.channels) return;
+    const Run r(p, row);
+    const int n = tokens(p, r.b), end = min(r.t1, n);
     float w[W][V], bias[V], win[W - 1][V];     // win: the inputs in front, oldest first
+    load_weights<V, W>(p, c, w, bias);
+    const int64_t at = (r.b * p.length + r.t0) * p.channels + c;
+    T *y = static_cast<T *>(p.y) + at;
+    const T *x = static_cast<const T *>(p.x) + at;
+    if (r.t0 < end) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = p.w[(int64_t)(c + i) * W + j];
-        bias[i] = p.bias ? p.bias[c + i] : 0.0f;
+        for (int j = 0; j < W - 1; ++j) input<T, V, W>(p, r.b, r.t0 - (W - 1) + j, c, win[j]);
     }
-    T *y = static_cast<T *>(p.y) + (b * p.length + t0) * p.channels + c;
-    const int64_t end = min(t1, n);
-    if (t0 < end) {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) input<T, V, W>(p, b, t0 - (W - 1) + j, c, win[j]);
-    }
-    const T *x = static_cast<const T *>(p.x) + (b * p.length + t0) * p.channels + c;
-    for (int64_t t = t0; t < end; t += U) {
+    for (int t = r.t0; t < end; t += U) {
         Pack<T, V> in[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
@@ -122,96 +148,93 @@ k_conv(const Args p) {
                 for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
                 win[W - 2][i] = v[i];
             }
-            store<T, V>(y + (int64_t)k * p.channels, o);
+            store<T, V>(y, o);
+            y += p.channels;
         }
         x += (int64_t)U * p.channels;
-        y += (int64_t)U * p.channels;
     }
     const float zero[V] = {};
-    for (int64_t t = max(t0, end); t < t1; ++t)
-        store<T, V>(static_cast<T *>(p.y) + (b * p.length + t) * p.channels + c, zero);
-    if (p.sT && t0 == 0) {
+    y = static_cast<T *>(p.y) + at;
+    for (int t = max(r.t0, end); t < r.t1; ++t)
+        store<T, V>(y + (int64_t)(t - r.t0) * p.channels, zero);
+    if (p.sT && r.t0 == 0) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             float v[V];
-            input<T, V, W>(p, b, n - (W - 1) + j, c, v);
-            store<T, V>(static_cast<T *>(p.sT) + (b * (W - 1) + j) * p.channels + c, v);
+            input<T, V, W>(p, r.b, n - (W - 1) + j, c, v);
+            store<T, V>(static_cast<T *>(p.sT) + (r.b * (W - 1) + j) * p.channels + c, v);
         }
     }
 }
 
 // Gradients.  Token t's pre-activation gets g_t = dy_t act'(pre_t), worked out from the
 // inputs again; then dx_s = sum_j w_j g_{s + W - 1 - j}, for which a run goes on W - 1
-// tokens, and dw_j = sum_t g_t x_{t - W + 1 + j}.  A block is `across` threads over channels
-// times the rest over runs; every thread takes each (parts x rest)-th run, and the block
-// leaves one sum of its dw and dbias.
+// tokens, and dw_j = sum_t g_t x_{t - W + 1 + j}.  A block takes every gridDim.x-th group of
+// runs and leaves one sum of its dw and dbias.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads)
-k_conv_grad(const Args p, int across) {
-    extern __shared__ float sums[];            // [kThreads][V]
+k_conv_grad(const Args p) {
+    __shared__ float sums[kThreads * V];
     constexpr int U = 4;
-    const int lane = threadIdx.x % across, down = kThreads / across, rank = threadIdx.x / across;
-    const int c = (blockIdx.x * across + lane) * V;
-    const int64_t runs = (p.length + p.run - 1) / p.run, all = p.batch * runs;
+    const int lane = threadIdx.x % p.across, down = kThreads / p.across;
+    const int rank = threadIdx.x / p.across, c = (blockIdx.y * p.across + lane) * V;
     const bool there = c < p.channels;
     float w[W][V], bias[V], dw[W][V], db[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            w[j][i] = there ? p.w[(int64_t)(c + i) * W + j] : 0.0f;
-            dw[j][i] = 0.0f;
-        }
-        bias[i] = there && p.bias ? p.bias[c + i] : 0.0f;
-        db[i] = 0.0f;
+        for (int j = 0; j < W; ++j) w[j][i] = dw[j][i] = 0.0f;
+        bias[i] = db[i] = 0.0f;
     }
-    for (int64_t row = (int64_t)blockIdx.y * down + rank; there && row < all;
-         row += (int64_t)gridDim.y * down) {
-        const int64_t b = row / runs, t0 = (row - b * runs) * p.run;
-        const int64_t t1 = min(t0 + p.run, p.length), n = tokens(p, b);
+    if (there) load_weights<V, W>(p, c, w, bias);
+    for (int64_t row = (int64_t)blockIdx.x * down + rank; there && row < p.rows;
+         row += (int64_t)gridDim.x * down) {
+        const Run r(p, row);
+        const int n = tokens(p, r.b), t0 = r.t0, t1 = r.t1;
         // win: inputs t - W + 1 .. t; acc: the gradients of these inputs so far
         float win[W][V], acc[W][V];
-        const int64_t at = b * p.length * p.channels + c;
-        const int64_t end = min(t1 + W - 1, n);            // tokens that reach the run's inputs
+        const int64_t at = (r.b * p.length + t0) * p.channels + c;
+        const int end = min(t1 + W - 1, n);                // tokens that reach the run's inputs
         // gradients that come from the final state: input n - W + 1 + j has state j
-        const auto from_state = [&](int64_t s, float *v) {
-            const int64_t j = s - n + W - 1;
+        const auto from_state = [&](int s, float *v) {
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = 0.0f;
+            const int j = s - n + W - 1;
             if (p.dsT && s < n && j >= 0)
-                load<T, V>(static_cast<const T *>(p.dsT) + (b * (W - 1) + j) * p.channels + c, v);
+                load<T, V>(static_cast<const T *>(p.dsT) + (r.b * (W - 1) + j) * p.channels + c, v);
         };
-        const auto finish = [&](int64_t s, const float *v) {       // input s is complete
+        const auto finish = [&](int s, const float *v) {       // input s is complete
             if (s >= t0 && s < t1) {
-                store<T, V>(static_cast<T *>(p.dx) + at + s * p.channels, v);
+                store<T, V>(static_cast<T *>(p.dx) + at + (int64_t)(s - t0) * p.channels, v);
             } else if (s < 0 && t0 == 0 && p.ds0) {
-                store<T, V>(static_cast<T *>(p.ds0) + (b * (W - 1) + s + W - 1) * p.channels + c,
+                store<T, V>(static_cast<T *>(p.ds0) + (r.b * (W - 1) + s + W - 1) * p.channels + c,
                             v);
             }
         };
         if (t0 < n || t0 == 0) {
 #pragma unroll
             for (int j = 1; j < W; ++j) {
-                input<T, V, W>(p, b, t0 - W + j, c, win[j]);
+                input<T, V, W>(p, r.b, t0 - W + j, c, win[j]);
                 from_state(t0 - W + j, acc[j]);
             }
         }
-        int64_t t = t0;
-        for (; t < end; t += U) {
+        const T *x = static_cast<const T *>(p.x) + at, *dy = static_cast<const T *>(p.dy) + at;
+        for (int t = t0; t < end; t += U) {
             Pack<T, V> xin[U], gin[U];
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 if (t + k < end) {
-                    const int64_t o = at + (t + k) * p.channels;
-                    xin[k] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(p.x) + o);
-                    gin[k] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(p.dy) + o);
+                    xin[k] = *reinterpret_cast<const Pack<T, V> *>(x + (int64_t)k * p.channels);
+                    gin[k] = *reinterpret_cast<const Pack<T, V> *>(dy + (int64_t)k * p.channels);
                 }
+            x += (int64_t)U * p.channels;
+            dy += (int64_t)U * p.channels;
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 if (t + k >= end) break;
                 float last[V];
                 from_state(t + k, last);
-                const bool mine = t + k < t1;
+                const float mine = t + k < t1 ? 1.0f : 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -230,7 +253,7 @@ k_conv_grad(const Args p, int across) {
                     }
 #pragma unroll
                     for (int j = 0; j < W; ++j) acc[j][i] = fmaf(w[j][i], g, acc[j][i]);
-                    if (mine) {
+                    if (mine != 0.0f) {
 #pragma unroll
                         for (int j = 0; j < W; ++j) dw[j][i] = fmaf(g, win[j][i], dw[j][i]);
                         db[i] += g;
@@ -242,37 +265,33 @@ k_conv_grad(const Args p, int across) {
         // what the last tokens leave: inputs end - W + 1 .. end - 1 (those in front of the
         // first token where the sequence has none)
         if (t0 < n || t0 == 0) {
-            const int64_t e = max(end, t0);
+            const int e = max(end, t0);
 #pragma unroll
             for (int j = 1; j < W; ++j) finish(e - W + j, acc[j]);
         }
         const float zero[V] = {};
-        for (int64_t s = max(t0, n); s < t1; ++s)
-            store<T, V>(static_cast<T *>(p.dx) + at + s * p.channels, zero);
+        for (int s = max(t0, n); s < t1; ++s)
+            store<T, V>(static_cast<T *>(p.dx) + at + (int64_t)(s - t0) * p.channels, zero);
     }
-    float *out = p.part + (int64_t)blockIdx.y * (W + 1) * p.channels;
+    float *out = p.part + (int64_t)blockIdx.x * (W + 1) * p.channels;
+#pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float v = db[i];
-#pragma unroll
-            for (int jj = 0; jj < W; ++jj)
-                if (jj == j) v = dw[jj][i];
-            sums[(rank * V + i) * across + lane] = v;
-        }
+        for (int i = 0; i < V; ++i)
+            sums[(rank * V + i) * p.across + lane] = j < W ? dw[j < W ? j : 0][i] : db[i];
         __syncthreads();
-        for (int i = threadIdx.x; i < across * V; i += kThreads) {
+        for (int i = threadIdx.x; i < p.across * V; i += kThreads) {
             float v = 0.0f;
-            for (int r = 0; r < down; ++r) v += sums[r * V * across + i];
-            const int64_t ch = (int64_t)(blockIdx.x * across + i % across) * V + i / across;
+            for (int k = 0; k < down; ++k) v += sums[k * V * p.across + i];
+            const int64_t ch = (int64_t)(blockIdx.y * p.across + i % p.across) * V + i / p.across;
             if (ch < p.channels) out[(int64_t)j * p.channels + ch] = v;
         }
     }
 }
 
 // dw (channels, width) and dbias: the sums of the parts.
-constexpr int kSumRows = 16;
+constexpr int kSumRows = 32;
 __global__ void __launch_bounds__(32 * kSumRows)
 k_conv_sum(const float *__restrict__ part, float *__restrict__ dw, float *__restrict__ db,
            int channels, int width, int parts) {
@@ -341,11 +360,6 @@ fno_status_t with_width(int width, F &&f) {
         default: return f(std::integral_constant<int, 8>());
     }
 }
-// Channels of a thread: those of a 16-byte load (`most` at most) if rows are whole numbers
-// of them, else one.
-template <typename T>
-constexpr int widest(int most) { return kVec<T> < most ? kVec<T> : most; }
-
 struct Sizes {
     size_t row, w, c, s, len;    // bytes of x, w, bias, a state, lengths
 };
@@ -355,14 +369,22 @@ Sizes sizes(const fno_causal_conv_s &p, int64_t length) {
             (size_t)p.channels * 4, n * (p.width - 1) * p.channels * e, n * 4};
 }
 
-int backward_vector(const fno_causal_conv_s &p) {
-    const int v = p.width <= 4 ? 4 : 2;
-    return p.channels % v == 0 ? v : 1;
-}
-int backward_across(const fno_causal_conv_s &p) {
-    const int cols = p.channels / backward_vector(p);
+// Channels of a thread, and threads of a block over the channels.
+int vector(int channels) { return channels % 2 == 0 ? 2 : 1; }
+int across(int channels) {
+    const int cols = channels / vector(channels);
     int a = 1;
     while (a < 32 && a < cols) a *= 2;
+    return a;
+}
+Args common(const fno_causal_conv_s &p, int run) {
+    Args a{};
+    a.length = (int)p.length;
+    a.channels = p.channels;
+    a.run = run;
+    a.rows = p.batch * ceil_div(p.length, run);
+    a.across = across(p.channels);
+    a.silu = p.act == FNO_ACT_SILU;
     return a;
 }
 
@@ -379,7 +401,7 @@ fno_status_t fno_causal_conv_plan(fno_causal_conv_t *out, int64_t batch, int64_t
         (act != FNO_ACT_NONE && act != FNO_ACT_SILU) || !valid_dtype(dtype) ||
         (flags & ~FNO_CAUSAL_CONV_BACKWARD))
         return FNO_ERR_INVALID_ARG;
-    if (width > 8 || (double)batch * (double)(length + width) * channels > kMaxElems)
+    if (width > 8 || length > 2147483647 - 64 || (double)batch * (double)(length + width) * channels > kMaxElems)
         return FNO_ERR_UNSUPPORTED;
     if (inject("plan_alloc")) return FNO_ERR_OUT_OF_MEMORY;
     fno_causal_conv_s *p = new (std::nothrow) fno_causal_conv_s();
@@ -396,22 +418,22 @@ fno_status_t fno_causal_conv_plan(fno_causal_conv_t *out, int64_t batch, int64_t
         delete p;
         return st;
     }
-    // runs of 32 tokens, shorter ones (of 8 at least) while the threads do not fill the SMs
-    const int most = (int)elem_bytes(dtype) == 2 ? 8 : 4;
-    const int v = channels % most == 0 ? most : 1;
-    const int64_t want = (int64_t)p->sms * 1024;
+    // runs of 32 tokens, shorter ones (of 8 at least) while the threads do not fill the SMs;
+    // backward of 64 (its runs reach over 2 width tokens more), a wave or two of blocks
+    const int64_t cols = channels / vector(channels), want = (int64_t)p->sms * 1024;
     p->run = 32;
-    while (p->run > 8 && batch * ceil_div(length, p->run) * (channels / v) < want) p->run /= 2;
-    const int bv = backward_vector(*p), across = backward_across(*p), down = kThreads / across;
-    p->bwd_run = 32;
-    while (p->bwd_run > 8 && batch * ceil_div(length, p->bwd_run) * (channels / bv) < want)
-        p->bwd_run /= 2;
-    // blocks for the SMs twice over, as far as there are runs
-    const int64_t cols = ceil_div(channels / bv, across);
-    int64_t parts = ceil_div((int64_t)4 * p->sms, cols);
+    while (p->run > 8 && batch * ceil_div(length, p->run) * cols < want) p->run /= 2;
+    p->bwd_run = 64;
+    while (p->bwd_run > 16 && batch * ceil_div(length, p->bwd_run) * cols < want) p->bwd_run /= 2;
+    const int a = across(channels), down = kThreads / a;
+    const int64_t blocks = ceil_div(batch * ceil_div(length, p->run), down);
+    if (ceil_div(cols, a) > 65535 || blocks > 2147483647) {
+        delete p;
+        return FNO_ERR_UNSUPPORTED;
+    }
+    const int64_t most = ceil_div((int64_t)8 * p->sms, ceil_div(cols, a));
     const int64_t rows = ceil_div(batch * ceil_div(length, p->bwd_run), down);
-    parts = parts < rows ? parts : rows;
-    p->parts = (int)(parts < 65535 ? parts : 65535);
+    p->parts = (int)(most < rows ? most : rows);
     if (flags & FNO_CAUSAL_CONV_BACKWARD)
         p->workspace = (size_t)p->parts * (width + 1) * channels * 4;
     *out = p;
@@ -433,22 +455,19 @@ fno_status_t fno_causal_conv_forward(fno_causal_conv_t p, const void *x, const f
         {{x, n.row, false}, {w, n.w, false}, {bias, n.c, false}, {lengths, n.len, false},
          {s0, n.s, false}, {y, n.row, true}, {sT, n.s, true}});
     if (st != FNO_OK) return st;
-    Args a{};
+    if (inject("launch")) return FNO_ERR_CUDA;
+    Args a = common(*p, p->run);
     a.x = x, a.w = w, a.bias = bias, a.lengths = lengths, a.s0 = s0, a.y = y, a.sT = sT;
-    a.batch = p->batch, a.length = p->length, a.channels = p->channels, a.run = p->run;
-    a.silu = p->act == FNO_ACT_SILU;
+    const int v = vector(p->channels);
+    const dim3 grid((unsigned)ceil_div(a.rows, kThreads / a.across),
+                    (unsigned)ceil_div(p->channels / v, a.across));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
         return with_width(p->width, [&](auto width) {
-            constexpr int W = decltype(width)::value, V = widest<T>(8);
-            const int v = p->channels % V == 0 ? V : 1;
-            const int64_t all = p->batch * ceil_div(p->length, p->run) * (p->channels / v);
-            if (ceil_div(all, kThreads) > 2147483647) return FNO_ERR_UNSUPPORTED;
-            if (inject("launch")) return FNO_ERR_CUDA;
-            const unsigned blocks = (unsigned)ceil_div(all, kThreads);
-            cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-            if (v == V) k_conv<T, V, W><<<blocks, kThreads, 0, s>>>(a);
-            else k_conv<T, 1, W><<<blocks, kThreads, 0, s>>>(a);
+            constexpr int W = decltype(width)::value;
+            if (v == 2) k_conv<T, 2, W><<<grid, kThreads, 0, s>>>(a);
+            else k_conv<T, 1, W><<<grid, kThreads, 0, s>>>(a);
             return launched();
         });
     });
@@ -470,21 +489,18 @@ fno_status_t fno_causal_conv_backward(fno_causal_conv_t p, const void *x, const 
          {workspace, p->workspace, true}});
     if (st != FNO_OK) return st;
     if (inject("launch")) return FNO_ERR_CUDA;
-    Args a{};
+    Args a = common(*p, p->bwd_run);
     a.x = x, a.w = w, a.bias = bias, a.lengths = lengths, a.s0 = s0, a.dy = dy, a.dsT = dsT;
     a.dx = dx, a.ds0 = ds0, a.part = static_cast<float *>(workspace);
-    a.batch = p->batch, a.length = p->length, a.channels = p->channels, a.run = p->bwd_run;
-    a.silu = p->act == FNO_ACT_SILU;
+    const int v = vector(p->channels);
+    const dim3 grid((unsigned)p->parts, (unsigned)ceil_div(p->channels / v, a.across));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
         return with_width(p->width, [&](auto width) {
-            constexpr int W = decltype(width)::value, V = W <= 4 ? 4 : 2;
-            const int v = backward_vector(*p), across = backward_across(*p);
-            const dim3 grid((unsigned)ceil_div(p->channels / v, across), (unsigned)p->parts);
-            const size_t bytes = (size_t)kThreads * v * 4;
-            if (v == V) k_conv_grad<T, V, W><<<grid, kThreads, bytes, s>>>(a, across);
-            else k_conv_grad<T, 1, W><<<grid, kThreads, bytes, s>>>(a, across);
+            constexpr int W = decltype(width)::value;
+            if (v == 2) k_conv_grad<T, 2, W><<<grid, kThreads, 0, s>>>(a);
+            else k_conv_grad<T, 1, W><<<grid, kThreads, 0, s>>>(a);
             const int64_t outs = (int64_t)p->channels * (W + 1);
             k_conv_sum<<<(unsigned)ceil_div(outs, 32), dim3(32, kSumRows), 0, s>>>(
                 a.part, dw, dbias, p->channels, W, p->parts);

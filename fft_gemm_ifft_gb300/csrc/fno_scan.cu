@@ -20,34 +20,93 @@ FNO_SCAN_EXTERN(__nv_bfloat16)
 
 namespace {
 
-// A thread per (sequence, channel, state): the segments' local values are loaded eight
-// at a time ahead of the chain of multiply-adds.
-__global__ void __launch_bounds__(256)
-k_scan_join(float *__restrict__ local, const float *__restrict__ steps,
-            const float *__restrict__ A, const float *__restrict__ first, int64_t cn, int states,
-            int channels, int segments, bool reverse) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
-    if (e >= cn) return;
-    const int c = (int)(e / states);
-    const float a2 = A[e] * kLog2e;
-    float z = first ? first[b * cn + e] : 0.0f;
-    const int64_t from = reverse ? segments - 1 : 0, dir = reverse ? -1 : 1;
-    float *v = local + (b * segments + from) * cn + e;
-    const float *d = steps + (b * segments + from) * channels + c;
-    for (int s = 0; s < segments; s += 8) {
-        float l[8], w[8];
+// The joining of the segments: a lane per (sequence, channel, state), the segments over a
+// block's warps.  Each warp puts its segments together, all warps go on from those in front
+// of them, and each writes its segments' states (74 segments of 2 x 1024 x 16 with one thread
+// for all of them: 20 us, all of it the latency of the reads).  The second half of the blocks
+// joins the gradients, from the last segment.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+k_scan_join(const Args p) {
+    __shared__ float2 ends[kJoinWarps][32];            // (local value, sum of the steps)
+    const int np = p.shape.np, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const bool reverse = blockIdx.z != 0;
+    const int64_t e = (int64_t)blockIdx.x * 32 + lane, b = blockIdx.y;
+    const int64_t row = (int64_t)p.channels * np, c = e / np;
+    const int n = (int)(e - c * np), each = (p.segments + kJoinWarps - 1) / kJoinWarps;
+    const bool mine = e < row && n < p.states;
+    const int64_t cn = c * p.states + n;
+    const float a2 = mine ? p.A[cn] * kLog2e : 0.0f;
+    const int first = w * each, count = mine ? max(0, min(each, p.segments - first)) : 0;
+    const int64_t dir = reverse ? -1 : 1;
+    const int64_t from = b * p.segments + (reverse ? p.segments - 1 - first : first);
+    float *const v = (reverse ? p.gseg : p.hseg) + from * row + e;
+    const float *const d = p.dseg + from * p.channels + c;
+    const auto walk = [&](float z, auto f) {
+        float steps = 0.0f;
+        for (int s = 0; s < count; s += 8) {
+            float l[8], t[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (s + k < segments) {
-                l[k] = v[dir * (s + k) * cn];
-                w[k] = d[dir * (s + k) * channels];
-            }
+            for (int k = 0; k < 8; ++k)
+                if (s + k < count) {
+                    l[k] = v[dir * (s + k) * row];
+                    t[k] = d[dir * (s + k) * p.channels];
+                }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (s + k < segments) {
-                v[dir * (s + k) * cn] = z;
-                z = fmaf(exp2_fast(a2 * w[k]), z, l[k]);
-            }
+            for (int k = 0; k < 8; ++k)
+                if (s + k < count) {
+                    f(s + k, z);
+                    z = fmaf(exp2_fast(a2 * t[k]), z, l[k]);
+                    steps += t[k];
+                }
+        }
+        return make_float2(z, steps);
+    };
+    ends[w][lane] = walk(0.0f, [](int, float) {});
+    __syncthreads();
+    const float *start = reverse ? p.gsT : p.s0;
+    float z = start && mine ? start[b * p.channels * p.states + cn] : 0.0f;
+    for (int k = 0; k < w; ++k) z = fmaf(exp2_fast(a2 * ends[k][lane].y), z, ends[k][lane].x);
+    walk(z, [&](int s, float at) { v[dir * s * row] = at; });
+}
+
+// Sums over the blocks' parts, in the order of the parts, of dA (channels, padded states) and
+// behind it of D's and the bias' gradients (2 x channels): COLS columns a block, its other
+// threads over the parts, so that many parts of few columns (512 of 1024: 10 us by 32 rows)
+// are read at once.
+template <int COLS>
+__global__ void __launch_bounds__(1024)
+k_scan_sum(const Args p, int64_t parts) {
+    constexpr int kRows = 1024 / COLS;
+    __shared__ float s[kRows][COLS + 1];
+    const int np = p.shape.np, col = threadIdx.x % COLS, r = threadIdx.x / COLS;
+    const int64_t states = (int64_t)p.channels * np, more = 2 * (int64_t)p.channels;
+    const int64_t i = (int64_t)blockIdx.x * COLS + col;
+    const bool of_a = i < states;
+    const float *in = of_a ? p.part_a + i : p.part_d + (i - states);
+    const int64_t n = of_a ? states : more;
+    float v = 0.0f;
+    if (i < states + more) {
+#pragma unroll 8
+        for (int64_t k = r; k < parts; k += kRows) v += in[k * n];
+    }
+    s[r][col] = v;
+    __syncthreads();
+    // by 32 rows, then by one
+    if (r < 32) {
+        for (int k = r + 32; k < kRows; k += 32) v += s[k][col];
+        s[r][col] = v;
+    }
+    __syncthreads();
+    if (r || i >= states + more) return;
+    for (int k = 1; k < 32; ++k) v += s[k][col];
+    if (of_a) {
+        const int64_t c = i / np;
+        if (i - c * np < p.states) p.dA[c * p.states + (i - c * np)] = v;
+    } else if (i - states < p.channels) {
+        if (p.dD) p.dD[i - states] = v;
+    } else if (p.dbias) {
+        p.dbias[i - states - p.channels] = v;
     }
 }
 
@@ -77,7 +136,7 @@ k_scan_step(const T *__restrict__ x, const T *__restrict__ dt, const float *__re
         xv = Storage<T>::load(x + at);
         float d = Storage<T>::load(dt + at);
         if (bias) d += bias[c];
-        if (plus) d = softplus(d);
+        if (plus) d = softplus2(f2(d)).x;
         const float u = d * xv;
         for (int n = q * V; n < states; n += lanes * V) {
             Pack<float, V> h = *reinterpret_cast<const Pack<float, V> *>(state + sn + n);
@@ -97,7 +156,7 @@ k_scan_step(const T *__restrict__ x, const T *__restrict__ dt, const float *__re
             if (D) sum = fmaf(D[c], xv, sum);
             if (z) {
                 const float zv = Storage<T>::load(z + at);
-                sum *= zv * logistic(zv);
+                sum *= zv * logistic2(f2(zv)).x;
             }
         }
         Storage<T>::store(y + at, live ? sum : 0.0f);
@@ -149,14 +208,11 @@ Args common(const fno_scan_s &p) {
     const int e = (int)elem_bytes(d.dtype);
     a.vec_c = vector_bytes(e, {d.channels, a.per_group});
     a.vec_n = vector_bytes(e, {d.states});
+    a.units = (int)ceil_div(a.per_group, 64);
+    a.shape = forward_shape(d);
+    a.seg_len = p.seg_len, a.segments = p.segments;
+    a.span_len = p.span_len, a.spans = p.spans, a.rows = p.rows;
     return a;
-}
-
-int slabs(const fno_scan_s &p, int width, int warps) {
-    const int per = p.d.channels / p.d.groups, nw = state_warps(p.d.states);
-    int s = 1;
-    while (2 * s * nw <= warps && s * width < per) s *= 2;
-    return s;
 }
 
 }  // namespace
@@ -164,22 +220,31 @@ int slabs(const fno_scan_s &p, int width, int warps) {
 namespace fno {
 namespace scan {
 
-fno_status_t join(const Args &a, bool reverse, cudaStream_t s) {
-    const int64_t cn = (int64_t)a.channels * a.states;
-    const dim3 grid((unsigned)ceil_div(cn, 256), (unsigned)a.batch);
-    k_scan_join<<<grid, 256, 0, s>>>(reverse ? a.gseg : a.hseg, a.dseg, a.A,
-                                     reverse ? a.gsT : a.s0, cn, a.states, a.channels, a.segments,
-                                     reverse);
+fno_status_t join(const Args &a, bool both, cudaStream_t s) {
+    Args p = a;
+    p.shape.np = padded_states(a.states);
+    const dim3 grid((unsigned)ceil_div((int64_t)a.channels * p.shape.np, 32), (unsigned)a.batch,
+                    both ? 2 : 1);
+    k_scan_join<<<grid, 32 * kJoinWarps, 0, s>>>(p);
+    return launched();
+}
+
+fno_status_t sum_parts(const Args &a, cudaStream_t s) {
+    const int64_t parts = a.rows * a.spans, cols = (int64_t)a.channels * (a.shape.np + 2);
+    if (parts >= 128) k_scan_sum<8><<<(unsigned)ceil_div(cols, 8), 1024, 0, s>>>(a, parts);
+    else k_scan_sum<32><<<(unsigned)ceil_div(cols, 32), 1024, 0, s>>>(a, parts);
     return launched();
 }
 
 BackwardParts backward_parts(const fno_scan_s &p) {
     const fno_scan_desc_t &d = p.d;
-    const size_t cn = (size_t)d.channels * d.states, b = (size_t)d.batch;
-    const size_t segs = b * p.bwd_segments, tiles = (size_t)ceil_div(d.length, kTile);
-    const bool split = p.bwd_segments > 1, kept = tiles > 1;
-    const int per = d.channels / d.groups;
-    const size_t blocks = (size_t)ceil_div(per, 16 * backward_slabs(p));
+    const size_t np = padded_states(d.states), b = (size_t)d.batch;
+    const size_t states = (size_t)d.channels * np;
+    const size_t segs = b * p.segments, tiles = (size_t)ceil_div(d.length, kTile);
+    const size_t parts = (size_t)p.rows * p.spans;
+    const bool split = p.segments > 1, kept = tiles > 1;
+    const size_t blocks = (size_t)backward_shape(d).chblocks;
+    const size_t units = (size_t)d.groups * ceil_div(d.channels / d.groups, 64);
     BackwardParts w{};
     size_t at = 0;
     const auto take = [&](size_t floats) {
@@ -187,20 +252,17 @@ BackwardParts backward_parts(const fno_scan_s &p) {
         at += (floats * 4 + 255) & ~size_t(255);
         return here;
     };
-    w.hseg = take(split ? segs * cn : 0);
-    w.gseg = take(split ? segs * cn : 0);
+    w.hseg = take(split ? segs * states : 0);
+    w.gseg = take(split ? segs * states : 0);
     w.dseg = take(split ? segs * d.channels : 0);
-    w.hchunk = take(kept ? b * tiles * cn : 0);
-    w.dchunk = take(kept ? b * tiles * d.channels : 0);
+    w.htile = take(kept ? b * tiles * units * 64 * np : 0);
+    w.dtile = take(kept ? b * tiles * d.channels : 0);
     w.part_bc = take(blocks > 1 ? blocks * b * d.length * d.groups * 2 * d.states : 0);
-    w.part_a = take(segs * cn);
-    w.part_d = take(segs * 2 * d.channels);
+    w.part_a = take(parts * states);
+    w.part_d = take(parts * 2 * d.channels);
     w.bytes = at;
     return w;
 }
-
-int forward_slabs(const fno_scan_s &p) { return slabs(p, 32, 4); }
-int backward_slabs(const fno_scan_s &p) { return slabs(p, 16, 8); }
 
 }  // namespace scan
 }  // namespace fno
@@ -217,7 +279,7 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
         return FNO_ERR_INVALID_ARG;
     const double wide = d.channels > (double)d.groups * d.states ? (double)d.channels
                                                                  : (double)d.groups * d.states;
-    if (d.states > kMaxStates || (double)d.batch > 65535.0 * 1024.0 ||
+    if (d.states > kMaxStates || d.length > 2147483647 - 2 * kTile || (double)d.batch > 65535.0 * 1024.0 ||
         (double)d.batch * (double)d.length * wide > kMaxElems ||
         (double)d.batch * d.channels * d.states > kMaxElems)
         return FNO_ERR_UNSUPPORTED;
@@ -230,21 +292,38 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
         delete p;
         return st;
     }
-    const int per = d.channels / d.groups, nw = state_warps(d.states);
-    const int fs = forward_slabs(*p), bs = backward_slabs(*p);
-    const int64_t rows = d.batch * d.groups;
-    split(d.length, rows * ceil_div(per, 32 * fs) * fs * nw, (int64_t)16 * p->sms, kTile,
-          &p->seg_len, &p->segments);
-    split(d.length, rows * ceil_div(per, 16 * bs) * bs * nw, (int64_t)16 * p->sms, kTile,
-          &p->bwd_seg_len, &p->bwd_segments);
-    const double blocks = (double)rows * (double)ceil_div(per, 16) *
-                          (p->segments > p->bwd_segments ? p->segments : p->bwd_segments);
-    if (blocks > 2147483647.0) {
+    // warps that the sequences and channels make, and that the SMs hold
+    const auto warps = [&](const Shape &s) {
+        return ceil_div(d.batch * d.groups, s.seqs) * s.chblocks * ceil_div(s.threads(), 32);
+    };
+    const Shape fw = forward_shape(d), bw = backward_shape(d);
+    split(d.length, warps(fw), (int64_t)16 * p->sms, kTile, &p->seg_len, &p->segments);
+    p->span_len = p->seg_len;
+    p->rows = d.batch;
+    if (p->segments > 1 && (d.flags & FNO_SCAN_BACKWARD)) {
+        // the last pass of the backward has twice the registers, half the warps: its spans
+        // are whole numbers of segments, a wave of blocks if they can
+        int spans;
+        split(d.length, warps(bw), (int64_t)8 * p->sms, kTile, &p->span_len, &spans);
+        const int64_t each = ceil_div(p->segments, spans);
+        p->seg_len = ceil_div(ceil_div(p->span_len, each), kTile) * kTile;
+        p->span_len = each * p->seg_len;
+        p->segments = (int)ceil_div(d.length, p->seg_len);
+    } else if (p->segments == 1) {
+        // a wave of its blocks; each goes on with further sequences, A's gradient in registers
+        const int64_t most = ceil_div((int64_t)8 * p->sms, warps(bw) / d.batch);
+        p->rows = ceil_div(d.batch, ceil_div(d.batch, most));
+    }
+    p->spans = (int)ceil_div(d.length, p->span_len);
+    // (blocks of a launch; the padded states of all sequences)
+    if ((double)warps(fw) * p->segments > 2147483647.0 ||
+        (double)warps(bw) * p->spans > 2147483647.0 ||
+        (double)d.batch * (d.channels + 63.0 * d.groups) * fw.np > 4.0 * kMaxElems) {
         delete p;
         return FNO_ERR_UNSUPPORTED;
     }
     if (p->segments > 1)
-        p->workspace = (size_t)d.batch * p->segments * d.channels * (d.states + 1) * 4;
+        p->workspace = (size_t)d.batch * p->segments * d.channels * (fw.np + 1) * 4;
     if (d.flags & FNO_SCAN_BACKWARD) {
         const size_t n = backward_parts(*p).bytes;
         if (n > p->workspace) p->workspace = n;
@@ -277,7 +356,7 @@ fno_status_t fno_scan_forward(fno_scan_t p, const void *x, const void *dt, const
     a.x = x, a.dt = dt, a.A = A, a.B = B, a.C = C, a.D = D, a.z = z, a.bias = dt_bias;
     a.lengths = lengths, a.s0 = s0, a.y = y, a.sT = sT;
     a.hseg = static_cast<float *>(workspace);
-    a.dseg = a.hseg ? a.hseg + (size_t)p->d.batch * p->segments * p->d.channels * p->d.states
+    a.dseg = a.hseg ? a.hseg + (size_t)p->d.batch * p->segments * p->d.channels * a.shape.np
                     : nullptr;
     return with_storage(p->d.dtype, [&](auto t) {
         return forward_of<decltype(t)>(*p, a, reinterpret_cast<cudaStream_t>(stream));
@@ -313,7 +392,7 @@ fno_status_t fno_scan_backward(fno_scan_t p, const void *x, const void *dt, cons
         return reinterpret_cast<float *>(static_cast<char *>(workspace) + at);
     };
     a.hseg = part(w.hseg), a.gseg = part(w.gseg), a.dseg = part(w.dseg);
-    a.hchunk = part(w.hchunk), a.dchunk = part(w.dchunk);
+    a.htile = part(w.htile), a.dtile = part(w.dtile);
     a.part_bc = part(w.part_bc), a.part_a = part(w.part_a), a.part_d = part(w.part_d);
     return with_storage(p->d.dtype, [&](auto t) {
         return backward_of<decltype(t)>(*p, a, reinterpret_cast<cudaStream_t>(stream));

@@ -6,20 +6,29 @@
 struct fno_scan_s {
     fno_scan_desc_t d;
     int sms;
-    // forward: the time axis in `segments` parts that run side by side
-    int64_t seg_len;
-    int segments;
-    // backward: parts of the time axis, in whole chunks
-    int64_t bwd_seg_len;
-    int bwd_segments;
+    // the time axis in `segments` parts that run side by side; for the last pass of the
+    // backward, `spans` of several segments each, and the sequences that run side by side
+    int64_t seg_len, span_len;
+    int segments, spans;
+    int64_t rows;
     size_t workspace;
 };
 
 namespace fno {
 namespace scan {
 
-constexpr int kMaxStates = 128;
-constexpr int kTile = 8;       // tokens staged at a time, and between two states kept for the backward
+constexpr int kMaxStates = 64;
+constexpr int kTile = 8;       // tokens staged at a time, and between two states kept for
+                               // the backward
+
+// How a kernel's block divides its work: `seqs` sequences (and groups) x `slabs` of 2 lanes
+// channels x `warps` that share a channel's states x `lanes` of two channels each.
+struct Shape {
+    int seqs, slabs, warps, lanes;
+    int chblocks;              // blocks of channels in a group
+    int np;                    // states, padded to whole lanes' shares
+    __host__ __device__ int threads() const { return seqs * slabs * warps * lanes; }
+};
 
 // The operands of a scan, and where its work lies in the workspace.
 struct Args {
@@ -28,109 +37,267 @@ struct Args {
     const int32_t *lengths;
     void *y, *dx, *ddt, *dB, *dC, *dz;
     float *sT, *dA, *dD, *dbias, *ds0;
-    // per (sequence, segment): states at its end and, after the joining, in front of
-    // it; likewise the gradients that reach its end; the sum of the steps
+    // per (sequence, segment), (channels, padded states): states at its end and, after the
+    // joining, in front of it; likewise the gradients that reach its end; the sums of the
+    // steps (channels)
     float *hseg, *gseg, *dseg;
-    // per (sequence, chunk): the state in front of it from zero at the segment's
-    // start, and the sum of the steps since then
-    float *hchunk, *dchunk;
-    // partial sums of the gradients: of B and C per block of channels, of A, D and the
-    // bias per (sequence, segment)
+    // per (sequence, tile): the state in front of it from zero at the segment's start (in
+    // the order of tile_at), and the sum of the steps since then
+    float *htile, *dtile;
+    // partial sums of the gradients: of B and C per block of channels, of A (channels,
+    // padded states), D and the bias per (row of blocks, span)
     float *part_bc, *part_a, *part_d;
     int64_t length, seg_len;
-    int batch, channels, per_group, groups, states, segments, chblocks;
-    int slabs;                 // of channels in a block
+    int64_t span_len, rows;    // last pass backward: tokens and sequences side by side
+    int batch, channels, per_group, groups, states, segments, spans;
+    int units;                 // of 64 channels in a group
     bool softplus;
     int vec_c, vec_n;          // bytes that rows of channels and of states may be moved in
+    Shape shape;
 };
 
 // What a plan needs of the workspace for the backward, and its parts.
 struct BackwardParts {
-    size_t hseg, gseg, dseg, hchunk, dchunk, part_bc, part_a, part_d, bytes;
+    size_t hseg, gseg, dseg, htile, dtile, part_bc, part_a, part_d, bytes;
 };
 BackwardParts backward_parts(const fno_scan_s &p);
 
 template <typename T> fno_status_t forward_of(const fno_scan_s &p, Args a, cudaStream_t s);
 template <typename T> fno_status_t backward_of(const fno_scan_s &p, Args a, cudaStream_t s);
-// The states in front of the segments from the local ones at their ends, in place
-// (reverse: the gradients that reach the segments' ends, from the last one).
-fno_status_t join(const Args &a, bool reverse, cudaStream_t s);
+// The states in front of the segments from the local ones at their ends, in place (both:
+// and the gradients that reach the segments' ends, from the last one).
+fno_status_t join(const Args &a, bool both, cudaStream_t s);
+// dA, dD and the bias' gradient from the blocks' parts.
+fno_status_t sum_parts(const Args &a, cudaStream_t s);
 
-// States per lane of a quad (1, 2 or 4) and warps that share a slab's states.
-inline int lane_states(int states) { return states <= 4 ? 1 : states <= 8 ? 2 : 4; }
-inline int state_warps(int states) {
-    int w = 1;
-    while (16 * w < states) w *= 2;
-    return w;
+inline int pow2_at_least(int64_t n) {
+    int v = 1;
+    while (v < n) v *= 2;
+    return v;
 }
-inline int padded_states(int states) { return 4 * lane_states(states) * state_warps(states); }
-int forward_slabs(const fno_scan_s &p);
-int backward_slabs(const fno_scan_s &p);
+// States of a lane forward, and padded to a power of two.
+inline int lane_states(int states) { return states <= 4 ? 4 : states <= 8 ? 8 : 16; }
+inline int padded_states(int states) { return pow2_at_least(states < 4 ? 4 : states); }
+// Blocks of four warps (as many as share a channel's states, if more).  Groups of up to 32
+// channels take half a warp, so that a block holds more sequences instead.
+inline Shape forward_shape(const fno_scan_desc_t &d) {
+    const int per = d.channels / d.groups;
+    Shape s{};
+    s.np = padded_states(d.states);
+    s.warps = s.np / lane_states(d.states);
+    s.lanes = s.warps > 1 || per > 32 ? 32 : 16;
+    const int64_t slabs = ops::ceil_div(per, 2 * s.lanes), all = d.batch * d.groups;
+    s.slabs = s.warps >= 4 ? 1 : 4 / s.warps;
+    while (s.slabs / 2 >= slabs) s.slabs /= 2;
+    s.seqs = 1;
+    while (2 * s.seqs * s.slabs * s.warps * s.lanes <= 128 && s.seqs < all) s.seqs *= 2;
+    s.chblocks = (int)ops::ceil_div(slabs, s.slabs);
+    return s;
+}
+// Backward a lane has eight states (four of four) and a unit is a whole warp.
+inline Shape backward_shape(const fno_scan_desc_t &d) {
+    Shape s{};
+    s.np = padded_states(d.states);
+    s.warps = s.np <= 4 ? 1 : s.np / 8;
+    s.lanes = 32;
+    const int64_t slabs = ops::ceil_div(d.channels / d.groups, 64);
+    s.slabs = s.warps >= 4 || slabs == 1 ? 1 : 4 / s.warps;
+    s.seqs = 1;
+    s.chblocks = (int)ops::ceil_div(slabs, s.slabs);
+    return s;
+}
 
 // ---------------------------------------------------------------------------
-// device helpers
+// a thread's elements
+// ---------------------------------------------------------------------------
+// Its place in the block: two channels from 2 lane on of its slab.
+struct Unit {
+    int lane, sub, slab, seq;
+    __device__ Unit(int tid, const Shape &s) {
+        const int r = tid / s.lanes, q = r / s.warps;
+        lane = tid - r * s.lanes;
+        sub = r - q * s.warps;
+        seq = q / s.slabs;
+        slab = q - seq * s.slabs;
+    }
+};
+
+// NS states of two channels from rows `pitch` apart, where `left` channels and `there`
+// states are left; zero where there are none.  `flip` exchanges the two quads of eight.
+template <int NS>
+__device__ __forceinline__ void read_states(const float *at, int left, int there, int pitch,
+                                            float (&v)[2][NS], int flip) {
+    const bool quads = pitch % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < NS / 4; ++q) {
+            const int n = 4 * (q ^ flip);
+            const float *p = at + (int64_t)j * pitch + n;
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (j < left) {
+                if (quads) {
+                    if (n < there) f = *reinterpret_cast<const float4 *>(p);
+                } else {
+                    if (n < there) f.x = p[0];
+                    if (n + 1 < there) f.y = p[1];
+                    if (n + 2 < there) f.z = p[2];
+                    if (n + 3 < there) f.w = p[3];
+                }
+            }
+            v[j][4 * q] = f.x, v[j][4 * q + 1] = f.y, v[j][4 * q + 2] = f.z, v[j][4 * q + 3] = f.w;
+        }
+}
+template <int NS>
+__device__ __forceinline__ void write_states(float *at, int left, int there, int pitch,
+                                             const float (&v)[2][NS], int flip) {
+    const bool quads = pitch % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < NS / 4; ++q) {
+            const int n = 4 * (q ^ flip);
+            float *p = at + (int64_t)j * pitch + n;
+            const float *f = v[j] + 4 * q;
+            if (j >= left) continue;
+            if (quads) {
+                if (n < there) *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < there) p[i] = f[i];
+            }
+        }
+}
+// The same as pairs of states.
+template <int NS>
+__device__ __forceinline__ void load_states(const float *at, int left, int there, int pitch,
+                                            float2 (&v)[2][NS / 2], int flip = 0) {
+    float f[2][NS];
+    read_states<NS>(at, left, there, pitch, f, flip);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) v[j][i] = make_float2(f[j][2 * i], f[j][2 * i + 1]);
+}
+template <int NS>
+__device__ __forceinline__ void store_states(float *at, int left, int there, int pitch,
+                                             const float2 (&v)[2][NS / 2], int flip = 0) {
+    float f[2][NS];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) f[j][2 * i] = v[j][i].x, f[j][2 * i + 1] = v[j][i].y;
+    write_states<NS>(at, left, there, pitch, f, flip);
+}
+// The tiles' states: units of 64 channels, their quads of states by channel pair, so that a
+// warp's accesses are whole lines.  The quad of channel c + j (of its group) from state n.
+__device__ __forceinline__ float4 *tile_at(const Args &p, int64_t tile, int grp, int c, int j,
+                                           int n) {
+    const int np = p.shape.np;
+    const int64_t unit = (tile * p.groups + grp) * p.units + c / 64;
+    return reinterpret_cast<float4 *>(p.htile) + (unit * (np / 2) + j * (np / 4) + n / 4) * 32 +
+           (c % 64) / 2;
+}
+
+// ---------------------------------------------------------------------------
+// functions
 // ---------------------------------------------------------------------------
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// (off by 2^-22.7 at most and by 2e-8 to 5e-8 on average, measured over [-20, 0])
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// e^{-|v|}: the product with log2 e in two parts, so that the error does not grow
-// with |v|
-__device__ __forceinline__ float exp_neg_abs(float v) {
-    const float m = -fabsf(v);
-    const float t = m * kLog2e;
-    const float r = fmaf(m, 1.92596299e-8f, fmaf(m, kLog2e, -t));
-    const float e = exp2_fast(t);
-    return m < -100.0f ? 0.0f : fmaf(e, r * kLn2, e);      // (an infinity's r is a NaN)
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 exp2_fast2(float2 x) {
+    return make_float2(exp2_fast(x.x), exp2_fast(x.y));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^{-|v|} in (0, 1], and
-//   log(1 + e) = 2 artanh(w) = 2 w (1 + w^2/3 + w^4/5 + ...),  w = e / (2 + e) <= 1/3
-// (the terms left out are below 2e-8 of the sum; small e keeps its digits)
-__device__ __forceinline__ float softplus(float v) {
-    const float e = exp_neg_abs(v);
-    const float w = __fdividef(e, 2.0f + e), q = w * w;
-    float s = 1.0f / 13.0f;
-    s = fmaf(s, q, 1.0f / 11.0f);
-    s = fmaf(s, q, 1.0f / 9.0f);
-    s = fmaf(s, q, 1.0f / 7.0f);
-    s = fmaf(s, q, 1.0f / 5.0f);
-    s = fmaf(s, q, 1.0f / 3.0f);
-    s = fmaf(s, q, 1.0f);
-    return fmaxf(v, 0.0f) + 2.0f * w * s;
+//   log(1 + e) = 2 artanh(w) = w p(w^2),  w = e / (2 + e) <= 1/3,
+// p by a polynomial fitted to 2 artanh(w) / w over w^2 in [0, 1/9] (4e-9); small e keeps its
+// digits.  The product of v with log2 e is taken in two parts, so that the error does not
+// grow with |v|.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+    using namespace ops;
+    const float2 m = make_float2(max_nan(-fabsf(v.x), -100.0f), max_nan(-fabsf(v.y), -100.0f));
+    const float2 nt = mul2(m, f2(-kLog2e));
+    const float2 r = fma2(m, f2(1.92596299e-8f), fma2(m, f2(kLog2e), nt));
+    float2 e = make_float2(exp2_fast(-nt.x), exp2_fast(-nt.y));
+    e = fma2(e, mul2(r, f2(kLn2)), e);
+    const float2 d = add2(e, f2(2.0f));
+    const float2 w = mul2(e, make_float2(rcp_fast(d.x), rcp_fast(d.y))), q = mul2(w, w);
+    float2 s = fma2(q, f2(0.2817833f), f2(0.27960604f));
+    s = fma2(s, q, f2(0.4002491f));
+    s = fma2(s, q, f2(0.66666317f));
+    s = fma2(s, q, f2(2.0f));
+    return fma2(w, s, make_float2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
 }
-// 1 / (1 + e^{-v})
-__device__ __forceinline__ float logistic(float v) {
-    const float e = exp_neg_abs(v);
-    return __fdividef(v < 0.0f ? e : 1.0f, 1.0f + e);
+// 1 / (1 + e^{-v}), to 1e-6 for |v| up to 10
+__device__ __forceinline__ float2 logistic2(float2 v) {
+    using namespace ops;
+    const float2 d = add2(exp2_fast2(mul2(v, f2(-kLog2e))), f2(1.0f));
+    return make_float2(rcp_fast(d.x), rcp_fast(d.y));
 }
 
-// Rows of a tile from global to shared memory: `rows` of them (the first `valid` are
-// there, the others become zero) of `cols` elements, zero beyond up to `pitch` (a power
-// of two); rows are `stride` elements apart in memory.  By asynchronous copies of `vec`
-// bytes, which rows, strides and cols are multiples of (2: element by element), or of as
-// many as a row holds here.
+// ---------------------------------------------------------------------------
+// pairs of channels in memory
+// ---------------------------------------------------------------------------
+template <typename T> struct Pair { uint32_t bits; };
+template <> struct Pair<float> { float2 v; };
+
 template <typename T>
-__device__ __forceinline__ void stage(T *dst, const T *src, int64_t stride, int rows, int valid,
-                                      int cols, int pitch, int vec, int tid, int threads) {
-    vec = min(vec, pitch * (int)sizeof(T));
-    const int per = vec / (int)sizeof(T), shift = 31 - __clz(pitch / per);
-#pragma unroll 1
-    for (int i = tid; i < rows << shift; i += threads) {
-        const int t = i >> shift, c = (i - (t << shift)) * per;
-        T *to = dst + t * pitch + c;
-        if (t < valid && c < cols) {
-            const T *from = src + t * stride + c;
-            const uint32_t at = ops::smem_u32(to);
-            if (vec == 16) ops::cp_async16(at, from);
-            else if (vec == 8) ops::cp_async8(at, from);
-            else if (vec == 4) ops::cp_async4(at, from);
-            else *to = *from;
+__device__ __forceinline__ float2 to_float2(const Pair<T> &p) {
+    return Storage<T>::load2(reinterpret_cast<const T *>(&p));
+}
+// (`wide`: pairs lie on their size; zero where nothing is left)
+template <typename T>
+__device__ __forceinline__ Pair<T> load_pair(const T *p, bool wide, int left) {
+    Pair<T> r;
+    if constexpr (sizeof(T) == 4) {
+        r.v = make_float2(0.0f, 0.0f);
+        if (wide) {
+            if (left > 0) r.v = *reinterpret_cast<const float2 *>(p);
         } else {
-            for (int k = 0; k < per; ++k) Storage<T>::store(to + k, 0.0f);
+            if (left > 0) r.v.x = p[0];
+            if (left > 1) r.v.y = p[1];
         }
+    } else {
+        r.bits = 0;
+        if (wide) {
+            if (left > 0) r.bits = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+            if (left > 0) r.bits = h[0];
+            if (left > 1) r.bits |= (uint32_t)h[1] << 16;
+        }
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_pair(T *p, float2 v, bool wide, int left) {
+    if (wide) {
+        ops::Pack<T, 2> o;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            *reinterpret_cast<__nv_bfloat162 *>(&o) = __floats2bfloat162_rn(v.x, v.y);
+        else if constexpr (std::is_same<T, __half>::value)
+            *reinterpret_cast<__half2 *>(&o) = __floats2half2_rn(v.x, v.y);
+        else o.v[0] = v.x, o.v[1] = v.y;
+        if (left > 0) *reinterpret_cast<ops::Pack<T, 2> *>(p) = o;
+    } else {
+        if (left > 0) Storage<T>::store(p, v.x);
+        if (left > 1) Storage<T>::store(p + 1, v.y);
     }
 }
 

@@ -9,18 +9,18 @@
 //
 // Nothing is kept from the forward.  A first pass (fno_scan_fwd.h) leaves the state in
 // front of every tile of 8 tokens, from zero at the segment's start, and, where time is
-// split, what the segment adds to the gradient in front of it (sum over t of
-// (a_1 .. a_t) C_t w_t); a kernel joins the segments in both directions.  The second pass
-// walks the tiles backwards: it runs four tokens at a time forward with their states and
-// decays in registers, then those four back.
+// split, a second one what each segment adds to the gradient in front of it; a kernel joins
+// the segments in both directions.  The last pass
+// walks the tiles backwards: it runs a tile forward with the state in front of every second
+// token put aside in shared memory, then goes back by two tokens at a time, whose states and
+// decays it works out again into registers.
 //
-// A warp holds 16 channels x 4 NN states: lane = 4 dl + nl has channels 2 dl and
-// 2 dl + 1 as pairs, and NN states.  The sums over states go over the four nl lanes, the
-// sums over channels over the eight dl lanes.  For the latter a lane's register i holds
-// state i ^ (dl & (NN - 1)): the half of the registers that it sends then is the same in
-// every lane, and no value has to be chosen.  The warps of a block add up their channels'
-// parts of dB and dC in shared memory; blocks of channels meet in the workspace, always in
-// the same order.
+// A lane holds two channels x 8 states.  The warps that share a channel's states prepare and
+// finish its tokens in turns and add up S1, S2 and y in shared memory.  dB and dC are summed
+// over a warp's lanes by shuffles that halve the values at each step: the upper half of the
+// lanes holds its two quads of states exchanged, so that all lanes send the same registers
+// first.  The block's warps add up theirs in shared memory, blocks of channels meet in the
+// workspace, always in the same order.
 #pragma once
 
 #include "fno_scan_fwd.h"
@@ -28,346 +28,383 @@
 namespace fno {
 namespace scan {
 
-constexpr int kSub = kTile / 2;
+constexpr int kSub = 2;                     // tokens whose states are in registers
+constexpr int kSubs = kTile / kSub;
 
-template <typename T>
+// Shared memory of a block of SLABS x WARPS warps.
+template <typename T, int NS, int WARPS, int SLABS>
 struct BackwardShared {
-    static __host__ __device__ size_t raw(int cb, int np) {
-        return (size_t)kTile * (4 * cb + 2 * np) * sizeof(T);
-    }
-    static __host__ __device__ size_t bytes(int cb, int np, int nw, int slabs) {
-        return 2 * raw(cb, np) +
-               (size_t)kTile * ((3 + 3 * nw) * cb * 4 + np * 16 + slabs * 2 * np * 4);
-    }
+    static constexpr int kPairs = SLABS * 32, kThreads = kPairs * WARPS, kNp = NS * WARPS;
+    float4 du[kTile][kPairs];                         // steps and inputs
+    float4 kept[kSubs - 1][NS / 2][kThreads];         // states in front of pairs of tokens
+    float2 w[kTile][kPairs];                          // output gradients
+    float2 out[3][WARPS][kTile][kPairs];              // S1, S2, y
+    Pair<T> raw[4][kTile][kPairs];                    // x, dt, dy, z
+    float bc[kTile][2][kNp];
+    float sums[SLABS][kTile][2][kNp];                 // dB, dC
 };
 
-template <typename T, int NN>
-__global__ void __launch_bounds__(256, 1)
+template <typename T, int NS, int WARPS, int SLABS>
+__global__ void __launch_bounds__(SLABS * WARPS * 32)
 k_scan_grad(const Args p) {
     using namespace ops;
+    using Shared = BackwardShared<T, NS, WARPS, SLABS>;
+    constexpr int NP = NS / 2, kThreads = Shared::kThreads, np = Shared::kNp;
+    constexpr int kOwn = WARPS < kTile ? kTile / WARPS : 1;      // tokens a thread prepares
     extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
-    const int cb = 16 * p.slabs, nw = threads / (2 * cb), np = 4 * NN * nw;
-    const int slab = (tid >> 5) / nw, sub = (tid >> 5) - slab * nw;
-    const int dl = lane >> 2, nl = lane & 3, perm = dl & (NN - 1);
+    Shared &sm = *reinterpret_cast<Shared *>(smem);
+    const int tid = threadIdx.x, lane = tid & 31, sub = (tid >> 5) % WARPS;
+    const int slab = (tid >> 5) / WARPS, my = slab * 32 + lane;
     int64_t at = blockIdx.x;
-    const int seg = (int)(at % p.segments);
-    at /= p.segments;
-    const int chb = (int)(at % p.chblocks);
-    at /= p.chblocks;
+    const int part = (int)(at % p.spans);
+    at /= p.spans;
+    const int chblocks = p.shape.chblocks, chb = (int)(at % chblocks);
+    at /= chblocks;
     const int grp = (int)(at % p.groups);
-    const int64_t b = at / p.groups;
-    const int c0 = chb * cb, cols = min(cb, p.per_group - c0);
-    const int64_t ch0 = (int64_t)grp * p.per_group + c0;
-    const int64_t len = p.lengths ? max((int64_t)0, min((int64_t)p.lengths[b], p.length))
-                                  : p.length;
-    const int64_t t0 = seg * p.seg_len;
-    const int64_t span = min(p.seg_len, p.length - t0);
-    const int64_t have = max((int64_t)0, min(span, len - t0));
-    const size_t raw_bytes = BackwardShared<T>::raw(cb, np);
-    float *sd = reinterpret_cast<float *>(smem + 2 * raw_bytes);
-    float *su = sd + kTile * cb, *sw = su + kTile * cb;
-    float *so = sw + kTile * cb;                       // S1, S2, y: [3][nw][kTile][cb]
-    float4 *sbc = reinterpret_cast<float4 *>(so + 3 * nw * kTile * cb);
-    float *sp = reinterpret_cast<float *>(sbc + kTile * np);    // [slabs][kTile][2][np]
+    const int64_t first_row = at / p.groups;
+    const int c = (chb * SLABS * 32 + my) * 2;        // in the group
+    const int left = p.per_group - c;
+    const int64_t ch = (int64_t)grp * p.per_group + c;
+    const int flip = NS == 8 ? lane >> 4 : 0, n0 = sub * NS;
+    const int64_t t0 = part * p.span_len;
+    const int span = (int)min(p.span_len, p.length - t0);
+    const int bc_stride = p.groups * p.states;
+    const bool wide = p.vec_c >= 2 * (int)sizeof(T), gated = p.z != nullptr;
+    const int64_t tiles = (p.length + kTile - 1) / kTile;
+    const bool kept_tiles = tiles > 1 && left > 0, before = p.segments > 1 || p.s0;
 
-    const int64_t row0 = b * p.length + t0, at0 = row0 * p.channels + ch0;
-    const T *gx = static_cast<const T *>(p.x) + at0;
-    const T *gdt = static_cast<const T *>(p.dt) + at0;
-    const T *gdy = static_cast<const T *>(p.dy) + at0;
-    const T *gz = p.z ? static_cast<const T *>(p.z) + at0 : nullptr;
-    const int64_t bc_stride = (int64_t)p.groups * p.states;
-    const int64_t bc0 = row0 * bc_stride + (int64_t)grp * p.states;
-    const T *gB = static_cast<const T *>(p.B) + bc0;
-    const T *gC = static_cast<const T *>(p.C) + bc0;
+    float2 a2[2][NP], da[2][NP];                      // log2 e A, and A's gradient
+    load_states<NS>(p.A + ch * p.states + n0, left, p.states - n0, p.states, a2, flip);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            a2[j][i] = mul2(a2[j][i], f2(kLog2e));
+            da[j][i] = f2(0.0f);
+        }
+    float2 bias = f2(0.0f), skip = f2(0.0f), dskip = f2(0.0f), dbias = f2(0.0f);
+    if (p.bias) bias = make_float2(left > 0 ? p.bias[ch] : 0.0f, left > 1 ? p.bias[ch + 1] : 0.0f);
+    if (p.D) skip = make_float2(left > 0 ? p.D[ch] : 0.0f, left > 1 ? p.D[ch + 1] : 0.0f);
+    // B and C of a tile, and their gradients: a thread has one state of one of them and every
+    // kRows-th token
+    constexpr int kMost = kThreads / (2 * np), kRows = kMost < kTile ? kMost : kTile;
+    constexpr int kRounds = kTile / kRows;
+    static_assert(kRows >= 1 && kTile % kRows == 0, "a block's threads cover B and C");
+    const int bc_k = tid / (2 * np), bc_at = tid % (2 * np), bc_which = bc_at / np;
+    const int bc_n = bc_at % np;
+    const bool bc_mine = bc_k < kRows && bc_n < p.states;
 
-    const auto fetch = [&](int stage_no, int64_t t) {
-        const int valid = (int)min((int64_t)kTile, have - t);
-        T *r = reinterpret_cast<T *>(smem + stage_no * raw_bytes);
-        const int64_t o = t * p.channels;
-        stage(r, gx + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid, threads);
-        stage(r + kTile * cb, gdt + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid, threads);
-        if (gz)
-            stage(r + 2 * kTile * cb, gz + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid,
-                  threads);
-        stage(r + 3 * kTile * cb, gdy + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid,
-              threads);
-        T *rb = r + 4 * kTile * cb;
-        const int64_t ob = t * bc_stride;
-        stage(rb, gB + ob, bc_stride, kTile, valid, p.states, np, p.vec_n, tid, threads);
-        stage(rb + kTile * np, gC + ob, bc_stride, kTile, valid, p.states, np, p.vec_n, tid,
-              threads);
-        cp_async_commit();
-    };
-
-    const int cl = slab * 16 + 2 * dl, n0 = (sub * 4 + nl) * NN;
-    const auto half = [](float2 &v, int k) -> float & { return k ? v.y : v.x; };
-    const auto each = [&](auto f) {            // f(state register, channel of the pair, index)
+    for (int64_t b = first_row; b < p.batch; b += p.rows) {
+        const int64_t len = p.lengths ? max(0, p.lengths[b]) : p.length;
+        const int have = (int)max((int64_t)0, min((int64_t)span, len - t0));
+        const int last = have > 0 ? (have - 1) / kTile * kTile : -1;
+        const int64_t row0 = b * p.length + t0, o0 = row0 * p.channels + ch;
+        const int64_t bc0 = row0 * bc_stride + grp * p.states;
+        // dB and dC of the span's token t, or this block's part of them
+        const auto put_bc = [&](int64_t t, float v) {
+            if (chblocks > 1) {
+                const int64_t all = (int64_t)p.batch * p.length * p.groups;
+                const int64_t row = (row0 + t) * p.groups + grp;
+                p.part_bc[((chb * all + row) * 2 + bc_which) * p.states + bc_n] = v;
+            } else {
+                T *o = static_cast<T *>(bc_which ? p.dC : p.dB);
+                Storage<T>::store(o + bc0 + t * bc_stride + bc_n, v);
+            }
+        };
+        // what the tile at t takes from memory
+        Pair<T> raw[4][kOwn];
+        T bc_raw[kRounds];
+        float2 h[2][NP], hin[2][NP], since;
+        const auto fetch = [&](int t) {
+#pragma unroll
+            for (int m = 0; m < kOwn; ++m) {
+                const int k = t + sub + m * WARPS;
+                const int n = k < have ? left : 0;
+                const int64_t o = o0 + (int64_t)k * p.channels;
+                raw[0][m] = load_pair(static_cast<const T *>(p.x) + o, wide, n);
+                raw[1][m] = load_pair(static_cast<const T *>(p.dt) + o, wide, n);
+                raw[2][m] = load_pair(static_cast<const T *>(p.dy) + o, wide, n);
+                if (gated) raw[3][m] = load_pair(static_cast<const T *>(p.z) + o, wide, n);
+            }
+            const T *from = static_cast<const T *>(bc_which ? p.C : p.B) + bc0 + bc_n;
+#pragma unroll
+            for (int m = 0; m < kRounds; ++m) {
+                const int k = t + bc_k + m * kRows;
+                Storage<T>::store(&bc_raw[m], 0.0f);
+                if (bc_mine && k < have) bc_raw[m] = from[(int64_t)k * bc_stride];
+            }
+            if (p.segments > 1)
+                load_states<NS>(p.hseg + ((b * p.segments + (t0 + t) / p.seg_len) * p.channels + ch) *
+                                             np + n0,
+                                left, NS, np, hin, flip);
+            else if (p.s0)
+                load_states<NS>(p.s0 + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
+                                p.states, hin, flip);
+            if (kept_tiles) {
+                const int64_t tile = b * tiles + (t0 + t) / kTile;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < NS / 4; ++q) {
+                        const float4 v = *tile_at(p, tile, grp, c, j, n0 + 4 * (q ^ flip));
+                        h[j][2 * q] = make_float2(v.x, v.y);
+                        h[j][2 * q + 1] = make_float2(v.z, v.w);
+                    }
+                if (before) {
+                    const float *d = p.dtile + tile * p.channels + ch;
+                    since = make_float2(d[0], left > 1 ? d[1] : 0.0f);
+                }
+            }
+        };
+        if (last >= 0) fetch(last);
+        float2 gp[2][NP];                             // a_{t+1} g_{t+1}
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < NN; ++i)
-                if (cl + j < cols && n0 + (i ^ perm) < p.states)
-                    f(i, j, (ch0 + cl + j) * p.states + n0 + (i ^ perm));
-    };
-    const int64_t cn = (int64_t)p.channels * p.states;
-    float2 a2[NN], da[NN], gp[NN];             // log2 e A; its gradient; a_{t+1} g_{t+1}
+            for (int i = 0; i < NP; ++i) gp[j][i] = f2(0.0f);
+        if (p.segments > 1)
+            load_states<NS>(p.gseg + ((b * p.segments + (t0 + span - 1) / p.seg_len) * p.channels +
+                                      ch) * np + n0,
+                            left, NS, np, gp, flip);
+        else if (p.gsT)
+            load_states<NS>(p.gsT + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
+                            p.states, gp, flip);
+        for (int t = last; t >= 0; t -= kTile) {
+            const int valid = min(kTile, have - t);
+            // the steps, inputs and output gradients of this thread's tokens; beyond the last
+            // token they are zero and change nothing
 #pragma unroll
-    for (int i = 0; i < NN; ++i) a2[i] = da[i] = gp[i] = f2(0.0f);
-    each([&](int i, int j, int64_t e) { half(a2[i], j) = p.A[e] * kLog2e; });
-    {
-        const float *from = p.segments > 1 ? p.gseg + (b * p.segments + seg) * cn
-                            : p.gsT        ? p.gsT + b * cn
-                                           : nullptr;
-        if (from) each([&](int i, int j, int64_t e) { half(gp[i], j) = from[e]; });
-    }
-    const float *hin = p.segments > 1 ? p.hseg + (b * p.segments + seg) * cn
-                       : p.s0         ? p.s0 + b * cn
-                                      : nullptr;
-    const int64_t tiles = (p.length + kTile - 1) / kTile;
-
-    const int pairs = cb / 2, pc = 2 * (tid & (pairs - 1)), pt = tid / pairs;
-    const int pt_step = threads / pairs;
-    const bool in0 = pc < cols, in1 = pc + 1 < cols;
-    const bool wide = p.vec_c >= 2 * (int)sizeof(T);
-    float2 bias = f2(0.0f), skip = f2(0.0f), dskip = f2(0.0f), dbias = f2(0.0f);
-    if (p.bias) bias = make_float2(in0 ? p.bias[ch0 + pc] : 0.0f, in1 ? p.bias[ch0 + pc + 1] : 0.0f);
-    if (p.D) skip = make_float2(in0 ? p.D[ch0 + pc] : 0.0f, in1 ? p.D[ch0 + pc + 1] : 0.0f);
-    const auto put = [&](void *out, int64_t t, float2 v) {
-        T *o = static_cast<T *>(out) + at0 + t * p.channels + pc;
-        if (wide && in0) {
-            Pack<T, 2> w2;
-            Storage<T>::store(&w2.v[0], v.x);
-            Storage<T>::store(&w2.v[1], v.y);
-            *reinterpret_cast<Pack<T, 2> *>(o) = w2;
-        } else {
-            if (in0) Storage<T>::store(o, v.x);
-            if (in1) Storage<T>::store(o + 1, v.y);
-        }
-    };
-    // dB and dC of the segment's token t, or this block's part of them
-    const auto put_bc = [&](int64_t t, int which, int n, float v) {
-        if (p.chblocks > 1) {
-            const int64_t rows = (int64_t)p.batch * p.length * p.groups;
-            const int64_t row = (row0 + t) * p.groups + grp;
-            p.part_bc[((chb * rows + row) * 2 + which) * p.states + n] = v;
-        } else {
-            T *o = static_cast<T *>(which ? p.dC : p.dB);
-            Storage<T>::store(o + bc0 + t * bc_stride + n, v);
-        }
-    };
-
-    const int64_t last = have > 0 ? (have - 1) / kTile * kTile : -1;
-    if (last >= 0) fetch(0, last);
-    int stage_no = 0;
-    for (int64_t t = last; t >= 0; t -= kTile, stage_no ^= 1) {
-        const int valid = (int)min((int64_t)kTile, have - t);
-        // the state in front of the tile
-        float2 h0[NN];
+            for (int m = 0; m < kOwn; ++m) {
+                const int k = sub + m * WARPS;
+                const float2 x = to_float2(raw[0][m]);
+                float2 d = add2(to_float2(raw[1][m]), bias), w = to_float2(raw[2][m]);
+                if (p.softplus) d = softplus2(d);
+                if (k >= valid) d = f2(0.0f);
+                if (gated) {
+                    const float2 z = to_float2(raw[3][m]);
+                    w = mul2(w, mul2(z, logistic2(z)));
+                    sm.raw[3][k][my] = raw[3][m];
+                }
+                const float2 du = mul2(d, x);
+                sm.du[k][my] = make_float4(d.x, d.y, du.x, du.y);
+                sm.w[k][my] = w;
 #pragma unroll
-        for (int i = 0; i < NN; ++i) h0[i] = f2(0.0f);
-        if (tiles > 1) {
-            const int64_t ck = b * tiles + (t0 + t) / kTile;
-            each([&](int i, int j, int64_t e) { half(h0[i], j) = p.hchunk[ck * cn + e]; });
-            if (hin) {
-                float since[2];
+                for (int f = 0; f < 3; ++f) sm.raw[f][k][my] = raw[f][m];
+            }
+#pragma unroll
+            for (int m = 0; m < kRounds; ++m)
+                if (bc_k < kRows) sm.bc[bc_k + m * kRows][bc_which][bc_n] = Storage<T>::load(&bc_raw[m]);
+            // the state in front of the tile
+            if (!kept_tiles) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    since[j] = cl + j < cols ? p.dchunk[ck * p.channels + ch0 + cl + j] : 0.0f;
-                each([&](int i, int j, int64_t e) {
-                    half(h0[i], j) =
-                        fmaf(exp2_fast(half(a2[i], j) * since[j]), hin[e], half(h0[i], j));
-                });
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) h[j][i] = before ? hin[j][i] : f2(0.0f);
+            } else if (before) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        h[j][i] = fma2(hin[j][i],
+                                       exp2_fast2(mul2(a2[j][i], f2(j ? since.y : since.x))),
+                                       h[j][i]);
             }
-        } else if (hin) {
-            each([&](int i, int j, int64_t e) { half(h0[i], j) = hin[e]; });
-        }
-        cp_async_wait<0>();
-        __syncthreads();
-        if (t >= kTile) fetch(stage_no ^ 1, t - kTile);
-        const T *r = reinterpret_cast<const T *>(smem + stage_no * raw_bytes);
-        const T *rb = r + 4 * kTile * cb;
-        for (int k = pt; k < kTile; k += pt_step) {
-            const float2 xv = Storage<T>::load2(r + k * cb + pc);
-            float2 d = add2(Storage<T>::load2(r + (kTile + k) * cb + pc), bias);
-            float2 w = Storage<T>::load2(r + (3 * kTile + k) * cb + pc);
-            if (p.softplus) d = make_float2(softplus(d.x), softplus(d.y));
-            if (k >= valid || !in0) d.x = 0.0f;
-            if (k >= valid || !in1) d.y = 0.0f;
-            if (gz) {
-                const float2 zv = Storage<T>::load2(r + (2 * kTile + k) * cb + pc);
-                w = make_float2(w.x * zv.x * logistic(zv.x), w.y * zv.y * logistic(zv.y));
-            }
-            *reinterpret_cast<float2 *>(sd + k * cb + pc) = d;
-            *reinterpret_cast<float2 *>(su + k * cb + pc) = mul2(d, xv);
-            *reinterpret_cast<float2 *>(sw + k * cb + pc) = w;
-        }
-        for (int i = tid; i < kTile * np; i += threads) {
-            const float bv = Storage<T>::load(rb + i), cv = Storage<T>::load(rb + kTile * np + i);
-            sbc[i] = make_float4(bv, bv, cv, cv);
-        }
-        __syncthreads();
+            __syncthreads();
 
-        // a tile's tokens beyond the last have d = u = w = 0: they change nothing
-        const auto step = [&](int k, float2 *a, const float2 *from, float2 *to) {
-            const float2 d = *reinterpret_cast<const float2 *>(sd + k * cb + cl);
-            const float2 u = *reinterpret_cast<const float2 *>(su + k * cb + cl);
+            const auto step = [&](int k, float2 (&a)[2][NP], const float2 (&from)[2][NP],
+                                  float2 (&to)[2][NP]) {
+                const float4 e = sm.du[k][my];
 #pragma unroll
-            for (int i = 0; i < NN; ++i) {
-                const float2 bv = *reinterpret_cast<const float2 *>(sbc + k * np + n0 + (i ^ perm));
-                const float2 q = mul2(a2[i], d);
-                a[i] = make_float2(exp2_fast(q.x), exp2_fast(q.y));
-                to[i] = fma2(a[i], from[i], mul2(u, bv));
-            }
-        };
-        float2 hm[NN];
+                for (int q = 0; q < NS / 4; ++q) {
+                    const float4 bq =
+                        *reinterpret_cast<const float4 *>(&sm.bc[k][0][n0 + 4 * (q ^ flip)]);
 #pragma unroll
-        for (int i = 0; i < NN; ++i) hm[i] = h0[i];
+                    for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                        const float2 bv = i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
 #pragma unroll
-        for (int k = 0; k < kSub; ++k) {
-            float2 a[NN];
-            step(k, a, hm, hm);
-        }
-#pragma unroll 1
-        for (int part = 1; part >= 0; --part) {
-            const int k0 = part * kSub;
-            float2 a[kSub][NN], h[kSub + 1][NN];
-#pragma unroll
-            for (int i = 0; i < NN; ++i) h[0][i] = part ? hm[i] : h0[i];
-#pragma unroll
-            for (int k = 0; k < kSub; ++k) step(k0 + k, a[k], h[k], h[k + 1]);
-#pragma unroll
-            for (int k = kSub - 1; k >= 0; --k) {
-                const int kk = k0 + k;
-                const float2 d = *reinterpret_cast<const float2 *>(sd + kk * cb + cl);
-                const float2 u = *reinterpret_cast<const float2 *>(su + kk * cb + cl);
-                const float2 w = *reinterpret_cast<const float2 *>(sw + kk * cb + cl);
-                float2 s1 = f2(0.0f), s2 = f2(0.0f), y = f2(0.0f);
-                float vb[NN], vc[NN];
-#pragma unroll
-                for (int i = 0; i < NN; ++i) {
-                    const float4 bc = sbc[kk * np + n0 + (i ^ perm)];
-                    const float2 bv = make_float2(bc.x, bc.y), cv = make_float2(bc.z, bc.w);
-                    const float2 g = fma2(cv, w, gp[i]);
-                    s1 = fma2(g, bv, s1);
-                    y = fma2(cv, h[k + 1][i], y);
-                    const float2 pb = mul2(g, u), pw = mul2(w, h[k + 1][i]);
-                    vb[i] = pb.x + pb.y;
-                    vc[i] = pw.x + pw.y;
-                    gp[i] = mul2(a[k][i], g);
-                    const float2 e = mul2(gp[i], h[k][i]);
-                    s2 = fma2(a2[i], e, s2);
-                    da[i] = fma2(d, e, da[i]);
-                }
-                // over the channels: a lane ends with one state of dB or of dC
-                if (NN == 4) {
-#pragma unroll
-                    for (int i = 0; i < NN / 2; ++i) {
-                        vb[i] += __shfl_xor_sync(0xffffffffu, vb[i + NN / 2], 8);
-                        vc[i] += __shfl_xor_sync(0xffffffffu, vc[i + NN / 2], 8);
+                        for (int j = 0; j < 2; ++j) {
+                            a[j][i] = exp2_fast2(mul2(a2[j][i], f2(j ? e.y : e.x)));
+                            to[j][i] = fma2(a[j][i], from[j][i], mul2(f2(j ? e.w : e.z), bv));
+                        }
                     }
                 }
-                if (NN >= 2) {
-                    vb[0] += __shfl_xor_sync(0xffffffffu, vb[NN / 2 == 2 ? 1 : NN - 1], 4);
-                    vc[0] += __shfl_xor_sync(0xffffffffu, vc[NN / 2 == 2 ? 1 : NN - 1], 4);
-                }
-                const bool second = dl & 4;
-                float v = (second ? vc[0] : vb[0]) +
-                          __shfl_xor_sync(0xffffffffu, second ? vb[0] : vc[0], 16);
-                if (NN < 4) v += __shfl_xor_sync(0xffffffffu, v, 8);
-                if (NN < 2) v += __shfl_xor_sync(0xffffffffu, v, 4);
-                if ((dl & 3) < NN)
-                    sp[((slab * kTile + kk) * 2 + (dl >> 2)) * np + n0 + perm] = v;
-                // over the states: even lanes the first channel, odd ones the second
-                const bool odd = nl & 1;
-                float o1 = (odd ? s1.y : s1.x) +
-                           __shfl_xor_sync(0xffffffffu, odd ? s1.x : s1.y, 1);
-                float o2 = (odd ? s2.y : s2.x) +
-                           __shfl_xor_sync(0xffffffffu, odd ? s2.x : s2.y, 1);
-                float o3 = (odd ? y.y : y.x) + __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
-                o1 += __shfl_xor_sync(0xffffffffu, o1, 2);
-                o2 += __shfl_xor_sync(0xffffffffu, o2, 2);
-                o3 += __shfl_xor_sync(0xffffffffu, o3, 2);
-                if (nl < 2) {
-                    float *o = so + (sub * kTile + kk) * cb + cl + nl;
-                    o[0] = o1;
-                    o[nw * kTile * cb] = o2;
-                    o[2 * nw * kTile * cb] = o3;
-                }
-            }
-        }
-        __syncthreads();
-        for (int k = pt; k < valid; k += pt_step) {
-            const float *o = so + k * cb + pc;
-            float2 v[3];
+            };
+            const int subs = (valid + kSub - 1) / kSub;
+#pragma unroll 1
+            for (int r = 0; r < subs - 1; ++r) {
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                v[q] = *reinterpret_cast<const float2 *>(o + q * nw * kTile * cb);
-                for (int w = 1; w < nw; ++w)
-                    v[q] = add2(v[q], *reinterpret_cast<const float2 *>(
-                                          o + (q * nw + w) * kTile * cb));
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < NS / 4; ++q)
+                        sm.kept[r][j * (NS / 4) + q][tid] =
+                            make_float4(h[j][2 * q].x, h[j][2 * q].y, h[j][2 * q + 1].x,
+                                        h[j][2 * q + 1].y);
+#pragma unroll
+                for (int k = 0; k < kSub; ++k) {
+                    float2 a[2][NP];
+                    step(r * kSub + k, a, h, h);
+                }
             }
-            const float2 xv = Storage<T>::load2(r + k * cb + pc);
-            const float2 d = *reinterpret_cast<const float2 *>(sd + k * cb + pc);
-            const float2 w = *reinterpret_cast<const float2 *>(sw + k * cb + pc);
-            put(p.dx, t + k, fma2(skip, w, mul2(d, v[0])));
-            dskip = fma2(w, xv, dskip);
-            float2 dd = fma2(xv, v[0], mul2(v[1], f2(kLn2)));
-            if (p.softplus) {
-                const float2 dtv = add2(Storage<T>::load2(r + (kTile + k) * cb + pc), bias);
-                dd = mul2(dd, make_float2(logistic(dtv.x), logistic(dtv.y)));
+#pragma unroll 1
+            for (int r = subs - 1; r >= 0; --r) {
+                float2 a[kSub][2][NP], hs[kSub][2][NP];
+                if (r < subs - 1) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int q = 0; q < NS / 4; ++q) {
+                            const float4 v = sm.kept[r][j * (NS / 4) + q][tid];
+                            h[j][2 * q] = make_float2(v.x, v.y);
+                            h[j][2 * q + 1] = make_float2(v.z, v.w);
+                        }
+                }
+                step(r * kSub, a[0], h, hs[0]);
+#pragma unroll
+                for (int k = 1; k < kSub; ++k) step(r * kSub + k, a[k], hs[k - 1], hs[k]);
+#pragma unroll
+                for (int k = kSub - 1; k >= 0; --k) {
+                    const int kk = r * kSub + k;
+                    const float4 e = sm.du[kk][my];
+                    const float2 w = sm.w[kk][my];
+                    float2 s1[2], s2[2], y[2], vb[NP], vc[NP];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) s1[j] = s2[j] = y[j] = f2(0.0f);
+#pragma unroll
+                    for (int q = 0; q < NS / 4; ++q) {
+                        const float4 bq =
+                            *reinterpret_cast<const float4 *>(&sm.bc[kk][0][n0 + 4 * (q ^ flip)]);
+                        const float4 cq =
+                            *reinterpret_cast<const float4 *>(&sm.bc[kk][1][n0 + 4 * (q ^ flip)]);
+#pragma unroll
+                        for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                            const float2 bv =
+                                i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
+                            const float2 cv =
+                                i & 1 ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float2 dv = f2(j ? e.y : e.x), uv = f2(j ? e.w : e.z);
+                                const float2 wv = f2(j ? w.y : w.x);
+                                const float2 earlier = k ? hs[k ? k - 1 : 0][j][i] : h[j][i];
+                                const float2 g = fma2(cv, wv, gp[j][i]);
+                                s1[j] = fma2(g, bv, s1[j]);
+                                y[j] = fma2(cv, hs[k][j][i], y[j]);
+                                vb[i] = j ? fma2(g, uv, vb[i]) : mul2(g, uv);
+                                vc[i] = j ? fma2(wv, hs[k][j][i], vc[i]) : mul2(wv, hs[k][j][i]);
+                                gp[j][i] = mul2(a[k][j][i], g);
+                                const float2 m = mul2(gp[j][i], earlier);
+                                s2[j] = fma2(a2[j][i], m, s2[j]);
+                                da[j][i] = fma2(dv, m, da[j][i]);
+                            }
+                        }
+                    }
+                    sm.out[0][sub][kk][my] = make_float2(s1[0].x + s1[0].y, s1[1].x + s1[1].y);
+                    sm.out[1][sub][kk][my] = make_float2(s2[0].x + s2[0].y, s2[1].x + s2[1].y);
+                    sm.out[2][sub][kk][my] = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+                    // over the lanes: quads, then dB or dC, then pairs, then one state
+                    const auto add_from = [](float2 v, float2 send, int mask) {
+                        return add2(v, make_float2(__shfl_xor_sync(0xffffffffu, send.x, mask),
+                                                   __shfl_xor_sync(0xffffffffu, send.y, mask)));
+                    };
+                    if constexpr (NS == 8) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            vb[i] = add_from(vb[i], vb[i + 2], 16);
+                            vc[i] = add_from(vc[i], vc[i + 2], 16);
+                        }
+                    }
+                    const bool is_c = lane & 8, second = lane & 4, odd = lane & 2;
+                    float2 v[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        v[i] = add_from(is_c ? vc[i] : vb[i], is_c ? vb[i] : vc[i], 8);
+                    const float2 m = add_from(second ? v[1] : v[0], second ? v[0] : v[1], 4);
+                    float one = (odd ? m.y : m.x) +
+                                __shfl_xor_sync(0xffffffffu, odd ? m.x : m.y, 2);
+                    one += __shfl_xor_sync(0xffffffffu, one, 1);
+                    if constexpr (NS == 4) one += __shfl_xor_sync(0xffffffffu, one, 16);
+                    if (!(lane & (NS == 8 ? 1 : 17)))
+                        sm.sums[slab][kk][is_c ? 1 : 0]
+                               [n0 + 4 * flip + (second ? 2 : 0) + (odd ? 1 : 0)] = one;
+                }
             }
-            put(p.ddt, t + k, dd);
-            dbias = add2(dbias, dd);
-            if (gz) {
-                const float2 zv = Storage<T>::load2(r + (2 * kTile + k) * cb + pc);
-                const float2 gy = Storage<T>::load2(r + (3 * kTile + k) * cb + pc);
-                const float2 y = fma2(skip, xv, v[2]);
-                const float2 l = make_float2(logistic(zv.x), logistic(zv.y));
-                put(p.dz, t + k,
-                    make_float2(gy.x * y.x * l.x * fmaf(zv.x, 1.0f - l.x, 1.0f),
-                                gy.y * y.y * l.y * fmaf(zv.y, 1.0f - l.y, 1.0f)));
+            __syncthreads();
+            if (t > 0) fetch(t - kTile);
+#pragma unroll 1
+            for (int m = 0; m < kOwn; ++m) {
+                const int k = sub + m * WARPS;
+                if (k >= valid) break;
+                float2 v[3];
+#pragma unroll
+                for (int q = 0; q < 3; ++q) {
+                    v[q] = sm.out[q][0][k][my];
+#pragma unroll
+                    for (int i = 1; i < WARPS; ++i) v[q] = add2(v[q], sm.out[q][i][k][my]);
+                }
+                const float2 x = to_float2(sm.raw[0][k][my]), w = sm.w[k][my];
+                const float4 e = sm.du[k][my];
+                const int64_t o = o0 + (int64_t)(t + k) * p.channels;
+                store_pair(static_cast<T *>(p.dx) + o,
+                           fma2(skip, w, mul2(make_float2(e.x, e.y), v[0])), wide, left);
+                dskip = fma2(w, x, dskip);
+                float2 dd = fma2(x, v[0], mul2(v[1], f2(kLn2)));
+                if (p.softplus)
+                    dd = mul2(dd, logistic2(add2(to_float2(sm.raw[1][k][my]), bias)));
+                store_pair(static_cast<T *>(p.ddt) + o, dd, wide, left);
+                dbias = add2(dbias, dd);
+                if (gated) {
+                    const float2 z = to_float2(sm.raw[3][k][my]), l = logistic2(z);
+                    const float2 gy = to_float2(sm.raw[2][k][my]), y = fma2(skip, x, v[2]);
+                    // silu' = l (1 + z (1 - l))
+                    store_pair(static_cast<T *>(p.dz) + o,
+                               mul2(mul2(gy, y), mul2(l, fma2(z, sub2(f2(1.0f), l), f2(1.0f)))),
+                               wide, left);
+                }
+            }
+            if (bc_mine) {
+#pragma unroll
+                for (int m = 0; m < kRounds; ++m) {
+                    const int k = bc_k + m * kRows;
+                    if (k >= valid) break;
+                    float v = sm.sums[0][k][bc_which][bc_n];
+#pragma unroll
+                    for (int i = 1; i < SLABS; ++i) v += sm.sums[i][k][bc_which][bc_n];
+                    put_bc(t + k, v);
+                }
             }
         }
-        for (int i = tid; i < valid * 2 * np; i += threads) {
-            const int n = i & (np - 1), which = (i / np) & 1, k = i / (2 * np);
-            if (n >= p.states) continue;
-            float v = 0.0f;
-            for (int s = 0; s < p.slabs; ++s) v += sp[((s * kTile + k) * 2 + which) * np + n];
-            put_bc(t + k, which, n, v);
+        for (int t = have + sub; t < span; t += WARPS) {
+            const int64_t o = o0 + (int64_t)t * p.channels;
+            store_pair(static_cast<T *>(p.dx) + o, f2(0.0f), wide, left);
+            store_pair(static_cast<T *>(p.ddt) + o, f2(0.0f), wide, left);
+            if (gated) store_pair(static_cast<T *>(p.dz) + o, f2(0.0f), wide, left);
         }
+        if (bc_mine)
+            for (int t = have + bc_k; t < span; t += kRows) put_bc(t, 0.0f);
+        if (p.ds0 && part == 0)
+            store_states<NS>(p.ds0 + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
+                             p.states, gp, flip);
+        __syncthreads();          // (shared memory is read before the next sequence writes it)
     }
-    for (int64_t t = have + pt; t < span; t += pt_step) {
-        put(p.dx, t, f2(0.0f));
-        put(p.ddt, t, f2(0.0f));
-        if (gz) put(p.dz, t, f2(0.0f));
-    }
-    for (int64_t i = have * 2 * np + tid; i < span * 2 * np; i += threads) {
-        const int n = (int)(i & (np - 1));
-        if (n < p.states) put_bc(i / (2 * np), (int)(i / np) & 1, n, 0.0f);
-    }
-    const int64_t s = b * p.segments + seg;
-    each([&](int i, int j, int64_t e) { p.part_a[s * cn + e] = half(da[i], j); });
-    if (p.ds0 && seg == 0)
-        each([&](int i, int j, int64_t e) { p.ds0[b * cn + e] = half(gp[i], j); });
-    // the bias' and D's gradients: the threads that share a pair of channels
+    const int64_t r = first_row * p.spans + part;
+    store_states<NS>(p.part_a + (r * p.channels + ch) * np + n0, left, NS, np, da, flip);
+    // the bias' and D's gradients: the warps that share these channels
+    sm.out[0][sub][0][my] = dskip;
+    sm.out[1][sub][0][my] = dbias;
     __syncthreads();
-    float4 *sum = reinterpret_cast<float4 *>(so);
-    sum[tid] = make_float4(dskip.x, dskip.y, dbias.x, dbias.y);
-    __syncthreads();
-    if (pt == 0) {
-        float4 v = sum[tid];
-        for (int k = 1; k < pt_step; ++k) {
-            const float4 o = sum[tid + k * pairs];
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    if (sub == 0) {
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) {
+            dskip = add2(dskip, sm.out[0][i][0][my]);
+            dbias = add2(dbias, sm.out[1][i][0][my]);
         }
-        float *o = p.part_d + s * 2 * p.channels + ch0 + pc;
-        if (in0) o[0] = v.x, o[p.channels] = v.z;
-        if (in1) o[1] = v.y, o[p.channels + 1] = v.w;
+        float *o = p.part_d + r * 2 * p.channels + ch;
+        if (left > 0) o[0] = dskip.x, o[p.channels] = dbias.x;
+        if (left > 1) o[1] = dskip.y, o[p.channels + 1] = dbias.y;
     }
 }
 
-// dB and dC: the sum of the blocks' parts (rows of 2 x states) of the tokens there.
+// dB and dC: the sum of the blocks' parts (rows of 2 x states).
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_scan_sum_bc(const Args p) {
@@ -375,86 +412,60 @@ k_scan_sum_bc(const Args p) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     float v = p.part_bc[i];
-    for (int k = 1; k < p.chblocks; ++k) v += p.part_bc[k * n + i];
+#pragma unroll 8
+    for (int k = 1; k < p.shape.chblocks; ++k) v += p.part_bc[k * n + i];
     const int64_t row = i / (2 * p.states);
     const int e = (int)(i - row * 2 * p.states);
     T *o = static_cast<T *>(e >= p.states ? p.dC : p.dB);
     Storage<T>::store(o + row * p.states + (e >= p.states ? e - p.states : e), v);
 }
 
-// out[i] = the sum of `parts` values n apart: 32 columns a block, its 16 rows of threads
-// over the parts; scaled (dA's pairs carry no factor, so 1).
-constexpr int kSumRows = 16;
-template <int kOuts>
-__global__ void __launch_bounds__(32 * kSumRows)
-k_scan_sum(const float *__restrict__ in, float *__restrict__ out0, float *__restrict__ out1,
-           int64_t n, int64_t parts) {
-    __shared__ float s[kSumRows][33];
-    const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    float v = 0.0f;
-    if (i < n) {
-#pragma unroll 8
-        for (int64_t k = threadIdx.y; k < parts; k += kSumRows) v += in[k * n + i];
-    }
-    s[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    if (threadIdx.y || i >= n) return;
-    for (int k = 1; k < kSumRows; ++k) v += s[k][threadIdx.x];
-    if (kOuts == 1) out0[i] = v;
-    else if (i < n / 2) { if (out0) out0[i] = v; }
-    else if (out1) out1[i - n / 2] = v;
-}
-
-template <typename T, int NN>
+template <typename T, int NS, int WARPS, int SLABS>
 fno_status_t launch_grad(const Args &a, cudaStream_t s) {
-    const int nw = NN == 4 ? state_warps(a.states) : 1, cb = 16 * a.slabs;
-    const size_t bytes = BackwardShared<T>::bytes(cb, 4 * NN * nw, nw, a.slabs);
-    const auto kernel = k_scan_grad<T, NN>;
-    if (bytes > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-            cudaSuccess) {
+    using Shared = BackwardShared<T, NS, WARPS, SLABS>;
+    const auto kernel = k_scan_grad<T, NS, WARPS, SLABS>;
+    if (sizeof(Shared) > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(Shared)) != cudaSuccess) {
         cudaGetLastError();
         return FNO_ERR_CUDA;
     }
-    const int64_t blocks = (int64_t)a.batch * a.groups * a.chblocks * a.segments;
-    kernel<<<(unsigned)blocks, 2 * cb * nw, bytes, s>>>(a);
+    const int64_t blocks = a.rows * a.groups * a.shape.chblocks * a.spans;
+    kernel<<<(unsigned)blocks, Shared::kThreads, sizeof(Shared), s>>>(a);
     return ops::launched();
+}
+// The kernel of the plan's shape.
+template <typename T>
+fno_status_t grad_pass(const Args &a, cudaStream_t s) {
+    const bool one = a.shape.slabs == 1;
+    if (a.shape.np == 4) return one ? launch_grad<T, 4, 1, 1>(a, s) : launch_grad<T, 4, 1, 4>(a, s);
+    switch (a.shape.warps) {
+        case 1: return one ? launch_grad<T, 8, 1, 1>(a, s) : launch_grad<T, 8, 1, 4>(a, s);
+        case 2: return one ? launch_grad<T, 8, 2, 1>(a, s) : launch_grad<T, 8, 2, 2>(a, s);
+        case 4: return launch_grad<T, 8, 4, 1>(a, s);
+        default: return launch_grad<T, 8, 8, 1>(a, s);
+    }
 }
 
 template <typename T>
 fno_status_t backward_of(const fno_scan_s &p, Args a, cudaStream_t s) {
     using ops::ceil_div;
-    a.segments = p.bwd_segments;
-    a.seg_len = p.bwd_seg_len;
     fno_status_t st = FNO_OK;
+    if (a.length <= kTile) a.htile = nullptr;
+    if (a.segments > 1 || a.htile) st = scan_pass<T, kStates>(p, a, s);
     if (a.segments > 1) {
-        st = scan_pass<T, kBoth>(a, forward_slabs(p), s);
-        if (st == FNO_OK) st = join(a, false, s);
+        if (st == FNO_OK) st = scan_pass<T, kBack>(p, a, s);
         if (st == FNO_OK) st = join(a, true, s);
-    } else if (a.length > kTile) {
-        st = scan_pass<T, kTiles>(a, forward_slabs(p), s);
     }
     if (st != FNO_OK) return st;
-    a.slabs = backward_slabs(p);
-    a.chblocks = (int)ceil_div(a.per_group, 16 * a.slabs);
-    switch (lane_states(a.states)) {
-        case 1: st = launch_grad<T, 1>(a, s); break;
-        case 2: st = launch_grad<T, 2>(a, s); break;
-        default: st = launch_grad<T, 4>(a, s); break;
-    }
+    a.shape = backward_shape(p.d);
+    st = grad_pass<T>(a, s);
     if (st != FNO_OK) return st;
-    if (a.chblocks > 1) {
+    if (a.shape.chblocks > 1) {
         const int64_t n = (int64_t)a.batch * a.length * a.groups * 2 * a.states;
         k_scan_sum_bc<T><<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(a);
     }
-    const int64_t cn = (int64_t)a.channels * a.states, parts = (int64_t)a.batch * a.segments;
-    const dim3 threads(32, kSumRows);
-    k_scan_sum<1><<<(unsigned)ceil_div(cn, 32), threads, 0, s>>>(a.part_a, a.dA, nullptr, cn,
-                                                                 parts);
-    if (a.dD || a.dbias)
-        k_scan_sum<2><<<(unsigned)ceil_div(2 * a.channels, 32), threads, 0, s>>>(
-            a.part_d, a.dD, a.dbias, 2 * (int64_t)a.channels, parts);
-    return ops::launched();
+    return sum_parts(a, s);
 }
 
 }  // namespace scan

@@ -4,16 +4,17 @@
 // For each channel c and state n of a sequence
 //   h_t = e^{d_t A} h_{t-1} + (d_t x_t) B_t,   y_t = sum_n C_t h_t,
 // one exponential and four multiply-adds an element (c, n) and token, and no matrix
-// product: the decay differs for every element.  So the exponentials and the issue
-// slots bound it, not memory (16 states: 8 to 12 bytes a channel and token).
+// product: the decay differs for every element.  So the exponentials (32 a cycle and SM),
+// the issue slots and the reads of shared memory bound it, not device memory (16 states: 8
+// to 12 bytes a channel and token).
 //
-// A warp holds 32 channels x 4 NN states in registers: lane = 4 dl + nl has channels
-// 4 dl .. 4 dl + 3 and the NN states from nl NN on, pairs of channels in one
-// instruction.  The steps d and the inputs u = d x are computed once for each channel
-// and token, by threads side by side, and read from shared memory as float4; B and C lie
-// there twice each, as the packed products want them.  A token's sums over states take
-// three shuffles for 16 elements: each lane ends with one channel.  More than 16 states
-// are shared by several warps, whose sums meet in shared memory.
+// A lane holds two channels x up to 16 states in registers, so that nothing is summed over
+// lanes: its channels' steps, inputs and outputs stay in its registers, from and to global
+// memory.  B and C, which all channels share, lie in shared memory as floats; a read there
+// costs its bytes times the lanes, whether they read the same or not, and two channels a
+// lane make that one cycle an element (four channels x four states a lane: 3.2, and 2.2
+// times the time).  More than 16 states are shared by several warps, whose sums meet in
+// shared memory.
 //
 // When the sequences and channels do not fill the GPU, time is split into segments:
 // one pass finds each segment's state from zero, a kernel joins them by
@@ -25,292 +26,275 @@
 namespace fno {
 namespace scan {
 
-// The outputs; the segments' states; the segments' and tiles' states and the gradients'
-// sums; the tiles' states of an unsplit time axis.
-enum Mode { kFull, kStates, kBoth, kTiles };
-constexpr bool with_c(Mode m) { return m == kFull || m == kBoth; }
-constexpr int fields_of(Mode m) { return m == kFull ? 3 : m == kBoth ? 4 : 2; }
-
-template <typename T>
-struct ForwardShared {
-    // raw tiles (two stages): x, dt, z (or dy, z backward), B, C; float tiles: the steps,
-    // the inputs, the output's gradients, B and C twice each, the partial sums of y
-    static __host__ __device__ size_t raw(int cb, int np, int fields) {
-        return (size_t)kTile * (fields * cb + 2 * np) * sizeof(T);
-    }
-    static __host__ __device__ size_t bytes(int cb, int np, int warps, Mode m) {
-        const int rows = 2 + (m == kFull ? warps : m == kBoth ? 1 : 0);
-        return 2 * raw(cb, np, fields_of(m)) + (size_t)kTile * (rows * cb * 4 + np * 16);
-    }
-};
-
-template <typename T, int NN, Mode M>
-__global__ void __launch_bounds__(256, 2)
+// The outputs from the states in front of the segments; the states at the segments' ends
+// and in front of the tiles (each if wanted); from the last token, what each segment adds to
+// the gradient of the state in front of it: r_t = a_t (r_{t+1} + C_t w_t), w = dy silu(z).
+enum Mode { kFull, kStates, kBack };
+template <typename T, int NS, Mode M>
+__global__ void __maxnreg__(128)
 k_scan(const Args p) {
     using namespace ops;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
-    const int cb = 32 * p.slabs, nw = threads / cb, np = 4 * NN * nw;
-    const int slab = (tid >> 5) / nw, sub = (tid >> 5) - slab * nw;
-    const int dl = lane >> 2, nl = lane & 3;
+    constexpr int G = 1;                              // tokens whose loads are in flight
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;    // pairs of B or C fetched ahead
+    extern __shared__ __align__(16) float sbc[];      // [2][seqs][kTile][2][np], sums of y
+    const int tid = threadIdx.x, threads = blockDim.x;
+    const Shape s = p.shape;
+    const int np = s.np;
+    const Unit u(tid, s);
     int64_t at = blockIdx.x;
     const int seg = (int)(at % p.segments);
     at /= p.segments;
-    const int chb = (int)(at % p.chblocks);
-    at /= p.chblocks;
-    const int grp = (int)(at % p.groups);
-    const int64_t b = at / p.groups;
-    const int c0 = chb * cb, cols = min(cb, p.per_group - c0);      // in the group
-    const int64_t ch0 = (int64_t)grp * p.per_group + c0;            // of all channels
-    const int64_t len = p.lengths ? max((int64_t)0, min((int64_t)p.lengths[b], p.length))
-                                  : p.length;
+    const int chb = (int)(at % s.chblocks);
+    const int64_t seq0 = at / s.chblocks * s.seqs, all = (int64_t)p.batch * p.groups;
+    const int64_t seq = seq0 + u.seq, b = min(seq, all - 1) / p.groups;
+    const int grp = (int)(min(seq, all - 1) - b * p.groups);
+    const int c = ((chb * s.slabs + u.slab) * s.lanes + u.lane) * 2;     // in the group
+    const int left = seq < all ? p.per_group - c : 0;
+    const int64_t ch = (int64_t)grp * p.per_group + c;
     const int64_t t0 = seg * p.seg_len;
-    const int64_t span = min(p.seg_len, p.length - t0);             // tokens of the segment
-    const int64_t have = max((int64_t)0, min(span, len - t0));      // that are there
-    constexpr int kFields = fields_of(M);
-    const size_t raw_bytes = ForwardShared<T>::raw(cb, np, kFields);
-    float *sd = reinterpret_cast<float *>(smem + 2 * raw_bytes);
-    float *su = sd + kTile * cb;
-    float *sy = su + kTile * cb;                                    // kBoth: dy silu(z)
-    float4 *sbc = reinterpret_cast<float4 *>(sy + (M == kFull ? nw : M == kBoth ? 1 : 0) *
-                                                      kTile * cb);
-
+    const int span = (int)min(p.seg_len, p.length - t0);
+    const auto tokens = [&](int64_t sequence) {       // of the segment that are there
+        const int64_t n = p.lengths ? max(0, p.lengths[sequence]) : p.length;
+        return (int)max((int64_t)0, min((int64_t)span, n - t0));
+    };
+    const int have = tokens(b);
+    int most = have;                                  // of any sequence of the block
+    for (int k = 0; k < s.seqs && p.lengths; ++k)
+        most = max(most, tokens(min(seq0 + k, all - 1) / p.groups));
     const int64_t row0 = b * p.length + t0;
-    const T *gx = static_cast<const T *>(p.x) + row0 * p.channels + ch0;
-    const T *gdt = static_cast<const T *>(p.dt) + row0 * p.channels + ch0;
-    const T *gz = p.z && with_c(M) ? static_cast<const T *>(p.z) + row0 * p.channels + ch0
-                                      : nullptr;
-    const T *gdy = M == kBoth ? static_cast<const T *>(p.dy) + row0 * p.channels + ch0 : nullptr;
-    const int64_t bc_stride = (int64_t)p.groups * p.states;
-    const T *gB = static_cast<const T *>(p.B) + row0 * bc_stride + (int64_t)grp * p.states;
-    const T *gC = static_cast<const T *>(p.C) + row0 * bc_stride + (int64_t)grp * p.states;
+    const bool wide = p.vec_c >= 2 * (int)sizeof(T);
 
-    const auto fetch = [&](int stage_no, int64_t t) {
-        const int valid = (int)min((int64_t)kTile, have - t);
-        T *r = reinterpret_cast<T *>(smem + stage_no * raw_bytes);
-        const int64_t o = t * p.channels;
-        stage(r, gx + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid, threads);
-        stage(r + kTile * cb, gdt + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid, threads);
-        if (gz)
-            stage(r + 2 * kTile * cb, gz + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid,
-                  threads);
-        if (M == kBoth)
-            stage(r + 3 * kTile * cb, gdy + o, p.channels, kTile, valid, cols, cb, p.vec_c, tid,
-                  threads);
-        T *rb = r + kFields * kTile * cb;
-        stage(rb, gB + t * bc_stride, bc_stride, kTile, valid, p.states, np, p.vec_n, tid,
-              threads);
-        if (with_c(M))
-            stage(rb + kTile * np, gC + t * bc_stride, bc_stride, kTile, valid, p.states, np,
-                  p.vec_n, tid, threads);
-        cp_async_commit();
+    // B and C of a tile: a thread has one pair of states of one of them (of a sequence) and
+    // every bc_step-th token
+    const int combos = s.seqs * np;                   // (no more than there are threads)
+    const int bc_step = threads / combos, bc_k = tid / combos, bc_tile = 2 * kTile * combos;
+    const T *bc_from;
+    int bc_to, bc_have, bc_left;
+    {
+        const int i = tid - bc_k * combos, q = i / np, which = (i - q * np) / (np / 2);
+        const int n = 2 * (i - q * np - which * (np / 2));
+        const int64_t sq = min(seq0 + q, all - 1), bb = sq / p.groups;
+        bc_have = p.lengths ? tokens(bb) : span;
+        bc_from = static_cast<const T *>(which || M == kBack ? p.C : p.B) +
+                  ((bb * p.length + t0 + (M == kBack ? bc_have - 1 - bc_k : bc_k)) * p.groups +
+                   (sq - bb * p.groups)) * p.states + n;
+        bc_to = ((q * kTile + bc_k) * 2 + which) * np + n;
+        bc_left = bc_k < bc_step && (!which || M == kFull) ? p.states - n : 0;
+    }
+    const bool bc_wide = p.vec_n >= 2 * (int)sizeof(T);
+    const int64_t bc_row = (M == kBack ? -1 : 1) * (int64_t)p.groups * p.states;
+    // the thread's m-th pair of the tile at t
+    const auto bc_load = [&](int m, int t) {
+        const int k = bc_k + m * bc_step;
+        return load_pair(bc_from + (int64_t)(t + m * bc_step) * bc_row, bc_wide,
+                         k < kTile && t + k < bc_have ? bc_left : 0);
+    };
+    const auto bc_store = [&](int buffer, int m, Pair<T> v) {
+        if (bc_k + m * bc_step < kTile && bc_k < bc_step)
+            *reinterpret_cast<float2 *>(sbc + buffer * bc_tile + bc_to + m * bc_step * 2 * np) =
+                to_float2(v);
     };
 
-    // this lane's elements: channels cl + j, states n0 + i, as pairs of channels
-    const int cl = slab * 32 + 4 * dl, n0 = (sub * 4 + nl) * NN;
-    float2 a2[2][NN], h[2][NN], pr[2][NN], g[2][NN];
-    float dsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const auto each = [&](auto f) {                     // f(pair, half, state, index in (c, n))
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < NN; ++i)
-                if (cl + j < cols && n0 + i < p.states)
-                    f(j >> 1, j & 1, i, (ch0 + cl + j) * p.states + n0 + i);
-    };
-    const auto half = [](float2 &v, int k) -> float & { return k ? v.y : v.x; };
-    const int64_t cn = (int64_t)p.channels * p.states;
+    float2 a2[2][NS / 2], h[2][NS / 2], dsum = f2(0.0f);
+    const int n0 = u.sub * NS;
+    load_states<NS>(p.A + ch * p.states + n0, left, p.states - n0, p.states, a2);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < NN; ++i) {
-            a2[j][i] = h[j][i] = g[j][i] = f2(0.0f);
-            pr[j][i] = f2(1.0f);
+        for (int i = 0; i < NS / 2; ++i) {
+            a2[j][i] = mul2(a2[j][i], f2(kLog2e));
+            h[j][i] = f2(0.0f);
         }
-    each([&](int j, int k, int i, int64_t e) { half(a2[j][i], k) = p.A[e] * kLog2e; });
-    if (M == kFull) {
-        const float *from = p.segments > 1 ? p.hseg + (b * p.segments + seg) * cn
-                            : p.s0         ? p.s0 + b * cn
-                                           : nullptr;
-        if (from) each([&](int j, int k, int i, int64_t e) { half(h[j][i], k) = from[e]; });
+    float2 bias = f2(0.0f), skip = f2(0.0f);
+    if (p.bias) bias = make_float2(left > 0 ? p.bias[ch] : 0.0f, left > 1 ? p.bias[ch + 1] : 0.0f);
+    if (M == kFull && p.D)
+        skip = make_float2(left > 0 ? p.D[ch] : 0.0f, left > 1 ? p.D[ch + 1] : 0.0f);
+    if (M == kFull && left > 0) {
+        if (p.segments > 1)
+            load_states<NS>(p.hseg + ((b * p.segments + seg) * p.channels + ch) * np + n0, left, NS,
+                            np, h);
+        else if (p.s0)
+            load_states<NS>(p.s0 + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
+                            p.states, h);
     }
 
-    // the pair of channels that this thread prepares and finishes, and its tokens
-    const int pairs = cb / 2, pc = 2 * (tid & (pairs - 1)), pt = tid / pairs;
-    const int pt_step = threads / pairs;
-    const bool in0 = pc < cols, in1 = pc + 1 < cols;
-    const bool wide = p.vec_c >= 2 * (int)sizeof(T);
-    float2 bias = f2(0.0f), skip = f2(0.0f);
-    if (p.bias) bias = make_float2(in0 ? p.bias[ch0 + pc] : 0.0f, in1 ? p.bias[ch0 + pc + 1] : 0.0f);
-    if (M == kFull && p.D)
-        skip = make_float2(in0 ? p.D[ch0 + pc] : 0.0f, in1 ? p.D[ch0 + pc + 1] : 0.0f);
-
-    if (have > 0) fetch(0, 0);
-    int stage_no = 0;
-    for (int64_t t = 0; t < have; t += kTile, stage_no ^= 1) {
-        const int valid = (int)min((int64_t)kTile, have - t);
-        cp_async_wait<0>();
+    const bool gated = M != kStates && p.z;
+    const int64_t o0 = row0 * p.channels + ch;
+    // x (back: dy), dt and z of the next G tokens
+    const T *const xs = static_cast<const T *>(M == kBack ? p.dy : p.x);
+    const int64_t row = M == kBack ? -(int64_t)p.channels : (int64_t)p.channels;
+    Pair<T> xr[G], dr[G], zr[G];
+    int64_t next = o0 + (M == kBack ? (have - 1) * (int64_t)p.channels : 0);
+    const auto fetch = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const int n = t + k < have ? left : 0;
+            xr[k] = load_pair(xs + next, wide, n);
+            dr[k] = load_pair(static_cast<const T *>(p.dt) + next, wide, n);
+            if (gated) zr[k] = load_pair(static_cast<const T *>(p.z) + next, wide, n);
+            next += row;
+        }
+    };
+    if (most > 0) {
+        for (int m = 0; m * bc_step < kTile; ++m) bc_store(0, m, bc_load(m, 0));
+        fetch(0);
+    }
+    float2 *sy = reinterpret_cast<float2 *>(sbc + 2 * bc_tile) + tid;     // [kTile][threads]
+    T *out = M == kFull ? static_cast<T *>(p.y) + o0 : nullptr;
+    int buffer = 0;
+    for (int t = 0; t < most; t += kTile, buffer ^= 1) {
         __syncthreads();
-        if (t + kTile < have) fetch(stage_no ^ 1, t + kTile);
-        const T *r = reinterpret_cast<const T *>(smem + stage_no * raw_bytes);
-        const T *rb = r + kFields * kTile * cb;
-        for (int k = pt; k < kTile; k += pt_step) {
-            const float2 xv = Storage<T>::load2(r + k * cb + pc);
-            float2 d = Storage<T>::load2(r + (kTile + k) * cb + pc);
-            d = add2(d, bias);
-            if (p.softplus) d = make_float2(softplus(d.x), softplus(d.y));
-            // (nothing lies beyond the last token or channel)
-            if (k >= valid || !in0) d.x = 0.0f;
-            if (k >= valid || !in1) d.y = 0.0f;
-            *reinterpret_cast<float2 *>(sd + k * cb + pc) = d;
-            *reinterpret_cast<float2 *>(su + k * cb + pc) = mul2(d, xv);
-            if (M == kBoth) {
-                float2 gy = Storage<T>::load2(r + (3 * kTile + k) * cb + pc);
-                if (gz) {
-                    const float2 zv = Storage<T>::load2(r + (2 * kTile + k) * cb + pc);
-                    gy = make_float2(gy.x * zv.x * logistic(zv.x), gy.y * zv.y * logistic(zv.y));
+        const bool more = t + kTile < most;
+        Pair<T> ahead[kAhead];
+        if (more) {
+#pragma unroll
+            for (int m = 0; m < kAhead; ++m) ahead[m] = bc_load(m, t + kTile);
+        }
+        if (M == kStates && p.htile && t < have && left > 0) {
+            const int64_t tile = b * ((p.length + kTile - 1) / kTile) + (t0 + t) / kTile;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < NS / 4; ++q) {
+                    const float2 v = h[j][2 * q], w = h[j][2 * q + 1];
+                    *tile_at(p, tile, grp, c, j, n0 + 4 * q) = make_float4(v.x, v.y, w.x, w.y);
                 }
-                *reinterpret_cast<float2 *>(sy + k * cb + pc) = gy;
+            if (u.sub == 0) {
+                float *d = p.dtile + tile * p.channels + ch;
+                d[0] = dsum.x;
+                if (left > 1) d[1] = dsum.y;
             }
         }
-        for (int i = tid; i < kTile * np; i += threads) {
-            const float bv = Storage<T>::load(rb + i);
-            const float cv = with_c(M) ? Storage<T>::load(rb + kTile * np + i) : 0.0f;
-            sbc[i] = make_float4(bv, bv, cv, cv);
-        }
-        __syncthreads();
-        if (M == kBoth || M == kTiles) {
-            const int64_t ck = b * ((p.length + kTile - 1) / kTile) + (t0 + t) / kTile;
-            each([&](int j, int k, int i, int64_t e) { p.hchunk[ck * cn + e] = half(h[j][i], k); });
-            if (sub == 0 && nl == 0)
+        const float *bc = sbc + buffer * bc_tile + u.seq * kTile * 2 * np + n0;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kTile && t + k0 < most; k0 += G) {
+            float2 d[G], x[G], z[G];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (cl + j < cols) p.dchunk[ck * p.channels + ch0 + cl + j] = dsum[j];
-        }
-#pragma unroll 2
-        for (int k = 0; k < kTile; ++k) {
-            if (k >= valid) break;
-            const float4 d4 = *reinterpret_cast<const float4 *>(sd + k * cb + cl);
-            const float4 u4 = *reinterpret_cast<const float4 *>(su + k * cb + cl);
-            const float2 d[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
-            const float2 u[2] = {make_float2(u4.x, u4.y), make_float2(u4.z, u4.w)};
-            float2 gy[2];
-            if (M == kBoth) {
-                const float4 g4 = *reinterpret_cast<const float4 *>(sy + k * cb + cl);
-                gy[0] = make_float2(g4.x, g4.y), gy[1] = make_float2(g4.z, g4.w);
+            for (int k = 0; k < G; ++k) {
+                x[k] = to_float2(xr[k]);
+                d[k] = add2(to_float2(dr[k]), bias);
+                if (p.softplus) d[k] = softplus2(d[k]);
+                if (t + k0 + k >= have) d[k] = f2(0.0f);
+                if (gated) z[k] = to_float2(zr[k]);
+                if (M == kBack && gated) x[k] = mul2(x[k], mul2(z[k], logistic2(z[k])));
             }
-            if (M != kFull) dsum[0] += d4.x, dsum[1] += d4.y, dsum[2] += d4.z, dsum[3] += d4.w;
-            float2 y[2] = {f2(0.0f), f2(0.0f)};
+            fetch(t + k0 + G);
 #pragma unroll
-            for (int i = 0; i < NN; ++i) {
-                const float4 bc = sbc[k * np + n0 + i];
-                const float2 bv = make_float2(bc.x, bc.y), cv = make_float2(bc.z, bc.w);
+            for (int k = 0; k < G; ++k) {
+                // (back: the output's gradient in the input's place, C in B's)
+                const float2 du = M == kBack ? x[k] : mul2(d[k], x[k]);
+                if (M == kStates) dsum = add2(dsum, d[k]);
+                float2 y[2] = {f2(0.0f), f2(0.0f)};
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 q = mul2(a2[j][i], d[j]);
-                    const float2 a = make_float2(exp2_fast(q.x), exp2_fast(q.y));
-                    h[j][i] = fma2(a, h[j][i], mul2(u[j], bv));
-                    if (M == kFull) y[j] = fma2(cv, h[j][i], y[j]);
-                    if (M == kBoth) {
-                        pr[j][i] = mul2(pr[j][i], a);
-                        g[j][i] = fma2(pr[j][i], mul2(cv, gy[j]), g[j][i]);
+                for (int q = 0; q < NS / 4; ++q) {
+                    const float4 bq = *reinterpret_cast<const float4 *>(bc + 4 * q);
+                    float4 cq;
+                    if (M == kFull) cq = *reinterpret_cast<const float4 *>(bc + np + 4 * q);
+#pragma unroll
+                    for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                        const float2 bv = i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
+                        const float2 cv = i & 1 ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 a = exp2_fast2(mul2(a2[j][i], f2(j ? d[k].y : d[k].x)));
+                            const float2 uv = f2(j ? du.y : du.x);
+                            if (M == kBack) h[j][i] = mul2(a, fma2(uv, bv, h[j][i]));
+                            else h[j][i] = fma2(a, h[j][i], mul2(uv, bv));
+                            if (M == kFull) y[j] = fma2(cv, h[j][i], y[j]);
+                        }
                     }
                 }
-            }
-            if (M == kFull) {
-                // the quad's sums: lane nl ends with channel 4 dl + nl
-                const bool hi = nl & 2, odd = nl & 1;
-                float2 keep = hi ? y[1] : y[0];
-                const float2 send = hi ? y[0] : y[1];
-                keep.x += __shfl_xor_sync(0xffffffffu, send.x, 2);
-                keep.y += __shfl_xor_sync(0xffffffffu, send.y, 2);
-                const float v = (odd ? keep.y : keep.x) +
-                                __shfl_xor_sync(0xffffffffu, odd ? keep.x : keep.y, 1);
-                sy[(sub * kTile + k) * cb + slab * 32 + lane] = v;
+                bc += 2 * np;
+                if (M == kFull) {
+                    float2 v = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+                    if (s.warps > 1) {
+                        sy[(k0 + k) * threads] = v;
+                        continue;
+                    }
+                    v = fma2(skip, x[k], v);
+                    if (gated) v = mul2(v, mul2(z[k], logistic2(z[k])));
+                    store_pair(out, v, wide, t + k0 + k < have ? left : 0);
+                    out += p.channels;
+                }
             }
         }
-        if (M == kFull) {
+        if (M == kFull && s.warps > 1) {
+            // the warps that share these channels' states take the tokens in turns
             __syncthreads();
-            T *out = static_cast<T *>(p.y) + (row0 + t) * p.channels + ch0 + pc;
-            for (int k = pt; k < valid; k += pt_step) {
-                float2 v = *reinterpret_cast<const float2 *>(sy + k * cb + pc);
-                for (int w = 1; w < nw; ++w)
-                    v = add2(v, *reinterpret_cast<const float2 *>(sy + (w * kTile + k) * cb + pc));
-                v = fma2(skip, Storage<T>::load2(r + k * cb + pc), v);
-                if (gz) {
-                    const float2 zv = Storage<T>::load2(r + (2 * kTile + k) * cb + pc);
-                    v = make_float2(v.x * zv.x * logistic(zv.x), v.y * zv.y * logistic(zv.y));
+            for (int k = u.sub; k < kTile && t + k < have; k += s.warps) {
+                float2 v = f2(0.0f);
+                for (int i = 0; i < s.warps; ++i)
+                    v = add2(v, sy[k * threads + (i - u.sub) * s.lanes]);
+                const int64_t o = o0 + (int64_t)(t + k) * p.channels;
+                v = fma2(skip, to_float2(load_pair(static_cast<const T *>(p.x) + o, wide, left)), v);
+                if (gated) {
+                    const float2 zv =
+                        to_float2(load_pair(static_cast<const T *>(p.z) + o, wide, left));
+                    v = mul2(v, mul2(zv, logistic2(zv)));
                 }
-                T *o = out + (int64_t)k * p.channels;
-                if (wide && in0) {
-                    Pack<T, 2> w2;
-                    Storage<T>::store(&w2.v[0], v.x);
-                    Storage<T>::store(&w2.v[1], v.y);
-                    *reinterpret_cast<Pack<T, 2> *>(o) = w2;
-                } else {
-                    if (in0) Storage<T>::store(o, v.x);
-                    if (in1) Storage<T>::store(o + 1, v.y);
-                }
+                store_pair(static_cast<T *>(p.y) + o, v, wide, left);
             }
+        }
+        if (more) {
+#pragma unroll
+            for (int m = 0; m < kAhead; ++m) bc_store(buffer ^ 1, m, ahead[m]);
+            for (int m = kAhead; m * bc_step < kTile; ++m)
+                bc_store(buffer ^ 1, m, bc_load(m, t + kTile));
         }
     }
     if (M == kFull) {
-        T *out = static_cast<T *>(p.y) + row0 * p.channels + ch0 + pc;
-        for (int64_t t = have + pt; t < span; t += pt_step) {
-            if (in0) Storage<T>::store(out + t * p.channels, 0.0f);
-            if (in1) Storage<T>::store(out + t * p.channels + 1, 0.0f);
-        }
+        for (int t = have + u.sub; t < span; t += s.warps)
+            store_pair(static_cast<T *>(p.y) + o0 + (int64_t)t * p.channels, f2(0.0f), wide, left);
         if (p.sT && seg == p.segments - 1)
-            each([&](int j, int k, int i, int64_t e) { p.sT[b * cn + e] = half(h[j][i], k); });
-    } else if (M != kTiles) {
-        const int64_t s = b * p.segments + seg;
-        each([&](int j, int k, int i, int64_t e) { p.hseg[s * cn + e] = half(h[j][i], k); });
-        if (M == kBoth)
-            each([&](int j, int k, int i, int64_t e) { p.gseg[s * cn + e] = half(g[j][i], k); });
-        if (sub == 0 && nl == 0)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (cl + j < cols) p.dseg[s * p.channels + ch0 + cl + j] = dsum[j];
+            store_states<NS>(p.sT + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
+                             p.states, h);
+    } else if (p.segments > 1) {
+        const int64_t r = (b * p.segments + seg) * p.channels + ch;
+        store_states<NS>((M == kBack ? p.gseg : p.hseg) + r * np + n0, left, NS, np, h);
+        if (M == kStates && u.sub == 0) {
+            if (left > 0) p.dseg[r] = dsum.x;
+            if (left > 1) p.dseg[r + 1] = dsum.y;
+        }
     }
 }
 
-template <typename T, int NN, Mode M>
+template <typename T, int NS, Mode M>
 fno_status_t launch_scan(const Args &a, cudaStream_t s) {
-    const int cb = 32 * a.slabs, nw = NN == 4 ? state_warps(a.states) : 1;
-    const size_t bytes = ForwardShared<T>::bytes(cb, 4 * NN * nw, nw, M);
-    const auto kernel = k_scan<T, NN, M>;
+    const Shape &h = a.shape;
+    const int threads = h.threads();
+    const int bytes = h.seqs * kTile * h.np * 16 +
+                      (M == kFull && h.warps > 1 ? kTile * threads * 8 : 0);
+    const auto kernel = k_scan<T, NS, M>;
     if (bytes > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
             cudaSuccess) {
         cudaGetLastError();
         return FNO_ERR_CUDA;
     }
-    const int64_t blocks = (int64_t)a.batch * a.groups * a.chblocks * a.segments;
-    kernel<<<(unsigned)blocks, cb * nw, bytes, s>>>(a);
+    const int64_t blocks = ops::ceil_div((int64_t)a.batch * a.groups, h.seqs) * h.chblocks *
+                           a.segments;
+    kernel<<<(unsigned)blocks, threads, bytes, s>>>(a);
     return ops::launched();
 }
 template <typename T, Mode M>
-fno_status_t scan_pass(Args a, int slabs, cudaStream_t s) {
-    a.slabs = slabs;
-    a.chblocks = (int)ops::ceil_div(a.per_group, 32 * slabs);
+fno_status_t scan_pass(const fno_scan_s &p, Args a, cudaStream_t s) {
+    a.shape = forward_shape(p.d);
     switch (lane_states(a.states)) {
-        case 1: return launch_scan<T, 1, M>(a, s);
-        case 2: return launch_scan<T, 2, M>(a, s);
-        default: return launch_scan<T, 4, M>(a, s);
+        case 4: return launch_scan<T, 4, M>(a, s);
+        case 8: return launch_scan<T, 8, M>(a, s);
+        default: return launch_scan<T, 16, M>(a, s);
     }
 }
 
 template <typename T>
 fno_status_t forward_of(const fno_scan_s &p, Args a, cudaStream_t s) {
-    const int slabs = forward_slabs(p);
-    a.segments = p.segments;
-    a.seg_len = p.seg_len;
+    a.htile = nullptr;
     if (a.segments > 1) {
-        fno_status_t st = scan_pass<T, kStates>(a, slabs, s);
+        fno_status_t st = scan_pass<T, kStates>(p, a, s);
         if (st == FNO_OK) st = join(a, false, s);
         if (st != FNO_OK) return st;
     }
-    return scan_pass<T, kFull>(a, slabs, s);
+    return scan_pass<T, kFull>(p, a, s);
 }
 
 }  // namespace scan

@@ -323,7 +323,7 @@ typedef struct fno_causal_conv_s *fno_causal_conv_t;
 
 #define FNO_CAUSAL_CONV_BACKWARD 1u   /* the workspace is that of the backward              */
 
-/* batch, length, channels >= 1; 2 <= width <= 8.  Errors: INVALID_ARG, UNSUPPORTED,
+/* batch, length, channels >= 1, length below 2^31 - 64; 2 <= width <= 8.  Errors: INVALID_ARG, UNSUPPORTED,
  * OUT_OF_MEMORY, CUDA.                                                        */
 fno_status_t fno_causal_conv_plan(fno_causal_conv_t *plan, int64_t batch, int64_t length,
                                   int32_t channels, int32_t width, fno_act_t act,
@@ -376,9 +376,9 @@ typedef struct fno_scan_s *fno_scan_t;
 #define FNO_SCAN_BACKWARD 1u   /* the workspace also covers the backward                    */
 
 typedef struct fno_scan_desc_s {
-    int64_t batch, length;    /* >= 1                                                     */
+    int64_t batch, length;    /* >= 1; length below 2^31 - 16                             */
     int32_t channels;         /* >= 1, a multiple of groups                               */
-    int32_t states;           /* 1 .. 128                                                 */
+    int32_t states;           /* 1 .. 64                                                  */
     int32_t groups;           /* >= 1                                                     */
     int32_t softplus;         /* 0: d = dt + dt_bias                                      */
     fno_dtype_t dtype;

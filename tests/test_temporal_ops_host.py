@@ -36,7 +36,7 @@ def rotary_desc(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(batch=0), BAD), (dict(length=0), BAD), (dict(channels=0), BAD), (dict(states=0), BAD),
     (dict(groups=0), BAD), (dict(groups=4), BAD), (dict(dtype=3), BAD), (dict(flags=2), BAD),
-    (dict(batch=-1), BAD), (dict(states=129), UNS), (dict(length=1 << 40), UNS),
+    (dict(batch=-1), BAD), (dict(states=65), UNS), (dict(length=1 << 40), UNS),
     (dict(batch=1 << 36), UNS),
 ])
 def test_scan_plan_rejects(kw, code):
