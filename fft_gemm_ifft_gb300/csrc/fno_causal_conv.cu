@@ -1,8 +1,7 @@
 // fno_causal_conv.cu -- short causal convolutions of every channel along time, with their
 // activation: whole sequences, gradients, single tokens.
 //
-// 2 width multiply-adds an element: bound by bytes.  A thread takes two channels (one, where
-// their number is odd) of a run of tokens with the last inputs in registers, so that an input
+// 2 width multiply-adds an element: bound by bytes.  A thread takes two channels of a run of tokens with the last inputs in registers, so that an input
 // is loaded once and the width - 1 in front of a run once more.  Two channels and no more:
 // the weights, the window and eight tokens' loads then take few enough registers for the
 // warps that keep enough loads on their way.
@@ -40,60 +39,56 @@ struct Args {
 };
 
 // v / (1 + e^-v) and its slope (fast quotient and exponential, 1e-6 for |v| up to 10)
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float silu(float v) {
+    return v * rcp_fast(1.0f + exp2_fast(-kLog2e * v));
+}
 __device__ __forceinline__ float silu_slope(float v) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-v));
+    const float s = rcp_fast(1.0f + exp2_fast(-kLog2e * v));
     return s * fmaf(v, 1.0f - s, 1.0f);
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void load(const T *p, float *v) {
-    const Pack<T, V> a = *reinterpret_cast<const Pack<T, V> *>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = Storage<T>::load(&a.v[i]);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store(T *p, const float *v) {
-    Pack<T, V> a;
-#pragma unroll
-    for (int i = 0; i < V; ++i) Storage<T>::store(&a.v[i], v[i]);
-    *reinterpret_cast<Pack<T, V> *>(p) = a;
-}
-
 // Input s of a sequence (s < 0: of its initial state).
-template <typename T, int V, int W>
-__device__ __forceinline__ void input(const Args &p, int64_t b, int s, int c, float *v) {
-    if (s >= 0) {
-        load<T, V>(static_cast<const T *>(p.x) + (b * p.length + s) * p.channels + c, v);
-    } else if (p.s0) {
-        load<T, V>(static_cast<const T *>(p.s0) + (b * (W - 1) + s + W - 1) * p.channels + c, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.0f;
-    }
+template <typename T, bool WIDE, int W>
+__device__ __forceinline__ float2 input(const Args &p, int64_t b, int s, int c, int left) {
+    if (s >= 0)
+        return to_float2(load_pair(static_cast<const T *>(p.x) + (b * p.length + s) * p.channels + c,
+                                   WIDE, left));
+    if (!p.s0) return f2(0.0f);
+    return to_float2(load_pair(
+        static_cast<const T *>(p.s0) + (b * (W - 1) + s + W - 1) * p.channels + c, WIDE, left));
 }
 __device__ __forceinline__ int tokens(const Args &p, int64_t b) {
     return p.lengths ? max(0, min(p.lengths[b], p.length)) : p.length;
 }
-// The weights (channels, W) of V channels, tap by tap.
-template <int V, int W>
-__device__ __forceinline__ void load_weights(const Args &p, int c, float (&w)[W][V],
-                                             float (&bias)[V]) {
-    float flat[V * W];
+// The weights (channels, W) of two channels, tap by tap.
+template <int W>
+__device__ __forceinline__ void load_weights(const Args &p, int c, int left, float2 (&w)[W],
+                                             float2 &bias) {
     const float *from = p.w + (int64_t)c * W;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        const Pack<float, V> a = *reinterpret_cast<const Pack<float, V> *>(from + k * V);
-#pragma unroll
-        for (int i = 0; i < V; ++i) flat[k * V + i] = a.v[i];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = flat[i * W + j];
-        bias[i] = p.bias ? p.bias[c + i] : 0.0f;
+    for (int j = 0; j < W; ++j)
+        w[j] = make_float2(left > 0 ? from[j] : 0.0f, left > 1 ? from[W + j] : 0.0f);
+    bias = f2(0.0f);
+    if (p.bias) bias = make_float2(left > 0 ? p.bias[c] : 0.0f, left > 1 ? p.bias[c + 1] : 0.0f);
+}
+// A pair as it was loaded.
+template <typename T>
+__device__ __forceinline__ void store_raw(T *p, const Pair<T> &v, bool wide, int left) {
+    const T *e = reinterpret_cast<const T *>(&v);
+    if (wide) *reinterpret_cast<Pair<T> *>(p) = v;
+    else {
+        p[0] = e[0];
+        if (left > 1) p[1] = e[1];
     }
 }
+template <int W>
+__device__ __forceinline__ float2 taps(const float2 (&w)[W], const float2 (&win)[W], float2 s) {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        s = make_float2(fmaf(w[j].x, win[j].x, s.x), fmaf(w[j].y, win[j].y, s.y));
+    return s;
+}
+
 // A block: `across` threads over channels (all blockIdx.y make), the rest over runs.  Which
 // run of which sequence:
 struct Run {
@@ -107,63 +102,58 @@ struct Run {
     }
 };
 
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool WIDE, int W>
+__global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 3)
 k_conv(const Args p) {
-    constexpr int U = 8;                       // tokens whose loads are in flight
+    constexpr int U = 8;                       // tokens whose loads are on their way
     const int lane = threadIdx.x % p.across, rank = threadIdx.x / p.across;
-    const int c = (blockIdx.y * p.across + lane) * V;
+    const int c = (blockIdx.y * p.across + lane) * 2, left = p.channels - c;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / p.across) + rank;
-    if (row >= p.rows || c >= p.channels) return;
+    if (row >= p.rows || left <= 0) return;
     const Run r(p, row);
     const int n = tokens(p, r.b), end = min(r.t1, n);
-    float w[W][V], bias[V], win[W - 1][V];     // win: the inputs in front, oldest first
-    load_weights<V, W>(p, c, w, bias);
+    float2 w[W], bias, win[W];                 // win: the last W inputs, oldest first
+    load_weights<W>(p, c, left, w, bias);
     const int64_t at = (r.b * p.length + r.t0) * p.channels + c;
     T *y = static_cast<T *>(p.y) + at;
     const T *x = static_cast<const T *>(p.x) + at;
-    if (r.t0 < end) {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) input<T, V, W>(p, r.b, r.t0 - (W - 1) + j, c, win[j]);
-    }
-    for (int t = r.t0; t < end; t += U) {
-        Pack<T, V> in[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (t + k < end)
-                in[k] = *reinterpret_cast<const Pack<T, V> *>(x + (int64_t)k * p.channels);
+    Pair<T> next[U];
+    const auto fetch = [&](int t) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (t + k >= end) break;
-            float v[V], o[V];
+            next[k] = load_pair(x, WIDE, t + k < end ? left : 0);
+            x += p.channels;
+        }
+    };
+    if (r.t0 < end) {
+        fetch(r.t0);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v[i] = Storage<T>::load(&in[k].v[i]);
-                float s = bias[i];
+        for (int j = 1; j < W; ++j) win[j] = input<T, WIDE, W>(p, r.b, r.t0 - W + j, c, left);
+    }
+    for (int t = r.t0; t < end; t += U) {
+        Pair<T> in[U];
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
-                s = fmaf(w[W - 1][i], v[i], s);
-                o[i] = p.silu ? silu(s) : s;
+        for (int k = 0; k < U; ++k) in[k] = next[k];
+        if (t + U < end) fetch(t + U);
 #pragma unroll
-                for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
-                win[W - 2][i] = v[i];
-            }
-            store<T, V>(y, o);
+        for (int k = 0; k < U; ++k) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+            win[W - 1] = to_float2(in[k]);
+            float2 s = taps<W>(w, win, bias);
+            if (p.silu) s = make_float2(silu(s.x), silu(s.y));
+            store_pair(y, s, WIDE, t + k < end ? left : 0);
             y += p.channels;
         }
-        x += (int64_t)U * p.channels;
     }
-    const float zero[V] = {};
     y = static_cast<T *>(p.y) + at;
     for (int t = max(r.t0, end); t < r.t1; ++t)
-        store<T, V>(y + (int64_t)(t - r.t0) * p.channels, zero);
+        store_pair(y + (int64_t)(t - r.t0) * p.channels, f2(0.0f), WIDE, left);
     if (p.sT && r.t0 == 0) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            float v[V];
-            input<T, V, W>(p, r.b, n - (W - 1) + j, c, v);
-            store<T, V>(static_cast<T *>(p.sT) + (r.b * (W - 1) + j) * p.channels + c, v);
-        }
+        for (int j = 0; j < W - 1; ++j)
+            store_pair(static_cast<T *>(p.sT) + (r.b * (W - 1) + j) * p.channels + c,
+                       input<T, WIDE, W>(p, r.b, n - (W - 1) + j, c, left), WIDE, left);
     }
 }
 
@@ -171,93 +161,86 @@ k_conv(const Args p) {
 // inputs again; then dx_s = sum_j w_j g_{s + W - 1 - j}, for which a run goes on W - 1
 // tokens, and dw_j = sum_t g_t x_{t - W + 1 + j}.  A block takes every gridDim.x-th group of
 // runs and leaves one sum of its dw and dbias.
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool WIDE, int W>
+__global__ void __launch_bounds__(kThreads, W <= 4 ? 3 : 2)
 k_conv_grad(const Args p) {
-    __shared__ float sums[kThreads * V];
+    __shared__ float2 sums[kThreads];
     constexpr int U = 4;
     const int lane = threadIdx.x % p.across, down = kThreads / p.across;
-    const int rank = threadIdx.x / p.across, c = (blockIdx.y * p.across + lane) * V;
-    const bool there = c < p.channels;
-    float w[W][V], bias[V], dw[W][V], db[V];
+    const int rank = threadIdx.x / p.across, c = (blockIdx.y * p.across + lane) * 2;
+    const int left = p.channels - c;
+    float2 w[W], bias, dw[W], db = f2(0.0f);
+    load_weights<W>(p, c, left, w, bias);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = dw[j][i] = 0.0f;
-        bias[i] = db[i] = 0.0f;
-    }
-    if (there) load_weights<V, W>(p, c, w, bias);
-    for (int64_t row = (int64_t)blockIdx.x * down + rank; there && row < p.rows;
+    for (int j = 0; j < W; ++j) dw[j] = f2(0.0f);
+    for (int64_t row = (int64_t)blockIdx.x * down + rank; left > 0 && row < p.rows;
          row += (int64_t)gridDim.x * down) {
         const Run r(p, row);
         const int n = tokens(p, r.b), t0 = r.t0, t1 = r.t1;
         // win: inputs t - W + 1 .. t; acc: the gradients of these inputs so far
-        float win[W][V], acc[W][V];
+        float2 win[W], acc[W];
         const int64_t at = (r.b * p.length + t0) * p.channels + c;
         const int end = min(t1 + W - 1, n);                // tokens that reach the run's inputs
         // gradients that come from the final state: input n - W + 1 + j has state j
-        const auto from_state = [&](int s, float *v) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = 0.0f;
+        const auto from_state = [&](int s) {
             const int j = s - n + W - 1;
-            if (p.dsT && s < n && j >= 0)
-                load<T, V>(static_cast<const T *>(p.dsT) + (r.b * (W - 1) + j) * p.channels + c, v);
+            if (!p.dsT || s >= n || j < 0) return f2(0.0f);
+            return to_float2(load_pair(static_cast<const T *>(p.dsT) +
+                                           (r.b * (W - 1) + j) * p.channels + c, WIDE, left));
         };
-        const auto finish = [&](int s, const float *v) {       // input s is complete
-            if (s >= t0 && s < t1) {
-                store<T, V>(static_cast<T *>(p.dx) + at + (int64_t)(s - t0) * p.channels, v);
-            } else if (s < 0 && t0 == 0 && p.ds0) {
-                store<T, V>(static_cast<T *>(p.ds0) + (r.b * (W - 1) + s + W - 1) * p.channels + c,
-                            v);
+        T *const dx = static_cast<T *>(p.dx) + at;
+        const auto finish = [&](int s, float2 v) {             // input s is complete
+            if (s >= t0 && s < t1)
+                store_pair(dx + (int64_t)(s - t0) * p.channels, v, WIDE, left);
+            else if (s < 0 && t0 == 0 && p.ds0)
+                store_pair(static_cast<T *>(p.ds0) + (r.b * (W - 1) + s + W - 1) * p.channels + c,
+                           v, WIDE, left);
+        };
+        const T *x = static_cast<const T *>(p.x) + at, *dy = static_cast<const T *>(p.dy) + at;
+        Pair<T> xn[U], gn[U];
+        const auto fetch = [&](int t) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                xn[k] = load_pair(x, WIDE, t + k < end ? left : 0);
+                gn[k] = load_pair(dy, WIDE, t + k < end ? left : 0);
+                x += p.channels;
+                dy += p.channels;
             }
         };
         if (t0 < n || t0 == 0) {
+            if (t0 < end) fetch(t0);
 #pragma unroll
             for (int j = 1; j < W; ++j) {
-                input<T, V, W>(p, r.b, t0 - W + j, c, win[j]);
-                from_state(t0 - W + j, acc[j]);
+                win[j] = input<T, WIDE, W>(p, r.b, t0 - W + j, c, left);
+                acc[j] = from_state(t0 - W + j);
             }
         }
-        const T *x = static_cast<const T *>(p.x) + at, *dy = static_cast<const T *>(p.dy) + at;
         for (int t = t0; t < end; t += U) {
-            Pack<T, V> xin[U], gin[U];
+            Pair<T> xin[U], gin[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-                if (t + k < end) {
-                    xin[k] = *reinterpret_cast<const Pack<T, V> *>(x + (int64_t)k * p.channels);
-                    gin[k] = *reinterpret_cast<const Pack<T, V> *>(dy + (int64_t)k * p.channels);
-                }
-            x += (int64_t)U * p.channels;
-            dy += (int64_t)U * p.channels;
+            for (int k = 0; k < U; ++k) xin[k] = xn[k], gin[k] = gn[k];
+            if (t + U < end) fetch(t + U);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 if (t + k >= end) break;
-                float last[V];
-                from_state(t + k, last);
-                const float mine = t + k < t1 ? 1.0f : 0.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
+                for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1], acc[j] = acc[j + 1];
+                win[W - 1] = to_float2(xin[k]);
+                acc[W - 1] = from_state(t + k);
+                float2 g = to_float2(gin[k]);
+                if (p.silu) {
+                    const float2 s = taps<W>(w, win, bias);
+                    g = make_float2(g.x * silu_slope(s.x), g.y * silu_slope(s.y));
+                }
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
-                        win[j][i] = win[j + 1][i];
-                        acc[j][i] = acc[j + 1][i];
-                    }
-                    win[W - 1][i] = Storage<T>::load(&xin[k].v[i]);
-                    acc[W - 1][i] = last[i];
-                    float g = Storage<T>::load(&gin[k].v[i]);
-                    if (p.silu) {
-                        float s = bias[i];
+                for (int j = 0; j < W; ++j)
+                    acc[j] = make_float2(fmaf(w[j].x, g.x, acc[j].x), fmaf(w[j].y, g.y, acc[j].y));
+                if (t + k < t1) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) s = fmaf(w[j][i], win[j][i], s);
-                        g *= silu_slope(s);
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; ++j) acc[j][i] = fmaf(w[j][i], g, acc[j][i]);
-                    if (mine != 0.0f) {
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][i] = fmaf(g, win[j][i], dw[j][i]);
-                        db[i] += g;
-                    }
+                    for (int j = 0; j < W; ++j)
+                        dw[j] = make_float2(fmaf(g.x, win[j].x, dw[j].x),
+                                            fmaf(g.y, win[j].y, dw[j].y));
+                    db = add2(db, g);
                 }
                 finish(t + k - W + 1, acc[0]);
             }
@@ -269,23 +252,20 @@ k_conv_grad(const Args p) {
 #pragma unroll
             for (int j = 1; j < W; ++j) finish(e - W + j, acc[j]);
         }
-        const float zero[V] = {};
         for (int s = max(t0, n); s < t1; ++s)
-            store<T, V>(static_cast<T *>(p.dx) + at + (int64_t)(s - t0) * p.channels, zero);
+            store_pair(dx + (int64_t)(s - t0) * p.channels, f2(0.0f), WIDE, left);
     }
     float *out = p.part + (int64_t)blockIdx.x * (W + 1) * p.channels;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            sums[(rank * V + i) * p.across + lane] = j < W ? dw[j < W ? j : 0][i] : db[i];
+        sums[threadIdx.x] = j < W ? dw[j < W ? j : 0] : db;
         __syncthreads();
-        for (int i = threadIdx.x; i < p.across * V; i += kThreads) {
-            float v = 0.0f;
-            for (int k = 0; k < down; ++k) v += sums[k * V * p.across + i];
-            const int64_t ch = (int64_t)(blockIdx.y * p.across + i % p.across) * V + i / p.across;
-            if (ch < p.channels) out[(int64_t)j * p.channels + ch] = v;
+        if (rank == 0) {
+            float2 v = sums[lane];
+            for (int k = 1; k < down; ++k) v = add2(v, sums[k * p.across + lane]);
+            if (left > 0) out[(int64_t)j * p.channels + c] = v.x;
+            if (left > 1) out[(int64_t)j * p.channels + c + 1] = v.y;
         }
     }
 }
@@ -312,39 +292,38 @@ k_conv_sum(const float *__restrict__ part, float *__restrict__ dw, float *__rest
     else if (db) db[c] = v;
 }
 
-template <typename T, int V, int W>
+template <typename T, bool WIDE, int W>
 __global__ void __launch_bounds__(kThreads)
 k_conv_step(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
             const int32_t *__restrict__ slots, int64_t num_slots, const T *state, T *new_state,
-            T *__restrict__ y, int64_t batch, int channels, bool act) {
-    const int cols = channels / V;
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x, b = id / cols;
-    if (b >= batch) return;
-    const int c = (int)(id - b * cols) * V;
+            T *__restrict__ y, int channels, int blocks_a_row, bool act) {
+    const int64_t b = blockIdx.x / blocks_a_row;
+    const int c = ((int)(blockIdx.x - b * blocks_a_row) * kThreads + threadIdx.x) * 2;
+    const int left = channels - c;
+    if (left <= 0) return;
     const int64_t slot = slots ? (int64_t)slots[b] : b;
-    float o[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.0f;
+    float2 s = f2(0.0f);
     if (slot >= 0 && slot < num_slots) {
-        Pack<T, V> in[W];
+        Pair<T> in[W];
         const int64_t at = slot * (W - 1) * channels + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            in[j] = *reinterpret_cast<const Pack<T, V> *>(state + at + (int64_t)j * channels);
-        in[W - 1] = *reinterpret_cast<const Pack<T, V> *>(x + b * channels + c);
+            in[j] = load_pair(state + at + (int64_t)j * channels, WIDE, left);
+        in[W - 1] = load_pair(x + b * channels + c, WIDE, left);
+        const float *from = w + (int64_t)c * W;
+        if (bias) s = make_float2(bias[c], left > 1 ? bias[c + 1] : 0.0f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float s = bias ? bias[c + i] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                s = fmaf(w[(int64_t)(c + i) * W + j], Storage<T>::load(&in[j].v[i]), s);
-            o[i] = act ? silu(s) : s;
+        for (int j = 0; j < W; ++j) {
+            const float2 v = to_float2(in[j]);
+            s.x = fmaf(from[j], v.x, s.x);
+            if (left > 1) s.y = fmaf(from[W + j], v.y, s.y);
         }
+        if (act) s = make_float2(silu(s.x), silu(s.y));
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            *reinterpret_cast<Pack<T, V> *>(new_state + at + (int64_t)j * channels) = in[j + 1];
+            store_raw(new_state + at + (int64_t)j * channels, in[j + 1], WIDE, left);
     }
-    store<T, V>(y + b * channels + c, o);
+    store_pair(y + b * channels + c, s, WIDE, left);
 }
 
 // Calls f with the width as a constant.
@@ -369,12 +348,10 @@ Sizes sizes(const fno_causal_conv_s &p, int64_t length) {
             (size_t)p.channels * 4, n * (p.width - 1) * p.channels * e, n * 4};
 }
 
-// Channels of a thread, and threads of a block over the channels.
-int vector(int channels) { return channels % 2 == 0 ? 2 : 1; }
+// Threads of a block over the channels.
 int across(int channels) {
-    const int cols = channels / vector(channels);
     int a = 1;
-    while (a < 32 && a < cols) a *= 2;
+    while (a < 32 && 2 * a < channels) a *= 2;
     return a;
 }
 Args common(const fno_causal_conv_s &p, int run) {
@@ -419,8 +396,8 @@ fno_status_t fno_causal_conv_plan(fno_causal_conv_t *out, int64_t batch, int64_t
         return st;
     }
     // runs of 32 tokens, shorter ones (of 8 at least) while the threads do not fill the SMs;
-    // backward of 64 (its runs reach over 2 width tokens more), a wave or two of blocks
-    const int64_t cols = channels / vector(channels), want = (int64_t)p->sms * 1024;
+    // backward of 16 at least (its runs reach over 2 width tokens more), a few waves of blocks
+    const int64_t cols = ceil_div(channels, 2), want = (int64_t)p->sms * 1024;
     p->run = 32;
     while (p->run > 8 && batch * ceil_div(length, p->run) * cols < want) p->run /= 2;
     p->bwd_run = 64;
@@ -458,16 +435,15 @@ fno_status_t fno_causal_conv_forward(fno_causal_conv_t p, const void *x, const f
     if (inject("launch")) return FNO_ERR_CUDA;
     Args a = common(*p, p->run);
     a.x = x, a.w = w, a.bias = bias, a.lengths = lengths, a.s0 = s0, a.y = y, a.sT = sT;
-    const int v = vector(p->channels);
     const dim3 grid((unsigned)ceil_div(a.rows, kThreads / a.across),
-                    (unsigned)ceil_div(p->channels / v, a.across));
+                    (unsigned)ceil_div(p->channels, 2 * a.across));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
         return with_width(p->width, [&](auto width) {
             constexpr int W = decltype(width)::value;
-            if (v == 2) k_conv<T, 2, W><<<grid, kThreads, 0, s>>>(a);
-            else k_conv<T, 1, W><<<grid, kThreads, 0, s>>>(a);
+            if (p->channels % 2) k_conv<T, false, W><<<grid, kThreads, 0, s>>>(a);
+            else k_conv<T, true, W><<<grid, kThreads, 0, s>>>(a);
             return launched();
         });
     });
@@ -492,15 +468,14 @@ fno_status_t fno_causal_conv_backward(fno_causal_conv_t p, const void *x, const 
     Args a = common(*p, p->bwd_run);
     a.x = x, a.w = w, a.bias = bias, a.lengths = lengths, a.s0 = s0, a.dy = dy, a.dsT = dsT;
     a.dx = dx, a.ds0 = ds0, a.part = static_cast<float *>(workspace);
-    const int v = vector(p->channels);
-    const dim3 grid((unsigned)p->parts, (unsigned)ceil_div(p->channels / v, a.across));
+    const dim3 grid((unsigned)p->parts, (unsigned)ceil_div(p->channels, 2 * a.across));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
         return with_width(p->width, [&](auto width) {
             constexpr int W = decltype(width)::value;
-            if (v == 2) k_conv_grad<T, 2, W><<<grid, kThreads, 0, s>>>(a);
-            else k_conv_grad<T, 1, W><<<grid, kThreads, 0, s>>>(a);
+            if (p->channels % 2) k_conv_grad<T, false, W><<<grid, kThreads, 0, s>>>(a);
+            else k_conv_grad<T, true, W><<<grid, kThreads, 0, s>>>(a);
             const int64_t outs = (int64_t)p->channels * (W + 1);
             k_conv_sum<<<(unsigned)ceil_div(outs, 32), dim3(32, kSumRows), 0, s>>>(
                 a.part, dw, dbias, p->channels, W, p->parts);
@@ -523,22 +498,22 @@ fno_status_t fno_causal_conv_step(fno_causal_conv_t p, const void *x, const floa
         {{x, n.row, false}, {w, n.w, false}, {bias, n.c, false}, {slots, n.len, false},
          {state, sb, false}, {new_state, sb, true, state}, {y, n.row, true}});
     if (st != FNO_OK) return st;
+    const int64_t a_row = ceil_div(p->channels, 2 * kThreads);
+    if ((double)a_row * (double)p->batch > 2147483647.0) return FNO_ERR_UNSUPPORTED;
+    if (inject("launch")) return FNO_ERR_CUDA;
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);
         return with_width(p->width, [&](auto width) {
-            constexpr int W = decltype(width)::value, V = 2;
-            const int v = p->channels % V == 0 ? V : 1;
-            const int64_t blocks = ceil_div(p->batch * (p->channels / v), kThreads);
-            if (blocks > 2147483647) return FNO_ERR_UNSUPPORTED;
-            if (inject("launch")) return FNO_ERR_CUDA;
+            constexpr int W = decltype(width)::value;
             const auto run = [&](auto kernel) {
-                kernel<<<(unsigned)blocks, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+                kernel<<<(unsigned)(a_row * p->batch), kThreads, 0,
+                         reinterpret_cast<cudaStream_t>(stream)>>>(
                     static_cast<const T *>(x), w, bias, slots, num_slots,
                     static_cast<const T *>(state), static_cast<T *>(new_state),
-                    static_cast<T *>(y), p->batch, p->channels, p->act == FNO_ACT_SILU);
+                    static_cast<T *>(y), p->channels, (int)a_row, p->act == FNO_ACT_SILU);
             };
-            if (v == V) run(k_conv_step<T, V, W>);
-            else run(k_conv_step<T, 1, W>);
+            if (p->channels % 2) run(k_conv_step<T, false, W>);
+            else run(k_conv_step<T, true, W>);
             return launched();
         });
     });

@@ -153,6 +153,68 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, f2(-1.0f), a); }
 
+// Exponential and reciprocal of the multi-function unit; subnormal results are 0.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// (off by 2^-22.7 at most and by 2e-8 to 5e-8 on average, measured over [-20, 0])
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two neighbouring elements as they lie in memory.
+template <typename T> struct Pair { uint32_t bits; };
+template <> struct Pair<float> { float2 v; };
+
+template <typename T>
+__device__ __forceinline__ float2 to_float2(const Pair<T> &p) {
+    return Storage<T>::load2(reinterpret_cast<const T *>(&p));
+}
+// (`wide`: pairs lie on their size; zero where nothing is left)
+template <typename T>
+__device__ __forceinline__ Pair<T> load_pair(const T *p, bool wide, int left) {
+    Pair<T> r;
+    if constexpr (sizeof(T) == 4) {
+        r.v = make_float2(0.0f, 0.0f);
+        if (wide) {
+            if (left > 0) r.v = *reinterpret_cast<const float2 *>(p);
+        } else {
+            if (left > 0) r.v.x = p[0];
+            if (left > 1) r.v.y = p[1];
+        }
+    } else {
+        r.bits = 0;
+        if (wide) {
+            if (left > 0) r.bits = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+            if (left > 0) r.bits = h[0];
+            if (left > 1) r.bits |= (uint32_t)h[1] << 16;
+        }
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_pair(T *p, float2 v, bool wide, int left) {
+    if (wide) {
+        Pack<T, 2> o;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            *reinterpret_cast<__nv_bfloat162 *>(&o) = __floats2bfloat162_rn(v.x, v.y);
+        else if constexpr (std::is_same<T, __half>::value)
+            *reinterpret_cast<__half2 *>(&o) = __floats2half2_rn(v.x, v.y);
+        else o.v[0] = v.x, o.v[1] = v.y;
+        if (left > 0) *reinterpret_cast<Pack<T, 2> *>(p) = o;
+    } else {
+        if (left > 0) Storage<T>::store(p, v.x);
+        if (left > 1) Storage<T>::store(p + 1, v.y);
+    }
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }

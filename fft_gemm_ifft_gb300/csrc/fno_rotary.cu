@@ -7,9 +7,9 @@
 // turn, exactly, for any 32-bit p (a negative one too), and its upper 32 bits go to the
 // sine and cosine.
 //
-// Bound by bytes: each element is read and written once.  A thread keeps the sines and
-// cosines of the pairs in one 16-byte vector (half layout: of two vectors, which hold the
-// pairs' two sides) and goes over the token's heads, so that they cost a few percent.
+// Bound by bytes: each element is read and written once.  A block works out the cosines and
+// sines of its tokens' positions once, into shared memory, and then goes over all heads of
+// these tokens, vector after vector as they lie in memory.
 #include "fno_ops_internal.h"
 
 #include <cmath>
@@ -26,11 +26,18 @@ struct fno_rotary_s {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;
 
 struct Turns {
     uint64_t v[kMaxPairs];
+};
+// i / d for i below 2^16, d at most 2^16, by a product: ceil(2^32 / d) is off by less than
+// one, i times which stays below 2^32 / d.
+struct Divisor {
+    uint32_t d, m;
+    explicit Divisor(int n) : d((uint32_t)n), m((uint32_t)((0x100000000ull + n - 1) / n)) {}
+    __device__ uint32_t div(uint32_t i) const { return d == 1 ? i : __umulhi(i, m); }
 };
 struct Args {
     const void *q, *k;
@@ -38,102 +45,130 @@ struct Args {
     const int32_t *positions, *offsets;
     int64_t rows, length;
     int heads, kv_heads, dim, rotary;
-    int units, lanes;          // vectors of a head; threads that share a token's heads
+    int tokens;                // of a block
+    Divisor units, token;      // vectors of a head; of all heads of a token
     float magnitude;
     bool transpose;
 };
 
-// HALF: a thread turns V elements of the first side with V of the second; interleaved: the
-// pairs in a run of max(V, 2) elements.  The units beyond the pairs are V elements copied.
+// Cosine and sine of x half turns, |x| <= 1.  For 16-bit types by the multi-function unit:
+// off by 2^-20 at most, which their roundings (2^-11, 2^-8) hide.
+template <typename T>
+__device__ __forceinline__ void cos_sin(float x, float *c, float *s) {
+    if constexpr (sizeof(T) == 4) sincospif(x, s, c);
+    else __sincosf(3.14159265f * x, s, c);
+}
+// Two pairs (a, b) turned; two neighbouring elements as one pair.
+template <typename T>
+__device__ __forceinline__ Pair<T> from_float2(float2 v) {
+    Pair<T> r;
+    store_pair(reinterpret_cast<T *>(&r), v, true, 2);
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void turn2(Pair<T> &a, Pair<T> &b, float2 c, float2 s) {
+    const float2 av = to_float2(a), bv = to_float2(b);
+    const float2 bs = mul2(bv, s);
+    a = from_float2<T>(fma2(av, c, make_float2(-bs.x, -bs.y)));
+    b = from_float2<T>(fma2(bv, c, mul2(av, s)));
+}
+template <typename T>
+__device__ __forceinline__ void turn1(T &a, T &b, float c, float s) {
+    const float av = Storage<T>::load(&a), bv = Storage<T>::load(&b);
+    Storage<T>::store(&a, fmaf(av, c, -(bv * s)));
+    Storage<T>::store(&b, fmaf(bv, c, av * s));
+}
+
+// HALF: a vector of V elements of the first side turns with one of the second; interleaved:
+// the pairs in a run of max(V, 2) elements.  The units beyond the pairs are V elements copied.
 // V divides the rotary part's sides (half) or the rotary part, and the head.
 template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(kThreads)
 k_rotary(const Args p, const __grid_constant__ Turns turns) {
     constexpr int R = HALF || V > 1 ? V : 2, N = HALF ? V : R / 2;      // a run, its pairs
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int per_token = p.units * p.lanes;
-    const int64_t row = id / per_token;
-    if (row >= p.rows) return;
-    const int rest = (int)(id - row * per_token), first = rest / p.units;
-    const int unit = rest - first * p.units;
+    constexpr int kUnroll = HALF ? 2 : 4;      // units of a thread whose loads are on their way
+    extern __shared__ __align__(16) float table[];     // [tokens][2][pairs]: cosines, sines
     const int half = p.rotary / 2;
-    const int turning = HALF ? half / V : p.rotary / R;        // units that turn
-    const int heads = p.heads + p.kv_heads;
-    const int64_t base = row * p.heads * p.dim, kbase = row * p.kv_heads * p.dim;
-    const auto head = [&](int h, const T *&from, T *&to) {
-        if (h < p.heads) {
-            from = static_cast<const T *>(p.q) + base + (int64_t)h * p.dim;
-            to = static_cast<T *>(p.qo) + base + (int64_t)h * p.dim;
+    const int turning = HALF ? half / V : p.rotary / R;                 // units that turn
+    const int64_t row0 = (int64_t)blockIdx.x * p.tokens;
+    const int tokens = (int)min((int64_t)p.tokens, p.rows - row0);
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int k = i / half, pair = i - k * half;
+        const int64_t row = row0 + k;
+        int64_t pos;
+        if (p.positions) {
+            pos = p.positions[row];
         } else {
-            const int64_t o = kbase + (int64_t)(h - p.heads) * p.dim;
-            from = static_cast<const T *>(p.k) + o;
-            to = static_cast<T *>(p.ko) + o;
+            const int64_t b = p.rows <= 0xffffffffll
+                                  ? (int64_t)((uint32_t)row / (uint32_t)p.length)
+                                  : row / p.length;
+            pos = row - b * p.length;
+            if (p.offsets) pos += p.offsets[b];
         }
-    };
-    if (unit >= turning) {
-        if (p.q == p.qo && p.k == p.ko) return;
-        const int at = p.rotary + (unit - turning) * V;
-#pragma unroll 2
-        for (int h = first; h < heads; h += p.lanes) {
-            const T *from;
-            T *to;
-            head(h, from, to);
-            *reinterpret_cast<Pack<T, V> *>(to + at) =
-                *reinterpret_cast<const Pack<T, V> *>(from + at);
-        }
-        return;
-    }
-    int64_t pos = row;
-    if (p.positions) {
-        pos = p.positions[row];
-    } else {
-        const int64_t b = row / p.length;
-        pos = row - b * p.length;
-        if (p.offsets) pos += p.offsets[b];
-    }
-    float co[N], si[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint64_t turn = (uint64_t)pos * turns.v[unit * N + i];
+        const uint64_t turn = (uint64_t)pos * turns.v[pair];
         // the upper half as a signed number: -1/2 .. 1/2 of a turn
         const float x = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;    // 2^-31
         float s, c;
-        sincospif(x, &s, &c);
-        co[i] = p.magnitude * c;
-        si[i] = p.transpose ? -p.magnitude * s : p.magnitude * s;
+        cos_sin<T>(x, &c, &s);
+        table[2 * k * half + pair] = p.magnitude * c;
+        table[(2 * k + 1) * half + pair] = p.transpose ? -p.magnitude * s : p.magnitude * s;
     }
-    const int at = unit * R;
-#pragma unroll 2
-    for (int h = first; h < heads; h += p.lanes) {
-        const T *from;
-        T *to;
-        head(h, from, to);
-        if constexpr (HALF) {
-            const Pack<T, V> a = *reinterpret_cast<const Pack<T, V> *>(from + at);
-            const Pack<T, V> b = *reinterpret_cast<const Pack<T, V> *>(from + half + at);
-            Pack<T, V> x, y;
+    __syncthreads();
+    const bool copies = p.q != p.qo || p.k != p.ko;
+    const uint32_t all = (uint32_t)tokens * p.token.d;
+    for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kThreads * kUnroll) {
+        Pack<T, V> a[kUnroll][R / V], b[kUnroll];
+        T *to[kUnroll];
+        int unit[kUnroll], at_table[kUnroll];          // unit -1: nothing
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float av = Storage<T>::load(&a.v[i]), bv = Storage<T>::load(&b.v[i]);
-                Storage<T>::store(&x.v[i], fmaf(av, co[i], -(bv * si[i])));
-                Storage<T>::store(&y.v[i], fmaf(bv, co[i], av * si[i]));
+        for (int u = 0; u < kUnroll; ++u) {
+            const uint32_t i = i0 + u * kThreads;
+            unit[u] = -1;
+            if (i >= all) continue;
+            const uint32_t k = p.token.div(i), rest = i - k * p.token.d;
+            const uint32_t head = p.units.div(rest), n = rest - head * p.units.d;
+            if ((int)n >= turning && !copies) continue;
+            unit[u] = (int)n;
+            const bool is_q = (int)head < p.heads;
+            const int at = (int)n < turning ? n * R : p.rotary + (n - turning) * V;
+            const int64_t o = (is_q ? ((row0 + k) * p.heads + head)
+                                    : ((row0 + k) * p.kv_heads + (head - p.heads))) * p.dim + at;
+            const T *from = static_cast<const T *>(is_q ? p.q : p.k) + o;
+            to[u] = static_cast<T *>(is_q ? p.qo : p.ko) + o;
+            at_table[u] = 2 * k * half + n * N;
+#pragma unroll
+            for (int j = 0; j < R / V; ++j)
+                if (j == 0 || (int)n < turning)
+                    a[u][j] = *reinterpret_cast<const Pack<T, V> *>(from + j * V);
+            if (HALF && (int)n < turning) b[u] = *reinterpret_cast<const Pack<T, V> *>(from + half);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (unit[u] < 0) continue;
+            if (unit[u] < turning) {
+                const float *at = table + at_table[u];
+                const Pack<float, N> c = *reinterpret_cast<const Pack<float, N> *>(at);
+                const Pack<float, N> s = *reinterpret_cast<const Pack<float, N> *>(at + half);
+                T *e = a[u][0].v;
+                if constexpr (HALF && V > 1) {
+                    Pair<T> *first = reinterpret_cast<Pair<T> *>(e);
+                    Pair<T> *second = reinterpret_cast<Pair<T> *>(b[u].v);
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j)
+                        turn2(first[j], second[j], make_float2(c.v[2 * j], c.v[2 * j + 1]),
+                              make_float2(s.v[2 * j], s.v[2 * j + 1]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        turn1(HALF ? e[j] : e[2 * j], HALF ? b[u].v[j] : e[2 * j + 1], c.v[j],
+                              s.v[j]);
+                }
+                if (HALF) *reinterpret_cast<Pack<T, V> *>(to[u] + half) = b[u];
             }
-            *reinterpret_cast<Pack<T, V> *>(to + at) = x;
-            *reinterpret_cast<Pack<T, V> *>(to + half + at) = y;
-        } else {
-            Pack<T, V> a[R / V];
 #pragma unroll
-            for (int i = 0; i < R / V; ++i)
-                a[i] = *reinterpret_cast<const Pack<T, V> *>(from + at + i * V);
-            T *e = a[0].v;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float av = Storage<T>::load(e + 2 * i), bv = Storage<T>::load(e + 2 * i + 1);
-                Storage<T>::store(e + 2 * i, fmaf(av, co[i], -(bv * si[i])));
-                Storage<T>::store(e + 2 * i + 1, fmaf(bv, co[i], av * si[i]));
-            }
-#pragma unroll
-            for (int i = 0; i < R / V; ++i) *reinterpret_cast<Pack<T, V> *>(to + at + i * V) = a[i];
+            for (int j = 0; j < R / V; ++j)
+                if (j == 0 || unit[u] < turning)
+                    *reinterpret_cast<Pack<T, V> *>(to[u] + j * V) = a[u][j];
         }
     }
 }
@@ -142,18 +177,19 @@ template <typename T, int V>
 fno_status_t launch(const fno_rotary_s &plan, Args a, const Turns &turns, cudaStream_t s) {
     const bool half = plan.d.layout == FNO_ROTARY_HALF;
     const int turning = half ? a.rotary / 2 / V : a.rotary / (V > 1 ? V : 2);
-    a.units = turning + (a.dim - a.rotary) / V;
-    // a token's heads go over as many threads as it takes to fill the SMs, so that the
-    // sines are worked out as few times as that allows
-    const int heads = a.heads + a.kv_heads;
-    const int64_t want = (int64_t)plan.sms * 1024;
-    int lanes = 1;
-    while (lanes < heads && a.rows * a.units * lanes < want) lanes *= 2;
-    a.lanes = lanes < heads ? lanes : heads;
-    const int64_t blocks = ceil_div(a.rows * a.units * a.lanes, kThreads);
+    a.units = Divisor(turning + (a.dim - a.rotary) / V);
+    a.token = Divisor((int)a.units.d * (a.heads + a.kv_heads));
+    // up to 2048 vectors and 32 tokens a block, fewer while the blocks do not fill the SMs
+    // twice
+    a.tokens = 32;
+    while (a.tokens > 1 && (a.tokens * (int64_t)a.token.d > 2048 ||
+                            ceil_div(a.rows, a.tokens) < 4 * plan.sms))
+        a.tokens /= 2;
+    const int64_t blocks = ceil_div(a.rows, a.tokens);
     if (blocks > 2147483647) return FNO_ERR_UNSUPPORTED;
-    if (half) k_rotary<T, V, true><<<(unsigned)blocks, kThreads, 0, s>>>(a, turns);
-    else k_rotary<T, V, false><<<(unsigned)blocks, kThreads, 0, s>>>(a, turns);
+    const size_t bytes = (size_t)a.tokens * a.rotary * 4;
+    if (half) k_rotary<T, V, true><<<(unsigned)blocks, kThreads, bytes, s>>>(a, turns);
+    else k_rotary<T, V, false><<<(unsigned)blocks, kThreads, bytes, s>>>(a, turns);
     return launched();
 }
 
@@ -180,6 +216,7 @@ fno_status_t fno_rotary_plan(fno_rotary_t *out, const fno_rotary_desc_t *desc) {
           std::isfinite(d.fast)))
         return FNO_ERR_INVALID_ARG;
     if (d.dim > 1024 || d.rotary_dim > 2 * kMaxPairs ||
+        ((double)d.heads + d.kv_heads) * d.dim > 65536.0 ||
         (double)d.batch * (double)d.length * ((double)d.heads + d.kv_heads) * d.dim > kMaxElems)
         return FNO_ERR_UNSUPPORTED;
     if (inject("plan_alloc")) return FNO_ERR_OUT_OF_MEMORY;
@@ -226,7 +263,7 @@ fno_status_t fno_rotary_apply(fno_rotary_t p, const void *q, const void *k,
     if (st != FNO_OK) return st;
     if (inject("launch")) return FNO_ERR_CUDA;
     Args a{q, k, qo, ko, positions, offsets, (int64_t)n, d.length, d.heads, d.kv_heads, d.dim,
-           d.rotary_dim, 0, 0, p->magnitude, transpose != 0};
+           d.rotary_dim, 1, Divisor(1), Divisor(1), p->magnitude, transpose != 0};
     Turns turns;
     std::memcpy(turns.v, p->turns, sizeof turns.v);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -266,7 +266,7 @@ fno_status_t fno_linattn_destroy(fno_linattn_t plan);
  *                      `slow` or fewer k = 0, and k is linear in the turns between;
  *                      m = 1 + 0.1 log(factor)
  * Angles are exact to 2^-32 of a turn and to what f_i's 53 bits give at any position of
- * 32 bits; cosines and sines are float32's.
+ * 32 bits; cosines and sines are float32's (for 16-bit types good to 2^-20).
  * ------------------------------------------------------------------------- */
 typedef enum fno_rotary_layout_e {
     FNO_ROTARY_HALF = 0, FNO_ROTARY_INTERLEAVED = 1
@@ -282,7 +282,7 @@ typedef struct fno_rotary_desc_s {
     int64_t batch, length;    /* >= 1                                                     */
     int32_t heads;            /* of q, >= 1                                               */
     int32_t kv_heads;         /* of k, >= 0 (0: there is no k)                            */
-    int32_t dim;              /* of a head, 1 .. 1024                                     */
+    int32_t dim;              /* of a head, 1 .. 1024; (heads + kv_heads) dim <= 65536    */
     int32_t rotary_dim;       /* even, 2 .. min(dim, 256)                                 */
     fno_rotary_layout_t layout;
     fno_rotary_scaling_t scaling;
