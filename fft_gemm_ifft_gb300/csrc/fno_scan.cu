@@ -129,36 +129,37 @@ k_scan_step(const T *__restrict__ x, const T *__restrict__ dt, const float *__re
     const int64_t slot = slots ? (int64_t)slots[b] : b;
     const bool there = c < channels, live = there && slot >= 0 && slot < num_slots;
     const int64_t at = b * channels + c;
-    float sum = 0.0f, xv = 0.0f;
+    float sum = 0.0f, xv = 0.0f, d = 0.0f, zv = 0.0f, skip = 0.0f;
+    if (there) {                       // (on their way with the slot's number)
+        xv = Storage<T>::load(x + at);
+        d = Storage<T>::load(dt + at);
+        if (bias) d += bias[c];
+        if (z) zv = Storage<T>::load(z + at);
+        if (D) skip = D[c];
+    }
     if (live) {
         const int64_t bc = (b * (channels / per_group) + c / per_group) * states;
         const int64_t cn = (int64_t)c * states, sn = slot * channels * states + cn;
-        xv = Storage<T>::load(x + at);
-        float d = Storage<T>::load(dt + at);
-        if (bias) d += bias[c];
         if (plus) d = softplus2(f2(d)).x;
         const float u = d * xv;
         for (int n = q * V; n < states; n += lanes * V) {
             Pack<float, V> h = *reinterpret_cast<const Pack<float, V> *>(state + sn + n);
             const Pack<float, V> a = *reinterpret_cast<const Pack<float, V> *>(A + cn + n);
+            const Pack<T, V> bv = *reinterpret_cast<const Pack<T, V> *>(B + bc + n);
+            const Pack<T, V> cv = *reinterpret_cast<const Pack<T, V> *>(C + bc + n);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 h.v[i] = fmaf(exp2_fast(a.v[i] * kLog2e * d), h.v[i],
-                              u * Storage<T>::load(B + bc + n + i));
-                sum = fmaf(Storage<T>::load(C + bc + n + i), h.v[i], sum);
+                              u * Storage<T>::load(&bv.v[i]));
+                sum = fmaf(Storage<T>::load(&cv.v[i]), h.v[i], sum);
             }
             *reinterpret_cast<Pack<float, V> *>(new_state + sn + n) = h;
         }
     }
     for (int o = lanes / 2; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (there && q == 0) {
-        if (live) {
-            if (D) sum = fmaf(D[c], xv, sum);
-            if (z) {
-                const float zv = Storage<T>::load(z + at);
-                sum *= zv * logistic2(f2(zv)).x;
-            }
-        }
+        sum = fmaf(skip, xv, sum);
+        if (z) sum *= zv * logistic2(f2(zv)).x;
         Storage<T>::store(y + at, live ? sum : 0.0f);
     }
 }
@@ -242,7 +243,7 @@ BackwardParts backward_parts(const fno_scan_s &p) {
     const size_t states = (size_t)d.channels * np;
     const size_t segs = b * p.segments, tiles = (size_t)ceil_div(d.length, kTile);
     const size_t parts = (size_t)p.rows * p.spans;
-    const bool split = p.segments > 1, kept = tiles > 1;
+    const bool split = p.segments > 1, kept = tiles > 2;
     const size_t blocks = (size_t)backward_shape(d).chblocks;
     const size_t units = (size_t)d.groups * ceil_div(d.channels / d.groups, 64);
     BackwardParts w{};

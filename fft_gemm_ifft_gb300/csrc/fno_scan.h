@@ -94,16 +94,15 @@ inline Shape forward_shape(const fno_scan_desc_t &d) {
     s.chblocks = (int)ops::ceil_div(slabs, s.slabs);
     return s;
 }
-// Backward a lane has eight states (four of four) and a unit is a whole warp.
+// Backward a lane has eight states (four of four), and a block the warps that share the states
+// of 64 channels.
 inline Shape backward_shape(const fno_scan_desc_t &d) {
     Shape s{};
     s.np = padded_states(d.states);
     s.warps = s.np <= 4 ? 1 : s.np / 8;
     s.lanes = 32;
-    const int64_t slabs = ops::ceil_div(d.channels / d.groups, 64);
-    s.slabs = s.warps >= 4 || slabs == 1 ? 1 : 4 / s.warps;
-    s.seqs = 1;
-    s.chblocks = (int)ops::ceil_div(slabs, s.slabs);
+    s.seqs = s.slabs = 1;
+    s.chblocks = (int)ops::ceil_div(d.channels / d.groups, 64);
     return s;
 }
 

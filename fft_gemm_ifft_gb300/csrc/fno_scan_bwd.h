@@ -19,8 +19,7 @@
 // finish its tokens in turns and add up S1, S2 and y in shared memory.  dB and dC are summed
 // over a warp's lanes by shuffles that halve the values at each step: the upper half of the
 // lanes holds its two quads of states exchanged, so that all lanes send the same registers
-// first.  The block's warps add up theirs in shared memory, blocks of channels meet in the
-// workspace, always in the same order.
+// first.  Blocks of channels meet in the workspace, always in the same order.
 #pragma once
 
 #include "fno_scan_fwd.h"
@@ -31,30 +30,31 @@ namespace scan {
 constexpr int kSub = 2;                     // tokens whose states are in registers
 constexpr int kSubs = kTile / kSub;
 
-// Shared memory of a block of SLABS x WARPS warps.
-template <typename T, int NS, int WARPS, int SLABS>
+// Shared memory of a block: WARPS warps that share the states of 64 channels.
+template <typename T, int NS, int WARPS>
 struct BackwardShared {
-    static constexpr int kPairs = SLABS * 32, kThreads = kPairs * WARPS, kNp = NS * WARPS;
-    float4 du[kTile][kPairs];                         // steps and inputs
+    static constexpr int kThreads = 32 * WARPS, kNp = NS * WARPS;
+    float4 du[kTile][32];                             // steps and inputs
     float4 kept[kSubs - 1][NS / 2][kThreads];         // states in front of pairs of tokens
-    float2 w[kTile][kPairs];                          // output gradients
-    float2 out[3][WARPS][kTile][kPairs];              // S1, S2, y
-    Pair<T> raw[4][kTile][kPairs];                    // x, dt, dy, z
+    float2 w[kTile][32];                              // output gradients
+    float2 out[3][WARPS][kTile][32];                  // S1, S2, y
+    Pair<T> raw[4][kTile][32];                        // x, dt, dy, z
     float bc[kTile][2][kNp];
-    float sums[SLABS][kTile][2][kNp];                 // dB, dC
+    float sums[kTile][2][kNp];                        // dB, dC
 };
 
-template <typename T, int NS, int WARPS, int SLABS>
-__global__ void __launch_bounds__(SLABS * WARPS * 32)
+// AHEAD: sequences of up to two tiles, whose states the first pass did not leave: the second
+// tile's by a run over the first one (2048 x 12 tokens, 64 channels: a pass of 18 us less).
+template <typename T, int NS, int WARPS, bool AHEAD>
+__global__ void __launch_bounds__(32 * WARPS)
 k_scan_grad(const Args p) {
     using namespace ops;
-    using Shared = BackwardShared<T, NS, WARPS, SLABS>;
+    using Shared = BackwardShared<T, NS, WARPS>;
     constexpr int NP = NS / 2, kThreads = Shared::kThreads, np = Shared::kNp;
     constexpr int kOwn = WARPS < kTile ? kTile / WARPS : 1;      // tokens a thread prepares
     extern __shared__ __align__(16) unsigned char smem[];
     Shared &sm = *reinterpret_cast<Shared *>(smem);
-    const int tid = threadIdx.x, lane = tid & 31, sub = (tid >> 5) % WARPS;
-    const int slab = (tid >> 5) / WARPS, my = slab * 32 + lane;
+    const int tid = threadIdx.x, lane = tid & 31, sub = tid >> 5;
     int64_t at = blockIdx.x;
     const int part = (int)(at % p.spans);
     at /= p.spans;
@@ -62,7 +62,7 @@ k_scan_grad(const Args p) {
     at /= chblocks;
     const int grp = (int)(at % p.groups);
     const int64_t first_row = at / p.groups;
-    const int c = (chb * SLABS * 32 + my) * 2;        // in the group
+    const int c = (chb * 32 + lane) * 2;              // in the group
     const int left = p.per_group - c;
     const int64_t ch = (int64_t)grp * p.per_group + c;
     const int flip = NS == 8 ? lane >> 4 : 0, n0 = sub * NS;
@@ -71,7 +71,7 @@ k_scan_grad(const Args p) {
     const int bc_stride = p.groups * p.states;
     const bool wide = p.vec_c >= 2 * (int)sizeof(T), gated = p.z != nullptr;
     const int64_t tiles = (p.length + kTile - 1) / kTile;
-    const bool kept_tiles = tiles > 1 && left > 0, before = p.segments > 1 || p.s0;
+    const bool kept_tiles = !AHEAD && p.htile && left > 0, before = p.segments > 1 || p.s0;
 
     float2 a2[2][NP], da[2][NP];                      // log2 e A, and A's gradient
     load_states<NS>(p.A + ch * p.states + n0, left, p.states - n0, p.states, a2, flip);
@@ -156,7 +156,8 @@ k_scan_grad(const Args p) {
                 }
             }
         };
-        if (last >= 0) fetch(last);
+        bool ahead = AHEAD && last > 0;
+        if (last >= 0) fetch(ahead ? 0 : last);
         float2 gp[2][NP];                             // a_{t+1} g_{t+1}
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -169,7 +170,7 @@ k_scan_grad(const Args p) {
         else if (p.gsT)
             load_states<NS>(p.gsT + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
                             p.states, gp, flip);
-        for (int t = last; t >= 0; t -= kTile) {
+        for (int t = ahead ? 0 : last; t >= 0; t -= kTile) {
             const int valid = min(kTile, have - t);
             // the steps, inputs and output gradients of this thread's tokens; beyond the last
             // token they are zero and change nothing
@@ -183,23 +184,43 @@ k_scan_grad(const Args p) {
                 if (gated) {
                     const float2 z = to_float2(raw[3][m]);
                     w = mul2(w, mul2(z, logistic2(z)));
-                    sm.raw[3][k][my] = raw[3][m];
+                    sm.raw[3][k][lane] = raw[3][m];
                 }
                 const float2 du = mul2(d, x);
-                sm.du[k][my] = make_float4(d.x, d.y, du.x, du.y);
-                sm.w[k][my] = w;
+                sm.du[k][lane] = make_float4(d.x, d.y, du.x, du.y);
+                sm.w[k][lane] = w;
 #pragma unroll
-                for (int f = 0; f < 3; ++f) sm.raw[f][k][my] = raw[f][m];
+                for (int f = 0; f < 3; ++f) sm.raw[f][k][lane] = raw[f][m];
             }
 #pragma unroll
             for (int m = 0; m < kRounds; ++m)
                 if (bc_k < kRows) sm.bc[bc_k + m * kRows][bc_which][bc_n] = Storage<T>::load(&bc_raw[m]);
             // the state in front of the tile
+            const auto put_aside = [&](int r) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < NS / 4; ++q)
+                        sm.kept[r][j * (NS / 4) + q][tid] =
+                            make_float4(h[j][2 * q].x, h[j][2 * q].y, h[j][2 * q + 1].x,
+                                        h[j][2 * q + 1].y);
+            };
+            const auto take_back = [&](int r) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < NS / 4; ++q) {
+                        const float4 v = sm.kept[r][j * (NS / 4) + q][tid];
+                        h[j][2 * q] = make_float2(v.x, v.y);
+                        h[j][2 * q + 1] = make_float2(v.z, v.w);
+                    }
+            };
             if (!kept_tiles) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int i = 0; i < NP; ++i) h[j][i] = before ? hin[j][i] : f2(0.0f);
+                if (AHEAD && t > 0) take_back(0);
             } else if (before) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -213,7 +234,7 @@ k_scan_grad(const Args p) {
 
             const auto step = [&](int k, float2 (&a)[2][NP], const float2 (&from)[2][NP],
                                   float2 (&to)[2][NP]) {
-                const float4 e = sm.du[k][my];
+                const float4 e = sm.du[k][lane];
 #pragma unroll
                 for (int q = 0; q < NS / 4; ++q) {
                     const float4 bq =
@@ -229,16 +250,23 @@ k_scan_grad(const Args p) {
                     }
                 }
             };
+            if (AHEAD && ahead) {
+#pragma unroll 2
+                for (int k = 0; k < kTile; ++k) {
+                    float2 a[2][NP];
+                    step(k, a, h, h);
+                }
+                put_aside(0);
+                ahead = false;
+                t = last + kTile;
+                fetch(last);
+                __syncthreads();
+                continue;
+            }
             const int subs = (valid + kSub - 1) / kSub;
 #pragma unroll 1
             for (int r = 0; r < subs - 1; ++r) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < NS / 4; ++q)
-                        sm.kept[r][j * (NS / 4) + q][tid] =
-                            make_float4(h[j][2 * q].x, h[j][2 * q].y, h[j][2 * q + 1].x,
-                                        h[j][2 * q + 1].y);
+                put_aside(r);
 #pragma unroll
                 for (int k = 0; k < kSub; ++k) {
                     float2 a[2][NP];
@@ -248,24 +276,15 @@ k_scan_grad(const Args p) {
 #pragma unroll 1
             for (int r = subs - 1; r >= 0; --r) {
                 float2 a[kSub][2][NP], hs[kSub][2][NP];
-                if (r < subs - 1) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int q = 0; q < NS / 4; ++q) {
-                            const float4 v = sm.kept[r][j * (NS / 4) + q][tid];
-                            h[j][2 * q] = make_float2(v.x, v.y);
-                            h[j][2 * q + 1] = make_float2(v.z, v.w);
-                        }
-                }
+                if (r < subs - 1) take_back(r);
                 step(r * kSub, a[0], h, hs[0]);
 #pragma unroll
                 for (int k = 1; k < kSub; ++k) step(r * kSub + k, a[k], hs[k - 1], hs[k]);
 #pragma unroll
                 for (int k = kSub - 1; k >= 0; --k) {
                     const int kk = r * kSub + k;
-                    const float4 e = sm.du[kk][my];
-                    const float2 w = sm.w[kk][my];
+                    const float4 e = sm.du[kk][lane];
+                    const float2 w = sm.w[kk][lane];
                     float2 s1[2], s2[2], y[2], vb[NP], vc[NP];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) s1[j] = s2[j] = y[j] = f2(0.0f);
@@ -298,9 +317,9 @@ k_scan_grad(const Args p) {
                             }
                         }
                     }
-                    sm.out[0][sub][kk][my] = make_float2(s1[0].x + s1[0].y, s1[1].x + s1[1].y);
-                    sm.out[1][sub][kk][my] = make_float2(s2[0].x + s2[0].y, s2[1].x + s2[1].y);
-                    sm.out[2][sub][kk][my] = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+                    sm.out[0][sub][kk][lane] = make_float2(s1[0].x + s1[0].y, s1[1].x + s1[1].y);
+                    sm.out[1][sub][kk][lane] = make_float2(s2[0].x + s2[0].y, s2[1].x + s2[1].y);
+                    sm.out[2][sub][kk][lane] = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
                     // over the lanes: quads, then dB or dC, then pairs, then one state
                     const auto add_from = [](float2 v, float2 send, int mask) {
                         return add2(v, make_float2(__shfl_xor_sync(0xffffffffu, send.x, mask),
@@ -324,7 +343,7 @@ k_scan_grad(const Args p) {
                     one += __shfl_xor_sync(0xffffffffu, one, 1);
                     if constexpr (NS == 4) one += __shfl_xor_sync(0xffffffffu, one, 16);
                     if (!(lane & (NS == 8 ? 1 : 17)))
-                        sm.sums[slab][kk][is_c ? 1 : 0]
+                        sm.sums[kk][is_c ? 1 : 0]
                                [n0 + 4 * flip + (second ? 2 : 0) + (odd ? 1 : 0)] = one;
                 }
             }
@@ -337,24 +356,24 @@ k_scan_grad(const Args p) {
                 float2 v[3];
 #pragma unroll
                 for (int q = 0; q < 3; ++q) {
-                    v[q] = sm.out[q][0][k][my];
+                    v[q] = sm.out[q][0][k][lane];
 #pragma unroll
-                    for (int i = 1; i < WARPS; ++i) v[q] = add2(v[q], sm.out[q][i][k][my]);
+                    for (int i = 1; i < WARPS; ++i) v[q] = add2(v[q], sm.out[q][i][k][lane]);
                 }
-                const float2 x = to_float2(sm.raw[0][k][my]), w = sm.w[k][my];
-                const float4 e = sm.du[k][my];
+                const float2 x = to_float2(sm.raw[0][k][lane]), w = sm.w[k][lane];
+                const float4 e = sm.du[k][lane];
                 const int64_t o = o0 + (int64_t)(t + k) * p.channels;
                 store_pair(static_cast<T *>(p.dx) + o,
                            fma2(skip, w, mul2(make_float2(e.x, e.y), v[0])), wide, left);
                 dskip = fma2(w, x, dskip);
                 float2 dd = fma2(x, v[0], mul2(v[1], f2(kLn2)));
                 if (p.softplus)
-                    dd = mul2(dd, logistic2(add2(to_float2(sm.raw[1][k][my]), bias)));
+                    dd = mul2(dd, logistic2(add2(to_float2(sm.raw[1][k][lane]), bias)));
                 store_pair(static_cast<T *>(p.ddt) + o, dd, wide, left);
                 dbias = add2(dbias, dd);
                 if (gated) {
-                    const float2 z = to_float2(sm.raw[3][k][my]), l = logistic2(z);
-                    const float2 gy = to_float2(sm.raw[2][k][my]), y = fma2(skip, x, v[2]);
+                    const float2 z = to_float2(sm.raw[3][k][lane]), l = logistic2(z);
+                    const float2 gy = to_float2(sm.raw[2][k][lane]), y = fma2(skip, x, v[2]);
                     // silu' = l (1 + z (1 - l))
                     store_pair(static_cast<T *>(p.dz) + o,
                                mul2(mul2(gy, y), mul2(l, fma2(z, sub2(f2(1.0f), l), f2(1.0f)))),
@@ -366,10 +385,7 @@ k_scan_grad(const Args p) {
                 for (int m = 0; m < kRounds; ++m) {
                     const int k = bc_k + m * kRows;
                     if (k >= valid) break;
-                    float v = sm.sums[0][k][bc_which][bc_n];
-#pragma unroll
-                    for (int i = 1; i < SLABS; ++i) v += sm.sums[i][k][bc_which][bc_n];
-                    put_bc(t + k, v);
+                    put_bc(t + k, sm.sums[k][bc_which][bc_n]);
                 }
             }
         }
@@ -389,14 +405,14 @@ k_scan_grad(const Args p) {
     const int64_t r = first_row * p.spans + part;
     store_states<NS>(p.part_a + (r * p.channels + ch) * np + n0, left, NS, np, da, flip);
     // the bias' and D's gradients: the warps that share these channels
-    sm.out[0][sub][0][my] = dskip;
-    sm.out[1][sub][0][my] = dbias;
+    sm.out[0][sub][0][lane] = dskip;
+    sm.out[1][sub][0][lane] = dbias;
     __syncthreads();
     if (sub == 0) {
 #pragma unroll
         for (int i = 1; i < WARPS; ++i) {
-            dskip = add2(dskip, sm.out[0][i][0][my]);
-            dbias = add2(dbias, sm.out[1][i][0][my]);
+            dskip = add2(dskip, sm.out[0][i][0][lane]);
+            dbias = add2(dbias, sm.out[1][i][0][lane]);
         }
         float *o = p.part_d + r * 2 * p.channels + ch;
         if (left > 0) o[0] = dskip.x, o[p.channels] = dbias.x;
@@ -420,10 +436,10 @@ k_scan_sum_bc(const Args p) {
     Storage<T>::store(o + row * p.states + (e >= p.states ? e - p.states : e), v);
 }
 
-template <typename T, int NS, int WARPS, int SLABS>
+template <typename T, int NS, int WARPS, bool AHEAD>
 fno_status_t launch_grad(const Args &a, cudaStream_t s) {
-    using Shared = BackwardShared<T, NS, WARPS, SLABS>;
-    const auto kernel = k_scan_grad<T, NS, WARPS, SLABS>;
+    using Shared = BackwardShared<T, NS, WARPS>;
+    const auto kernel = k_scan_grad<T, NS, WARPS, AHEAD>;
     if (sizeof(Shared) > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sizeof(Shared)) != cudaSuccess) {
@@ -434,16 +450,15 @@ fno_status_t launch_grad(const Args &a, cudaStream_t s) {
     kernel<<<(unsigned)blocks, Shared::kThreads, sizeof(Shared), s>>>(a);
     return ops::launched();
 }
-// The kernel of the plan's shape.
-template <typename T>
+// The kernel of the plan's states.
+template <typename T, bool AHEAD>
 fno_status_t grad_pass(const Args &a, cudaStream_t s) {
-    const bool one = a.shape.slabs == 1;
-    if (a.shape.np == 4) return one ? launch_grad<T, 4, 1, 1>(a, s) : launch_grad<T, 4, 1, 4>(a, s);
-    switch (a.shape.warps) {
-        case 1: return one ? launch_grad<T, 8, 1, 1>(a, s) : launch_grad<T, 8, 1, 4>(a, s);
-        case 2: return one ? launch_grad<T, 8, 2, 1>(a, s) : launch_grad<T, 8, 2, 2>(a, s);
-        case 4: return launch_grad<T, 8, 4, 1>(a, s);
-        default: return launch_grad<T, 8, 8, 1>(a, s);
+    switch (a.shape.np) {
+        case 4: return launch_grad<T, 4, 1, AHEAD>(a, s);
+        case 8: return launch_grad<T, 8, 1, AHEAD>(a, s);
+        case 16: return launch_grad<T, 8, 2, AHEAD>(a, s);
+        case 32: return launch_grad<T, 8, 4, AHEAD>(a, s);
+        default: return launch_grad<T, 8, 8, AHEAD>(a, s);
     }
 }
 
@@ -451,7 +466,8 @@ template <typename T>
 fno_status_t backward_of(const fno_scan_s &p, Args a, cudaStream_t s) {
     using ops::ceil_div;
     fno_status_t st = FNO_OK;
-    if (a.length <= kTile) a.htile = nullptr;
+    // (up to two tiles the last pass works out for itself)
+    if (a.length <= 2 * kTile) a.htile = nullptr;
     if (a.segments > 1 || a.htile) st = scan_pass<T, kStates>(p, a, s);
     if (a.segments > 1) {
         if (st == FNO_OK) st = scan_pass<T, kBack>(p, a, s);
@@ -459,7 +475,7 @@ fno_status_t backward_of(const fno_scan_s &p, Args a, cudaStream_t s) {
     }
     if (st != FNO_OK) return st;
     a.shape = backward_shape(p.d);
-    st = grad_pass<T>(a, s);
+    st = a.segments == 1 && !a.htile ? grad_pass<T, true>(a, s) : grad_pass<T, false>(a, s);
     if (st != FNO_OK) return st;
     if (a.shape.chblocks > 1) {
         const int64_t n = (int64_t)a.batch * a.length * a.groups * 2 * a.states;
