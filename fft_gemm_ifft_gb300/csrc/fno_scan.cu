@@ -25,7 +25,7 @@ namespace {
 // of them, and each writes its segments' states (74 segments of 2 x 1024 x 16 with one thread
 // for all of them: 20 us, all of it the latency of the reads).  The second half of the blocks
 // joins the gradients, from the last segment.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinHold = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps)
 k_scan_join(const Args p) {
     __shared__ float2 ends[kJoinWarps][32];            // (local value, sum of the steps)
@@ -42,32 +42,51 @@ k_scan_join(const Args p) {
     const int64_t from = b * p.segments + (reverse ? p.segments - 1 - first : first);
     float *const v = (reverse ? p.gseg : p.hseg) + from * row + e;
     const float *const d = p.dseg + from * p.channels + c;
-    const auto walk = [&](float z, auto f) {
-        float steps = 0.0f;
-        for (int s = 0; s < count; s += 8) {
-            float l[8], t[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (s + k < count) {
-                    l[k] = v[dir * (s + k) * row];
-                    t[k] = d[dir * (s + k) * p.channels];
-                }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (s + k < count) {
-                    f(s + k, z);
-                    z = fmaf(exp2_fast(a2 * t[k]), z, l[k]);
-                    steps += t[k];
-                }
-        }
-        return make_float2(z, steps);
-    };
-    ends[w][lane] = walk(0.0f, [](int, float) {});
-    __syncthreads();
     const float *start = reverse ? p.gsT : p.s0;
-    float z = start && mine ? start[b * p.channels * p.states + cn] : 0.0f;
-    for (int k = 0; k < w; ++k) z = fmaf(exp2_fast(a2 * ends[k][lane].y), z, ends[k][lane].x);
-    walk(z, [&](int s, float at) { v[dir * s * row] = at; });
+    const float given = start && mine ? start[b * p.channels * p.states + cn] : 0.0f;
+    const auto in_front = [&]() {                     // of this warp's segments
+        float z = given;
+        for (int k = 0; k < w; ++k) z = fmaf(exp2_fast(a2 * ends[k][lane].y), z, ends[k][lane].x);
+        return z;
+    };
+    if (each <= kJoinHold) {
+        float l[kJoinHold], t[kJoinHold], z = 0.0f, steps = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kJoinHold; ++k)
+            if (k < count) l[k] = v[dir * k * row], t[k] = d[dir * k * p.channels];
+#pragma unroll
+        for (int k = 0; k < kJoinHold; ++k)
+            if (k < count) {
+                steps += t[k];
+                t[k] = exp2_fast(a2 * t[k]);
+                z = fmaf(t[k], z, l[k]);
+            }
+        ends[w][lane] = make_float2(z, steps);
+        __syncthreads();
+        z = in_front();
+#pragma unroll
+        for (int k = 0; k < kJoinHold; ++k)
+            if (k < count) {
+                v[dir * k * row] = z;
+                z = fmaf(t[k], z, l[k]);
+            }
+        return;
+    }
+    // more segments than a lane holds are read again
+    float z = 0.0f, steps = 0.0f;
+    for (int k = 0; k < count; ++k) {
+        const float t = d[dir * k * p.channels];
+        z = fmaf(exp2_fast(a2 * t), z, v[dir * k * row]);
+        steps += t;
+    }
+    ends[w][lane] = make_float2(z, steps);
+    __syncthreads();
+    z = in_front();
+    for (int k = 0; k < count; ++k) {
+        const float l = v[dir * k * row];
+        v[dir * k * row] = z;
+        z = fmaf(exp2_fast(a2 * d[dir * k * p.channels]), z, l);
+    }
 }
 
 // Sums over the blocks' parts, in the order of the parts, of dA (channels, padded states) and
@@ -298,7 +317,7 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
         return ceil_div(d.batch * d.groups, s.seqs) * s.chblocks * ceil_div(s.threads(), 32);
     };
     const Shape fw = forward_shape(d), bw = backward_shape(d);
-    split(d.length, warps(fw), (int64_t)16 * p->sms, kTile, &p->seg_len, &p->segments);
+    split(d.length, warps(fw), (int64_t)12 * p->sms, kTile, &p->seg_len, &p->segments);
     p->span_len = p->seg_len;
     p->rows = d.batch;
     if (p->segments > 1 && (d.flags & FNO_SCAN_BACKWARD)) {

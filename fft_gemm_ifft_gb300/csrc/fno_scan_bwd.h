@@ -244,7 +244,8 @@ k_scan_grad(const Args p) {
                         const float2 bv = i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            a[j][i] = exp2_fast2(mul2(a2[j][i], f2(j ? e.y : e.x)));
+                            const float dv = j ? e.y : e.x;
+                            a[j][i] = exp2_fast2(make_float2(a2[j][i].x * dv, a2[j][i].y * dv));
                             to[j][i] = fma2(a[j][i], from[j][i], mul2(f2(j ? e.w : e.z), bv));
                         }
                     }

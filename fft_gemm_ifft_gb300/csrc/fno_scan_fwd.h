@@ -30,11 +30,15 @@ namespace scan {
 // and in front of the tiles (each if wanted); from the last token, what each segment adds to
 // the gradient of the state in front of it: r_t = a_t (r_{t+1} + C_t w_t), w = dy silu(z).
 enum Mode { kFull, kStates, kBack };
-template <typename T, int NS, Mode M>
-__global__ void __maxnreg__(128)
+// At 168 registers an SM holds 12 warps (4096 tokens of 2048 channels: 47 us; at 128 registers
+// and 16 warps 51 us); short sequences, which are mostly the latency of their first loads, take
+// the 16 warps (4096 x 12 tokens of 64 channels: 42 us; 48 us at 168).
+constexpr int kShort = 32;
+template <typename T, int NS, Mode M, int REGS>
+__global__ void __maxnreg__(REGS)
 k_scan(const Args p) {
     using namespace ops;
-    constexpr int G = 1;                              // tokens whose loads are in flight
+    constexpr int G = M == kFull ? 1 : 2;             // tokens worked on together
     constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;    // pairs of B or C fetched ahead
     extern __shared__ __align__(16) float sbc[];      // [2][seqs][kTile][2][np], sums of y
     const int tid = threadIdx.x, threads = blockDim.x;
@@ -58,11 +62,16 @@ k_scan(const Args p) {
         return (int)max((int64_t)0, min((int64_t)span, n - t0));
     };
     const int have = tokens(b);
-    int most = have;                                  // of any sequence of the block
-    for (int k = 0; k < s.seqs && p.lengths; ++k)
-        most = max(most, tokens(min(seq0 + k, all - 1) / p.groups));
+    int most = have, least = have;                    // of any sequence of the block
+    for (int k = 0; k < s.seqs && p.lengths; ++k) {
+        const int n = tokens(min(seq0 + k, all - 1) / p.groups);
+        most = max(most, n);
+        least = min(least, n);
+    }
     const int64_t row0 = b * p.length + t0;
     const bool wide = p.vec_c >= 2 * (int)sizeof(T);
+    const bool whole_block = wide && (chb + 1) * s.slabs * s.lanes * 2 <= p.per_group &&
+                             seq0 + s.seqs <= all;
 
     // B and C of a tile: a thread has one pair of states of one of them (of a sequence) and
     // every bc_step-th token
@@ -125,19 +134,21 @@ k_scan(const Args p) {
     const int64_t row = M == kBack ? -(int64_t)p.channels : (int64_t)p.channels;
     Pair<T> xr[G], dr[G], zr[G];
     int64_t next = o0 + (M == kBack ? (have - 1) * (int64_t)p.channels : 0);
-    const auto fetch = [&](int t) {
+    // (WHOLE: every token and channel is there, and pairs lie on their size)
+    const auto fetch = [&](int t, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
         for (int k = 0; k < G; ++k) {
-            const int n = t + k < have ? left : 0;
-            xr[k] = load_pair(xs + next, wide, n);
-            dr[k] = load_pair(static_cast<const T *>(p.dt) + next, wide, n);
-            if (gated) zr[k] = load_pair(static_cast<const T *>(p.z) + next, wide, n);
+            const int n = WHOLE ? 2 : t + k < have ? left : 0;
+            xr[k] = load_pair(xs + next, WHOLE || wide, n);
+            dr[k] = load_pair(static_cast<const T *>(p.dt) + next, WHOLE || wide, n);
+            if (gated) zr[k] = load_pair(static_cast<const T *>(p.z) + next, WHOLE || wide, n);
             next += row;
         }
     };
     if (most > 0) {
         for (int m = 0; m * bc_step < kTile; ++m) bc_store(0, m, bc_load(m, 0));
-        fetch(0);
+        fetch(0, std::false_type());
     }
     float2 *sy = reinterpret_cast<float2 *>(sbc + 2 * bc_tile) + tid;     // [kTile][threads]
     T *out = M == kFull ? static_cast<T *>(p.y) + o0 : nullptr;
@@ -166,58 +177,67 @@ k_scan(const Args p) {
             }
         }
         const float *bc = sbc + buffer * bc_tile + u.seq * kTile * 2 * np + n0;
+        const auto tokens_of = [&](auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll 1
-        for (int k0 = 0; k0 < kTile && t + k0 < most; k0 += G) {
-            float2 d[G], x[G], z[G];
+            for (int k0 = 0; k0 < kTile && (WHOLE || t + k0 < most); k0 += G) {
+                float2 d[G], x[G], z[G];
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                x[k] = to_float2(xr[k]);
-                d[k] = add2(to_float2(dr[k]), bias);
-                if (p.softplus) d[k] = softplus2(d[k]);
-                if (t + k0 + k >= have) d[k] = f2(0.0f);
-                if (gated) z[k] = to_float2(zr[k]);
-                if (M == kBack && gated) x[k] = mul2(x[k], mul2(z[k], logistic2(z[k])));
-            }
-            fetch(t + k0 + G);
+                for (int k = 0; k < G; ++k) {
+                    x[k] = to_float2(xr[k]);
+                    d[k] = add2(to_float2(dr[k]), bias);
+                    if (p.softplus) d[k] = softplus2(d[k]);
+                    if (!WHOLE && t + k0 + k >= have) d[k] = f2(0.0f);
+                    if (gated) z[k] = to_float2(zr[k]);
+                    if (M == kBack && gated) x[k] = mul2(x[k], mul2(z[k], logistic2(z[k])));
+                }
+                fetch(t + k0 + G, whole);
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                // (back: the output's gradient in the input's place, C in B's)
-                const float2 du = M == kBack ? x[k] : mul2(d[k], x[k]);
-                if (M == kStates) dsum = add2(dsum, d[k]);
-                float2 y[2] = {f2(0.0f), f2(0.0f)};
+                for (int k = 0; k < G; ++k) {
+                    // (back: the output's gradient in the input's place, C in B's)
+                    const float2 du = M == kBack ? x[k] : mul2(d[k], x[k]);
+                    if (M == kStates) dsum = add2(dsum, d[k]);
+                    float2 y[2] = {f2(0.0f), f2(0.0f)};
 #pragma unroll
-                for (int q = 0; q < NS / 4; ++q) {
-                    const float4 bq = *reinterpret_cast<const float4 *>(bc + 4 * q);
-                    float4 cq;
-                    if (M == kFull) cq = *reinterpret_cast<const float4 *>(bc + np + 4 * q);
+                    for (int q = 0; q < NS / 4; ++q) {
+                        const float4 bq = *reinterpret_cast<const float4 *>(bc + 4 * q);
+                        float4 cq;
+                        if (M == kFull) cq = *reinterpret_cast<const float4 *>(bc + np + 4 * q);
 #pragma unroll
-                    for (int i = 2 * q; i < 2 * q + 2; ++i) {
-                        const float2 bv = i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
-                        const float2 cv = i & 1 ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y);
+                        for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                            const float2 bv = i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
+                            const float2 cv = i & 1 ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float2 a = exp2_fast2(mul2(a2[j][i], f2(j ? d[k].y : d[k].x)));
-                            const float2 uv = f2(j ? du.y : du.x);
-                            if (M == kBack) h[j][i] = mul2(a, fma2(uv, bv, h[j][i]));
-                            else h[j][i] = fma2(a, h[j][i], mul2(uv, bv));
-                            if (M == kFull) y[j] = fma2(cv, h[j][i], y[j]);
+                            for (int j = 0; j < 2; ++j) {
+                                const float2 a = exp2_fast2(
+                                    M == kFull ? make_float2(a2[j][i].x * (j ? d[k].y : d[k].x),
+                                                             a2[j][i].y * (j ? d[k].y : d[k].x))
+                                               : mul2(a2[j][i], f2(j ? d[k].y : d[k].x)));
+                                const float2 uv = f2(j ? du.y : du.x);
+                                if (M == kBack) h[j][i] = mul2(a, fma2(uv, bv, h[j][i]));
+                                else h[j][i] = fma2(a, h[j][i], mul2(uv, bv));
+                                if (M == kFull) y[j] = fma2(cv, h[j][i], y[j]);
+                            }
                         }
                     }
-                }
-                bc += 2 * np;
-                if (M == kFull) {
-                    float2 v = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
-                    if (s.warps > 1) {
-                        sy[(k0 + k) * threads] = v;
-                        continue;
+                    bc += 2 * np;
+                    if (M == kFull) {
+                        float2 v = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+                        if (s.warps > 1) {
+                            sy[(k0 + k) * threads] = v;
+                            continue;
+                        }
+                        v = fma2(skip, x[k], v);
+                        if (gated) v = mul2(v, mul2(z[k], logistic2(z[k])));
+                        store_pair(out, v, WHOLE || wide,
+                                   WHOLE ? 2 : t + k0 + k < have ? left : 0);
+                        out += p.channels;
                     }
-                    v = fma2(skip, x[k], v);
-                    if (gated) v = mul2(v, mul2(z[k], logistic2(z[k])));
-                    store_pair(out, v, wide, t + k0 + k < have ? left : 0);
-                    out += p.channels;
                 }
             }
-        }
+        };
+        if (whole_block && t + kTile + G <= least) tokens_of(std::true_type());
+        else tokens_of(std::false_type());
         if (M == kFull && s.warps > 1) {
             // the warps that share these channels' states take the tokens in turns
             __syncthreads();
@@ -258,13 +278,13 @@ k_scan(const Args p) {
     }
 }
 
-template <typename T, int NS, Mode M>
+template <typename T, int NS, Mode M, int REGS = 168>
 fno_status_t launch_scan(const Args &a, cudaStream_t s) {
     const Shape &h = a.shape;
     const int threads = h.threads();
     const int bytes = h.seqs * kTile * h.np * 16 +
                       (M == kFull && h.warps > 1 ? kTile * threads * 8 : 0);
-    const auto kernel = k_scan<T, NS, M>;
+    const auto kernel = k_scan<T, NS, M, REGS>;
     if (bytes > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
             cudaSuccess) {
@@ -282,8 +302,11 @@ fno_status_t scan_pass(const fno_scan_s &p, Args a, cudaStream_t s) {
     switch (lane_states(a.states)) {
         case 4: return launch_scan<T, 4, M>(a, s);
         case 8: return launch_scan<T, 8, M>(a, s);
-        default: return launch_scan<T, 16, M>(a, s);
+        default: break;
     }
+    if constexpr (M == kFull)
+        if (a.length <= kShort) return launch_scan<T, 16, M, 128>(a, s);
+    return launch_scan<T, 16, M>(a, s);
 }
 
 template <typename T>

@@ -32,6 +32,7 @@ GROUP = capi.FNO_ACT8_GROUP
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream, t):
@@ -418,6 +419,7 @@ class _DevicePlan(_Plan):
             st, self.workspace_bytes = getattr(capi, f"fno_{name}_workspace_size")(handle)
             check(st)
         self.device = torch.cuda.current_device()
+        self._torch_device = torch.device("cuda", self.device)
 
     def device_error(self, stream=None) -> int:
         """These kernels have no device-side waits or checks to report."""
@@ -425,23 +427,24 @@ class _DevicePlan(_Plan):
 
     def _at(self, t, dtype, shape, name):
         """t's pointer, once its type, shape, layout and device are those wanted."""
-        p = _field(t, dtype, shape, name)
-        if t.get_device() != self.device:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous() and t.get_device() == self.device):
+            _require(t, dtype, shape, name)
             raise ValueError(f"{name} must be on cuda:{self.device}, got {t.device}")
-        return p
+        return t.data_ptr()
 
     def _maybe_at(self, t, dtype, shape, name):
         return None if t is None else self._at(t, dtype, shape, name)
 
     def _launch_stream(self, stream):
-        if torch.cuda.current_device() != self.device:
+        if _current_device() != self.device:
             raise ValueError(f"the plan is of cuda:{self.device}, which is not the current device")
         if stream is None and _raw_stream is not None:
             return _raw_stream(self.device)
         return _stream_handle(stream)
 
     def _empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
+        return torch.empty(shape, dtype=dtype, device=self._torch_device)
 
     def _out(self, t, dtype, shape, name):
         if t is None:
