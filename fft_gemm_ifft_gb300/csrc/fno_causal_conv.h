@@ -47,8 +47,8 @@ __device__ __forceinline__ float silu_slope(float v) {
 template <typename T, bool WIDE, int W>
 __device__ __forceinline__ float2 input(const Args &p, int64_t b, int s, int c, int left) {
     if (s >= 0)
-        return to_float2(load_pair(static_cast<const T *>(p.x) + (b * p.length + s) * p.channels + c,
-                                   WIDE, left));
+        return to_float2(load_pair(
+            static_cast<const T *>(p.x) + (b * p.length + s) * p.channels + c, WIDE, left));
     if (!p.s0) return f2(0.0f);
     return to_float2(load_pair(
         static_cast<const T *>(p.s0) + (b * (W - 1) + s + W - 1) * p.channels + c, WIDE, left));

@@ -10,10 +10,14 @@
 // Nothing is kept from the forward.  A first pass (fno_scan_fwd.h) leaves the state in
 // front of every tile of 8 tokens, from zero at the segment's start, and, where time is
 // split, a second one what each segment adds to the gradient in front of it; a kernel joins
-// the segments in both directions.  The last pass
-// walks the tiles backwards: it runs a tile forward with the state in front of every second
-// token put aside in shared memory, then goes back by two tokens at a time, whose states and
-// decays it works out again into registers.
+// the segments in both directions.  The last pass walks the tiles backwards: it runs a tile
+// forward with the state in front of every second token put aside in shared memory, then goes
+// back by two tokens at a time, whose states and decays it works out again into registers.
+//
+// Bound by the latency of its instructions: they fill 45 % of the issue slots (2 x 4096 tokens,
+// 1024 channels, 16 states, gated, in bfloat16: 180 us of the call's 290).  It needs 255
+// registers, so 8 warps an SM; at 168 registers and 12 warps values loaded ahead are spilled,
+// which waits for their loads: 310 us.  Four states a lane and 16 warps: 190 us.
 //
 // A lane holds two channels x 8 states.  The warps that share a channel's states prepare and
 // finish its tokens in turns and add up S1, S2 and y in shared memory.  dB and dC are summed
@@ -134,9 +138,9 @@ k_scan_grad(const Args p) {
                 if (bc_mine && k < have) bc_raw[m] = from[(int64_t)k * bc_stride];
             }
             if (p.segments > 1)
-                load_states<NS>(p.hseg + ((b * p.segments + (t0 + t) / p.seg_len) * p.channels + ch) *
-                                             np + n0,
-                                left, NS, np, hin, flip);
+                load_states<NS>(
+                    p.hseg + ((b * p.segments + (t0 + t) / p.seg_len) * p.channels + ch) * np + n0,
+                    left, NS, np, hin, flip);
             else if (p.s0)
                 load_states<NS>(p.s0 + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
                                 p.states, hin, flip);
@@ -194,7 +198,8 @@ k_scan_grad(const Args p) {
             }
 #pragma unroll
             for (int m = 0; m < kRounds; ++m)
-                if (bc_k < kRows) sm.bc[bc_k + m * kRows][bc_which][bc_n] = Storage<T>::load(&bc_raw[m]);
+                if (bc_k < kRows)
+                    sm.bc[bc_k + m * kRows][bc_which][bc_n] = Storage<T>::load(&bc_raw[m]);
             // the state in front of the tile
             const auto put_aside = [&](int r) {
 #pragma unroll

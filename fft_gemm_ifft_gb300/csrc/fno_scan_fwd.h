@@ -4,17 +4,19 @@
 // For each channel c and state n of a sequence
 //   h_t = e^{d_t A} h_{t-1} + (d_t x_t) B_t,   y_t = sum_n C_t h_t,
 // one exponential and four multiply-adds an element (c, n) and token, and no matrix
-// product: the decay differs for every element.  So the exponentials (32 a cycle and SM),
-// the issue slots and the reads of shared memory bound it, not device memory (16 states: 8
-// to 12 bytes a channel and token).
+// product: the decay differs for every element.  So instructions bound it, not device memory
+// (16 states: 8 to 12 bytes a channel and token).  With everything in registers this loop takes
+// 1.7 cycles of an SM for 32 elements (a packed multiply-add occupies two issue slots, as two
+// single ones do); the kernel, with softplus, gates, loads and stores, takes 3.2 (4096 tokens
+// of 2048 channels and 16 states in bfloat16: 47 us), half of the issue slots at 12 warps an SM.
 //
 // A lane holds two channels x up to 16 states in registers, so that nothing is summed over
 // lanes: its channels' steps, inputs and outputs stay in its registers, from and to global
-// memory.  B and C, which all channels share, lie in shared memory as floats; a read there
-// costs its bytes times the lanes, whether they read the same or not, and two channels a
-// lane make that one cycle an element (four channels x four states a lane: 3.2, and 2.2
-// times the time).  More than 16 states are shared by several warps, whose sums meet in
-// shared memory.
+// memory.  B and C, which all channels share, lie in shared memory as floats, and a whole warp
+// reads the same ones at once.  (Four channels x four states a lane read four addresses a warp,
+// for which shared memory takes four times as long, and staged the steps there as well: 62 us;
+// pairs of lanes sharing 16 states, 20 warps an SM in place of 12: 59 us.)  More than 16 states
+// are shared by several warps, whose sums meet in shared memory.
 //
 // When the sequences and channels do not fill the GPU, time is split into segments:
 // one pass finds each segment's state from zero, a kernel joins them by
@@ -32,7 +34,7 @@ namespace scan {
 enum Mode { kFull, kStates, kBack };
 // At 168 registers an SM holds 12 warps (4096 tokens of 2048 channels: 47 us; at 128 registers
 // and 16 warps 51 us); short sequences, which are mostly the latency of their first loads, take
-// the 16 warps (4096 x 12 tokens of 64 channels: 42 us; 48 us at 168).
+// the 16 warps (4096 x 12 tokens of 64 channels in float32: 42 us; 48 us at 168).
 constexpr int kShort = 32;
 template <typename T, int NS, Mode M, int REGS>
 __global__ void __maxnreg__(REGS)
@@ -205,10 +207,13 @@ k_scan(const Args p) {
                         if (M == kFull) cq = *reinterpret_cast<const float4 *>(bc + np + 4 * q);
 #pragma unroll
                         for (int i = 2 * q; i < 2 * q + 2; ++i) {
-                            const float2 bv = i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
-                            const float2 cv = i & 1 ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y);
+                            const float2 bv =
+                                i & 1 ? make_float2(bq.z, bq.w) : make_float2(bq.x, bq.y);
+                            const float2 cv =
+                                i & 1 ? make_float2(cq.z, cq.w) : make_float2(cq.x, cq.y);
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
+                                // (the packed product would want d twice, in two registers)
                                 const float2 a = exp2_fast2(
                                     M == kFull ? make_float2(a2[j][i].x * (j ? d[k].y : d[k].x),
                                                              a2[j][i].y * (j ? d[k].y : d[k].x))
@@ -246,7 +251,8 @@ k_scan(const Args p) {
                 for (int i = 0; i < s.warps; ++i)
                     v = add2(v, sy[k * threads + (i - u.sub) * s.lanes]);
                 const int64_t o = o0 + (int64_t)(t + k) * p.channels;
-                v = fma2(skip, to_float2(load_pair(static_cast<const T *>(p.x) + o, wide, left)), v);
+                const float2 xv = to_float2(load_pair(static_cast<const T *>(p.x) + o, wide, left));
+                v = fma2(skip, xv, v);
                 if (gated) {
                     const float2 zv =
                         to_float2(load_pair(static_cast<const T *>(p.z) + o, wide, left));

@@ -421,6 +421,11 @@ class _DevicePlan(_Plan):
         self.device = torch.cuda.current_device()
         self._torch_device = torch.device("cuda", self.device)
 
+    def _workspace(self):
+        if self.workspace is None and self.workspace_bytes:
+            self.workspace = self._empty((self.workspace_bytes,), torch.uint8)
+        return _ptr(self.workspace)
+
     def device_error(self, stream=None) -> int:
         """These kernels have no device-side waits or checks to report."""
         return capi.FNO_OK

@@ -323,8 +323,8 @@ typedef struct fno_causal_conv_s *fno_causal_conv_t;
 
 #define FNO_CAUSAL_CONV_BACKWARD 1u   /* the workspace is that of the backward              */
 
-/* batch, length, channels >= 1, length below 2^31 - 64; 2 <= width <= 8.  Errors: INVALID_ARG, UNSUPPORTED,
- * OUT_OF_MEMORY, CUDA.                                                        */
+/* batch, length, channels >= 1, length below 2^31 - 64; 2 <= width <= 8.
+ * Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_MEMORY, CUDA.                      */
 fno_status_t fno_causal_conv_plan(fno_causal_conv_t *plan, int64_t batch, int64_t length,
                                   int32_t channels, int32_t width, fno_act_t act,
                                   fno_dtype_t dtype, uint32_t flags);
@@ -369,7 +369,10 @@ fno_status_t fno_causal_conv_destroy(fno_causal_conv_t plan);
  *     and the gradients beyond are 0 and the inputs beyond are not looked at; a sequence of
  *     no tokens returns its initial state
  * All arithmetic is float32 on the stored inputs; a decay is good to 2e-7 of itself, softplus
- * and silu to 1e-6.  An infinity in a token may come out as a NaN.
+ * to 1e-6 (a step below 2^-126 is 0), silu to 1e-6 for |z| up to 10.  A is finite, and d A
+ * meant to be at most 0: time is split, so that where states grow the product of all of a
+ * sequence's e^{d A} has to be below 2^127.  An infinity in a token may come out as a NaN, in
+ * that token or a later one of its channel.
  * ------------------------------------------------------------------------- */
 typedef struct fno_scan_s *fno_scan_t;
 
