@@ -166,6 +166,10 @@ __device__ __forceinline__ float rcp_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Asks for p's line to be in L2 when it is loaded.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 // Two neighbouring elements as they lie in memory.
 template <typename T> struct Pair { uint32_t bits; };

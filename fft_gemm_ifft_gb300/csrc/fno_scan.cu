@@ -302,7 +302,7 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
                                                                  : (double)d.groups * d.states;
     if (d.states > kMaxStates || d.length > 2147483647 - 2 * kTile ||
         (double)d.batch * (double)d.length * wide > kMaxElems ||
-        (double)d.batch * d.channels * d.states > kMaxElems || d.batch > 2147483647)
+        (double)d.batch * d.channels * d.states > kMaxElems || d.batch >= (1 << 30) - 64)
         return FNO_ERR_UNSUPPORTED;
     if (inject("plan_alloc")) return FNO_ERR_OUT_OF_MEMORY;
     fno_scan_s *p = new (std::nothrow) fno_scan_s();
@@ -318,7 +318,8 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
         return ceil_div(d.batch * d.groups, s.seqs) * s.chblocks * ceil_div(s.threads(), 32);
     };
     const Shape fw = forward_shape(d), bw = backward_shape(d);
-    split(d.length, warps(fw), (int64_t)12 * p->sms, kTile, &p->seg_len, &p->segments);
+    const int held = scan_warps(scan_registers(lane_states(d.states)));
+    split(d.length, warps(fw), (int64_t)held * p->sms, kTile, &p->seg_len, &p->segments);
     p->span_len = p->seg_len;
     p->rows = d.batch;
     if (p->segments > 1 && (d.flags & FNO_SCAN_BACKWARD)) {

@@ -51,6 +51,7 @@ struct Args {
     int64_t span_len, rows;    // last pass backward: tokens and sequences side by side
     int batch, channels, per_group, groups, states, segments, spans;
     int units;                 // of 64 channels in a group
+    int step;                  // forward: sequences between those of a block, of one group
     bool softplus;
     int vec_c, vec_n;          // bytes that rows of channels and of states may be moved in
     Shape shape;
@@ -77,6 +78,11 @@ inline int pow2_at_least(int64_t n) {
 }
 // States of a lane forward, and padded to a power of two.
 inline int lane_states(int states) { return states <= 4 ? 4 : states <= 8 ? 8 : 16; }
+// Registers of a thread of the forward kernels (see there), and the warps an SM then holds.
+constexpr int scan_registers(int lane_states) {
+    return lane_states == 4 ? 96 : lane_states == 8 ? 112 : 168;
+}
+constexpr int scan_warps(int registers) { return 65536 / (32 * registers) / 4 * 4; }
 inline int padded_states(int states) { return pow2_at_least(states < 4 ? 4 : states); }
 // Blocks of four warps (as many as share a channel's states, if more).  Groups of up to 32
 // channels take half a warp, so that a block holds more sequences instead.

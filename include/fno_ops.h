@@ -379,7 +379,7 @@ typedef struct fno_scan_s *fno_scan_t;
 #define FNO_SCAN_BACKWARD 1u   /* the workspace also covers the backward                    */
 
 typedef struct fno_scan_desc_s {
-    int64_t batch, length;    /* >= 1; length below 2^31 - 16                             */
+    int64_t batch, length;    /* >= 1, below 2^30 - 64 and 2^31 - 16                      */
     int32_t channels;         /* >= 1, a multiple of groups                               */
     int32_t states;           /* 1 .. 64                                                  */
     int32_t groups;           /* >= 1                                                     */
