@@ -32,7 +32,7 @@ k_scan_join(const Args p) {
     const int np = p.shape.np, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const bool reverse = blockIdx.z != 0;
     const int64_t e = (int64_t)blockIdx.x * 32 + lane, b = blockIdx.y;
-    const int64_t row = (int64_t)p.channels * np, c = e / np;
+    const int64_t row = (int64_t)p.channels * np, c = over(e, np);
     const int n = (int)(e - c * np), each = (p.segments + kJoinWarps - 1) / kJoinWarps;
     const bool mine = e < row && n < p.states;
     const int64_t cn = c * p.states + n;
@@ -120,7 +120,7 @@ k_scan_sum(const Args p, int64_t parts) {
     if (r || i >= states + more) return;
     for (int k = 1; k < 32; ++k) v += s[k][col];
     if (of_a) {
-        const int64_t c = i / np;
+        const int64_t c = over(i, np);
         if (i - c * np < p.states) p.dA[c * p.states + (i - c * np)] = v;
     } else if (i - states < p.channels) {
         if (p.dD) p.dD[i - states] = v;

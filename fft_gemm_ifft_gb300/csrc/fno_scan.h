@@ -112,6 +112,11 @@ inline Shape backward_shape(const fno_scan_desc_t &d) {
     return s;
 }
 
+// a / b of counts; in 32 bits, a fifth of the instructions, where a has no more.
+__device__ __forceinline__ int64_t over(int64_t a, int b) {
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // ---------------------------------------------------------------------------
 // a thread's elements
 // ---------------------------------------------------------------------------

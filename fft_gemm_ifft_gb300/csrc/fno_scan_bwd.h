@@ -59,7 +59,7 @@ k_scan_grad(const Args p) {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared &sm = *reinterpret_cast<Shared *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, sub = tid >> 5;
-    int64_t at = blockIdx.x;
+    unsigned at = blockIdx.x;
     const int part = (int)(at % p.spans);
     at /= p.spans;
     const int chblocks = p.shape.chblocks, chb = (int)(at % chblocks);
@@ -139,7 +139,8 @@ k_scan_grad(const Args p) {
             }
             if (p.segments > 1)
                 load_states<NS>(
-                    p.hseg + ((b * p.segments + (t0 + t) / p.seg_len) * p.channels + ch) * np + n0,
+                    p.hseg + ((b * p.segments + over(t0 + t, (int)p.seg_len)) * p.channels + ch) *
+                                 np + n0,
                     left, NS, np, hin, flip);
             else if (p.s0)
                 load_states<NS>(p.s0 + (b * p.channels + ch) * p.states + n0, left, p.states - n0,
@@ -436,7 +437,7 @@ k_scan_sum_bc(const Args p) {
     float v = p.part_bc[i];
 #pragma unroll 8
     for (int k = 1; k < p.shape.chblocks; ++k) v += p.part_bc[k * n + i];
-    const int64_t row = i / (2 * p.states);
+    const int64_t row = over(i, 2 * p.states);
     const int e = (int)(i - row * 2 * p.states);
     T *o = static_cast<T *>(e >= p.states ? p.dC : p.dB);
     Storage<T>::store(o + row * p.states + (e >= p.states ? e - p.states : e), v);

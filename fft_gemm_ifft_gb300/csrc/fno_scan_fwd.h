@@ -52,15 +52,15 @@ k_scan(const Args p) {
     const Shape s = p.shape;
     const int np = s.np;
     const Unit u(tid, s);
-    int64_t at = blockIdx.x;
+    unsigned at = blockIdx.x;
     const int seg = (int)(at % p.segments);
     at /= p.segments;
     const int chb = (int)(at % s.chblocks);
     // the block's sequences (of any group), and those `step` sequences of the batch further on
-    int64_t seq0 = at / s.chblocks * s.seqs;
+    int64_t seq0 = (int64_t)(at / s.chblocks) * s.seqs;
     const int64_t all = (int64_t)p.batch * p.groups;
     const int step = p.step;
-    int b = (int)((seq0 + u.seq) / p.groups);
+    int b = (int)over(seq0 + u.seq, p.groups);
     const int grp = (int)(seq0 + u.seq - (int64_t)b * p.groups);
     const int c = ((chb * s.slabs + u.slab) * s.lanes + u.lane) * 2;     // in the group
     const int there = p.per_group - c;
@@ -71,7 +71,7 @@ k_scan(const Args p) {
     // tokens of the segment that are there: a lane has those of one of the block's sequences
     // (none of those that do not exist)
     const unsigned warp = threads < 32 ? (1u << threads) - 1 : 0xffffffffu;
-    int lane_b = (int)((seq0 + (tid & (s.seqs - 1))) / p.groups);
+    int lane_b = (int)over(seq0 + (tid & (s.seqs - 1)), p.groups);
     const auto length_of = [&](int sequence) {
         return sequence >= p.batch ? 0 : p.lengths ? p.lengths[sequence] : (int)p.length;
     };
@@ -92,7 +92,7 @@ k_scan(const Args p) {
         const int i = tid - bc_k * combos, r = i & (np - 1), which = r / (np / 2);
         const int n = 2 * (r - which * (np / 2));
         bc_seq = min(i / np, s.seqs - 1);
-        const int64_t sq = seq0 + bc_seq, bb = sq / p.groups;
+        const int64_t sq = seq0 + bc_seq, bb = over(sq, p.groups);
         const int n_bb = __shfl_sync(warp, lens, bc_seq);
         bc_from = static_cast<const T *>(which || M == kBack ? p.C : p.B) +
                   ((bb * p.length + t0 + (M == kBack ? n_bb - 1 - bc_k : bc_k)) * p.groups +
