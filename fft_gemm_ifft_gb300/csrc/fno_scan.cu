@@ -332,8 +332,11 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
         p->span_len = each * p->seg_len;
         p->segments = (int)ceil_div(d.length, p->seg_len);
     } else if (p->segments == 1) {
-        // a wave of its blocks; each goes on with further sequences, A's gradient in registers
-        const int64_t most = ceil_div((int64_t)8 * p->sms, warps(bw) / d.batch);
+        // a wave of its blocks, each of which goes on with further sequences, A's gradient in
+        // registers; four, if a sequence's blocks make a quarter of one (64 x 20 tokens of 20000
+        // channels: 868 us; 1181 by one and a bit)
+        const int64_t wave = (int64_t)8 * p->sms, each = warps(bw) / d.batch;
+        const int64_t most = ceil_div(4 * each > wave ? 4 * wave : wave, each);
         p->rows = ceil_div(d.batch, ceil_div(d.batch, most));
     }
     p->spans = (int)ceil_div(d.length, p->span_len);

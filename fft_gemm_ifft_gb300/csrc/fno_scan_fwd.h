@@ -377,12 +377,13 @@ fno_status_t launch_scan(const Args &a, int sms, cudaStream_t s) {
     if (M == kFull && a.segments == 1) {
         // a wave of blocks, which go on with further sequences (of the same groups) and load
         // their first tokens ahead (16384 x 4 tokens, 32 channels, float32: 41 us as many blocks,
-        // 34 so)
-        int64_t fits = 65536 / ((int64_t)REGS * threads) * sms / h.chblocks;
+        // 34 so), where whole rounds of channels and groups nearly make one (64 x 30 tokens, 300
+        // groups of 128 channels: 434 us by many blocks, 620 by a wave and a third)
+        const int64_t wave = 65536 / ((int64_t)REGS * threads) * sms;
         const int64_t unit = a.groups / std::gcd(a.groups, h.seqs);
-        fits = (fits < 1 ? unit : ops::ceil_div(fits, unit) * unit);
-        if (fits < across) {
-            across = fits;
+        const int64_t some = wave / h.chblocks / unit * unit;
+        if (4 * some * h.chblocks >= 3 * wave && some < across) {
+            across = some;
             b.step = (int)(across * h.seqs / a.groups);
         }
     }

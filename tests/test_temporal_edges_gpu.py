@@ -55,6 +55,8 @@ REGIMES = [  # batch, length, channels, states, groups
     # as many sequences as fill the GPU, of one tile, two, and more
     (300, 8, 64, 16, 1), (300, 13, 64, 16, 1), (500, 16, 66, 4, 1), (260, 16, 32, 64, 2),
     (700, 41, 70, 16, 1), (420, 33, 40, 24, 1), (1000, 17, 5, 9, 1),
+    # more groups than a wave has blocks, odd ones of several sequences a block, many channels
+    (5, 9, 2400, 4, 600), (900, 5, 42, 8, 7), (6, 9, 20002, 2, 1),
     # groups of 32 channels and fewer, whose blocks hold several sequences
     (37, 30, 96, 16, 3), (11, 90, 16, 3, 4),
 ]
