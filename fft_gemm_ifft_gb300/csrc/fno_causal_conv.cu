@@ -20,8 +20,8 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 3)
 k_conv(const Args p) {
     constexpr int U = W <= 4 ? 8 : 4;          // tokens whose loads are on their way
     const int lane = threadIdx.x % p.across, rank = threadIdx.x / p.across;
-    const int c = (blockIdx.y * p.across + lane) * 2, left = p.channels - c;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / p.across) + rank;
+    const int c = (chunk(p) * p.across + lane) * 2, left = p.channels - c;
+    const int64_t row = (int64_t)block(p) * (kThreads / p.across) + rank;
     if (row >= p.rows || left <= 0) return;
     const Run r(p, row);
     const int n = tokens(p, r.b), end = min(r.t1, n);
@@ -126,6 +126,7 @@ Args common(const fno_causal_conv_s &p, int run) {
     a.run = run;
     a.rows = p.batch * ceil_div(p.length, run);
     a.across = across(p.channels);
+    a.chunks = (int)ceil_div(p.channels, 2 * a.across);
     a.silu = p.act == FNO_ACT_SILU;
     return a;
 }
@@ -161,16 +162,24 @@ fno_status_t fno_causal_conv_plan(fno_causal_conv_t *out, int64_t batch, int64_t
         delete p;
         return st;
     }
-    // runs of 32 tokens, shorter ones (of 8 at least) while the threads do not fill the SMs;
-    // backward of 16 at least (its runs reach over 2 width tokens more), a few waves of blocks
+    // runs of 32 tokens, shorter ones (of 8 at least) while the threads do not fill the SMs
     const int64_t cols = ceil_div(channels, 2), want = (int64_t)p->sms * 1024;
     p->run = 32;
     while (p->run > 8 && batch * ceil_div(length, p->run) * cols < want) p->run /= 2;
-    p->bwd_run = 64;
-    while (p->bwd_run > 16 && batch * ceil_div(length, p->bwd_run) * cols < want) p->bwd_run /= 2;
     const int a = across(channels), down = kThreads / a;
+    // backward the shortest from 16 to 40 that make no more than a wave of blocks (3 an SM, 2
+    // from 5 taps on; 4096 tokens of 2048 channels: 36 us, with runs of 32 44), or 64 for several
+    // waves (5 x 4099 tokens of 1001 channels, ragged: 51 us; 59 with 32, 65 with 96 in a wave)
+    const int64_t wave = (int64_t)(width <= 4 ? 3 : 2) * p->sms;
+    const auto backward_blocks = [&](int run) {
+        return ceil_div(batch * ceil_div(length, run), down) * ceil_div(cols, a);
+    };
+    p->bwd_run = 16;
+    while (p->bwd_run <= 40 && backward_blocks(p->bwd_run) > wave) p->bwd_run += 8;
+    if (p->bwd_run > 40) p->bwd_run = 64;
     const int64_t blocks = ceil_div(batch * ceil_div(length, p->run), down);
-    if (ceil_div(cols, a) > 65535 || blocks > 2147483647) {
+    if ((double)ceil_div(cols, a) * (double)blocks > 2147483647.0 ||
+        ceil_div(cols, a) > 65535) {
         delete p;
         return FNO_ERR_UNSUPPORTED;
     }
@@ -201,8 +210,7 @@ fno_status_t fno_causal_conv_forward(fno_causal_conv_t p, const void *x, const f
     if (inject("launch")) return FNO_ERR_CUDA;
     Args a = common(*p, p->run);
     a.x = x, a.w = w, a.bias = bias, a.lengths = lengths, a.s0 = s0, a.y = y, a.sT = sT;
-    const dim3 grid((unsigned)ceil_div(a.rows, kThreads / a.across),
-                    (unsigned)ceil_div(p->channels, 2 * a.across));
+    const unsigned grid = (unsigned)(ceil_div(a.rows, kThreads / a.across) * a.chunks);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_storage(p->dtype, [&](auto t) {
         using T = decltype(t);

@@ -30,7 +30,7 @@ struct Args {
     void *y, *sT, *dx, *ds0;
     float *part;               // per part: dw (width, channels), then dbias
     int64_t rows;              // runs of all sequences
-    int length, channels, run, across;
+    int length, channels, run, across, chunks;
     bool silu;
 };
 
@@ -85,8 +85,14 @@ __device__ __forceinline__ float2 taps(const float2 (&w)[W], const float2 (&win)
     return s;
 }
 
-// A block: `across` threads over channels (all blockIdx.y make), the rest over runs.  Which
-// run of which sequence:
+// A block: `across` threads over a chunk of the channels, the rest over runs.  Neighbouring
+// blocks have neighbouring chunks, so that whole rows are read at about the same time (forward,
+// 5 x 4099 tokens of 1001 channels in fp16, ragged: 34 us; 42 with neighbouring runs).
+__device__ __forceinline__ int chunk(const Args &p) {
+    return (int)(blockIdx.x % (unsigned)p.chunks);
+}
+__device__ __forceinline__ unsigned block(const Args &p) { return blockIdx.x / (unsigned)p.chunks; }
+// Which run of which sequence:
 struct Run {
     int64_t b;
     int t0, t1;

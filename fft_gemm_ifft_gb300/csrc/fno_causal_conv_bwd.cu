@@ -8,24 +8,27 @@ namespace {
 
 // Gradients.  Token t's pre-activation gets g_t = dy_t act'(pre_t), worked out from the
 // inputs again; then dx_s = sum_j w_j g_{s + W - 1 - j}, for which a run goes on W - 1
-// tokens, and dw_j = sum_t g_t x_{t - W + 1 + j}.  A block takes every gridDim.x-th group of
-// runs and leaves one sum of its dw and dbias.  Runs of 64 tokens: shorter ones cost more for
-// their start than they balance (5 x 4099 tokens of 1001 channels in fp16, ragged: 45 us of
-// the call's 51, with runs of 32 the call takes 59).
+// tokens, and dw_j = sum_t g_t x_{t - W + 1 + j}.  A block takes every `parts`-th group of
+// runs and leaves one sum of its dw and dbias.  Neighbouring blocks have neighbouring channels
+// (4 x 8192 tokens of 2048 channels in bfloat16: 173 us; 196 with neighbouring runs), but runs
+// where rows are odd and read by elements (5 x 4099 tokens of 1001 channels in fp16, ragged:
+// 51 us, the kernel 45; 56 with neighbouring channels).
 template <typename T, bool WIDE, int W>
 __global__ void __launch_bounds__(kThreads, W <= 4 ? 3 : 2)
 k_conv_grad(const Args p) {
     __shared__ float2 sums[kThreads];
     constexpr int U = W <= 4 ? 4 : 2;          // tokens whose loads are on their way
     const int lane = threadIdx.x % p.across, down = kThreads / p.across;
-    const int rank = threadIdx.x / p.across, c = (blockIdx.y * p.across + lane) * 2;
+    const int rank = threadIdx.x / p.across;
+    const int c = ((int)(WIDE ? blockIdx.x : blockIdx.y) * p.across + lane) * 2;
     const int left = p.channels - c;
     float2 w[W], bias, dw[W], db = f2(0.0f);
     load_weights<W>(p, c, left, w, bias);
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j] = f2(0.0f);
-    for (int64_t row = (int64_t)blockIdx.x * down + rank; left > 0 && row < p.rows;
-         row += (int64_t)gridDim.x * down) {
+    for (int64_t row = (int64_t)(WIDE ? blockIdx.y : blockIdx.x) * down + rank;
+         left > 0 && row < p.rows;
+         row += (int64_t)(WIDE ? gridDim.y : gridDim.x) * down) {
         const Run r(p, row);
         const int n = tokens(p, r.b), t0 = r.t0, t1 = r.t1;
         // win: inputs t - W + 1 .. t; acc: the gradients of these inputs so far
@@ -106,7 +109,7 @@ k_conv_grad(const Args p) {
         for (int s = max(t0, n); s < t1; ++s)
             store_pair(dx + (int64_t)(s - t0) * p.channels, f2(0.0f), WIDE, left);
     }
-    float *out = p.part + (int64_t)blockIdx.x * (W + 1) * p.channels;
+    float *out = p.part + (int64_t)(WIDE ? blockIdx.y : blockIdx.x) * (W + 1) * p.channels;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
@@ -150,7 +153,8 @@ namespace conv {
 
 fno_status_t gradients(const fno_causal_conv_s &p, const Args &a, float *dw, float *db,
                        cudaStream_t s) {
-    const dim3 grid((unsigned)p.parts, (unsigned)ceil_div(p.channels, 2 * a.across));
+    const dim3 grid = p.channels % 2 ? dim3((unsigned)p.parts, (unsigned)a.chunks)
+                                     : dim3((unsigned)a.chunks, (unsigned)p.parts);
     return with_storage(p.dtype, [&](auto t) {
         using T = decltype(t);
         return with_width(p.width, [&](auto width) {
