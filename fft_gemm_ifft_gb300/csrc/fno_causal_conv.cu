@@ -167,10 +167,10 @@ fno_status_t fno_causal_conv_plan(fno_causal_conv_t *out, int64_t batch, int64_t
     p->run = 32;
     while (p->run > 8 && batch * ceil_div(length, p->run) * cols < want) p->run /= 2;
     const int a = across(channels), down = kThreads / a;
-    // backward the shortest from 16 to 40 that make no more than a wave of blocks (3 an SM, 2
-    // from 5 taps on; 4096 tokens of 2048 channels: 36 us, with runs of 32 44), or 64 for several
-    // waves (5 x 4099 tokens of 1001 channels, ragged: 51 us; 59 with 32, 65 with 96 in a wave)
-    const int64_t wave = (int64_t)(width <= 4 ? 3 : 2) * p->sms;
+    // backward the shortest from 16 to 40 that make no more than a wave of blocks (4096
+    // tokens of 2048 channels: 36 us, with runs of 32 44), or 64 for several waves (5 x 4099
+    // tokens of 1001 channels, ragged: 51 us; 59 with 32, 65 with 96 in a wave)
+    const int64_t wave = (int64_t)grad_blocks(width, (int)elem_bytes(dtype)) * p->sms;
     const auto backward_blocks = [&](int run) {
         return ceil_div(batch * ceil_div(length, run), down) * ceil_div(cols, a);
     };

@@ -22,6 +22,12 @@ namespace conv {
 using namespace ops;
 
 constexpr int kThreads = 256;
+// Blocks of the gradients' kernel on an SM: 3 (80 registers) up to 4 taps of 16-bit types and 3
+// of float32, else 2, as more is spilled than the warps hide (4 taps, 4 x 4096 tokens of 2048
+// channels, float32: 110 us, by 3 blocks 126; 4 x 8192 in bfloat16: 173 by 3, 208 by 2).
+constexpr int grad_blocks(int width, int elem_bytes) {
+    return width <= (elem_bytes == 4 ? 3 : 4) ? 3 : 2;
+}
 
 struct Args {
     const void *x, *s0, *dy, *dsT;

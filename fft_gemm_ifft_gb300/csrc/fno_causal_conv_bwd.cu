@@ -14,7 +14,7 @@ namespace {
 // where rows are odd and read by elements (5 x 4099 tokens of 1001 channels in fp16, ragged:
 // 51 us, the kernel 45; 56 with neighbouring channels).
 template <typename T, bool WIDE, int W>
-__global__ void __launch_bounds__(kThreads, W <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, grad_blocks(W, sizeof(T)))
 k_conv_grad(const Args p) {
     __shared__ float2 sums[kThreads];
     constexpr int U = W <= 4 ? 4 : 2;          // tokens whose loads are on their way
