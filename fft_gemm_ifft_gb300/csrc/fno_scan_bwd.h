@@ -72,7 +72,7 @@ k_scan_grad(const Args p) {
     const int flip = NS == 8 ? lane >> 4 : 0, n0 = sub * NS;
     const int64_t t0 = part * p.span_len;
     const int span = (int)min(p.span_len, p.length - t0);
-    const int bc_stride = p.groups * p.states;
+    const int64_t bc_stride = (int64_t)p.groups * p.states;      // (may pass 2^31)
     const bool wide = p.vec_c >= 2 * (int)sizeof(T), gated = p.z != nullptr;
     const int64_t tiles = (p.length + kTile - 1) / kTile;
     const bool kept_tiles = !AHEAD && p.htile && left > 0, before = p.segments > 1 || p.s0;
@@ -103,7 +103,7 @@ k_scan_grad(const Args p) {
         const int have = (int)max((int64_t)0, min((int64_t)span, len - t0));
         const int last = have > 0 ? (have - 1) / kTile * kTile : -1;
         const int64_t row0 = b * p.length + t0, o0 = row0 * p.channels + ch;
-        const int64_t bc0 = row0 * bc_stride + grp * p.states;
+        const int64_t bc0 = row0 * bc_stride + (int64_t)grp * p.states;
         // dB and dC of the span's token t, or this block's part of them
         const auto put_bc = [&](int64_t t, float v) {
             if (chblocks > 1) {
@@ -135,7 +135,7 @@ k_scan_grad(const Args p) {
             for (int m = 0; m < kRounds; ++m) {
                 const int k = t + bc_k + m * kRows;
                 Storage<T>::store(&bc_raw[m], 0.0f);
-                if (bc_mine && k < have) bc_raw[m] = from[(int64_t)k * bc_stride];
+                if (bc_mine && k < have) bc_raw[m] = from[k * bc_stride];
             }
             if (p.segments > 1)
                 load_states<NS>(
