@@ -300,7 +300,9 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
         return FNO_ERR_INVALID_ARG;
     const double wide = d.channels > (double)d.groups * d.states ? (double)d.channels
                                                                  : (double)d.groups * d.states;
+    // (a block's channels, up to 256 of them, are counted in 32 bits)
     if (d.states > kMaxStates || d.length > 2147483647 - 2 * kTile ||
+        d.channels > 2147483647 - 256 ||
         (double)d.batch * (double)d.length * wide > kMaxElems ||
         (double)d.batch * d.channels * d.states > kMaxElems || d.batch >= (1 << 30) - 64)
         return FNO_ERR_UNSUPPORTED;

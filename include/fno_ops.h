@@ -380,7 +380,7 @@ typedef struct fno_scan_s *fno_scan_t;
 
 typedef struct fno_scan_desc_s {
     int64_t batch, length;    /* >= 1, below 2^30 - 64 and 2^31 - 16                      */
-    int32_t channels;         /* >= 1, a multiple of groups                               */
+    int32_t channels;         /* >= 1, below 2^31 - 256, a multiple of groups              */
     int32_t states;           /* 1 .. 64                                                  */
     int32_t groups;           /* >= 1                                                     */
     int32_t softplus;         /* 0: d = dt + dt_bias                                      */
