@@ -230,6 +230,7 @@ Args common(const fno_scan_s &p) {
     a.vec_c = vector_bytes(e, {d.channels, a.per_group});
     a.vec_n = vector_bytes(e, {d.states});
     a.units = (int)ceil_div(a.per_group, 64);
+    a.unit_shift = unit_shift(a.per_group);
     a.shape = forward_shape(d);
     a.seg_len = p.seg_len, a.segments = p.segments;
     a.span_len = p.span_len, a.spans = p.spans, a.rows = p.rows;
@@ -265,7 +266,9 @@ BackwardParts backward_parts(const fno_scan_s &p) {
     const size_t parts = (size_t)p.rows * p.spans;
     const bool split = p.segments > 1, kept = tiles > 2;
     const size_t blocks = (size_t)backward_shape(d).chblocks;
-    const size_t units = (size_t)d.groups * ceil_div(d.channels / d.groups, 64);
+    const int per_group = d.channels / d.groups;
+    const size_t kept_channels =
+        (size_t)d.groups * ceil_div(per_group, 64) * (2 << unit_shift(per_group));
     BackwardParts w{};
     size_t at = 0;
     const auto take = [&](size_t floats) {
@@ -276,7 +279,7 @@ BackwardParts backward_parts(const fno_scan_s &p) {
     w.hseg = take(split ? segs * states : 0);
     w.gseg = take(split ? segs * states : 0);
     w.dseg = take(split ? segs * d.channels : 0);
-    w.htile = take(kept ? b * tiles * units * 64 * np : 0);
+    w.htile = take(kept ? b * tiles * kept_channels * np : 0);
     w.dtile = take(kept ? b * tiles * d.channels : 0);
     w.part_bc = take(blocks > 1 ? blocks * b * d.length * d.groups * 2 * d.states : 0);
     w.part_a = take(parts * states);
@@ -354,6 +357,10 @@ fno_status_t fno_scan_plan(fno_scan_t *out, const fno_scan_desc_t *desc) {
     if (d.flags & FNO_SCAN_BACKWARD) {
         const size_t n = backward_parts(*p).bytes;
         if (n > p->workspace) p->workspace = n;
+    }
+    if ((double)p->workspace > kMaxElems) {           // (bytes that no GPU has)
+        delete p;
+        return FNO_ERR_UNSUPPORTED;
     }
     *out = p;
     return FNO_OK;

@@ -50,7 +50,8 @@ struct Args {
     int64_t length, seg_len;
     int64_t span_len, rows;    // last pass backward: tokens and sequences side by side
     int batch, channels, per_group, groups, states, segments, spans;
-    int units;                 // of 64 channels in a group
+    int units, unit_shift;     // kept states: units of up to 64 channels in a group, and
+                               // the channel pairs of one as a power of two
     int step;                  // forward: sequences between those of a block, of one group
     bool softplus;
     int vec_c, vec_n;          // bytes that rows of channels and of states may be moved in
@@ -200,14 +201,21 @@ __device__ __forceinline__ void store_states(float *at, int left, int there, int
         for (int i = 0; i < NS / 2; ++i) f[j][2 * i] = v[j][i].x, f[j][2 * i + 1] = v[j][i].y;
     write_states<NS>(at, left, there, pitch, f, flip);
 }
-// The tiles' states: units of 64 channels, their quads of states by channel pair, so that a
-// warp's accesses are whole lines.  The quad of channel c + j (of its group) from state n.
+// A unit of the kept states has 32 channel pairs, or as many (a power of two) as a group of fewer
+// channels, so that many small groups keep little more than their own states.
+inline int unit_shift(int per_group) {
+    int s = 0;
+    while (s < 5 && (2 << s) < per_group) ++s;
+    return s;
+}
+// The tiles' states: by units, their quads of states by channel pair, so that a warp's accesses
+// are whole lines.  The quad of channel c + j (of its group) from state n.
 __device__ __forceinline__ float4 *tile_at(const Args &p, int64_t tile, int grp, int c, int j,
                                            int n) {
     const int np = p.shape.np;
     const int64_t unit = (tile * p.groups + grp) * p.units + c / 64;
-    return reinterpret_cast<float4 *>(p.htile) + (unit * (np / 2) + j * (np / 4) + n / 4) * 32 +
-           (c % 64) / 2;
+    return reinterpret_cast<float4 *>(p.htile) +
+           ((unit * (np / 2) + j * (np / 4) + n / 4) << p.unit_shift) + (c % 64) / 2;
 }
 
 // ---------------------------------------------------------------------------

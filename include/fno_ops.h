@@ -388,7 +388,9 @@ typedef struct fno_scan_desc_s {
     uint32_t flags;
 } fno_scan_desc_t;
 
-/* Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_MEMORY, CUDA. */
+/* Errors: INVALID_ARG, UNSUPPORTED (also of a workspace beyond 2^38 bytes: the backward keeps
+ * the states, padded to at most twice the channels and a power of two of states, of every
+ * eighth token), OUT_OF_MEMORY, CUDA.                                         */
 fno_status_t fno_scan_plan(fno_scan_t *plan, const fno_scan_desc_t *desc);
 fno_status_t fno_scan_workspace_size(fno_scan_t plan, size_t *bytes);
 

@@ -3,6 +3,8 @@ sizes that pass 32 bits."""
 import pytest
 import torch
 
+import ops_ref as R
+import test_temporal_edges_gpu as edges
 import test_temporal_ops_gpu as base
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +55,47 @@ def test_scan_rows_of_b_and_c_of_more_than_31_bits(pkg):
         rest = got[name].narrow(axis, 0, G - K)
         for row in (rest[0].unbind(0) if axis == 2 else (rest,)):
             assert not row.any(), name
+
+
+@pytest.mark.parametrize("per_group", [1, 2, 3, 16, 33, 64, 100])
+@pytest.mark.parametrize("N", [4, 16, 40])
+def test_scan_workspace_goes_by_the_channels(pkg, per_group, N):
+    """What the backward keeps for every 8 tokens is a state of each channel, padded to twice
+    the channels and the next power of two of the states at most, however many groups there
+    are; nothing is allocated for it here."""
+    B, T, G = 4, 4096, 2048 // per_group
+    p = pkg.SelectiveScan(B, T, G * per_group, N, groups=G, backward=True)
+    padded = 1 << max(2, (N - 1).bit_length())
+    kept = 4 * B * (T // 8) * G * per_group * padded
+    # besides: a sum of the steps for each kept state, the segments' states (64 tokens at
+    # least, forwards and backwards), the blocks' parts of the gradients
+    chblocks = -(-per_group // 64)
+    rest = kept // padded + 3 * kept // 8 + 4 * B * (T // 64) * G * per_group * (padded + 2)
+    if chblocks > 1:
+        rest += 4 * chblocks * B * T * G * 2 * N
+    assert p.workspace is None and p.workspace_bytes <= 2 * kept + rest
+    p.close()
+
+
+@pytest.mark.parametrize("shape", [(2, 90, 6, 5, 3), (1, 200, 35, 16, 7), (3, 40, 102, 8, 6),
+                                   (2, 33, 130, 16, 2), (1, 70, 9, 24, 9), (2, 64, 132, 4, 4)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scan_kept_states_of_small_groups(pkg, shape, dtype):
+    """Groups of 1 to 65 channels keep their states in units of 2 to 64 channels."""
+    t = base.scan_inputs(shape, dtype, True, True, True, True, shape[0] > 1, True)
+    got, want, parts = edges.scan_call(pkg, t, shape, dtype)
+    f32, stored = R.tol("f32") + base.SCAN_EXTRA, R.tol(dtype) + base.SCAN_EXTRA
+    for name, ref in want.items():
+        # sums of terms of either sign: against the terms
+        scale = {"ddt": parts, "ddt_bias": parts, "dA": parts,
+                 "dD": (t["dy"].double().norm() * 0.5).item(),
+                 "dB": want["dB"].norm().item() + 1e-3}.get(name)
+        base.close(got[name], ref, stored if name in ("y", "dx", "ddt", "dB", "dC", "dz")
+                   else f32, scale)
+
+
+def test_scan_workspaces_that_no_gpu_has_are_refused(pkg):
+    """2^38 bytes: 64 sequences of 2^17 tokens keep 2^20 states of 4096 x 64."""
+    with pytest.raises(pkg.FnoError):
+        pkg.SelectiveScan(64, 1 << 17, 4096, 64, backward=True)
+    pkg.SelectiveScan(64, 1 << 17, 4096, 64).close()
