@@ -119,7 +119,8 @@ k_rotary(const Args p, const __grid_constant__ Turns turns) {
     const bool copies = p.q != p.qo || p.k != p.ko;
     const uint32_t all = (uint32_t)tokens * p.token.d;
     for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kThreads * kUnroll) {
-        Pack<T, V> a[kUnroll][R / V], b[kUnroll];
+        Pack<T, R> a[kUnroll];                         // (in R / V pieces)
+        Pack<T, V> b[kUnroll];
         T *to[kUnroll];
         int unit[kUnroll], at_table[kUnroll];          // unit -1: nothing
 #pragma unroll
@@ -141,7 +142,8 @@ k_rotary(const Args p, const __grid_constant__ Turns turns) {
 #pragma unroll
             for (int j = 0; j < R / V; ++j)
                 if (j == 0 || (int)n < turning)
-                    a[u][j] = *reinterpret_cast<const Pack<T, V> *>(from + j * V);
+                    *reinterpret_cast<Pack<T, V> *>(a[u].v + j * V) =
+                        *reinterpret_cast<const Pack<T, V> *>(from + j * V);
             if (HALF && (int)n < turning) b[u] = *reinterpret_cast<const Pack<T, V> *>(from + half);
         }
 #pragma unroll
@@ -151,7 +153,7 @@ k_rotary(const Args p, const __grid_constant__ Turns turns) {
                 const float *at = table + at_table[u];
                 const Pack<float, N> c = *reinterpret_cast<const Pack<float, N> *>(at);
                 const Pack<float, N> s = *reinterpret_cast<const Pack<float, N> *>(at + half);
-                T *e = a[u][0].v;
+                T *e = a[u].v;
                 if constexpr (HALF && V > 1) {
                     Pair<T> *first = reinterpret_cast<Pair<T> *>(e);
                     Pair<T> *second = reinterpret_cast<Pair<T> *>(b[u].v);
@@ -170,7 +172,8 @@ k_rotary(const Args p, const __grid_constant__ Turns turns) {
 #pragma unroll
             for (int j = 0; j < R / V; ++j)
                 if (j == 0 || unit[u] < turning)
-                    *reinterpret_cast<Pack<T, V> *>(to[u] + j * V) = a[u][j];
+                    *reinterpret_cast<Pack<T, V> *>(to[u] + j * V) =
+                        *reinterpret_cast<const Pack<T, V> *>(a[u].v + j * V);
         }
     }
 }
@@ -181,8 +184,8 @@ fno_status_t launch(const fno_rotary_s &plan, Args a, const Turns &turns, cudaSt
     const int turning = half ? a.rotary / 2 / V : a.rotary / (V > 1 ? V : 2);
     a.units = Divisor(turning + (a.dim - a.rotary) / V);
     a.token = Divisor((int)a.units.d * (a.heads + a.kv_heads));
-    // up to 2048 vectors and 32 tokens a block, fewer while the blocks do not fill the SMs
-    // twice
+    // up to 2048 vectors and 32 tokens a block, fewer while there are less than four blocks, half
+    // of the threads that it holds, for every SM
     a.tokens = 32;
     while (a.tokens > 1 && (a.tokens * (int64_t)a.token.d > 2048 ||
                             ceil_div(a.rows, a.tokens) < 4 * plan.sms))

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import ops_ref as R
+import temporal_ref as M
 import test_temporal_edges_gpu as edges
 import test_temporal_ops_gpu as base
 
@@ -99,3 +100,36 @@ def test_scan_workspaces_that_no_gpu_has_are_refused(pkg):
     with pytest.raises(pkg.FnoError):
         pkg.SelectiveScan(64, 1 << 17, 4096, 64, backward=True)
     pkg.SelectiveScan(64, 1 << 17, 4096, 64).close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 3, 2, 1, 3, 2), (2, 50, 7, 3, 9, 4), (3, 7, 40, 9, 33, 32),
+                                   (1, 400, 5, 5, 5, 2), (2, 19, 3, 2, 10, 6), (1, 21, 4, 4, 6, 6)])
+def test_rotary_of_neighbours_element_by_element(pkg, dtype, shape):
+    """Pairs of neighbours in heads of odd (or odd numbers of pairs of) elements, which are read
+    one or two at a time; in place, and beside elements that are copied."""
+    B, T, H, K, dim, r = shape
+    g = base.gen(sum(shape))
+    q, k = base.rand(g, (B, T, H, dim), dtype), base.rand(g, (B, T, K, dim), dtype)
+    p = pkg.Rotary(B, T, H, K, dim, rotary_dim=r, layout="interleaved", dtype=dtype)
+    pos = torch.arange(T).expand(B, T)
+    for call, sign in ((p.forward, 1), (p.backward, -1)):
+        a, b = q.cuda(), k.cuda()
+        oq, ok = call(a, b)
+        call(a, b, q_out=a, k_out=b)
+        assert torch.equal(a, oq) and torch.equal(b, ok)
+        for got, x in ((oq, q), (ok, k)):
+            # element by element, besides half a step of the type (2^-25 below fp16's normal
+            # numbers), relative to the pair: in float32 pi 2^-25 of the angle, a unit (2^-24) of
+            # cosine and sine each, and 2^-24 of the product: below 2^-21; in 16 bits the angle's
+            # product with pi (2^-21) and the fast cosines (2^-21 each): below 2^-19
+            want = M.rotate(x.double(), sign * pos, r, "interleaved")
+            eps = torch.finfo(x.dtype).eps / 2
+            size = want.abs() + 0
+            size[..., :r] = x.double()[..., :r].unflatten(-1, (-1, 2)).norm(
+                dim=-1, keepdim=True).expand(B, T, x.shape[2], r // 2, 2).flatten(-2)
+            bound = (eps * want.abs() + 2.0 ** (-21 if dtype == "f32" else -19) * size
+                     + (2.0 ** -25 if dtype == "f16" else 0.0))
+            assert ((got.cpu().double() - want).abs() <= bound).all()
+            assert torch.equal(got[..., r:].cpu(), x[..., r:])
+    p.close()
