@@ -215,7 +215,13 @@ fno_status_t fno_rotary_plan(fno_rotary_t *out, const fno_rotary_desc_t *desc) {
     if (d.scaling < FNO_ROTARY_NONE || d.scaling > FNO_ROTARY_RAMP) return FNO_ERR_INVALID_ARG;
     if (d.scaling != FNO_ROTARY_NONE && !(d.factor >= 1.0 && std::isfinite(d.factor)))
         return FNO_ERR_INVALID_ARG;
-    if (d.scaling == FNO_ROTARY_BASE && d.rotary_dim == 2) return FNO_ERR_INVALID_ARG;
+    const double r = d.rotary_dim;
+    double base = d.base;
+    if (d.scaling == FNO_ROTARY_BASE) {
+        if (d.rotary_dim == 2) return FNO_ERR_INVALID_ARG;
+        base *= std::pow(d.factor, r / (r - 2.0));
+        if (!std::isfinite(base)) return FNO_ERR_INVALID_ARG;
+    }
     if (d.scaling == FNO_ROTARY_RAMP &&
         !(d.original > 0.0 && std::isfinite(d.original) && d.slow >= 0.0 && d.fast > d.slow &&
           std::isfinite(d.fast)))
@@ -234,9 +240,7 @@ fno_status_t fno_rotary_plan(fno_rotary_t *out, const fno_rotary_desc_t *desc) {
         delete p;
         return st;
     }
-    const double pi = 3.14159265358979323846, r = d.rotary_dim;
-    double base = d.base;
-    if (d.scaling == FNO_ROTARY_BASE) base *= std::pow(d.factor, r / (r - 2.0));
+    const double pi = 3.14159265358979323846;
     if (d.scaling == FNO_ROTARY_RAMP) p->magnitude = (float)(1.0 + 0.1 * std::log(d.factor));
     for (int i = 0; i < d.rotary_dim / 2; ++i) {
         double f = std::pow(base, -2.0 * i / r);

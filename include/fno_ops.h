@@ -260,7 +260,8 @@ fno_status_t fno_linattn_destroy(fno_linattn_t plan);
  * and the rest of the head is copied.  For contexts longer than those trained on
  * (`factor` times):
  *   FNO_ROTARY_LINEAR  f_i / factor
- *   FNO_ROTARY_BASE    base times factor^(rotary_dim / (rotary_dim - 2))  (rotary_dim > 2)
+ *   FNO_ROTARY_BASE    base times factor^(rotary_dim / (rotary_dim - 2)), which has to be finite
+ *                      (rotary_dim > 2)
  *   FNO_ROTARY_RAMP    f_i (k + (1 - k) / factor), where a pair that makes `fast` turns or
  *                      more over `original` positions has k = 1 (it stays), one that makes
  *                      `slow` or fewer k = 0, and k is linear in the turns between;
