@@ -10,6 +10,11 @@
 // single ones do); the kernel, with softplus, gates, loads and stores, takes 3.0 (8191 tokens
 // of 2048 channels and 16 states in bfloat16: 87 us), half of the issue slots at 12 warps an SM.
 //
+// The decay is the multi-function unit's power of two of (A log2 e) d, so what is rounded to
+// float32 before it, log2 e (1.4e-8) and two products (2^-24 each), is 1.4e-7 |d A| of the
+// result, and the unit adds 1.5e-7.  Carrying the products' remainders along would add two
+// multiply-adds or more to an element's five instructions.
+//
 // A lane holds two channels x up to 16 states in registers, so that nothing is summed over
 // lanes: its channels' steps, inputs and outputs stay in its registers, from and to global
 // memory.  B and C, which all channels share, lie in shared memory as floats, and a whole warp

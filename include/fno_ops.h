@@ -369,11 +369,12 @@ fno_status_t fno_causal_conv_destroy(fno_causal_conv_t plan);
  *   lengths (batch) int32 or NULL: sequence b has max(0, min(lengths[b], length)) tokens; y
  *     and the gradients beyond are 0 and the inputs beyond are not looked at; a sequence of
  *     no tokens returns its initial state
- * All arithmetic is float32 on the stored inputs; a decay is good to 2e-7 of itself, softplus
- * to 1e-6 (a step below 2^-126 is 0), silu to 1e-6 for |z| up to 10.  A is finite, and d A
- * meant to be at most 0: time is split, so that where states grow the product of all of a
- * sequence's e^{d A} has to be below 2^127.  An infinity in a token may come out as a NaN, in
- * that token or a later one of its channel.
+ * All arithmetic is float32 on the stored inputs.  A decay e^{d A} is good to 1.5e-7 +
+ * 1.4e-7 |d A| of itself (below 2^-126 it is 0), a state that remembers n tokens to n times
+ * that and its sums' roundings; softplus to 1e-6 (a step below 2^-126 is 0), silu to 1e-6 for
+ * |z| up to 10.  A is finite, and d A meant to be at most 0: time is split, so that where states
+ * grow the product of all of a sequence's e^{d A} has to be below 2^127.  An infinity in a token
+ * may come out as a NaN, in that token or a later one of its channel.
  * ------------------------------------------------------------------------- */
 typedef struct fno_scan_s *fno_scan_t;
 

@@ -133,3 +133,79 @@ def test_rotary_of_neighbours_element_by_element(pkg, dtype, shape):
             assert ((got.cpu().double() - want).abs() <= bound).all()
             assert torch.equal(got[..., r:].cpu(), x[..., r:])
     p.close()
+
+
+@pytest.mark.parametrize("call", ["step", "forward"])
+def test_scan_decays(pkg, call):
+    """One token without an input: the state times e^{d A}, for |d A| from 0.001 to 100.  The
+    exponent is d times A log2 e, each product rounded (2^-24) and log2 e itself (1.4e-8), which
+    is 1.4e-7 |d A| of the result, and the power of two is good to 1.5e-7."""
+    D, N = 64, 16
+    g = base.gen(5)
+    x = torch.exp(torch.empty(D, N).uniform_(-6.9, 4.6, generator=g))            # |d A|
+    d = torch.exp(torch.empty(1, 1, D).uniform_(-7, 3, generator=g))
+    A = -(x / d.view(D, 1)).contiguous()
+    zero, h = torch.zeros(1, 1, D).cuda(), torch.ones(1, D, N).cuda()
+    bc = torch.ones(1, 1, 1, N).cuda()
+    p = pkg.SelectiveScan(1, 1, D, N, softplus=False)
+    if call == "forward":
+        _, h = p.forward(zero, d.cuda(), A.cuda(), bc, bc, state=h, want_state=True)
+    else:
+        p.step(zero[:, 0], d[:, 0].cuda(), A.cuda(), bc[:, 0], bc[:, 0], h)
+    dA = A.double() * d.double().view(D, 1)
+    want = torch.exp(dA)
+    bound = (1.5e-7 + 1.4e-7 * dA.abs()) * want + 2.0 ** -126
+    assert ((h.cpu().double()[0] - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 4000, 8), (40, 3000, 64)])
+def test_scan_that_remembers_a_thousand_tokens(pkg, B, T, D):
+    """Steps of 0.001 at a rate of 1, with terms of one sign, so that nothing cancels."""
+    N, memory = 8, 1000.0
+    g = base.gen(T)
+
+    def some(*shape):
+        return (0.5 + torch.rand(shape, generator=g)).cuda()
+
+    x, Bm, Cm, dy = some(B, T, D), some(B, T, 1, N), some(B, T, 1, N), some(B, T, D)
+    d, A = torch.full((B, T, D), 1e-3, device="cuda"), -torch.ones(D, N, device="cuda")
+    p = pkg.SelectiveScan(B, T, D, N, softplus=False, backward=True)
+    y, sT = p.forward(x, d, A, Bm, Cm, want_state=True)
+    got = p.backward(x, d, A, Bm, Cm, dy)
+    # 64 bits: all decays are a = e^{d A}, so that sums over earlier tokens are products with
+    # powers of a, here by blocks of 500 tokens
+    a = torch.exp(d[0, 0, 0].double() * A[0, 0].double())
+
+    def run(u, reverse=False):
+        """s_t = a s_{t-1} + u_t along axis 1."""
+        u = u.flip(1) if reverse else u
+        out, s = [], torch.zeros_like(u[:, 0])
+        for part in u.split(500, 1):
+            n = part.shape[1]
+            i = torch.arange(n, device="cuda")
+            low = torch.where(i[:, None] >= i, a ** (i[:, None] - i).clamp(min=0), 0.0 * a)
+            o = torch.einsum("ts,bs...->bt...", low, part)
+            o = o + torch.einsum("t,b...->bt...", a ** (i + 1), s)
+            out.append(o)
+            s = o[:, -1]
+        o = torch.cat(out, 1)
+        return o.flip(1) if reverse else o
+
+    dd = d.double()
+    u = (dd * x.double())[..., None] * Bm.double()
+    h = run(u)
+    # a decay is good to 1.5e-7 and a sum's rounding is 2^-24, for each token remembered
+    bound = memory * (1.5e-7 + 2.0 ** -24) + 1e-5
+    base.close(y, (h * Cm.double()).sum(-1).cpu(), bound)
+    base.close(sT, h[:, -1].cpu(), bound)
+    gr = run(Cm.double() * dy.double()[..., None], reverse=True)
+    s1 = (gr * Bm.double()).sum(-1)
+    base.close(got["dx"], (dd * s1).cpu(), bound)
+    base.close(got["dB"], (gr * (dd * x.double())[..., None]).sum(2, keepdim=True).cpu(), bound)
+    base.close(got["dC"], (h * dy.double()[..., None]).sum(2, keepdim=True).cpu(), bound)
+    before = torch.cat([torch.zeros_like(h[:, :1]), h[:, :-1]], 1)
+    e = a * gr * before                                  # of two such sums
+    base.close(got["dA"], (dd[..., None] * e).sum((0, 1)).cpu(), 2 * bound)
+    first, second = x.double() * s1, (A.double() * e).sum(-1)
+    base.close(got["ddt"], (first + second).cpu(), 2 * bound,
+               (first.norm() + second.norm()).item())
