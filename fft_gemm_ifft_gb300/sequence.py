@@ -13,13 +13,16 @@
                       tokens, gradients
 
 As in the rest of the package, the classes marshal arguments: a plan, a
-workspace from torch, tensor pointers and the current stream.  A plan object
-holds one workspace, so calls on it have to be ordered (one stream).  A call with
+workspace from torch, tensor pointers and the current stream.  A plan is of the
+device that was current when it was made, and takes that device's tensors while it
+is the current one.  A plan object holds one workspace, so calls on it have to be ordered (one stream).  A call with
 ``stream=`` is launched there and allocates its results on the current stream:
 that stream has to wait for the current one's work before the call, and the
 current one for it before the results are used or dropped.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
@@ -35,11 +38,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream, t):
-    """The handle of ``stream``, or of the current stream of t's device (by the
-    raw query where torch has it: the call is most of a small operator's cost)."""
+def _stream(device, stream):
+    """The handle of ``stream``, or of the current stream of ``device`` (by the raw
+    query where torch has it: the call is most of a small operator's cost).  That has
+    to be the current device, where the launch goes."""
+    if _current_device() != device:
+        raise ValueError(f"the operands are on cuda:{device}, which is not the current device")
     if stream is None and _raw_stream is not None:
-        return _raw_stream(t.device.index)
+        return _raw_stream(device)
     return _stream_handle(stream)
 
 
@@ -47,16 +53,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _field(t, dtype, shape, name):
-    """t's pointer, once its type, shape and layout are those wanted."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous()):
+def _field(device, t, dtype, shape, name):
+    """t's pointer, once its type, shape, layout and device are those wanted."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == device):
         _require(t, dtype, shape, name)
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     return t.data_ptr()
-
-
-def _maybe(t, dtype, shape, name):
-    return None if t is None else _field(t, dtype, shape, name)
 
 
 class PackedActivation:
@@ -70,9 +73,12 @@ class PackedActivation:
             raise TypeError("codes must be a CUDA tensor")
         if codes.dim() < 1 or codes.numel() < 1:
             raise ValueError("codes must have at least one element")
-        _field(codes, torch.int8, codes.shape, "codes")
-        _field(scales, torch.float32, codes.shape[:-1] + (-(-codes.shape[-1] // GROUP),),
-               "scales")
+        if not codes.is_cuda:
+            raise TypeError("codes must be a CUDA tensor")
+        device = codes.get_device()
+        _field(device, codes, torch.int8, codes.shape, "codes")
+        _field(device, scales, torch.float32,
+               codes.shape[:-1] + (-(-codes.shape[-1] // GROUP),), "scales")
         self.codes, self.scales, self.dtype = codes, scales, dtype
         self.shape = codes.shape
 
@@ -82,25 +88,27 @@ class PackedActivation:
 
     def values(self, out=None, stream=None):
         """The values that the codes stand for, in the storage type."""
+        device = self.codes.get_device()
         if out is None:
             out = torch.empty(self.shape, dtype=self.dtype, device=self.codes.device)
-        ptr = _field(out, self.dtype, self.shape, "out")
+        ptr = _field(device, out, self.dtype, self.shape, "out")
         rows, cols = self._rows()
         check(capi.fno_act8_unpack(rows, cols, _CODES[self.dtype], self.codes.data_ptr(),
-                                   self.scales.data_ptr(), ptr, _stream(stream, out)),
+                                   self.scales.data_ptr(), ptr, _stream(device, stream)),
               "fno_act8_unpack")
         return out
 
     def gelu_backward(self, dy, out=None, stream=None):
         """dy * GELU'(values); ``out`` may be dy."""
-        dyp = _field(dy, self.dtype, self.shape, "dy")
+        device = self.codes.get_device()
+        dyp = _field(device, dy, self.dtype, self.shape, "dy")
         if out is None:
             out = torch.empty_like(dy)
-        ptr = _field(out, self.dtype, self.shape, "out")
+        ptr = _field(device, out, self.dtype, self.shape, "out")
         rows, cols = self._rows()
         check(capi.fno_act8_gelu_backward(rows, cols, _CODES[self.dtype], self.codes.data_ptr(),
                                           self.scales.data_ptr(), dyp, ptr,
-                                          _stream(stream, dy)), "fno_act8_gelu_backward")
+                                          _stream(device, stream)), "fno_act8_gelu_backward")
         return out
 
 
@@ -119,33 +127,64 @@ def pack_activation(x, stream=None) -> PackedActivation:
         raise TypeError("x must be a float32, float16 or bfloat16 CUDA tensor")
     if x.dim() < 1 or x.numel() < 1:
         raise ValueError("x must have at least one element")
-    ptr = _field(x, x.dtype, x.shape, "x")
+    if not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    ptr = _field(x.get_device(), x, x.dtype, x.shape, "x")
     p = _empty_packed(x.shape, x.dtype, x.device)
     rows, cols = p._rows()
     check(capi.fno_act8_pack(rows, cols, _CODES[x.dtype], ptr, p.codes.data_ptr(),
-                             p.scales.data_ptr(), _stream(stream, x)), "fno_act8_pack")
+                             p.scales.data_ptr(), _stream(x.get_device(), stream)),
+          "fno_act8_pack")
     return p
 
 
 class _Plan:
-    """A plan handle with its workspace."""
+    """A plan handle with its workspace, of the device that was current when it was
+    made: its calls take that device's tensors while it is the current one."""
 
-    def _own(self, status, handle, name):
+    def _own(self, status, handle, name, workspace=True):
         check(status, f"fno_{name}_plan")
         self.handle, self._name = handle, name
-        st, self.workspace_bytes = getattr(capi, f"fno_{name}_workspace_size")(handle)
-        check(st)
-        self.workspace = None
+        self.workspace, self.workspace_bytes = None, 0
+        if workspace:
+            st, self.workspace_bytes = getattr(capi, f"fno_{name}_workspace_size")(handle)
+            check(st)
+        self.device = torch.cuda.current_device()
+        self._torch_device = torch.device("cuda", self.device)
+        # (partials: methods in their place take about 1 us more of a call)
+        self._at = functools.partial(_field, self.device)
+        self._launch_stream = functools.partial(_stream, self.device)
 
     def _workspace(self):
         """Allocated at the first call that needs it, then kept."""
         if self.workspace is None and self.workspace_bytes:
-            self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device="cuda")
+            self.workspace = self._empty((self.workspace_bytes,), torch.uint8)
         return _ptr(self.workspace)
 
     def device_error(self, stream=None) -> int:
         return getattr(capi, f"fno_{self._name}_get_device_error")(self.handle,
                                                                    _stream_handle(stream))
+
+    def _maybe_at(self, t, dtype, shape, name):
+        return None if t is None else self._at(t, dtype, shape, name)
+
+    def _empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self._torch_device)
+
+    def _out(self, t, dtype, shape, name):
+        if t is None:
+            t = self._empty(shape, dtype)
+            return t, t.data_ptr()
+        return t, self._at(t, dtype, shape, name)
+
+    def _packed(self, p, dtype, shape, name):
+        """The pointers of a PackedActivation's codes and scales."""
+        if tuple(p.shape) != tuple(shape) or p.dtype is not dtype:
+            raise ValueError(f"{name} must hold {tuple(shape)} {dtype}, got {tuple(p.shape)} "
+                             f"{p.dtype}")
+        if p.codes.get_device() != self.device:
+            raise ValueError(f"{name} must be on cuda:{self.device}, got {p.codes.device}")
+        return p.codes.data_ptr(), p.scales.data_ptr()
 
     def close(self):
         if getattr(self, "handle", None):
@@ -196,29 +235,26 @@ class SandwichNorm(_Plan):
             return None
         if name not in params:
             raise ValueError(f"params needs {name!r}")
-        return _field(params[name], torch.float32, (self.channels,), name)
+        return self._at(params[name], torch.float32, (self.channels,), name)
 
     def _gate(self, gate):
         if self.gate_kind == "none":
             if gate is not None:
                 raise ValueError("this plan has no gate")
             return None
-        return _field(gate, self.gate_dtype, self.gate_shape, "gate")
+        return self._at(gate, self.gate_dtype, self.gate_shape, "gate")
 
     def _new(self, t, name):
-        if t is None:
-            return torch.empty(self.shape, dtype=self.torch_dtype, device="cuda")
-        _require(t, self.torch_dtype, self.shape, name)
-        return t
+        return self._out(t, self.torch_dtype, self.shape, name)[0]
 
     def pre(self, x, params, u=None, stream=None):
         """u = n1(x) * w1 + b1: the norm in front of the first block."""
-        xp = _field(x, self.torch_dtype, self.shape, "x")
+        xp = self._at(x, self.torch_dtype, self.shape, "x")
         u = self._new(u, "u")
         check(capi.fno_sandwich_forward(self.handle, xp, None, None, None, None, None,
                                         self._vec(params, "w1"),
                                         self._vec(params, "b1", self.layer), None, u.data_ptr(),
-                                        None, None, _stream(stream, x)),
+                                        None, None, self._launch_stream(stream)),
               "fno_sandwich_forward")
         return u
 
@@ -228,7 +264,7 @@ class SandwichNorm(_Plan):
         unless ``want_u``) and the 8-bit checkpoint of f (None unless
         ``save8``).  ``y`` may be x."""
         dt, shape = self.torch_dtype, self.shape
-        xp, fp = _field(x, dt, shape, "x"), _field(f, dt, shape, "f")
+        xp, fp = self._at(x, dt, shape, "x"), self._at(f, dt, shape, "f")
         gp = self._gate(gate)
         y = self._new(y, "y")
         u = self._new(u, "u") if want_u else None
@@ -239,7 +275,7 @@ class SandwichNorm(_Plan):
             self._vec(params, "b2", layer), self._vec(params, "w1", want_u),
             self._vec(params, "b1", layer and want_u), y.data_ptr(), _ptr(u),
             f8.codes.data_ptr() if save8 else None, f8.scales.data_ptr() if save8 else None,
-            _stream(stream, x)), "fno_sandwich_forward")
+            self._launch_stream(stream)), "fno_sandwich_forward")
         return y, u, f8
 
     __call__ = forward
@@ -249,14 +285,13 @@ class SandwichNorm(_Plan):
         dw1, (db1).  ``f`` is the field, its PackedActivation, or None for the
         backward of ``pre`` (y is then its x).  ``dy`` may be None (zero)."""
         dt, shape, C = self.torch_dtype, self.shape, self.channels
-        yp = _field(y, dt, shape, "y")
+        yp = self._at(y, dt, shape, "y")
         packed = isinstance(f, PackedActivation)
-        if packed and (tuple(f.shape) != shape or f.dtype != dt):
-            raise ValueError(f"f must hold {shape} {dt}, got {tuple(f.shape)} {f.dtype}")
+        codes, scales = self._packed(f, dt, shape, "f") if packed else (None, None)
         block = f is not None
-        fp = _field(f, dt, shape, "f") if block and not packed else None
+        fp = self._at(f, dt, shape, "f") if block and not packed else None
         gp = self._gate(gate) if block else None
-        dyp, dup = _maybe(dy, dt, shape, "dy"), _maybe(du, dt, shape, "du")
+        dyp, dup = self._maybe_at(dy, dt, shape, "dy"), self._maybe_at(du, dt, shape, "du")
         layer = self.layer
         out = {"dx": torch.empty_like(y)}
         names = (["s", "w2"] + ["b2"] * layer if block else []) + \
@@ -271,12 +306,12 @@ class SandwichNorm(_Plan):
             out["d" + n] = row
         ptr = {n: t.data_ptr() for n, t in out.items()}
         check(capi.fno_sandwich_backward(
-            self.handle, yp, fp, f.codes.data_ptr() if packed else None,
-            f.scales.data_ptr() if packed else None, gp, self._vec(params, "s", block),
+            self.handle, yp, fp, codes, scales, gp, self._vec(params, "s", block),
             self._vec(params, "w2", block), self._vec(params, "b2", block and layer),
             self._vec(params, "w1", du is not None), dyp, dup, ptr["dx"], ptr.get("df"),
             ptr.get("dgate"), ptr.get("ds"), ptr.get("dw2"), ptr.get("db2"), ptr.get("dw1"),
-            ptr.get("db1"), self._workspace(), _stream(stream, y)), "fno_sandwich_backward")
+            ptr.get("db1"), self._workspace(), self._launch_stream(stream)),
+              "fno_sandwich_backward")
         return out
 
 
@@ -292,17 +327,16 @@ class LinearGrad(_Plan):
                                              capi.DTYPE_CODES[dtype]), "linear_grad")
 
     def backward(self, dy, x8, stream=None):
-        dyp = _field(dy, self.torch_dtype, self.dy_shape, "dy")
+        dyp = self._at(dy, self.torch_dtype, self.dy_shape, "dy")
         if not isinstance(x8, PackedActivation):
             raise TypeError("x8 must be a PackedActivation")
-        if tuple(x8.shape) != self.x_shape:
-            raise ValueError(f"x8 must have shape {self.x_shape}, got {tuple(x8.shape)}")
+        codes, scales = self._packed(x8, x8.dtype, self.x_shape, "x8")
         cout, cin = self.dy_shape[1], self.x_shape[1]
         dw = torch.empty((cout, cin), dtype=torch.float32, device=dy.device)
         db = torch.empty((cout,), dtype=torch.float32, device=dy.device)
-        check(capi.fno_linear_grad(self.handle, dyp, x8.codes.data_ptr(), x8.scales.data_ptr(),
-                                   dw.data_ptr(), db.data_ptr(), self._workspace(),
-                                   _stream(stream, dy)), "fno_linear_grad")
+        check(capi.fno_linear_grad(self.handle, dyp, codes, scales, dw.data_ptr(), db.data_ptr(),
+                                   self._workspace(), self._launch_stream(stream)),
+              "fno_linear_grad")
         return dw, db
 
     __call__ = backward
@@ -330,9 +364,9 @@ class LinearAttention(_Plan):
 
     def _qkv(self, q, k, v, log_decay, shapes):
         dt = self.torch_dtype
-        return (_field(q, dt, shapes[0], "q"), _field(k, dt, shapes[1], "k"),
-                _field(v, dt, shapes[2], "v"),
-                _field(log_decay, torch.float32, (self.heads,), "log_decay"))
+        return (self._at(q, dt, shapes[0], "q"), self._at(k, dt, shapes[1], "k"),
+                self._at(v, dt, shapes[2], "v"),
+                self._at(log_decay, torch.float32, (self.heads,), "log_decay"))
 
     def _scale(self, scale):
         return self.dk ** -0.5 if scale is None else float(scale)
@@ -342,16 +376,14 @@ class LinearAttention(_Plan):
         """(o, final state or None).  ``lengths`` int32 (batch,): tokens of each
         sequence; ``state``: the initial state (None: zero)."""
         ptrs = self._qkv(q, k, v, log_decay, self._shapes)
-        lp = _maybe(lengths, torch.int32, (self.batch,), "lengths")
-        sp = _maybe(state, torch.float32, self.state_shape, "state")
-        if out is None:
-            out = torch.empty(self.o_shape, dtype=self.torch_dtype, device=q.device)
-        op = _field(out, self.torch_dtype, self.o_shape, "out")
+        lp = self._maybe_at(lengths, torch.int32, (self.batch,), "lengths")
+        sp = self._maybe_at(state, torch.float32, self.state_shape, "state")
+        out, op = self._out(out, self.torch_dtype, self.o_shape, "out")
         final = (torch.empty(self.state_shape, dtype=torch.float32, device=q.device)
                  if want_state else None)
         check(capi.fno_linattn_forward(self.handle, *ptrs, self._scale(scale), lp, sp,
                                        op, _ptr(final), self._workspace(),
-                                       _stream(stream, q)), "fno_linattn_forward")
+                                       self._launch_stream(stream)), "fno_linattn_forward")
         return out, final
 
     __call__ = forward
@@ -361,15 +393,15 @@ class LinearAttention(_Plan):
         """(dq, dk, dv, gradient of the initial state or None).  ``dstate`` is
         the gradient of the final state (None: zero)."""
         ptrs = self._qkv(q, k, v, log_decay, self._shapes)
-        lp = _maybe(lengths, torch.int32, (self.batch,), "lengths")
-        sp = _maybe(state, torch.float32, self.state_shape, "state")
-        dop = _field(do, self.torch_dtype, self.o_shape, "do")
-        dsp = _maybe(dstate, torch.float32, self.state_shape, "dstate")
+        lp = self._maybe_at(lengths, torch.int32, (self.batch,), "lengths")
+        sp = self._maybe_at(state, torch.float32, self.state_shape, "state")
+        dop = self._at(do, self.torch_dtype, self.o_shape, "do")
+        dsp = self._maybe_at(dstate, torch.float32, self.state_shape, "dstate")
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ds0 = torch.empty_like(state) if state is not None else None
         check(capi.fno_linattn_backward(self.handle, *ptrs, self._scale(scale), lp, sp, dop, dsp,
                                         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0),
-                                        self._workspace(), _stream(stream, q)),
+                                        self._workspace(), self._launch_stream(stream)),
               "fno_linattn_backward")
         return dq, dk, dv, ds0
 
@@ -381,16 +413,14 @@ class LinearAttention(_Plan):
         (batch,) says which state a row has (outside: the row is idle)."""
         ptrs = self._qkv(q, k, v, log_decay, self._step_shapes)
         n = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() else 0
-        sp = _field(state, torch.float32, (n,) + self.state_shape[1:], "state")
-        tp = _maybe(slots, torch.int32, (self.batch,), "slots")
-        np_ = sp if new_state is None else _field(new_state, torch.float32, state.shape,
-                                                  "new_state")
+        sp = self._at(state, torch.float32, (n,) + self.state_shape[1:], "state")
+        tp = self._maybe_at(slots, torch.int32, (self.batch,), "slots")
+        np_ = sp if new_state is None else self._at(new_state, torch.float32, state.shape,
+                                                    "new_state")
         shape = (self.batch, self.heads, self.dv)
-        if out is None:
-            out = torch.empty(shape, dtype=self.torch_dtype, device=q.device)
-        op = _field(out, self.torch_dtype, shape, "out")
+        out, op = self._out(out, self.torch_dtype, shape, "out")
         check(capi.fno_linattn_step(self.handle, *ptrs, self._scale(scale), tp, n, sp, np_,
-                                    op, _stream(stream, q)), "fno_linattn_step")
+                                    op, self._launch_stream(stream)), "fno_linattn_step")
         return out
 
 
@@ -407,55 +437,12 @@ def _code(codes, key, name):
     return codes[key]
 
 
-class _DevicePlan(_Plan):
-    """A plan of the device that was current when it was made: its calls take that
-    device's tensors while it is the current one."""
-
-    def _own(self, status, handle, name, workspace=True):
-        check(status, f"fno_{name}_plan")
-        self.handle, self._name = handle, name
-        self.workspace, self.workspace_bytes = None, 0
-        if workspace:
-            st, self.workspace_bytes = getattr(capi, f"fno_{name}_workspace_size")(handle)
-            check(st)
-        self.device = torch.cuda.current_device()
-        self._torch_device = torch.device("cuda", self.device)
-
-    def _workspace(self):
-        if self.workspace is None and self.workspace_bytes:
-            self.workspace = self._empty((self.workspace_bytes,), torch.uint8)
-        return _ptr(self.workspace)
+class _TimePlan(_Plan):
+    """A plan of an operator along time."""
 
     def device_error(self, stream=None) -> int:
         """These kernels have no device-side waits or checks to report."""
         return capi.FNO_OK
-
-    def _at(self, t, dtype, shape, name):
-        """t's pointer, once its type, shape, layout and device are those wanted."""
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-                and t.is_contiguous() and t.get_device() == self.device):
-            _require(t, dtype, shape, name)
-            raise ValueError(f"{name} must be on cuda:{self.device}, got {t.device}")
-        return t.data_ptr()
-
-    def _maybe_at(self, t, dtype, shape, name):
-        return None if t is None else self._at(t, dtype, shape, name)
-
-    def _launch_stream(self, stream):
-        if _current_device() != self.device:
-            raise ValueError(f"the plan is of cuda:{self.device}, which is not the current device")
-        if stream is None and _raw_stream is not None:
-            return _raw_stream(self.device)
-        return _stream_handle(stream)
-
-    def _empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self._torch_device)
-
-    def _out(self, t, dtype, shape, name):
-        if t is None:
-            t = self._empty(shape, dtype)
-            return t, t.data_ptr()
-        return t, self._at(t, dtype, shape, name)
 
     def _slots(self, state, new_state, slots, dtype, rest):
         """(number of slots, pointers of slots, state and new state) of a step."""
@@ -469,7 +456,7 @@ class _DevicePlan(_Plan):
         return n, self._maybe_at(slots, torch.int32, (self.batch,), "slots"), sp, np_
 
 
-class Rotary(_DevicePlan):
+class Rotary(_TimePlan):
     """Rotary positions (``fno_rotary_*``): the pairs in the first ``rotary_dim``
     elements (default: all) of every head of q (batch, length, heads, dim) and k
     (batch, length, kv_heads, dim; none for kv_heads=0) turned by position times
@@ -534,7 +521,7 @@ class Rotary(_DevicePlan):
         return self._apply(dq, dk, positions, offsets, q_out, k_out, 1, stream)
 
 
-class CausalConv(_DevicePlan):
+class CausalConv(_TimePlan):
     """y_t = act(bias + sum_j w[:, j] x_{t - width + 1 + j}) for each channel of x
     (batch, length, channels) (``fno_causal_conv_*``).  w (channels, width) and bias
     (channels,) are float32; ``act`` is "silu" or "none"; states (batch, width - 1,
@@ -604,7 +591,7 @@ class CausalConv(_DevicePlan):
         return out
 
 
-class SelectiveScan(_DevicePlan):
+class SelectiveScan(_TimePlan):
     """The selective state space scan (``fno_scan_*``): with d = softplus(dt + dt_bias)
     (or the sum itself for softplus=False),
 
