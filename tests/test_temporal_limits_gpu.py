@@ -1,5 +1,5 @@
 """Convolution, scan and rotary positions at the ends of what their plans take: products of
-sizes that pass 32 bits."""
+sizes that pass 32 bits, workspaces, digits, what lies around the operands, streams."""
 import pytest
 import torch
 
@@ -7,6 +7,7 @@ import ops_ref as R
 import temporal_ref as M
 import test_temporal_edges_gpu as edges
 import test_temporal_ops_gpu as base
+from fft_gemm_ifft_gb300 import capi
 
 pytestmark = pytest.mark.gpu
 
@@ -209,3 +210,291 @@ def test_scan_that_remembers_a_thousand_tokens(pkg, B, T, D):
     first, second = x.double() * s1, (A.double() * e).sum(-1)
     base.close(got["ddt"], (first + second).cpu(), 2 * bound,
                (first.norm() + second.norm()).item())
+
+
+# ---------------------------------------------------------------------------
+# what lies around the operands
+# ---------------------------------------------------------------------------
+ZONE = 4096                                            # bytes in front and behind
+
+
+class Zones:
+    """Operands between zones of bytes 0xff (a NaN in every type), which no call writes; what
+    an operand holds before it is written is NaN as well."""
+
+    def __init__(self):
+        self.bufs = []
+
+    def new(self, nbytes):
+        buf = torch.full((2 * ZONE + -(-nbytes // 256) * 256,), 0xff, dtype=torch.uint8,
+                         device="cuda")
+        self.bufs.append((buf, nbytes))
+        return buf[ZONE:ZONE + nbytes]
+
+    def empty(self, shape, dtype):
+        n = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+        return self.new(n).view(dtype).view(shape)
+
+    def of(self, t):
+        return None if t is None else self.empty(t.shape, t.dtype).copy_(t)
+
+    def check(self):
+        for buf, n in self.bufs:
+            assert (buf[:ZONE] == 0xff).all() and (buf[ZONE + n:] == 0xff).all()
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def ws_of(plan, zones):
+    return zones.new(plan.workspace_bytes).data_ptr() if plan.workspace_bytes else None
+
+
+def same(got, want):
+    for name, t in want.items():
+        assert torch.equal(got[name], t), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(3, 13, 21, 5, 1), (1, 300, 33, 16, 3), (2, 90, 130, 24, 2),
+                                   (5, 17, 10, 4, 5), (1, 700, 7, 64, 7), (300, 9, 34, 16, 1),
+                                   (2, 1, 3, 2, 1)])
+def test_scan_leaves_what_lies_around(pkg, dtype, shape):
+    """Every output and a workspace of exactly its size, filled with NaN beforehand."""
+    B, T, D, N, G = shape
+    t = base.scan_inputs(shape, dtype, True, True, True, True, B > 1, True)
+    c = {k: base.cuda(v) for k, v in t.items()}
+    p = pkg.SelectiveScan(B, T, D, N, groups=G, dtype=dtype, backward=True)
+    more = dict(D=c["D"], z=c["z"], dt_bias=c["bias"], lengths=c["lengths"], state=c["state"])
+    args = [c[k] for k in ("x", "dt", "A", "B", "C")]
+    y, sT = p.forward(*args, want_state=True, **more)
+    back = p.backward(*args, c["dy"], dstate=c["dstate"], **more)
+    zones, s = Zones(), torch.cuda.current_stream().cuda_stream
+    ins = [ptr(zones.of(v)) for v in (*args, c["D"], c["z"], c["bias"], c["lengths"], c["state"])]
+    got = {"y": zones.empty(y.shape, y.dtype), "sT": zones.empty(sT.shape, sT.dtype)}
+    pkg.check(capi.fno_scan_forward(p.handle, *ins, ptr(got["y"]), ptr(got["sT"]),
+                                    ws_of(p, zones), s))
+    got.update({k: zones.empty(v.shape, v.dtype) for k, v in back.items()})
+    order = ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dstate")
+    pkg.check(capi.fno_scan_backward(p.handle, *ins, ptr(zones.of(c["dy"])),
+                                     ptr(zones.of(c["dstate"])), *(ptr(got[k]) for k in order),
+                                     ws_of(p, zones), s))
+    torch.cuda.synchronize()
+    zones.check()
+    same(got, {"y": y, "sT": sT, **back})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(3, 13, 21, 3), (1, 300, 33, 8), (2, 90, 130, 4), (5, 1, 1, 2),
+                                   (300, 9, 34, 5)])
+def test_conv_leaves_what_lies_around(pkg, dtype, shape):
+    B, T, D, W = shape
+    c = {k: base.cuda(v) for k, v in
+         base.conv_inputs(shape, dtype, True, B > 1, True).items()}
+    p = pkg.CausalConv(B, T, D, W, dtype=dtype, backward=True)
+    more = dict(bias=c["bias"], lengths=c["lengths"], state=c["state"])
+    y, sT = p.forward(c["x"], c["w"], want_state=True, **more)
+    back = p.backward(c["x"], c["w"], c["dy"], dstate=c["dstate"], **more)
+    zones, s = Zones(), torch.cuda.current_stream().cuda_stream
+    ins = [ptr(zones.of(c[k])) for k in ("x", "w", "bias", "lengths", "state")]
+    got = {"y": zones.empty(y.shape, y.dtype), "sT": zones.empty(sT.shape, sT.dtype)}
+    pkg.check(capi.fno_causal_conv_forward(p.handle, *ins, ptr(got["y"]), ptr(got["sT"]), s))
+    outs = {k: zones.empty(v.shape, v.dtype) for k, v in zip(("dx", "dw", "db", "ds"), back)}
+    pkg.check(capi.fno_causal_conv_backward(
+        p.handle, *ins, ptr(zones.of(c["dy"])), ptr(zones.of(c["dstate"])),
+        *(ptr(v) for v in outs.values()), ws_of(p, zones), s))
+    torch.cuda.synchronize()
+    zones.check()
+    same({**got, **outs}, {"y": y, "sT": sT, **dict(zip(outs, back))})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,N,G,W", [(21, 5, 1, 3), (34, 16, 2, 4), (3, 64, 3, 8), (1, 1, 1, 2)])
+def test_steps_leave_what_lies_around(pkg, dtype, D, N, G, W):
+    B, slots = 4, 6
+    at = torch.tensor([5, -1, 0, 6], dtype=torch.int32).cuda()            # two rows are idle
+    t = {k: base.cuda(v) for k, v in base.scan_inputs(
+        (B, 1, D, N, G), dtype, True, True, True, True, False, False).items()}
+    row = [t[k][:, 0].contiguous() for k in ("x", "dt", "B", "C", "z")]
+    s = torch.cuda.current_stream().cuda_stream
+    scan = pkg.SelectiveScan(B, 1, D, N, groups=G, dtype=dtype)
+    conv = pkg.CausalConv(B, 1, D, W, dtype=dtype)
+    state = torch.randn(slots, D, N, device="cuda")
+    inputs = torch.randn(slots, W - 1, D, device="cuda").to(row[0].dtype)
+    w, bias = torch.randn(D, W, device="cuda"), torch.randn(D, device="cuda")
+    h, u = state.clone(), inputs.clone()
+    y = scan.step(row[0], row[1], t["A"], row[2], row[3], h, D=t["D"], z=row[4],
+                  dt_bias=t["bias"], slots=at)
+    v = conv.step(row[0], w, u, bias=bias, slots=at)
+    zones = Zones()
+    oy, ov = zones.empty(y.shape, y.dtype), zones.empty(v.shape, v.dtype)
+    nh, nu = zones.of(state), zones.of(inputs)
+    ins = [ptr(zones.of(x)) for x in (row[0], row[1], t["A"], row[2], row[3], t["D"], row[4],
+                                      t["bias"], at)]
+    pkg.check(capi.fno_scan_step(scan.handle, *ins, slots, ptr(zones.of(state)), ptr(nh), ptr(oy),
+                                 s))
+    pkg.check(capi.fno_causal_conv_step(
+        conv.handle, *(ptr(zones.of(x)) for x in (row[0], w, bias, at)), slots,
+        ptr(zones.of(inputs)), ptr(nu), ptr(ov), s))
+    torch.cuda.synchronize()
+    zones.check()
+    same({"y": oy, "v": ov, "h": nh, "u": nu}, {"y": y, "v": v, "h": h, "u": u})
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("shape", [(3, 13, 3, 2, 7, 4), (1, 65, 5, 1, 20, 10),
+                                   (2, 9, 4, 4, 64, 64)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rotary_leaves_what_lies_around(pkg, dtype, shape, layout):
+    B, T, H, K, dim, r = shape
+    g = base.gen(7)
+    q = base.rand(g, (B, T, H, dim), dtype).cuda()
+    k = base.rand(g, (B, T, K, dim), dtype).cuda()
+    off = torch.arange(B, dtype=torch.int32).cuda() * 1000
+    p = pkg.Rotary(B, T, H, K, dim, rotary_dim=r, layout=layout, dtype=dtype)
+    want = dict(zip("qk", p.forward(q, k, offsets=off)))
+    zones = Zones()
+    got = {n: zones.empty(v.shape, v.dtype) for n, v in want.items()}
+    pkg.check(capi.fno_rotary_apply(p.handle, ptr(zones.of(q)), ptr(zones.of(k)), None,
+                                    ptr(zones.of(off)), 0, ptr(got["q"]), ptr(got["k"]),
+                                    torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    zones.check()
+    same(got, want)
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+def test_calls_go_to_the_stream_they_are_given(pkg):
+    """Inputs that arrive late on a side stream: a call that went to the current stream in place
+    of stream= would have read what was there before."""
+    B, T, D, N, W, H = 2, 300, 72, 16, 4, 9
+    t = {k: base.cuda(v) for k, v in base.scan_inputs(
+        (B, T, D, N, 1), "bf16", True, True, True, True, False, True).items()}
+    w, busy = torch.randn(D, W, device="cuda"), torch.randn(4096, 4096, device="cuda")
+    scan = pkg.SelectiveScan(B, T, D, N, dtype="bf16", backward=True)
+    conv = pkg.CausalConv(B, T, D, W, dtype="bf16", backward=True)
+    one, first = pkg.SelectiveScan(B, 1, D, N, dtype="bf16"), pkg.CausalConv(B, 1, D, W,
+                                                                             dtype="bf16")
+    rot = pkg.Rotary(B, T, H, 0, D // H, dtype="bf16")
+    h, u = t["state"].clone(), torch.ones(B, W - 1, D, device="cuda").bfloat16()
+    x = torch.zeros_like(t["x"])
+    rows = {k: t[k][:, 0].contiguous() for k in ("x", "dt", "B", "C")}
+    x0 = torch.zeros_like(rows["x"])
+    args = (t["dt"], t["A"], t["B"], t["C"])
+    CALLS = {
+        "conv": lambda s: conv.forward(x, w, want_state=True, stream=s),
+        "conv.backward": lambda s: conv.backward(x, w, t["dy"], stream=s)[:2],
+        "conv.step": lambda s: (first.step(x0, w, u, new_state=torch.empty_like(u), stream=s),),
+        "scan": lambda s: scan.forward(x, *args, state=t["state"], want_state=True, stream=s),
+        "scan.backward": lambda s: tuple(scan.backward(x, *args, t["dy"], stream=s).values()),
+        "scan.step": lambda s: (one.step(x0, rows["dt"], t["A"], rows["B"], rows["C"], h,
+                                         new_state=torch.empty_like(h), stream=s),),
+        "rotary": lambda s: (rot.forward(x.view(B, T, H, D // H), stream=s)[0],),
+        "rotary.backward": lambda s: (rot.backward(x.view(B, T, H, D // H), stream=s)[0],),
+    }
+    side, current = torch.cuda.Stream(), torch.cuda.current_stream()
+    for name, call in CALLS.items():
+        x.copy_(t["x"])
+        x0.copy_(rows["x"])
+        want = [v.clone() for v in call(None)]
+        x.zero_()
+        x0.zero_()
+        zero = [v.clone() for v in call(None)]
+        assert any(not torch.equal(a, b) for a, b in zip(want, zero)), name
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(30):                                 # some milliseconds
+                torch.mm(busy, busy)
+            x.copy_(t["x"])
+            x0.copy_(rows["x"])
+        got = call(side)
+        current.wait_stream(side)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), name
+        torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# offsets of more than 31 bits
+# ---------------------------------------------------------------------------
+def test_scan_and_conv_rows_of_more_than_31_bits(pkg):
+    """2^31 + 2^27 elements a field, and twice as many in the states that the backward keeps:
+    the first and the last sequence have the same tokens and give the same bits; those between
+    have none."""
+    room(100)
+    B, T, D, N = 17, 1 << 17, 1 << 10, 16
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lengths[0] = lengths[-1] = T
+
+    def rows(*width, scale=1.0, mean=0.0):
+        t = torch.full((B, T, *width), float("nan"), dtype=torch.bfloat16, device="cuda")
+        t[0] = mean + scale * torch.randn(T, *width, device="cuda")
+        t[-1] = t[0]
+        return t
+
+    def check(t, name):
+        assert torch.isfinite(t[0]).all() and t[0].any(), name
+        assert torch.equal(t[0], t[-1]), name
+        for row in t[1:-1]:
+            assert not row.any(), name
+
+    x, dy = rows(D), rows(D)
+    w = torch.randn(D, 4, device="cuda")
+    conv = pkg.CausalConv(B, T, D, 4, dtype="bf16", backward=True)
+    check(conv.forward(x, w, lengths=lengths)[0], "conv")
+    dx, dw, _, _ = conv.backward(x, w, dy, lengths=lengths)
+    check(dx, "conv dx")
+    assert torch.isfinite(dw).all()
+    del dx, conv
+    dt, Bm, Cm = rows(D, scale=0.5, mean=-2.0), rows(1, N), rows(1, N)
+    A = -(0.5 + torch.rand(D, N, device="cuda"))
+    scan = pkg.SelectiveScan(B, T, D, N, dtype="bf16", backward=True)
+    y, sT = scan.forward(x, dt, A, Bm, Cm, lengths=lengths, want_state=True)
+    check(y, "y")
+    check(sT, "state")
+    del y
+    for name, t in scan.backward(x, dt, A, Bm, Cm, dy, lengths=lengths).items():
+        if name == "dA":
+            assert torch.isfinite(t).all()
+        else:
+            check(t, name)
+
+
+def test_slots_of_more_than_31_bits(pkg):
+    """States of 2^31 elements and more: a slot behind them is as one in front."""
+    room(40)
+    D, N, W = 1024, 64, 8
+    slots = (1 << 31) // (D * N) + 3
+    state = torch.zeros(slots, D, N, device="cuda")
+    state[0] = torch.randn(D, N, device="cuda")
+    state[-1] = state[0]
+    g = base.scan_inputs((1, 1, D, N, 1), "bf16", True, True, True, True, False, False)
+    row = {k: (v[:, 0] if k in ("x", "dt", "B", "C", "z") else v).cuda()
+           for k, v in g.items() if v is not None}
+    two = {k: row[k].expand(2, *row[k].shape[1:]).contiguous()
+           for k in ("x", "dt", "B", "C", "z")}
+    at = torch.tensor([0, slots - 1], dtype=torch.int32).cuda()
+    p = pkg.SelectiveScan(2, 1, D, N, dtype="bf16")
+    before = state[0].clone()
+    y = p.step(two["x"], two["dt"], row["A"], two["B"], two["C"], state, D=row["D"], z=two["z"],
+               dt_bias=row["bias"], slots=at)
+    assert torch.equal(y[0], y[1]) and torch.equal(state[0], state[-1])
+    assert not torch.equal(state[0], before)
+    for part in state[1:-1].split(4096):
+        assert not part.any()
+    del state
+    slots = (1 << 31) // (D * (W - 1)) + 3
+    inputs = torch.zeros(slots, W - 1, D, dtype=torch.bfloat16, device="cuda")
+    inputs[0] = torch.randn(W - 1, D, device="cuda")
+    inputs[-1] = inputs[0]
+    old = inputs[0].clone()
+    at = torch.tensor([0, slots - 1], dtype=torch.int32).cuda()
+    y = pkg.CausalConv(2, 1, D, W, dtype="bf16").step(two["x"], torch.randn(D, W, device="cuda"),
+                                                      inputs, slots=at)
+    assert torch.equal(y[0], y[1]) and torch.equal(inputs[0], inputs[-1])
+    assert torch.equal(inputs[0, :-1], old[1:]) and torch.equal(inputs[0, -1], two["x"][0])
+    for part in inputs[1:-1].split(65536):
+        assert not part.any()
