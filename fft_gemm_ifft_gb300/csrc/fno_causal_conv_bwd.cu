@@ -10,9 +10,14 @@ namespace {
 // inputs again; then dx_s = sum_j w_j g_{s + W - 1 - j}, for which a run goes on W - 1
 // tokens, and dw_j = sum_t g_t x_{t - W + 1 + j}.  A block takes every `parts`-th group of
 // runs and leaves one sum of its dw and dbias.  Neighbouring blocks have neighbouring channels
-// (4 x 8192 tokens of 2048 channels in bfloat16: 173 us; 196 with neighbouring runs), but runs
+// (4 x 8192 tokens of 2048 channels in bfloat16: 175 us; 198 with neighbouring runs), but runs
 // where rows are odd and read by elements (5 x 4099 tokens of 1001 channels in fp16, ragged:
-// 51 us, the kernel 45; 56 with neighbouring channels).
+// 51 us, the kernel 45; 56 with neighbouring channels.  Without ragged ends it is the other way
+// round: 75 and 73 us; 4 x 8192 of 2047 in bfloat16: 235 and 202; 8 x 2048 of 4095 in float32:
+// 237 and 212).
+//
+// Far from its bytes (59 us for these 2048 channels): x and dy of 4 tokens in registers are 24 KB
+// an SM on their way, of 2 tokens above 4 taps 8 KB (8 taps in fp16: 323 us).
 template <typename T, bool WIDE, int W>
 __global__ void __launch_bounds__(kThreads, grad_blocks(W, sizeof(T)))
 k_conv_grad(const Args p) {

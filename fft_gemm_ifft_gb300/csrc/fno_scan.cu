@@ -206,7 +206,16 @@ Sizes sizes(const fno_scan_desc_t &d, int64_t length) {
 
 // Segments of the time axis, multiples of `unit` tokens: one where the sequences and
 // channels alone give the SMs half of `warps` each, else as many as give them all, of 64
-// tokens at least (a segment costs a second pass over its tokens).
+// tokens at least (a segment costs a second pass over its tokens).  A call, forward and
+// gradients, by the rule and in one segment, 16 states:
+//   1 x 1000 tokens of 64 channels, bf16       16 segments:  63, 102 us; one: 444, 860
+//   8 x 200 of 256, f32                         4 segments:  63, 110 us; one:  98, 198
+//   16 x 300 of 512, bf16                       5 segments:  85, 165 us; one: 137, 281
+//   32 x 512 of 1024, bf16                      3 segments: 263, 773 us; one: 235, 563
+//   16 x 128 of 1024, bf16                      2 segments:  95, 198 us; one:  66, 131
+//   64 x 100 of 512, bf16                       2 segments: 138, 306 us; one:  54, 128
+// so four and more pay, and two or three, whose two passes are hardly shorter together than the
+// one, lose.
 void split(int64_t length, int64_t warps_there, int64_t warps, int unit, int64_t *seg_len,
            int *segments) {
     int64_t segs = 2 * warps_there >= warps ? 1 : warps / warps_there;

@@ -15,10 +15,10 @@
 As in the rest of the package, the classes marshal arguments: a plan, a
 workspace from torch, tensor pointers and the current stream.  A plan is of the
 device that was current when it was made, and takes that device's tensors while it
-is the current one.  A plan object holds one workspace, so calls on it have to be ordered (one stream).  A call with
-``stream=`` is launched there and allocates its results on the current stream:
-that stream has to wait for the current one's work before the call, and the
-current one for it before the results are used or dropped.
+is the current one.  A plan object holds one workspace, so calls on it have to be
+ordered (one stream).  A call with ``stream=`` is launched there and allocates its
+results on the current stream: that stream has to wait for the current one's work
+before the call, and the current one for it before the results are used or dropped.
 """
 from __future__ import annotations
 

@@ -266,8 +266,9 @@ fno_status_t fno_linattn_destroy(fno_linattn_t plan);
  *                      more over `original` positions has k = 1 (it stays), one that makes
  *                      `slow` or fewer k = 0, and k is linear in the turns between;
  *                      m = 1 + 0.1 log(factor)
- * Angles are exact to 2^-32 of a turn and to what f_i's 53 bits give at any position of
- * 32 bits; cosines and sines are float32's (for 16-bit types good to 2^-20).
+ * A position's fraction of a turn is exact to 2^-32 of a turn and to what f_i's 53 bits give at
+ * any position of 32 bits, then rounded to float32 (2^-26 of a turn at most); cosines and sines
+ * are float32's (for 16-bit types good to 2^-20).
  * ------------------------------------------------------------------------- */
 typedef enum fno_rotary_layout_e {
     FNO_ROTARY_HALF = 0, FNO_ROTARY_INTERLEAVED = 1
@@ -324,7 +325,8 @@ typedef struct fno_causal_conv_s *fno_causal_conv_t;
 
 #define FNO_CAUSAL_CONV_BACKWARD 1u   /* the workspace is that of the backward              */
 
-/* batch, length, channels >= 1, length below 2^31 - 64; 2 <= width <= 8.
+/* batch, length, channels >= 1, length below 2^31 - 64, channels up to 65535 x 64;
+ * 2 <= width <= 8.
  * Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_MEMORY, CUDA.                      */
 fno_status_t fno_causal_conv_plan(fno_causal_conv_t *plan, int64_t batch, int64_t length,
                                   int32_t channels, int32_t width, fno_act_t act,
