@@ -13,9 +13,9 @@
 // bfloat16: 58 us, 5.8 TB/s; 3 x 4097, 24 heads of 80 in float32: 30 us, 6.3 TB/s, where a
 // thread for one vector of every head, with the sines in registers, takes 1.4 times as long).
 // A vector is as wide as divides the head and the pairs' sides, so that sides of an odd count
-// take one element a unit and twice an odd count two, a unit as many instructions as of eight
-// (4 x 8192, 20 heads of 64 in bfloat16: 40 us a call with all 64 turned, 97 with 42; heads of
-// 80: 53 with all turned, 73 with 52).
+// take one element a vector and twice an odd count two, which costs time (4 x 8192, 20 heads of
+// 64 in bfloat16: 40 us a call with all 64 turned, 97 with 42; heads of 80: 53 with all turned,
+// 73 with 52).
 #include "fno_ops_internal.h"
 
 #include <cmath>

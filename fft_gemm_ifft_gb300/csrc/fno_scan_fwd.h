@@ -41,11 +41,11 @@ namespace scan {
 enum Mode { kFull, kStates, kBack };
 // 16 states take 168 registers, so an SM holds 12 warps; at 128 registers and 16 warps some are
 // spilled (8191 tokens of 2048 channels: a call of 192 us; 165 at 168).  Short sequences, which
-// are mostly the latency of their first loads, take the 16 warps all the same (2048 x 12 tokens
-// of 64 channels in float32: 26 us, at 168 28; 4096 x 30 of 32: 50 and 67; 512 x 20 of 256 in
-// bfloat16: 31 and 32; but 64 x 30 of 4096: 64 and 58; 1024 x 64 of 64: 63 and 43).  Fewer states have less to hold: 8 in 112
-// registers, 4 in 96 (the same tokens, 8 states: 123 us, with 168 registers 159; 4 in float32:
-// 108 us, 177).
+// are mostly the latency of their first loads, take the 16 warps all the same (2048 x 12 tokens of
+// 64 channels in float32: 26 us, at 168 28; 4096 x 30 of 32: 50 and 67; 512 x 20 of 256 in
+// bfloat16: 31 and 32; but 64 x 30 of 4096: 64 and 58; 1024 x 64 of 64: 63 and 43).  Fewer states
+// have less to hold: 8 in 112 registers, 4 in 96 (8191 tokens of 2048 channels, 8 states: 123 us,
+// with 168 registers 159; 4 in float32: 108 us, 177).
 constexpr int kShort = 32;
 template <typename T, int NS, Mode M, int REGS>
 __global__ void __maxnreg__(REGS)

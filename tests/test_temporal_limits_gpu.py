@@ -498,3 +498,25 @@ def test_slots_of_more_than_31_bits(pkg):
     assert torch.equal(inputs[0, :-1], old[1:]) and torch.equal(inputs[0, -1], two["x"][0])
     for part in inputs[1:-1].split(65536):
         assert not part.any()
+
+
+# ---------------------------------------------------------------------------
+# one more way of dividing a scan's work
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("shape", [(400, 130, 4, 16, 1), (160, 200, 70, 16, 1),
+                                   (100, 70, 6, 40, 2)])
+def test_scan_split_in_front_of_one_span(pkg, dtype, ragged, shape):
+    """Sequences that fill the last pass backward without a split in time but not the passes in
+    front of it, which are split: the gradient of the final state goes past the segments."""
+    t = base.scan_inputs(shape, dtype, True, True, True, True, ragged, True)
+    got, want, parts = edges.scan_call(pkg, t, shape, dtype)
+    f32, stored = R.tol("f32") + base.SCAN_EXTRA, R.tol(dtype) + base.SCAN_EXTRA
+    for name, ref in want.items():
+        # sums of terms of either sign: against the terms
+        scale = {"ddt": parts, "ddt_bias": parts, "dA": parts,
+                 "dD": (t["dy"].double().norm() * 0.5).item(),
+                 "dB": want["dB"].norm().item() + 1e-3}.get(name)
+        base.close(got[name], ref, stored if name in ("y", "dx", "ddt", "dB", "dC", "dz")
+                   else f32, scale)
